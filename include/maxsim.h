@@ -371,6 +371,175 @@ maxsim_status maxsim_backward_dd(const void *Q, int n_queries, int nq, int d,
                                  maxsim_dtype dtype, const int32_t *argmax, const float *dS,
                                  float *dD, void *stream);
 
+/*
+ * Operators of the token encoder whose embeddings MaxSim scores. They work on
+ * the CSR layout of maxsim_score_varlen: T packed tokens, document b owning
+ * tokens offsets[b] .. offsets[b+1]-1 (offsets[0] = 0, offsets[B] = T, int64).
+ * A padded batch [B, nd] is the same with offsets[b] = b * nd.
+ *
+ * maxsim_heads is a [T, heads, d] view of device memory with d contiguous
+ * elements and any token and head strides (in elements), so that q, k and v may
+ * lie side by side in one projection's output. The struct itself is on the
+ * host.
+ */
+typedef struct maxsim_heads {
+    void *data;
+    int64_t token_stride;
+    int64_t head_stride;
+} maxsim_heads;
+
+/*
+ * maxsim_rotary_frequencies -- the table of maxsim_rotary, on the HOST (no
+ * device call): freq_host[i], i < rot_dim / 2, is the turn of pair i from one
+ * position to the next, in units of 2^-64 of a whole turn.
+ *   theta_i = base^(-2i / rot_dim) radians, and with a factor s:
+ *   NONE    theta_i
+ *   LINEAR  theta_i / s (positions are interpolated)
+ *   NTK     theta_i with base * s^(rot_dim / (rot_dim - 2))
+ *   YARN    theta_i for pairs that turn often within original_length
+ *           positions, theta_i / s for those that turn less than once, a
+ *           linear ramp over i between them ("YaRN: Efficient Context Window
+ *           Extension of Large Language Models", 3.2, with 32 turns and 1)
+ * *amplitude receives 1, or 0.1 ln s + 1 for YARN (ibid., 3.4).
+ * rot_dim even and >= 2 (>= 4 for NTK), base > 1, s >= 1, original_length >= 1
+ * for YARN; otherwise MAXSIM_ERR_INVALID_ARG.
+ */
+typedef enum maxsim_rotary_scaling {
+    MAXSIM_ROTARY_NONE = 0,
+    MAXSIM_ROTARY_LINEAR = 1,
+    MAXSIM_ROTARY_NTK = 2,
+    MAXSIM_ROTARY_YARN = 3
+} maxsim_rotary_scaling;
+maxsim_status maxsim_rotary_frequencies(int rot_dim, double base, maxsim_rotary_scaling scaling,
+                                        double factor, int64_t original_length,
+                                        uint64_t *freq_host, float *amplitude);
+
+/*
+ * maxsim_rotary -- turns pair i of every head of token t by
+ * position(t) * freq[i]:
+ *   y1 = amplitude * (x1 cos - x2 sin),  y2 = amplitude * (x2 cos + x1 sin)
+ * with (x1, x2) = (x[i], x[i + rot_dim/2]), or (x[2i], x[2i+1]) when
+ * `interleaved` is not 0. Dimensions rot_dim .. d-1 are copied. `inverse` not
+ * 0 turns the other way: the gradient of the call with the same arguments.
+ *
+ *   x, out     [T, heads, d] views, dtype BF16, FP16 or FP32, aligned to their
+ *              elements; out may be x (same strides), and may not overlap it
+ *              otherwise
+ *   freq       [rot_dim / 2] uint64, device
+ *   offsets    [B+1] int64: positions count from each document's start; a
+ *              token outside every document, or in one with inconsistent
+ *              offsets, has position 0 and sets MAXSIM_DEVERR_BAD_INPUT
+ *   positions  [T] int32: positions as given (not with offsets). With neither,
+ *              token t has position t.
+ *
+ * Arithmetic is fp32, rounded once. The angle is made in 64-bit integers from
+ * the position, so it is as exact at position 10^6 as at 1.
+ * Limits: rot_dim even, 2 <= rot_dim <= d, d <= 4096, T < 2^31, heads <= 65535.
+ */
+maxsim_status maxsim_rotary(const maxsim_heads *x, int64_t T, int heads, int d, int rot_dim,
+                            const uint64_t *freq, const int64_t *offsets, int64_t B,
+                            const int32_t *positions, int interleaved, float amplitude, int inverse,
+                            maxsim_dtype dtype, const maxsim_heads *out, void *stream);
+
+/*
+ * maxsim_attention -- softmax attention within each packed document.
+ * With i and j counted within document b, and z over the keys that row i sees:
+ *   s_ij = scale * <q_i, k_j>
+ *   c_ij = cap * tanh(s_ij / cap) if cap > 0, else s_ij
+ *   z_ij = c_ij - slopes[h] * |i - j|   (slopes NULL: 0)
+ *   lse_i = ln(sum_j exp z_ij),  out_i = sum_j exp(z_ij - lse_i) v_j
+ * Row i sees key j if j < key_len[b] (NULL: the document's length) and
+ *   FULL     always
+ *   CAUSAL   j <= i
+ *   PREFIX   j <= i or j < prefix_len[b]
+ * Every token is a row, those at or past key_len[b] too (a query's mask
+ * tokens). A row that sees nothing (key_len[b] = 0) has out 0 and lse
+ * -infinity.
+ * Query head h reads key-value head h / (heads / kv_heads).
+ *
+ *   q, out     [T, heads, d] views; k, v [T, kv_heads, d] views
+ *   lse        [heads, T] fp32, or NULL; maxsim_attention_backward needs it
+ *
+ * Scores, softmax statistics and sums are fp32 on tensor-core products of the
+ * inputs; the weights are rounded to the inputs' type for their product with
+ * v. Keys at or past key_len[b], and other documents, never reach a row, even
+ * if they hold NaN or infinity. (A key that is hidden from a row only by the
+ * order of tokens has weight 0 there, so its v must be finite.)
+ *
+ * Limits: dtype BF16 or FP16 (FP32 returns MAXSIM_ERR_UNSUPPORTED); d a
+ * multiple of 8, 8 <= d <= 128; heads a multiple of kv_heads, heads <= 65535;
+ * T < 2^31 - 256; B < 2^31; scale > 0; all views 16-byte aligned with strides that are
+ * multiples of 8 elements, positive and below 2^39. out may overlap no input.
+ * Inconsistent offsets, a key_len outside [0, length] (clamped) or a negative
+ * prefix_len (taken as 0) set MAXSIM_DEVERR_BAD_INPUT; a document whose offsets
+ * leave [0, T], or with a decrease at its start or end, is skipped. Rows outside every document are not
+ * written.
+ */
+typedef enum maxsim_mask {
+    MAXSIM_MASK_FULL = 0,
+    MAXSIM_MASK_CAUSAL = 1,
+    MAXSIM_MASK_PREFIX = 2
+} maxsim_mask;
+
+typedef struct maxsim_attention_spec {
+    int64_t T, B;
+    int32_t heads, kv_heads, d;
+    maxsim_dtype dtype;
+    maxsim_mask mask;
+    float scale;
+    float cap;                  /* <= 0: scores are not capped */
+    const int64_t *offsets;     /* [B+1], device */
+    const int32_t *key_len;     /* [B], device, or NULL */
+    const int32_t *prefix_len;  /* [B], device; PREFIX only */
+    const float *slopes;        /* [heads], device, or NULL */
+} maxsim_attention_spec;
+
+maxsim_status maxsim_attention(const maxsim_attention_spec *spec, const maxsim_heads *q, const maxsim_heads *k,
+                               const maxsim_heads *v, const maxsim_heads *out, float *lse, void *stream);
+
+/*
+ * maxsim_attention_backward -- gradients of maxsim_attention, from its out
+ * and lse and the gradient dO of out:
+ *   dV_j = sum_i p_ij dO_i,  dP_ij = <dO_i, v_j>,  p_ij = exp(z_ij - lse_i)
+ *   dS_ij = p_ij (dP_ij - <dO_i, out_i>) (1 - (c_ij / cap)^2) scale
+ *   dQ_i = sum_j dS_ij k_j,  dK_j = sum_i dS_ij q_i
+ * dK and dV of a key-value head are the sums over its query heads. dQ, dK and
+ * dV [T, heads or kv_heads, d] have the inputs' dtype and are written once by
+ * the block that owns the row: no atomics, results do not depend on
+ * scheduling. Rows that see nothing and hidden keys have gradient 0. Slopes
+ * are constants.
+ * Sums are fp32; p and dS are rounded to the inputs' type for their products.
+ * Limits as in maxsim_attention, for dO and the gradients too. workspace: at least
+ * maxsim_attention_backward_workspace_size(spec) bytes, 16-byte aligned.
+ */
+size_t maxsim_attention_backward_workspace_size(const maxsim_attention_spec *spec);
+maxsim_status maxsim_attention_backward(const maxsim_attention_spec *spec, const maxsim_heads *dO,
+                                        const maxsim_heads *q, const maxsim_heads *k, const maxsim_heads *v,
+                                        const maxsim_heads *out, const float *lse, const maxsim_heads *dq,
+                                        const maxsim_heads *dk, const maxsim_heads *dv, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
+/*
+ * maxsim_clip_grad_norm -- the global 2-norm of many gradient tensors, and
+ * their clipping:
+ *   norm = sqrt(sum of all squares),  out = grad * min(1, max_norm / (norm + 1e-6))
+ * The four arrays are on the HOST and are read before the call returns;
+ * grads[i] and outs[i] are device pointers to sizes[i] contiguous elements of
+ * dtypes[i] (a maxsim_dtype; types may be mixed), aligned to their elements.
+ * outs[i] may be grads[i] (in place), and overlaps no other tensor otherwise.
+ * *norm (device, fp32) receives the norm before clipping. Squares are added in
+ * fp32 within a thread's part of a 64 KB chunk and in fp64 beyond, in an order that depends
+ * only on the sizes; values whose squares leave fp32's range are added in fp64.
+ * A NaN makes norm and all outputs NaN; an infinity makes norm infinite, itself
+ * NaN and every finite element 0.
+ * workspace: at least maxsim_clip_grad_norm_workspace_size(n_tensors) bytes,
+ * 16-byte aligned. n_tensors may be 0 (norm 0).
+ */
+size_t maxsim_clip_grad_norm_workspace_size(int n_tensors);
+maxsim_status maxsim_clip_grad_norm(const void *const *grads, void *const *outs, const int64_t *sizes,
+                                    const int32_t *dtypes, int n_tensors, float max_norm, float *norm,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -14,6 +14,8 @@ Operator (TileMaxSim deep reading §1; FLASH-MAXSIM, Abstract):
 from __future__ import annotations
 
 import ctypes
+import math
+import operator
 import os
 
 import torch
@@ -25,6 +27,8 @@ __all__ = [
     "maxsim_score_pq", "maxsim_score_pq_workspace_size", "maxsim_score_i8", "maxsim_backward",
     "maxsim_backward_workspace_size", "maxsim_backward_dq", "maxsim_backward_dd", "maxsim_device_status",
     "maxsim_version", "allreduce_dq",
+    "maxsim_rotary_frequencies", "maxsim_rotary", "maxsim_attention", "maxsim_attention_backward",
+    "maxsim_attention_backward_workspace_size", "maxsim_clip_grad_norm", "maxsim_clip_grad_norm_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -48,7 +52,26 @@ EXPORTS = (
     "maxsim_score_pq_workspace_size", "maxsim_score_pq", "maxsim_score_pq_noalloc",
     "maxsim_score_i8",
     "maxsim_backward_workspace_size", "maxsim_backward", "maxsim_backward_dq", "maxsim_backward_dd",
+    "maxsim_rotary_frequencies", "maxsim_rotary", "maxsim_attention",
+    "maxsim_attention_backward_workspace_size", "maxsim_attention_backward",
+    "maxsim_clip_grad_norm_workspace_size", "maxsim_clip_grad_norm",
 )
+
+ROTARY_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+MASKS = {"full": 0, "causal": 1, "prefix": 2}
+
+
+class _Heads(ctypes.Structure):
+    """maxsim_heads: a [T, heads, d] view, strides in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _AttentionSpec(ctypes.Structure):
+    """maxsim_attention_spec."""
+    _fields_ = [("T", ctypes.c_int64), ("B", ctypes.c_int64), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("dtype", ctypes.c_int), ("mask", ctypes.c_int), ("scale", ctypes.c_float),
+                ("cap", ctypes.c_float), ("offsets", ctypes.c_void_p), ("key_len", ctypes.c_void_p),
+                ("prefix_len", ctypes.c_void_p), ("slopes", ctypes.c_void_p)]
 
 
 class MaxSimError(RuntimeError):
@@ -112,6 +135,21 @@ def load_library():
     lib.maxsim_backward_dq.argtypes = [I32, I32, I32, P, I64, I32, P, I32, P, P, P, P, SZ, P]
     lib.maxsim_backward_dd.restype = I32
     lib.maxsim_backward_dd.argtypes = [P, I32, I32, I32, I64, I32, P, I32, P, P, P, P]
+    HP, SP, F32 = ctypes.POINTER(_Heads), ctypes.POINTER(_AttentionSpec), ctypes.c_float
+    lib.maxsim_rotary_frequencies.restype = I32
+    lib.maxsim_rotary_frequencies.argtypes = [I32, ctypes.c_double, I32, ctypes.c_double, I64, P, ctypes.POINTER(F32)]
+    lib.maxsim_rotary.restype = I32
+    lib.maxsim_rotary.argtypes = [HP, I64, I32, I32, I32, P, P, I64, P, I32, F32, I32, I32, HP, P]
+    lib.maxsim_attention.restype = I32
+    lib.maxsim_attention.argtypes = [SP, HP, HP, HP, HP, P, P]
+    lib.maxsim_attention_backward_workspace_size.restype = SZ
+    lib.maxsim_attention_backward_workspace_size.argtypes = [SP]
+    lib.maxsim_attention_backward.restype = I32
+    lib.maxsim_attention_backward.argtypes = [SP, HP, HP, HP, HP, HP, P, HP, HP, HP, P, SZ, P]
+    lib.maxsim_clip_grad_norm_workspace_size.restype = SZ
+    lib.maxsim_clip_grad_norm_workspace_size.argtypes = [I32]
+    lib.maxsim_clip_grad_norm.restype = I32
+    lib.maxsim_clip_grad_norm.argtypes = [P, P, P, P, I32, F32, P, P, SZ, P]
     _lib = lib
     return lib
 
@@ -486,3 +524,207 @@ def allreduce_dq(dQ, group=None):
         return dQ
     dist.all_reduce(dQ, op=dist.ReduceOp.SUM, group=group)
     return dQ
+
+
+# --------------------------------------------------------- the token encoder
+
+def _heads(t, name, shape, dtype, device):
+    """A [T, heads, d] CUDA tensor, its last dimension contiguous, as a maxsim_heads."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    token, head, last = t.stride()
+    if last != 1 and shape[2] != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if shape[1] == 1:  # the stride of a dimension of one element says nothing
+        head = shape[2]
+    if shape[0] == 1:
+        token = shape[1] * max(head, shape[2])
+    return _Heads(t.data_ptr(), token, head)
+
+
+def maxsim_rotary_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, original_length=0, device="cuda"):
+    """Frequency table of maxsim_rotary: (freq [rot_dim/2] int64 on ``device``,
+    amplitude). freq is in turns per position times 2^64. ``scaling``: "none",
+    "linear", "ntk" or "yarn" (which needs the ``original_length``), by ``factor``."""
+    lib = load_library()
+    if scaling not in ROTARY_SCALING:
+        raise ValueError(f"scaling must be one of {tuple(ROTARY_SCALING)}")
+    freq = torch.empty(max(rot_dim // 2, 1), dtype=torch.int64)
+    amplitude = ctypes.c_float(0.0)
+    st = lib.maxsim_rotary_frequencies(rot_dim, base, ROTARY_SCALING[scaling], factor, original_length, _ptr(freq),
+                                       ctypes.byref(amplitude))
+    _check(st, "maxsim_rotary_frequencies")
+    return freq.to(device), amplitude.value
+
+
+def maxsim_rotary(x, freq, offsets=None, positions=None, interleaved=False, amplitude=1.0, inverse=False, out=None,
+                  stream=None):
+    """Rotary positions: turns the first 2 * len(freq) dimensions of every head
+    of x [T, heads, d] (bf16/fp16/fp32; token and head strides may be any).
+    Positions count within the documents of ``offsets`` [B+1] int64, or are
+    ``positions`` [T] int32, or the token's index. ``inverse=True`` gives the
+    gradient. ``out`` may be x itself; a new tensor is made without it."""
+    lib = load_library()
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("x must be a [T, heads, d] tensor")
+    if x.dtype not in _DTYPE_CODE:
+        raise TypeError(f"x must be bf16, fp16 or fp32, got {x.dtype}")
+    src = _heads(x, "x", x.shape, x.dtype, x.device)
+    _dev(freq, "freq", torch.int64)
+    T, heads, d = x.shape
+    B = 0
+    if offsets is not None:
+        B = _dev(offsets, "offsets", torch.int64).numel() - 1
+    if positions is not None and _dev(positions, "positions", torch.int32).numel() != T:
+        raise ValueError("positions must have one entry a token")
+    if out is None:
+        out = torch.empty((T, heads, d), dtype=x.dtype, device=x.device)
+    dst = src if out is x else _heads(out, "out", x.shape, x.dtype, x.device)
+    st = lib.maxsim_rotary(src, T, heads, d, 2 * freq.numel(), freq.data_ptr(), _ptr(offsets), B, _ptr(positions),
+                           1 if interleaved else 0, amplitude, 1 if inverse else 0, _DTYPE_CODE[x.dtype], dst,
+                           _stream(stream))
+    _check(st, "maxsim_rotary")
+    return out
+
+
+def _attention_spec(q, k, offsets, key_len, mask, prefix_len, scale, cap, slopes):
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [T, heads, d] tensors")
+    if q.dtype not in _DTYPE_CODE:
+        raise TypeError(f"q must be bf16 or fp16, got {q.dtype}")
+    if mask not in MASKS:
+        raise ValueError(f"mask must be one of {tuple(MASKS)}")
+    T, heads, d = q.shape
+    B = _dev(offsets, "offsets", torch.int64).numel() - 1
+    if B < 0:
+        raise ValueError("offsets must have at least one entry")
+    if key_len is not None and _dev(key_len, "key_len", torch.int32).numel() != B:
+        raise ValueError("key_len must have one entry a document")
+    if (mask == "prefix") != (prefix_len is not None):
+        raise ValueError('prefix_len goes with mask="prefix"')
+    if prefix_len is not None and _dev(prefix_len, "prefix_len", torch.int32).numel() != B:
+        raise ValueError("prefix_len must have one entry a document")
+    if slopes is not None and _dev(slopes, "slopes", torch.float32).numel() != heads:
+        raise ValueError("slopes must have one entry a head")
+    return _AttentionSpec(T, B, heads, k.shape[1], d, _DTYPE_CODE[q.dtype], MASKS[mask],
+                          1.0 / math.sqrt(d) if scale is None else scale, cap, offsets.data_ptr(),
+                          None if key_len is None else key_len.data_ptr(),
+                          None if prefix_len is None else prefix_len.data_ptr(),
+                          None if slopes is None else slopes.data_ptr())
+
+
+def maxsim_attention(q, k, v, offsets, key_len=None, mask="full", prefix_len=None, scale=None, cap=0.0, slopes=None,
+                     out=None, lse=None, want_lse=False, stream=None):
+    """Softmax attention within each CSR-packed document. q [T, heads, d], k and
+    v [T, kv_heads, d] (bf16/fp16; views of one projection's output are fine);
+    offsets [B+1] int64; key_len [B] int32 hides the keys from there on (None:
+    none); mask "full", "causal" or "prefix" (with prefix_len [B] int32); scale
+    None: 1/sqrt(d); cap > 0: scores become cap * tanh(score / cap); slopes
+    [heads] fp32: minus slope * distance. Returns out [T, heads, d], and lse
+    [heads, T] fp32 when requested."""
+    lib = load_library()
+    spec = _attention_spec(q, k, offsets, key_len, mask, prefix_len, scale, cap, slopes)
+    dtype, device, kv_shape = q.dtype, q.device, (spec.T, spec.kv_heads, spec.d)
+    if out is None:
+        out = torch.empty(q.shape, dtype=dtype, device=device)
+    if lse is None and want_lse:
+        lse = torch.empty((spec.heads, spec.T), dtype=torch.float32, device=device)
+    if lse is not None and _dev(lse, "lse", torch.float32).shape != (spec.heads, spec.T):
+        raise ValueError("lse must be [heads, T]")
+    st = lib.maxsim_attention(spec, _heads(q, "q", q.shape, dtype, device), _heads(k, "k", kv_shape, dtype, device),
+                              _heads(v, "v", kv_shape, dtype, device), _heads(out, "out", q.shape, dtype, device),
+                              _ptr(lse), _stream(stream))
+    _check(st, "maxsim_attention")
+    return (out, lse) if lse is not None else out
+
+
+def maxsim_attention_backward_workspace_size(q, k, offsets, mask="full", prefix_len=None):
+    """Device bytes of the workspace of maxsim_attention_backward."""
+    spec = _attention_spec(q, k, offsets, None, mask, prefix_len, None, 0.0, None)
+    return int(load_library().maxsim_attention_backward_workspace_size(spec))
+
+
+def maxsim_attention_backward(dO, q, k, v, out, lse, offsets, key_len=None, mask="full", prefix_len=None, scale=None,
+                              cap=0.0, slopes=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradients of maxsim_attention for the gradient dO of its out, from its
+    out and lse; the other arguments as in that call. Returns dq, dk, dv in the
+    inputs' dtype (views of one buffer may be given)."""
+    lib = load_library()
+    spec = _attention_spec(q, k, offsets, key_len, mask, prefix_len, scale, cap, slopes)
+    dtype, device, kv_shape = q.dtype, q.device, (spec.T, spec.kv_heads, spec.d)
+    if _dev(lse, "lse", torch.float32).shape != (spec.heads, spec.T):
+        raise ValueError("lse must be [heads, T]")
+    dq = torch.empty(q.shape, dtype=dtype, device=device) if dq is None else dq
+    dk = torch.empty(kv_shape, dtype=dtype, device=device) if dk is None else dk
+    dv = torch.empty(kv_shape, dtype=dtype, device=device) if dv is None else dv
+    if workspace is None:
+        nbytes = lib.maxsim_attention_backward_workspace_size(spec)
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    _dev(workspace, "workspace", torch.uint8)
+    views = [_heads(t, name, shape, dtype, device)
+             for t, name, shape in ((dO, "dO", q.shape), (q, "q", q.shape), (k, "k", kv_shape), (v, "v", kv_shape),
+                                    (out, "out", q.shape), (dq, "dq", q.shape), (dk, "dk", kv_shape),
+                                    (dv, "dv", kv_shape))]
+    st = lib.maxsim_attention_backward(spec, *views[:5], lse.data_ptr(), *views[5:], workspace.data_ptr(),
+                                       workspace.numel(), _stream(stream))
+    _check(st, "maxsim_attention_backward")
+    return dq, dk, dv
+
+
+def maxsim_clip_grad_norm_workspace_size(n_tensors):
+    """Device bytes of the workspace of maxsim_clip_grad_norm (no GPU needed)."""
+    return int(load_library().maxsim_clip_grad_norm_workspace_size(n_tensors))
+
+
+def maxsim_clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, stream=None):
+    """Global 2-norm of the tensors ``grads`` (contiguous, bf16/fp16/fp32, types
+    may be mixed), which are scaled by min(1, max_norm / (norm + 1e-6)): in
+    place, or into the tensors ``out`` of the same sizes and types. Returns the
+    norm before clipping, [1] fp32 on the device."""
+    lib = load_library()
+    grads = list(grads)
+    n = len(grads)
+    outs = grads if out is None else list(out)
+    if not all(isinstance(t, torch.Tensor) for t in grads) or (out is not None and not all(
+            isinstance(t, torch.Tensor) for t in outs)):
+        raise TypeError("grads and out must be lists of torch.Tensor")
+    dtypes = list(map(operator.attrgetter("dtype"), grads))
+    sizes = list(map(torch.Tensor.numel, grads))
+    places = set(map(torch.Tensor.get_device, grads))
+    whole = all(map(torch.Tensor.is_contiguous, grads))
+    if out is not None:
+        if len(outs) != n or list(map(torch.Tensor.numel, outs)) != sizes or \
+                list(map(operator.attrgetter("dtype"), outs)) != dtypes:
+            raise ValueError("out must have a tensor of the same size and type for each of grads")
+        places |= set(map(torch.Tensor.get_device, outs))
+        whole = whole and all(map(torch.Tensor.is_contiguous, outs))
+    if len(places) > 1 or -1 in places:
+        raise ValueError("all tensors must be on one CUDA device (the library has no CPU path)")
+    if not whole:
+        raise ValueError("all tensors must be contiguous")
+    try:
+        codes = [_DTYPE_CODE[t] for t in dtypes]
+    except KeyError as e:
+        raise TypeError(f"gradients must be bf16, fp16 or fp32, got {e.args[0]}") from None
+    device = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=device)
+    _dev(norm, "norm", torch.float32)
+    if workspace is None:
+        workspace = torch.empty(lib.maxsim_clip_grad_norm_workspace_size(n), dtype=torch.uint8, device=device)
+    _dev(workspace, "workspace", torch.uint8)
+    pointers = (ctypes.c_void_p * n)(*map(torch.Tensor.data_ptr, grads))
+    targets = pointers if out is None else (ctypes.c_void_p * n)(*map(torch.Tensor.data_ptr, outs))
+    st = lib.maxsim_clip_grad_norm(pointers, targets, (ctypes.c_int64 * n)(*sizes), (ctypes.c_int32 * n)(*codes), n,
+                                   max_norm, norm.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                   _stream(stream))
+    _check(st, "maxsim_clip_grad_norm")
+    return norm

@@ -104,6 +104,19 @@ maxsim_status launch_backward(const void* Q, int n_queries, int nq, int d, const
                               const int32_t* doc_len, int is_bf16, const int32_t* argmax, const float* dS, float* dQ,
                               float* dD, float* workspace, int parts, cudaStream_t stream);
 
+// Rotary positions and gradient clipping; arguments as in maxsim.h, checked.
+maxsim_status launch_rotary(const maxsim_heads& x, int64_t T, int heads, int d, int rot_dim, const uint64_t* freq,
+                            const int64_t* offsets, int64_t B, const int32_t* positions, int interleaved,
+                            float amplitude, int inverse, int dtype, const maxsim_heads& out, cudaStream_t stream);
+size_t clip_workspace_bytes(int tensors);
+maxsim_status launch_clip(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* dtypes,
+                          int tensors, float max_norm, float* norm, void* workspace, cudaStream_t stream);
+
+// Packed attention (attn_common.cuh has the parameters).
+struct AttnParams;
+maxsim_status launch_attn_fwd(const AttnParams& p, int is_bf16, cudaStream_t stream);
+maxsim_status launch_attn_bwd(const AttnParams& p, int is_bf16, cudaStream_t stream);
+
 // Encodes a TMA tensor map through the driver entry point (no libcuda link).
 // dtype_code: 0 fp16, 1 bf16, 2 uint8, 3 fp32; swizzle: 0 none, 1 128-byte,
 // 2 64-byte. Returns false if the driver call is unavailable or rejects the
