@@ -1,5 +1,5 @@
-// attn.cu -- packed attention, one warp per row: forward, and backward in
-// which every gradient row is summed by the one warp that owns it.
+// attn_bwd.cu -- packed attention, backward: one warp per row, and every
+// gradient row is summed by the one warp that owns it.
 //
 //   s_ij = scale <q_i, k_j>;  c_ij = cap tanh(s_ij / cap) (cap > 0, else s_ij)
 //   z_ij = c_ij - slope |i - j|;  p_ij = exp(z_ij - lse_i) over the keys that
@@ -84,39 +84,6 @@ __device__ __forceinline__ float capped(float s, float cap, float& slope) {
 }
 
 template <typename T>
-__global__ void fwd_rows(const AttnParams p) {
-  const int h = blockIdx.y;
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (h == 0) check_docs(p, blockIdx.x * static_cast<int64_t>(kWarps * 32) + threadIdx.x, gridDim.x * int64_t(kWarps * 32));
-  if (t >= p.T) return;
-  Doc c;
-  int i;
-  if (!find_doc(p, t, c, i)) return;
-  const int g = h / (p.heads / p.kv_heads), end = row_end(c, p.mask, i);
-  const float bias = p.slopes ? p.slopes[h] : 0.f;
-  float q[kMaxPer], k[kMaxPer], v[kMaxPer], o[kMaxPer] = {};
-  load_row<T>(p.q, t, h, p.d, q);
-  float top = -INFINITY, sum = 0.f;
-  for (int j = 0; j < end; ++j) {
-    load_row<T>(p.k, c.start + j, g, p.d, k);
-    load_row<T>(p.v, c.start + j, g, p.d, v);
-    float slope;
-    const float z = capped(dot(q, k) * p.scale, p.cap, slope) - bias * abs(i - j);
-    const float now = fmaxf(top, z);
-    const float keep = expf(top - now), w = expf(z - now);
-    sum = sum * keep + w;
-#pragma unroll
-    for (int e = 0; e < kMaxPer; ++e) o[e] = fmaf(w, v[e], o[e] * keep);
-    top = now;
-  }
-  const float inv = end > 0 ? 1.f / sum : 0.f;
-#pragma unroll
-  for (int e = 0; e < kMaxPer; ++e) o[e] *= inv;
-  store_row<T>(p.out, t, h, p.d, o);
-  if (p.lse && (threadIdx.x & 31) == 0) p.lse[static_cast<int64_t>(h) * p.T + t] = end > 0 ? top + logf(sum) : -INFINITY;
-}
-
-template <typename T>
 __global__ void bwd_delta(const AttnParams p) {
   const int h = blockIdx.y;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -194,13 +161,6 @@ __global__ void bwd_dkv_rows(const AttnParams p) {
 }
 
 }  // namespace
-
-maxsim_status launch_attn_fwd(const AttnParams& p, int is_bf16, cudaStream_t stream) {
-  const dim3 grid((p.T + kWarps - 1) / kWarps, p.heads);
-  if (is_bf16) fwd_rows<__nv_bfloat16><<<grid, kWarps * 32, 0, stream>>>(p);
-  else fwd_rows<__half><<<grid, kWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MAXSIM_OK : MAXSIM_ERR_CUDA;
-}
 
 template <typename T>
 static void launch_bwd_typed(const AttnParams& p, cudaStream_t stream) {

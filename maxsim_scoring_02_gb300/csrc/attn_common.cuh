@@ -86,4 +86,118 @@ __device__ __forceinline__ int key_begin(const Doc& c, int mask, int j) {
   return mask == MAXSIM_MASK_FULL || j < c.prefix ? 0 : j;
 }
 
+// ------------------------------------------------ tiles for the tensor cores
+//
+// Work is cut into slots of R rows. Document b owns the slots from
+// offsets[b] / R + b on: as many as its rows can touch, so the slots of all
+// documents are known without a sum over their lengths (T / R + B in all). A
+// slot past its document's last row is empty.
+__device__ __forceinline__ int64_t slot_base(const AttnParams& p, int64_t b, int rows) {
+  const int64_t s = p.offsets[b];
+  return (s < 0 ? 0 : s > p.T ? p.T : s) / rows + b;
+}
+
+// The last document in [lo, hi) whose slots begin at or before `slot`; a whole
+// warp looks at 32 places at a time.
+__device__ __forceinline__ int64_t slot_doc(const AttnParams& p, int64_t slot, int rows, int64_t lo, int64_t hi) {
+  const int lane = threadIdx.x & 31;
+  while (hi - lo > 1) {
+    const int64_t step = (hi - lo + 31) / 32, m = lo + lane * step;
+    const bool at = lane == 0 || (m < hi && slot_base(p, m, rows) <= slot);
+    const unsigned set = __ballot_sync(0xffffffffu, at);
+    lo += (31 - __clz(set)) * step;
+    hi = lo + step < hi ? lo + step : hi;
+  }
+  return lo;
+}
+
+// One block's next piece of work, and what it needs to know of its document.
+struct Work {
+  int start, len, keys, prefix;  // Doc
+  int row0;                      // first row (or key) of the slot, within the document
+  int head;
+  int live;                      // 0: no work is left
+};
+
+// Walks over (slot, head) pairs: block c takes items c, 2G - 1 - c, 2G + c, ...
+// of G blocks, so that early (heavy) and late (light) items of one document
+// even out; with `reverse` the last rows, which see most keys, come first.
+struct Walk {
+  int64_t round = 0, slot_old = -1, doc_old = 0;
+
+  // The next slot that holds rows, for the whole warp. Slots of a document lie
+  // together, and every later document is at least one slot further, so the
+  // search starts from the last one found.
+  __device__ __forceinline__ Work next(const AttnParams& p, int rows, int heads, int reverse) {
+    const int64_t slots = p.T / rows + p.B, items = slots * heads, G = gridDim.x;
+    Work w;
+    w.live = 0;
+    for (;; ++round) {
+      const int64_t item = round * G + ((round & 1) ? G - 1 - static_cast<int64_t>(blockIdx.x) : blockIdx.x);
+      if (round * G >= items) break;
+      if (item >= items) continue;
+      const int64_t s = item / heads, slot = reverse ? slots - 1 - s : s;
+      int64_t lo = 0, hi = p.B;
+      if (slot_old >= 0) {
+        const int64_t far = slot > slot_old ? slot - slot_old : slot_old - slot;
+        lo = doc_old - far > 0 && slot < slot_old ? doc_old - far : slot < slot_old ? 0 : doc_old;
+        hi = slot < slot_old ? doc_old + 1 : doc_old + far + 1 < p.B ? doc_old + far + 1 : p.B;
+      }
+      const int64_t b = slot_doc(p, slot, rows, lo, hi);
+      slot_old = slot;
+      doc_old = b;
+      bool bad;
+      const Doc c = load_doc(p, b, bad);
+      const int64_t row0 = (slot - slot_base(p, b, rows)) * rows;
+      if (row0 < 0 || row0 >= c.len) continue;
+      w.start = c.start;
+      w.len = c.len;
+      w.keys = c.keys;
+      w.prefix = c.prefix;
+      w.row0 = static_cast<int>(row0);
+      w.head = static_cast<int>(item % heads);
+      w.live = 1;
+      ++round;
+      break;
+    }
+    return w;
+  }
+};
+
+__device__ __forceinline__ int row_end(const Work& c, int mask, int i) {
+  if (mask == MAXSIM_MASK_FULL) return c.keys;
+  return min(c.keys, max(i + 1, c.prefix));
+}
+
+// 2^x and 1/x in hardware (2 ulp, 1 ulp).
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// tanh(x) = 1 - 2 / (1 + e^2x); `x2` is 2 x log2(e). Off by 2^-22 absolutely,
+// for any x: e^2x may overflow to infinity or vanish.
+__device__ __forceinline__ float fast_tanh(float x2) { return fmaf(-2.f, fast_rcp(1.f + fast_exp2(x2)), 1.f); }
+
+// Two values as 16-bit ones in a word, `lo` in its low half.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (kBf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Tensor map of a view: 64 elements of one head (128 bytes, 128-byte swizzle)
+// by `box_rows` tokens. Elements past d and tokens past T read as zeros.
+bool attn_tmap(void* map, const HeadsView& v, int64_t T, int heads, int d, int is_bf16, int box_rows);
+
 }  // namespace msim

@@ -1,0 +1,496 @@
+// attn_fwd.cu -- packed attention, forward, on tcgen05.
+//
+// A block owns NQ tiles of 128 rows of one document and head and walks over
+// the keys that they see, 128 at a time:
+//   S = Q K^T        128 x 128, both operands in shared memory, S in TMEM
+//   P = 2^(S c - m)  by a warpgroup of 128 threads, one row each: no value
+//                    crosses threads; P goes back to TMEM in 16 bits, over S
+//   O += P V         P from TMEM, V as it lies in memory (N contiguous)
+// One warp loads tiles by TMA, one issues the products; mbarriers pass tiles
+// between them. The tensor cores run in order, so a product that reuses S or O
+// needs no barrier behind the one that read it.
+//
+// The running maximum m of a row is only raised (and O and the sum rescaled)
+// when it has grown by more than 2^8 since: weights then stay below 256, which
+// 16 bits and the fp32 sums hold without loss, and the pass over O in TMEM is
+// rare. Weights are rounded to the inputs' type for their product with V, as
+// the tensor cores take nothing wider at this rate; their sum is made of the
+// unrounded ones, so lse keeps fp32.
+//
+// Keys past a document's last visible one are cut off the products (to a
+// multiple of 16) and the up to 15 rows of V behind them are zeroed in shared
+// memory: 0 * NaN would reach the sum.
+#include <climits>
+
+#include "attn_common.cuh"
+
+namespace msim {
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kBoxRows = 64;
+constexpr int kRing = 2;
+constexpr float kRaise = 8.f;  // log2 of how far a weight may exceed 1
+
+template <int DH, int NQ>
+struct FwdShape {
+  static constexpr int kPanels = DH / 64;
+  static constexpr uint32_t kPanelBytes = kTile * 128;
+  static constexpr uint32_t kTileBytes = kPanels * kPanelBytes;
+  static constexpr int kStages = NQ == 1 ? (DH == 64 ? 2 : 1) : (DH == 64 ? 4 : 2);
+  static constexpr int kThreads = NQ * 128 + 128;  // softmax warpgroups; loader, issuer and two idle warps
+  static constexpr int kBlocks = NQ == 1 ? 2 : 1;  // resident on an SM
+  // Registers a thread: at launch (ptxas fills the launch bounds), and after
+  // the softmax threads, which hold a row's 128 scores, took over the others'.
+  static constexpr int kRegsLaunch = NQ == 1 ? 128 : 168;
+  static constexpr int kRegsSoftmax = NQ == 1 ? 200 : 224, kRegsOther = 56;
+  static_assert(NQ * kRegsSoftmax + kRegsOther <= (NQ + 1) * kRegsLaunch, "register split");
+  static constexpr uint32_t kTmemCols = NQ == 1 ? 256 : 512;
+  static constexpr uint32_t kO0 = NQ * kTile;  // TMEM columns: S of each tile, then O of each tile
+  // barriers: q_full, q_empty, k_full, k_empty, v_full, v_empty, s_full, p_full, o_full, info_full, info_empty, done
+  static constexpr int kBars = 2 + 4 * kStages + 3 * NQ + 2 * kRing + 1;
+  static constexpr uint32_t kSmem = 1024 + (NQ + 2 * kStages) * kTileBytes + 8 * kBars + kRing * sizeof(Work) + 16;
+};
+
+template <int DH, int NQ>
+struct FwdSmem {
+  using S = FwdShape<DH, NQ>;
+  uint32_t q, k, v, bars;
+  uint64_t* bar;
+  Work* info;
+  uint32_t* tmem_slot;
+  int* abort_flag;
+  __device__ __forceinline__ explicit FwdSmem(uint8_t* raw) {
+    uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    q = smem_u32(base);
+    k = q + NQ * S::kTileBytes;
+    v = k + S::kStages * S::kTileBytes;
+    bar = reinterpret_cast<uint64_t*>(base + (NQ + 2 * S::kStages) * S::kTileBytes);
+    bars = smem_u32(bar);
+    info = reinterpret_cast<Work*>(bar + S::kBars);
+    tmem_slot = reinterpret_cast<uint32_t*>(info + kRing);
+    abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  }
+  __device__ __forceinline__ uint32_t q_full() const { return bars; }
+  __device__ __forceinline__ uint32_t q_empty() const { return bars + 8; }
+  __device__ __forceinline__ uint32_t k_full(int s) const { return bars + 16 + 8 * s; }
+  __device__ __forceinline__ uint32_t k_empty(int s) const { return k_full(S::kStages + s); }
+  __device__ __forceinline__ uint32_t v_full(int s) const { return k_full(2 * S::kStages + s); }
+  __device__ __forceinline__ uint32_t v_empty(int s) const { return k_full(3 * S::kStages + s); }
+  __device__ __forceinline__ uint32_t s_full(int t) const { return k_full(4 * S::kStages + t); }
+  __device__ __forceinline__ uint32_t p_full(int t) const { return s_full(NQ + t); }
+  __device__ __forceinline__ uint32_t o_full(int t) const { return s_full(2 * NQ + t); }
+  __device__ __forceinline__ uint32_t info_full(int r) const { return s_full(3 * NQ + r); }
+  __device__ __forceinline__ uint32_t info_empty(int r) const { return s_full(3 * NQ + kRing + r); }
+  __device__ __forceinline__ uint32_t done() const { return s_full(3 * NQ + 2 * kRing); }
+  __device__ __forceinline__ uint64_t* at(uint32_t b) const { return bar + (b - bars) / 8; }
+};
+
+// Keys that tile t of the item needs (0: it has no rows, or they see nothing).
+__device__ __forceinline__ int tile_keys(const Work& w, int mask, int t) {
+  const int first = w.row0 + t * kTile;
+  return first < w.len ? row_end(w, mask, min(w.len, first + kTile) - 1) : 0;
+}
+__device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
+
+// ---------------------------------------------------------------- loads
+template <int DH, int NQ>
+__device__ void fwd_loader(const AttnParams& p, const FwdSmem<DH, NQ>& sm, const CUtensorMap* mq, const CUtensorMap* mk,
+                           const CUtensorMap* mv) {
+  using S = FwdShape<DH, NQ>;
+  const int lane = threadIdx.x & 31, group = p.heads / p.kv_heads;
+  Walk walk;
+  uint32_t item = 0, loads = 0, kv = 0;  // items with keys; key tiles
+  bool ok = true;
+  const auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int head, int token, int rows) {
+    const int boxes = (rows + kBoxRows - 1) / kBoxRows;
+    mbar_arrive_expect_tx_a(bar, boxes * S::kPanels * (kBoxRows * 128));
+    for (int b = 0; b < boxes; ++b)
+      for (int pn = 0; pn < S::kPanels; ++pn)
+        tma_load_3d_a(dst + pn * S::kPanelBytes + b * (kBoxRows * 128), map, bar, pn * 64, head, token + b * kBoxRows);
+  };
+  for (uint32_t n = 0; ok; ++n) {
+    const Work w = walk.next(p, NQ * kTile, p.heads, p.mask != MAXSIM_MASK_FULL);
+    if (lane == 0) {
+      const int r = n % kRing;
+      ok = mbar_wait_inl_a(sm.info_empty(r), ((n / kRing) & 1) ^ 1, sm.abort_flag, p.status);
+      if (ok) {
+        sm.info[r] = w;
+        mbar_arrive_a(sm.info_full(r));  // releases the write
+        int keys = 0;
+        for (int t = 0; w.live && t < NQ; ++t) keys = max(keys, tile_keys(w, p.mask, t));
+        const int nk = w.live ? tiles_of(keys) : 0;
+        if (nk > 0) {
+          ok = mbar_wait_inl_a(sm.q_empty(), (item & 1) ^ 1, sm.abort_flag, p.status);
+          if (ok) {
+            // tiles past the last row are not loaded: their products are not made either
+            const int rows = min(NQ * kTile, w.len - w.row0);
+            mbar_arrive_expect_tx_a(sm.q_full(), (rows + kBoxRows - 1) / kBoxRows * S::kPanels * (kBoxRows * 128));
+            for (int b = 0; b * kBoxRows < rows; ++b)
+              for (int pn = 0; pn < S::kPanels; ++pn)
+                tma_load_3d_a(sm.q + (b / 2) * S::kTileBytes + pn * S::kPanelBytes + (b % 2) * (kBoxRows * 128), mq,
+                              sm.q_full(), pn * 64, w.head, w.start + w.row0 + b * kBoxRows);
+            ++item;
+            ++loads;
+          }
+          for (int j = 0; ok && j < nk; ++j, ++kv) {
+            const int s = kv % S::kStages, rows = min(kTile, keys - j * kTile);
+            const uint32_t ph = ((kv / S::kStages) & 1) ^ 1;
+            ok = mbar_wait_inl_a(sm.k_empty(s), ph, sm.abort_flag, p.status);
+            if (!ok) break;
+            load(sm.k + s * S::kTileBytes, mk, sm.k_full(s), w.head / group, w.start + j * kTile, rows);
+            ok = mbar_wait_inl_a(sm.v_empty(s), ph, sm.abort_flag, p.status);
+            if (!ok) {  // K of this stage is in flight without its V
+              mbar_wait_drain(sm.at(sm.k_full(s)), ph ^ 1, p.status);
+              break;
+            }
+            load(sm.v + s * S::kTileBytes, mv, sm.v_full(s), w.head / group, w.start + j * kTile, rows);
+          }
+        }
+      }
+    }
+    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    if (!w.live) break;
+  }
+  if (!ok && lane == 0) {  // after an abort: wait (bounded) for the copies in flight
+    if (item > 0) mbar_wait_drain(sm.at(sm.q_full()), (item - 1) & 1, p.status);
+    for (uint32_t f = kv > S::kStages ? kv - S::kStages : 0; f < kv; ++f) {
+      mbar_wait_drain(sm.at(sm.k_full(f % S::kStages)), (f / S::kStages) & 1, p.status);
+      mbar_wait_drain(sm.at(sm.v_full(f % S::kStages)), (f / S::kStages) & 1, p.status);
+    }
+  }
+}
+
+// ------------------------------------------------------------- products
+template <int DH, int NQ, bool kBf16>
+__device__ void fwd_products(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint32_t tmem) {
+  using S = FwdShape<DH, NQ>;
+  const int lane = threadIdx.x & 31;
+  const uint32_t idesc = idesc_f16(kBf16, kTile, 0);
+  uint32_t item = 0, kv = 0, seen_k = 0;
+  uint32_t pn[NQ] = {};  // p_full phases passed
+  const auto wait = [&](uint32_t bar, uint32_t ph) {
+    return __all_sync(0xffffffffu, mbar_wait_inl_a(bar, ph & 1, sm.abort_flag, p.status));
+  };
+  bool ok = true;
+  for (uint32_t n = 0; ok; ++n) {
+    const int r = n % kRing;
+    if (!wait(sm.info_full(r), n / kRing)) break;
+    const Work w = sm.info[r];
+    __syncwarp();
+    if (lane == 0) mbar_arrive_a(sm.info_empty(r));
+    if (!w.live) break;
+    int keys[NQ], most = 0;
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) most = max(most, keys[t] = tile_keys(w, p.mask, t));
+    const int nk = tiles_of(most);
+    if (nk == 0) continue;
+    // S_t of key tile j (keys kv + j of the stages)
+    const auto score = [&](int t, int j) {
+      const int cols = (min(kTile, keys[t] - j * kTile) + 15) & ~15;
+      const uint32_t id = idesc | static_cast<uint32_t>(cols >> 3) << 17;
+      const uint64_t a = sdesc_k_sw128(sm.q + t * S::kTileBytes);
+      const uint64_t b = sdesc_k_sw128(sm.k + (kv + j) % S::kStages * S::kTileBytes);
+#pragma unroll
+      for (int kk = 0; kk < DH / 16; ++kk) {
+        const uint64_t step = (kk / 4) * (S::kPanelBytes >> 4) + (kk % 4) * 2;
+        umma_f16_el(tmem + t * kTile, a + step, b + step, id, kk != 0);
+      }
+      umma_commit_el(sm.s_full(t));
+    };
+    const auto need_k = [&](int j) -> bool {  // waits for key tile j once
+      if (seen_k > kv + j) return true;
+      seen_k = kv + j + 1;
+      return wait(sm.k_full((kv + j) % S::kStages), (kv + j) / S::kStages);
+    };
+    ok = wait(sm.q_full(), item) && need_k(0);
+    if (!ok) break;
+    tc_fence_after();
+#pragma unroll
+    for (int t = 0; t < NQ; ++t)
+      if (keys[t] > 0) score(t, 0);
+    umma_commit_el(sm.k_empty(kv % S::kStages));
+    if (nk == 1) umma_commit_el(sm.q_empty());
+    for (int j = 0; ok && j < nk; ++j) {
+      const int s = (kv + j) % S::kStages;
+      bool fresh = true;
+#pragma unroll
+      for (int t = 0; t < NQ; ++t) {
+        const int left = keys[t] - j * kTile;
+        if (left <= 0) continue;
+        if (fresh) {
+          fresh = false;
+          if (!(ok = wait(sm.v_full(s), (kv + j) / S::kStages))) break;
+          // rows of V behind the last key that any tile of this item sees
+          const int used = min(kTile, most - j * kTile), whole = (used + 15) & ~15;
+          if (used != whole) {
+            const uint32_t vec = (whole - used) * 8;
+            for (uint32_t e = lane; e < vec * S::kPanels; e += 32) {
+              const uint32_t dst = sm.v + s * S::kTileBytes + (e / vec) * S::kPanelBytes + used * 128 + (e % vec) * 16;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        if (!(ok = wait(sm.p_full(t), pn[t]))) break;
+        ++pn[t];
+        tc_fence_after();
+        const int steps = (min(kTile, left) + 15) / 16;
+        const uint64_t b = sdesc_mn_sw128(sm.v + s * S::kTileBytes, S::kPanelBytes);
+        for (int kk = 0; kk < steps; ++kk)
+          umma_f16_ts_el(tmem + S::kO0 + t * DH, tmem + t * kTile + kk * 8, b + kk * (2048 >> 4),
+                         idesc | static_cast<uint32_t>(DH >> 3) << 17 | kIdescBMnMajor, (j | kk) != 0);
+        if (left <= kTile) umma_commit_el(sm.o_full(t));
+        if (left > kTile) {
+          if (!(ok = need_k(j + 1))) break;
+          tc_fence_after();
+          score(t, j + 1);
+        }
+      }
+      if (!ok) break;
+      umma_commit_el(sm.v_empty(s));
+      if (j + 1 < nk) {
+        umma_commit_el(sm.k_empty((kv + j + 1) % S::kStages));
+        if (j + 2 == nk) umma_commit_el(sm.q_empty());
+      }
+    }
+    kv += nk;
+    ++item;
+  }
+  // every product issued here has completed before TMEM is freed
+  umma_commit_el(sm.done());
+  mbar_wait_drain(sm.at(sm.done()), 0, p.status);
+}
+
+// -------------------------------------------------------------- softmax
+template <int DH, int NQ, bool kBf16, bool kCap, bool kBias>
+__device__ void fwd_softmax(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint32_t tmem) {
+  using S = FwdShape<DH, NQ>;
+  const int t = threadIdx.x >> 7, lane = threadIdx.x & 31;
+  const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;  // this warp's 32 TMEM lanes
+  const uint32_t s_col = tmem + lanes + t * kTile, o_col = tmem + lanes + S::kO0 + t * DH;
+  // scores are brought to log2 units by c, or are there already once bent or biased
+  const float to_log2 = p.scale * kLog2e;
+  const float c = kCap || kBias ? 1.f : to_log2;
+  const float cap2 = p.cap * kLog2e, in_cap = kCap ? 2.f * kLog2e * p.scale / p.cap : 0.f;
+  uint32_t sn = 0, on = 0;
+  const auto wait = [&](uint32_t bar, uint32_t ph) { return mbar_wait_inl_a(bar, ph & 1, sm.abort_flag, p.status); };
+  for (uint32_t n = 0;; ++n) {
+    const int r = n % kRing;
+    if (!__all_sync(0xffffffffu, wait(sm.info_full(r), n / kRing))) return;
+    const Work w = sm.info[r];
+    __syncwarp();
+    if (lane == 0) mbar_arrive_a(sm.info_empty(r));
+    if (!w.live) return;
+    const int first = w.row0 + t * kTile, row = first + static_cast<int>(threadIdx.x & 127);
+    if (first >= w.len) continue;
+    const int keys = tile_keys(w, p.mask, t), nk = tiles_of(keys);
+    const int end = row_end(w, p.mask, min(row, w.len - 1)), all_see = row_end(w, p.mask, first);
+    const float slope2 = kBias ? p.slopes[w.head] * kLog2e : 0.f;
+    float m = -INFINITY, sum = 0.f;  // m is in the units of the scores held in v
+    for (int j = 0; j < nk; ++j) {
+      const int cols = min(kTile, keys - j * kTile);
+      if (!__all_sync(0xffffffffu, wait(sm.s_full(t), sn))) return;
+      ++sn;
+      tc_fence_after();
+      uint32_t u[4][32];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q * 32 < cols) tmem_ld_32x32b_x32_issue(s_col + q * 32, u[q]);
+      tmem_wait_ld_regs(u[0]);
+#pragma unroll
+      for (int q = 1; q < 4; ++q) reg_order(u[q]);
+      const bool masked = (j + 1) * kTile > all_see;
+      const int lim = end - j * kTile;
+      float top[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        top[q] = -INFINITY;
+        if (q * 32 >= cols) continue;
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+          float z = __uint_as_float(u[q][x]);
+          if constexpr (kCap) z = cap2 * fast_tanh(z * in_cap);
+          if constexpr (kBias) {
+            if constexpr (!kCap) z *= to_log2;
+            z = fmaf(-slope2, fabsf(static_cast<float>(row - (j * kTile + q * 32 + x))), z);
+          }
+          if (masked) z = q * 32 + x < lim ? z : -INFINITY;
+          u[q][x] = __float_as_uint(z);
+          top[q] = fmaxf(top[q], z);
+        }
+      }
+      const float now = fmaxf(fmaxf(m, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
+      // The first tile sets the maximum; later ones raise it when it has grown a lot.
+      if (j == 0) {
+        m = now;
+      } else if (__any_sync(0xffffffffu, (now - m) * c > kRaise)) {
+        const float keep = now == -INFINITY ? 1.f : fast_exp2((m - now) * c);
+        sum *= keep;
+        m = now;
+#pragma unroll
+        for (int q = 0; q < DH / 32; ++q) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32_issue(o_col + q * 32, o);
+          tmem_wait_ld_regs(o);
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
+          tmem_st_32x32b_x32_issue(o_col + q * 32, o);
+        }
+      }
+      const float shift = m == -INFINITY ? 0.f : -m * c;
+      float part[4] = {};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (q * 32 >= cols) continue;
+        uint32_t pk[16];
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          const float a = fast_exp2(fmaf(__uint_as_float(u[q][x]), c, shift));
+          const float b = fast_exp2(fmaf(__uint_as_float(u[q][x + 1]), c, shift));
+          part[x / 2 % 4] += a + b;
+          pk[x / 2] = pack2<kBf16>(a, b);
+        }
+        tmem_st_32x32b_x16_issue(s_col + q * 16, pk);
+      }
+      sum += (part[0] + part[1]) + (part[2] + part[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_a(sm.p_full(t));
+    }
+    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // a row that sees nothing is 0
+    if (nk > 0) {
+      if (!__all_sync(0xffffffffu, wait(sm.o_full(t), on))) return;
+      ++on;
+      tc_fence_after();
+    }
+    const int64_t token = w.start + row;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out.data) + token * p.out.token_stride +
+                                          w.head * p.out.head_stride);
+#pragma unroll
+    for (int q = 0; q < DH / 32; ++q) {
+      uint32_t o[32];
+      if (nk > 0) {
+        tmem_ld_32x32b_x32_issue(o_col + q * 32, o);
+        tmem_wait_ld_regs(o);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint4 y = make_uint4(0, 0, 0, 0);
+        if (nk > 0) {
+          const float* f = reinterpret_cast<const float*>(o) + x * 8;
+          y = make_uint4(pack2<kBf16>(f[0] * inv, f[1] * inv), pack2<kBf16>(f[2] * inv, f[3] * inv),
+                         pack2<kBf16>(f[4] * inv, f[5] * inv), pack2<kBf16>(f[6] * inv, f[7] * inv));
+        }
+        if (row < w.len && q * 32 + x * 8 < p.d) dst[q * 4 + x] = y;
+      }
+    }
+    if (p.lse && row < w.len)
+      p.lse[static_cast<int64_t>(w.head) * p.T + token] = sum > 0.f || sum != sum ? (m * c + log2f(sum)) * kLn2 : -INFINITY;
+  }
+}
+
+template <int DH, int NQ, bool kBf16, bool kCap, bool kBias>
+__global__ void __launch_bounds__(FwdShape<DH, NQ>::kThreads, FwdShape<DH, NQ>::kBlocks)
+    attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnParams p) {
+  using S = FwdShape<DH, NQ>;
+  extern __shared__ uint8_t raw[];
+  const FwdSmem<DH, NQ> sm(raw);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    mbar_init(sm.at(sm.q_full()), 1);
+    mbar_init(sm.at(sm.q_empty()), 1);
+    for (int s = 0; s < 4 * S::kStages; ++s) mbar_init(sm.at(sm.k_full(s)), 1);
+    for (int t = 0; t < NQ; ++t) {
+      mbar_init(sm.at(sm.s_full(t)), 1);
+      mbar_init(sm.at(sm.p_full(t)), 4);      // a warpgroup's warps
+      mbar_init(sm.at(sm.o_full(t)), 1);
+    }
+    for (int r = 0; r < kRing; ++r) {
+      mbar_init(sm.at(sm.info_full(r)), 1);
+      mbar_init(sm.at(sm.info_empty(r)), 4 * NQ + 1);  // softmax warps and the issuing warp
+    }
+    mbar_init(sm.at(sm.done()), 1);
+    *sm.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 4 * NQ + 1) {
+    tmem_alloc(sm.tmem_slot, S::kTmemCols);
+    tmem_relinquish();
+  }
+  check_docs(p, blockIdx.x * static_cast<int64_t>(S::kThreads) + threadIdx.x, gridDim.x * static_cast<int64_t>(S::kThreads));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *sm.tmem_slot;
+  if (warp >= 4 * NQ) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsOther));
+    if (warp == 4 * NQ) fwd_loader<DH, NQ>(p, sm, &mq, &mk, &mv);
+    else if (warp == 4 * NQ + 1) fwd_products<DH, NQ, kBf16>(p, sm, tmem);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsSoftmax));
+    fwd_softmax<DH, NQ, kBf16, kCap, kBias>(p, sm, tmem);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4 * NQ + 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kTmemCols);
+  }
+}
+
+template <int DH, int NQ, bool kBf16, bool kCap, bool kBias>
+cudaError_t fwd_launch(const CUtensorMap* m, const AttnParams& p, int sm_count, cudaStream_t stream) {
+  using S = FwdShape<DH, NQ>;
+  auto kern = attn_fwd_kernel<DH, NQ, kBf16, kCap, kBias>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t items = (p.T / (NQ * kTile) + p.B) * p.heads, most = static_cast<int64_t>(sm_count) * S::kBlocks;
+  kern<<<static_cast<int>(items < most ? items : most), S::kThreads, S::kSmem, stream>>>(m[0], m[1], m[2], p);
+  return cudaGetLastError();
+}
+
+template <int DH, int NQ, bool kBf16>
+cudaError_t fwd_variant(const CUtensorMap* m, const AttnParams& p, int sm_count, cudaStream_t stream) {
+  if (p.cap > 0.f)
+    return p.slopes ? fwd_launch<DH, NQ, kBf16, true, true>(m, p, sm_count, stream)
+                    : fwd_launch<DH, NQ, kBf16, true, false>(m, p, sm_count, stream);
+  return p.slopes ? fwd_launch<DH, NQ, kBf16, false, true>(m, p, sm_count, stream)
+                  : fwd_launch<DH, NQ, kBf16, false, false>(m, p, sm_count, stream);
+}
+
+template <int DH>
+cudaError_t fwd_typed(const CUtensorMap* m, const AttnParams& p, int nq, int is_bf16, int sm_count, cudaStream_t stream) {
+  if (nq == 1)
+    return is_bf16 ? fwd_variant<DH, 1, true>(m, p, sm_count, stream) : fwd_variant<DH, 1, false>(m, p, sm_count, stream);
+  return is_bf16 ? fwd_variant<DH, 2, true>(m, p, sm_count, stream) : fwd_variant<DH, 2, false>(m, p, sm_count, stream);
+}
+
+}  // namespace
+
+bool attn_tmap(void* map, const HeadsView& v, int64_t T, int heads, int d, int is_bf16, int box_rows) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(heads), static_cast<uint64_t>(T)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(v.head_stride) * 2, static_cast<uint64_t>(v.token_stride) * 2};
+  const uint32_t box[3] = {64, 1, static_cast<uint32_t>(box_rows)};
+  return encode_tmap(map, is_bf16 ? 1 : 0, 3, v.data, dims, strides, box, 1);
+}
+
+maxsim_status launch_attn_fwd(const AttnParams& p, int is_bf16, cudaStream_t stream) {
+  const DeviceInfo* dev = device_info();
+  if (!dev) return MAXSIM_ERR_CUDA;
+  alignas(64) CUtensorMap m[3];
+  if (!attn_tmap(&m[0], p.q, p.T, p.heads, p.d, is_bf16, kBoxRows) ||
+      !attn_tmap(&m[1], p.k, p.T, p.kv_heads, p.d, is_bf16, kBoxRows) ||
+      !attn_tmap(&m[2], p.v, p.T, p.kv_heads, p.d, is_bf16, kBoxRows))
+    return MAXSIM_ERR_CUDA;
+  const int nq = p.T / p.B >= 192 ? 2 : 1;
+  const cudaError_t e = p.d <= 64 ? fwd_typed<64>(m, p, nq, is_bf16, dev->sm_count, stream)
+                                  : fwd_typed<128>(m, p, nq, is_bf16, dev->sm_count, stream);
+  return e == cudaSuccess ? MAXSIM_OK : MAXSIM_ERR_CUDA;
+}
+
+}  // namespace msim
