@@ -148,7 +148,7 @@ maxsim_status maxsim_attention(const maxsim_attention_spec* spec, const maxsim_h
 
 size_t maxsim_attention_backward_workspace_size(const maxsim_attention_spec* spec) {
   if (check_spec(spec) != MAXSIM_OK) return 0;
-  return static_cast<size_t>(spec->T) * spec->heads * sizeof(float);
+  return static_cast<size_t>(spec->T) * spec->heads * 2 * sizeof(float);
 }
 
 maxsim_status maxsim_attention_backward(const maxsim_attention_spec* spec, const maxsim_heads* dO,

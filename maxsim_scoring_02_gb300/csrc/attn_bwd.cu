@@ -1,179 +1,633 @@
-// attn_bwd.cu -- packed attention, backward: one warp per row, and every
-// gradient row is summed by the one warp that owns it.
+// attn_bwd.cu -- packed attention, backward, on tcgen05.
 //
-//   s_ij = scale <q_i, k_j>;  c_ij = cap tanh(s_ij / cap) (cap > 0, else s_ij)
-//   z_ij = c_ij - slope |i - j|;  p_ij = exp(z_ij - lse_i) over the keys that
-//   row i sees;  o_i = sum_j p_ij v_j
-//   dV_j = sum_i p_ij dO_i;  dP_ij = <dO_i, v_j>
-//   dS_ij = p_ij (dP_ij - <dO_i, o_i>) (1 - (c_ij / cap)^2) scale
-//   dQ_i = sum_j dS_ij k_j;  dK_j = sum_i dS_ij q_i
-// A shared key-value head sums dK and dV over its query heads.
+// Three kernels. The first makes, for each row and head, its lse in log2 units
+// and delta = <dO, out>. The other two make each score again and own what they
+// write, so there are no atomics and results do not depend on scheduling:
 //
-// Bound by the CUDA cores: about 30 instructions of a warp a pair. Measured:
-// 16411 causal tokens, 8 heads of 128: 115 ms; 24 documents of 1024 tokens, 16
-// heads of 128, forward and backward: 174 ms.
-#include <cfloat>
-
+//   attn_dkv_kernel: 128 keys of one document and key-value head, walking
+//     over the query heads that share it and over the rows that see the keys:
+//       S^T = K Q^T, dP^T = V dO^T          (both operands in shared memory)
+//       P^T = 2^(S^T c - lse2), dS^T = P^T (dP^T - delta) bend
+//       dV += P^T dO, dK += dS^T Q          (A from TMEM, B as it lies in memory)
+//   attn_dq_kernel: 128 rows of one document and head, walking over the keys:
+//       S = Q K^T, dP = dO V^T, dS as above, dQ += dS K
+//
+// Seven products of 128 x 128 x d for a tile where five would do if dQ were
+// added up in memory by all key blocks, in an order that changes results.
+//
+// A tile passes through two phases of the arithmetic warps, P and dS. While
+// they are at dS of tile i the tensor cores make dV of tile i and S of tile
+// i + 1, while they are at P of tile i + 1 dK of tile i and dP of tile i + 1:
+// single buffers of S and dP are enough, because the tensor cores run in
+// order. P lies over S and dS over dP, each warpgroup's half in its own
+// columns. P and dS are rounded to the inputs' type for their products, as the
+// tensor cores take nothing wider at this rate; sums are fp32. `scale` is applied to
+// the sums.
 #include "attn_common.cuh"
 
 namespace msim {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kMaxPer = 4;  // d <= 128: elements of a head held by one lane
+constexpr int kTile = 128;
+constexpr int kBoxRows = 64;
+constexpr int kRing = 2;
+constexpr int kStages = 2;
 
-template <typename T>
-__device__ __forceinline__ float up(T x);
-template <>
-__device__ __forceinline__ float up(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <>
-__device__ __forceinline__ float up(__half x) { return __half2float(x); }
-template <typename T>
-__device__ __forceinline__ T down(float x);
-template <>
-__device__ __forceinline__ __nv_bfloat16 down(float x) { return __float2bfloat16_rn(x); }
-template <>
-__device__ __forceinline__ __half down(float x) { return __float2half_rn(x); }
+// DH: head size in shared memory; BC: columns of a score tile (rows of Q or
+// keys that are walked over), 64 for each arithmetic warpgroup.
+template <int DH, int BC, bool kDkv>
+struct BwdShape {
+  static constexpr int kGroups = BC / 64;
+  static constexpr int kPanels = DH / 64;
+  static constexpr uint32_t kOwnPanel = kTile * 128, kOwnBytes = kPanels * kOwnPanel;
+  static constexpr uint32_t kPanel = BC * 128, kBytes = kPanels * kPanel;
+  static constexpr int kThreads = kGroups * 128 + 128;
+  static constexpr int kBlocks = BC == 64 ? 2 : 1;
+  static constexpr int kRegsLaunch = BC == 64 ? 128 : 168;
+  static constexpr int kRegsMath = BC == 64 ? 200 : 224, kRegsOther = 56;
+  static_assert(kGroups * kRegsMath + kRegsOther <= (kGroups + 1) * kRegsLaunch, "register split");
+  // TMEM columns: S, dP, then the sums
+  static constexpr uint32_t kDp = BC, kSum0 = 2 * BC, kSum1 = 2 * BC + DH;
+  static constexpr uint32_t kNeed = kDkv ? 2 * BC + 2 * DH : 2 * BC + DH;
+  static constexpr uint32_t kTmemCols = kNeed <= 256 ? 256 : 512;
+  static constexpr int kBars = 2 + 2 * kStages + 5 + 2 * kRing + 1;
+  static constexpr uint32_t kSmem = 1024 + 2 * kOwnBytes + 2 * kStages * kBytes + 8 * kBars +
+                                    (kDkv ? kStages * BC * 8 : 0) + kRing * sizeof(Work) + 16 + 16;
+};
 
-template <typename T>
-__device__ __forceinline__ void load_row(const HeadsView& v, int64_t t, int h, int d, float (&r)[kMaxPer]) {
-  const T* src = static_cast<const T*>(v.data) + t * v.token_stride + h * v.head_stride;
-#pragma unroll
-  for (int k = 0; k < kMaxPer; ++k) {
-    const int c = k * 32 + (threadIdx.x & 31);
-    r[k] = c < d ? up<T>(src[c]) : 0.f;
+// own_a, own_b: the 128 rows that the block keeps (K and V, or Q and dO);
+// walk_a, walk_b: the stages of what it walks over (Q and dO, or K and V).
+template <class S, int BC>
+struct BwdSmem {
+  uint32_t own_a, own_b, walk_a, walk_b, bars;
+  uint64_t* bar;
+  float2* stats;  // kStages x BC: (lse2, delta) of the walked rows
+  Work* info;
+  uint32_t* tmem_slot;
+  int* abort_flag;
+  __device__ __forceinline__ explicit BwdSmem(uint8_t* raw, bool dkv) {
+    uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    own_a = smem_u32(base);
+    own_b = own_a + S::kOwnBytes;
+    walk_a = own_b + S::kOwnBytes;
+    walk_b = walk_a + kStages * S::kBytes;
+    uint8_t* end = base + 2 * S::kOwnBytes + 2 * kStages * S::kBytes;
+    stats = reinterpret_cast<float2*>(end);
+    bar = reinterpret_cast<uint64_t*>(end + (dkv ? kStages * BC * 8 : 0));
+    bars = smem_u32(bar);
+    info = reinterpret_cast<Work*>(bar + S::kBars);
+    tmem_slot = reinterpret_cast<uint32_t*>(info + kRing);
+    abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  }
+  __device__ __forceinline__ uint32_t own_full() const { return bars; }
+  __device__ __forceinline__ uint32_t own_empty() const { return bars + 8; }
+  __device__ __forceinline__ uint32_t walk_full(int s) const { return bars + 16 + 8 * s; }
+  __device__ __forceinline__ uint32_t walk_empty(int s) const { return bars + 16 + 8 * (kStages + s); }
+  __device__ __forceinline__ uint32_t s_full() const { return walk_full(2 * kStages); }
+  __device__ __forceinline__ uint32_t dp_full() const { return s_full() + 8; }
+  __device__ __forceinline__ uint32_t p_full() const { return s_full() + 16; }   // P written (dkv), S read (dq)
+  __device__ __forceinline__ uint32_t ds_full() const { return s_full() + 24; }
+  __device__ __forceinline__ uint32_t sum_full() const { return s_full() + 32; }
+  __device__ __forceinline__ uint32_t info_full(int r) const { return s_full() + 40 + 8 * r; }
+  __device__ __forceinline__ uint32_t info_empty(int r) const { return info_full(kRing + r); }
+  __device__ __forceinline__ uint32_t done() const { return info_full(2 * kRing); }
+  __device__ __forceinline__ uint64_t* at(uint32_t b) const { return bar + (b - bars) / 8; }
+};
+
+// The tiles that an item walks over: `steps` of BC columns for each of `heads`
+// heads, columns [begin, end) of the document.
+struct Range {
+  int begin, end, steps, heads;
+};
+template <bool kDkv, int BC>
+__device__ __forceinline__ Range range_of(const AttnParams& p, const Work& w) {
+  Range r;
+  if constexpr (kDkv) {
+    r.begin = w.row0 < w.keys ? (p.mask == MAXSIM_MASK_FULL || w.row0 < w.prefix ? 0 : w.row0) : w.len;
+    r.end = w.len;
+    r.heads = p.heads / p.kv_heads;
+  } else {
+    r.begin = 0;
+    r.end = row_end(w, p.mask, min(w.len, w.row0 + kTile) - 1);
+    r.heads = 1;
+  }
+  r.steps = (r.end - r.begin + BC - 1) / BC;
+  return r;
+}
+
+struct BwdMaps {
+  CUtensorMap own_a, own_b, walk_a, walk_b;
+};
+
+// ---------------------------------------------------------------- loads
+template <class S, int BC, bool kDkv>
+__device__ void bwd_loader(const AttnParams& p, const BwdSmem<S, BC>& sm, const BwdMaps& m) {
+  const int lane = threadIdx.x & 31, group = p.heads / p.kv_heads;
+  Walk walk;
+  uint32_t item = 0, step = 0;
+  bool ok = true;
+  const auto load = [&](uint32_t dst, uint32_t panel, const CUtensorMap* map, uint32_t bar, int head, int token, int boxes) {
+    for (int b = 0; b < boxes; ++b)
+      for (int pn = 0; pn < S::kPanels; ++pn)
+        tma_load_3d_a(dst + pn * panel + b * (kBoxRows * 128), map, bar, pn * 64, head, token + b * kBoxRows);
+  };
+  for (uint32_t n = 0; ok; ++n) {
+    const Work w = walk.next(p, kTile, kDkv ? p.kv_heads : p.heads, !kDkv && p.mask != MAXSIM_MASK_FULL);
+    if (lane == 0) {
+      const int r = n % kRing;
+      ok = mbar_wait_inl_a(sm.info_empty(r), ((n / kRing) & 1) ^ 1, sm.abort_flag, p.status);
+      if (ok) {
+        sm.info[r] = w;
+        mbar_arrive_a(sm.info_full(r));
+        const Range g = w.live ? range_of<kDkv, BC>(p, w) : Range{0, 0, 0, 0};
+        if (g.steps > 0) {
+          ok = mbar_wait_inl_a(sm.own_empty(), (item & 1) ^ 1, sm.abort_flag, p.status);
+          if (ok) {
+            const int boxes = (min(kTile, w.len - w.row0) + kBoxRows - 1) / kBoxRows;
+            mbar_arrive_expect_tx_a(sm.own_full(), 2 * boxes * S::kPanels * (kBoxRows * 128));
+            load(sm.own_a, S::kOwnPanel, &m.own_a, sm.own_full(), w.head, w.start + w.row0, boxes);
+            load(sm.own_b, S::kOwnPanel, &m.own_b, sm.own_full(), w.head, w.start + w.row0, boxes);
+            ++item;
+          }
+          for (int h = 0; ok && h < g.heads; ++h) {
+            const int head = kDkv ? w.head * group + h : w.head / group;
+            for (int j = 0; j < g.steps; ++j) {
+              const int s = step % kStages, from = g.begin + j * BC;
+              ok = mbar_wait_inl_a(sm.walk_empty(s), ((step / kStages) & 1) ^ 1, sm.abort_flag, p.status);
+              if (!ok) break;
+              const int boxes = (min(BC, g.end - from) + kBoxRows - 1) / kBoxRows;
+              mbar_arrive_expect_tx_a(sm.walk_full(s), 2 * boxes * S::kPanels * (kBoxRows * 128));
+              load(sm.walk_a + s * S::kBytes, S::kPanel, &m.walk_a, sm.walk_full(s), head, w.start + from, boxes);
+              load(sm.walk_b + s * S::kBytes, S::kPanel, &m.walk_b, sm.walk_full(s), head, w.start + from, boxes);
+              ++step;
+            }
+          }
+        }
+      }
+    }
+    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    if (!w.live) break;
+  }
+  if (!ok && lane == 0) {  // after an abort: wait (bounded) for the copies in flight
+    if (item > 0) mbar_wait_drain(sm.at(sm.own_full()), (item - 1) & 1, p.status);
+    for (uint32_t f = step > kStages ? step - kStages : 0; f < step; ++f)
+      mbar_wait_drain(sm.at(sm.walk_full(f % kStages)), (f / kStages) & 1, p.status);
   }
 }
-template <typename T>
-__device__ __forceinline__ void store_row(const HeadsView& v, int64_t t, int h, int d, const float (&r)[kMaxPer]) {
-  T* dst = static_cast<T*>(v.data) + t * v.token_stride + h * v.head_stride;
+
+// The walked rows' (lse2, delta), which every arithmetic thread needs: one
+// warp brings them to shared memory beside the tiles. Its arrival is part of
+// walk_full, so it also keeps an abort's drain from waiting for ever.
+template <class S, int BC>
+__device__ void bwd_stats(const AttnParams& p, const BwdSmem<S, BC>& sm) {
+  const int lane = threadIdx.x & 31, group = p.heads / p.kv_heads;
+  const float2* src = reinterpret_cast<const float2*>(p.delta);
+  uint32_t step = 0;
+  for (uint32_t n = 0;; ++n) {
+    const int r = n % kRing;
+    if (!__all_sync(0xffffffffu, mbar_wait_inl_a(sm.info_full(r), (n / kRing) & 1, sm.abort_flag, p.status))) return;
+    const Work w = sm.info[r];
+    __syncwarp();
+    if (lane == 0) mbar_arrive_a(sm.info_empty(r));
+    if (!w.live) return;
+    const Range g = range_of<true, BC>(p, w);
+    for (int h = 0; h < g.heads; ++h) {
+      const float2* row = src + static_cast<int64_t>(w.head * group + h) * p.T + w.start;
+      for (int j = 0; j < g.steps; ++j, ++step) {
+        const int s = step % kStages, from = g.begin + j * BC;
+        float2 v[BC / 32];
 #pragma unroll
-  for (int k = 0; k < kMaxPer; ++k) {
-    const int c = k * 32 + (threadIdx.x & 31);
-    if (c < d) dst[c] = down<T>(r[k]);
-  }
-}
-__device__ __forceinline__ float dot(const float (&a)[kMaxPer], const float (&b)[kMaxPer]) {
-  float s = 0.f;
+        for (int x = 0; x < BC / 32; ++x) {
+          const int i = from + x * 32 + lane;
+          v[x] = i < g.end ? row[i] : make_float2(INFINITY, 0.f);
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait_inl_a(sm.walk_empty(s), ((step / kStages) & 1) ^ 1, sm.abort_flag, p.status)))
+          return;
 #pragma unroll
-  for (int k = 0; k < kMaxPer; ++k) s = fmaf(a[k], b[k], s);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-  return s;
-}
-
-// The document of token t: the last one that starts at or before it.
-__device__ __forceinline__ bool find_doc(const AttnParams& p, int t, Doc& c, int& i) {
-  int64_t lo = 0, hi = p.B;  // answer in [lo, hi)
-  while (hi - lo > 1) {
-    const int64_t m = lo + (hi - lo) / 2;
-    if (p.offsets[m] <= t) lo = m; else hi = m;
-  }
-  bool bad;
-  c = load_doc(p, lo, bad);
-  i = t - c.start;
-  return i >= 0 && i < c.len;
-}
-
-__device__ __forceinline__ float capped(float s, float cap, float& slope) {
-  slope = 1.f;
-  if (cap <= 0.f) return s;
-  const float t = tanhf(s / cap);
-  slope = 1.f - t * t;
-  return cap * t;
-}
-
-template <typename T>
-__global__ void bwd_delta(const AttnParams p) {
-  const int h = blockIdx.y;
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= p.T) return;
-  float a[kMaxPer], b[kMaxPer];
-  load_row<T>(p.dO, t, h, p.d, a);
-  load_row<T>(p.out, t, h, p.d, b);
-  const float s = dot(a, b);
-  if ((threadIdx.x & 31) == 0) p.delta[static_cast<int64_t>(h) * p.T + t] = s;
-}
-
-// p_ij and dS_ij / dP_ij - delta_i of one pair.
-__device__ __forceinline__ void pair(const AttnParams& p, float qk, float dp, float lse, float delta, float far,
-                                     float& w, float& ds) {
-  float slope;
-  const float z = capped(qk * p.scale, p.cap, slope) - far;
-  w = expf(z - lse);
-  ds = w * (dp - delta) * slope * p.scale;
-}
-
-template <typename T>
-__global__ void bwd_dq_rows(const AttnParams p) {
-  const int h = blockIdx.y;
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= p.T) return;
-  Doc c;
-  int i;
-  if (!find_doc(p, t, c, i)) return;
-  const int g = h / (p.heads / p.kv_heads), end = row_end(c, p.mask, i);
-  const float bias = p.slopes ? p.slopes[h] : 0.f;
-  float q[kMaxPer], k[kMaxPer], v[kMaxPer], dO[kMaxPer], dq[kMaxPer] = {};
-  load_row<T>(p.q, t, h, p.d, q);
-  load_row<T>(p.dO, t, h, p.d, dO);
-  const float lse = p.lse[static_cast<int64_t>(h) * p.T + t], delta = p.delta[static_cast<int64_t>(h) * p.T + t];
-  for (int j = 0; j < end; ++j) {
-    load_row<T>(p.k, c.start + j, g, p.d, k);
-    load_row<T>(p.v, c.start + j, g, p.d, v);
-    float w, ds;
-    pair(p, dot(q, k), dot(dO, v), lse, delta, bias * abs(i - j), w, ds);
-#pragma unroll
-    for (int e = 0; e < kMaxPer; ++e) dq[e] = fmaf(ds, k[e], dq[e]);
-  }
-  store_row<T>(p.dq, t, h, p.d, dq);
-}
-
-template <typename T>
-__global__ void bwd_dkv_rows(const AttnParams p) {
-  const int g = blockIdx.y;
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= p.T) return;
-  Doc c;
-  int j;
-  if (!find_doc(p, t, c, j)) return;
-  float q[kMaxPer], k[kMaxPer], v[kMaxPer], dO[kMaxPer], dk[kMaxPer] = {}, dv[kMaxPer] = {};
-  load_row<T>(p.k, t, g, p.d, k);
-  load_row<T>(p.v, t, g, p.d, v);
-  const int group = p.heads / p.kv_heads;
-  for (int h = g * group; j < c.keys && h < (g + 1) * group; ++h) {
-    const float bias = p.slopes ? p.slopes[h] : 0.f;
-    for (int i = key_begin(c, p.mask, j); i < c.len; ++i) {
-      const int64_t r = static_cast<int64_t>(h) * p.T + c.start + i;
-      load_row<T>(p.q, c.start + i, h, p.d, q);
-      load_row<T>(p.dO, c.start + i, h, p.d, dO);
-      float w, ds;
-      pair(p, dot(q, k), dot(dO, v), p.lse[r], p.delta[r], bias * abs(i - j), w, ds);
-#pragma unroll
-      for (int e = 0; e < kMaxPer; ++e) {
-        dv[e] = fmaf(w, dO[e], dv[e]);
-        dk[e] = fmaf(ds, q[e], dk[e]);
+        for (int x = 0; x < BC / 32; ++x) sm.stats[s * BC + x * 32 + lane] = v[x];
+        __syncwarp();
+        if (lane == 0) mbar_arrive_a(sm.walk_full(s));
       }
     }
   }
-  store_row<T>(p.dk, t, g, p.d, dk);
-  store_row<T>(p.dv, t, g, p.d, dv);
+}
+
+// ------------------------------------------------------------- products
+template <class S, int DH, int BC, bool kDkv, bool kBf16>
+__device__ void bwd_products(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t tmem) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t idesc = idesc_f16(kBf16, kTile, 0);
+  const uint32_t idesc_sum = idesc | static_cast<uint32_t>(DH >> 3) << 17 | kIdescBMnMajor;
+  uint32_t item = 0, step = 0;
+  const auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait_inl_a(bar, ph & 1, sm.abort_flag, p.status));
+  };
+  // 128 x cols scores of the block's rows and the walked ones of stage s
+  const auto score = [&](uint32_t d_col, uint32_t own, uint32_t walked, int cols) {
+    const uint32_t id = idesc | static_cast<uint32_t>(cols >> 3) << 17;
+    const uint64_t a = sdesc_k_sw128(own), b = sdesc_k_sw128(walked);
+#pragma unroll
+    for (int kk = 0; kk < DH / 16; ++kk)
+      umma_f16_el(tmem + d_col, a + (kk / 4) * (S::kOwnPanel >> 4) + (kk % 4) * 2,
+                  b + (kk / 4) * (S::kPanel >> 4) + (kk % 4) * 2, id, kk != 0);
+  };
+  // sum += A (16-bit, over the score tile at a_col) * the walked rows of stage s
+  const auto add = [&](uint32_t d_col, uint32_t a_col, uint32_t walked, int cols, bool first) {
+    const uint64_t b = sdesc_mn_sw128(walked, S::kPanel);
+    for (int kk = 0; kk < cols / 16; ++kk)
+      umma_f16_ts_el(tmem + d_col, tmem + a_col + (kk / 4) * 64 + (kk % 4) * 8, b + kk * (2048 >> 4), idesc_sum,
+                     !first || kk != 0);
+  };
+  bool ok = true;
+  for (uint32_t n = 0; ok; ++n) {
+    const int r = n % kRing;
+    if (!wait(sm.info_full(r), n / kRing)) break;
+    const Work w = sm.info[r];
+    __syncwarp();
+    if (lane == 0) mbar_arrive_a(sm.info_empty(r));
+    if (!w.live) break;
+    const Range g = range_of<kDkv, BC>(p, w);
+    if (g.steps <= 0) continue;
+    const int total = g.steps * g.heads;
+    int at = 0;  // step within the head of the tile that is made ready next
+    // Waits for walked tile step + i, zeroes the rows behind its last one (up to
+    // a multiple of 16): their weights are 0, and 0 * NaN would reach the sums.
+    const auto ready = [&](int i, int& cols) -> bool {
+      const int s = (step + i) % kStages, used = min(BC, g.end - g.begin - at * BC);
+      if (++at == g.steps) at = 0;
+      if (!wait(sm.walk_full(s), (step + i) / kStages)) return false;
+      cols = (used + 15) & ~15;
+      if (used != cols) {
+        const uint32_t vec = (cols - used) * 8;
+        for (uint32_t e = lane; e < vec * S::kPanels * 2; e += 32) {
+          const uint32_t pn = (e / vec) % S::kPanels, base = e / vec < S::kPanels ? sm.walk_a : sm.walk_b;
+          const uint32_t dst = base + s * S::kBytes + pn * S::kPanel + used * 128 + (e % vec) * 16;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      return true;
+    };
+    int cols = 0, next = 0;
+    ok = wait(sm.own_full(), item) && ready(0, cols);
+    if (!ok) break;
+    tc_fence_after();
+    score(0, sm.own_a, sm.walk_a + step % kStages * S::kBytes, cols);
+    umma_commit_el(sm.s_full());
+    score(S::kDp, sm.own_b, sm.walk_b + step % kStages * S::kBytes, cols);
+    umma_commit_el(sm.dp_full());
+    for (int i = 0; i < total; ++i) {
+      const uint32_t u = step + i, s = u % kStages, s1 = (u + 1) % kStages;
+      if (!(ok = wait(sm.p_full(), u))) break;
+      tc_fence_after();
+      if constexpr (kDkv) add(S::kSum0, 0, sm.walk_b + s * S::kBytes, cols, i == 0);
+      if (i + 1 < total) {
+        if (!(ok = ready(i + 1, next))) break;
+        tc_fence_after();
+        score(0, sm.own_a, sm.walk_a + s1 * S::kBytes, next);
+        umma_commit_el(sm.s_full());
+      }
+      if (!(ok = wait(sm.ds_full(), u))) break;
+      tc_fence_after();
+      add(kDkv ? S::kSum1 : S::kSum0, S::kDp, sm.walk_a + s * S::kBytes, cols, i == 0);
+      umma_commit_el(sm.walk_empty(s));
+      if (i + 1 < total) {
+        score(S::kDp, sm.own_b, sm.walk_b + s1 * S::kBytes, next);
+        umma_commit_el(sm.dp_full());
+        if (i + 2 == total) umma_commit_el(sm.own_empty());
+      }
+      cols = next;
+    }
+    if (!ok) break;
+    if (total == 1) umma_commit_el(sm.own_empty());
+    umma_commit_el(sm.sum_full());
+    step += total;
+    ++item;
+  }
+  umma_commit_el(sm.done());
+  mbar_wait_drain(sm.at(sm.done()), 0, p.status);
+}
+
+// ----------------------------------------------------------- arithmetic
+// 32 columns of fp32 sums, times f, as 16-bit values of a row.
+template <bool kBf16>
+__device__ __forceinline__ void store_sums(uint32_t col, uint4* dst, int first, int d, float f, bool live, bool any) {
+  uint32_t o[32];
+  if (any) {
+    tmem_ld_32x32b_x32_issue(col, o);
+    tmem_wait_ld_regs(o);
+  }
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    uint4 y = make_uint4(0, 0, 0, 0);
+    if (any) {
+      const float* v = reinterpret_cast<const float*>(o) + x * 8;
+      y = make_uint4(pack2<kBf16>(v[0] * f, v[1] * f), pack2<kBf16>(v[2] * f, v[3] * f),
+                     pack2<kBf16>(v[4] * f, v[5] * f), pack2<kBf16>(v[6] * f, v[7] * f));
+    }
+    if (live && first + x * 8 < d) dst[first / 8 + x] = y;
+  }
+}
+__device__ __forceinline__ uint4* row_of(const HeadsView& v, int64_t token, int head) {
+  return reinterpret_cast<uint4*>(static_cast<uint16_t*>(v.data) + token * v.token_stride + head * v.head_stride);
+}
+
+template <class S, int DH, int BC, bool kDkv, bool kBf16, bool kCap, bool kBias>
+__device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t tmem) {
+  const int wg = threadIdx.x >> 7, lane = threadIdx.x & 31, group = p.heads / p.kv_heads;
+  const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;
+  const uint32_t s_col = tmem + lanes + wg * 64, dp_col = s_col + S::kDp;
+  const float c = kCap || kBias ? 1.f : p.scale * kLog2e;
+  const float to_log2 = p.scale * kLog2e, cap2 = p.cap * kLog2e, in_cap = kCap ? 2.f * kLog2e * p.scale / p.cap : 0.f;
+  uint32_t step = 0, item = 0;
+  const auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait_inl_a(bar, ph & 1, sm.abort_flag, p.status));
+  };
+  for (uint32_t n = 0;; ++n) {
+    const int r = n % kRing;
+    if (!wait(sm.info_full(r), n / kRing)) return;
+    const Work w = sm.info[r];
+    __syncwarp();
+    if (lane == 0) mbar_arrive_a(sm.info_empty(r));
+    if (!w.live) return;
+    const Range g = range_of<kDkv, BC>(p, w);
+    const int mine = w.row0 + static_cast<int>(threadIdx.x & 127);  // this thread's key, or row
+    // columns [lo, hi) of the document that meet this thread's row, and the
+    // columns from `clear` up to `clear_end` that meet every row of the block
+    int lo, hi, clear, clear_end;
+    float lse2 = 0.f, delta = 0.f;
+    if constexpr (kDkv) {
+      lo = mine < w.keys ? (p.mask == MAXSIM_MASK_FULL || mine < w.prefix ? 0 : mine) : w.len;
+      hi = w.len;
+      const int last = w.row0 + kTile - 1;
+      clear = last < w.keys ? (p.mask == MAXSIM_MASK_FULL || last < w.prefix ? 0 : last) : w.len;
+      clear_end = w.len;
+    } else {
+      lo = 0;
+      hi = row_end(w, p.mask, min(mine, w.len - 1));
+      clear = 0;
+      clear_end = w.row0 + kTile <= w.len ? row_end(w, p.mask, w.row0) : 0;
+      if (mine < w.len) {
+        const float2 st = reinterpret_cast<const float2*>(p.delta)[static_cast<int64_t>(w.head) * p.T + w.start + mine];
+        lse2 = st.x;
+        delta = st.y;
+      } else {
+        hi = 0;
+      }
+    }
+    for (int h = 0; h < g.heads; ++h) {
+      const float slope2 = kBias ? p.slopes[kDkv ? w.head * group + h : w.head] * kLog2e : 0.f;
+      for (int j = 0; j < g.steps; ++j, ++step) {
+        const int from = g.begin + j * BC + wg * 64, used = min(64, g.end - from);  // this warpgroup's columns
+        const bool masked = from < clear || g.begin + (j + 1) * BC > clear_end;
+        const float2* st = sm.stats + (step % kStages) * BC + wg * 64;
+        float v[64];  // weights, then weights * bend
+        if (!wait(sm.s_full(), step)) return;
+        // the statistics came with the walked tile, whose products have been made from it
+        if (kDkv && !wait(sm.walk_full(step % kStages), step / kStages)) return;
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (q * 32 < used) {
+            uint32_t u[32];
+            tmem_ld_32x32b_x32_issue(s_col + q * 32, u);
+            tmem_wait_ld_regs(u);
+            uint32_t pk[16];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const int col = from + q * 32 + x;
+              float z = __uint_as_float(u[x]), bend = 1.f;
+              if constexpr (kCap) {
+                const float t = fast_tanh(z * in_cap);
+                z = cap2 * t;
+                bend = fmaf(-t, t, 1.f);
+              }
+              if constexpr (kBias) {
+                if constexpr (!kCap) z *= to_log2;
+                z = fmaf(-slope2, fabsf(static_cast<float>(mine - col)), z);
+              }
+              float e = fast_exp2(fmaf(z, c, -(kDkv ? st[q * 32 + x].x : lse2)));
+              if (masked) e = col >= lo && col < hi ? e : 0.f;
+              v[q * 32 + x] = kCap ? (masked && e == 0.f ? 0.f : e * bend) : e;
+              if constexpr (kDkv) {
+                if (x & 1) pk[x / 2] = pack2<kBf16>(__uint_as_float(u[x - 1]), e);
+                else u[x] = __float_as_uint(e);
+              }
+            }
+            if constexpr (kDkv) tmem_st_32x32b_x16_issue(s_col + q * 16, pk);
+          }
+        }
+        if constexpr (kDkv) tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_a(sm.p_full());
+        if (!wait(sm.dp_full(), step)) return;
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (q * 32 < used) {
+            uint32_t u[32], pk[16];
+            tmem_ld_32x32b_x32_issue(dp_col + q * 32, u);
+            tmem_wait_ld_regs(u);
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              float a = __uint_as_float(u[x]) - (kDkv ? st[q * 32 + x].y : delta);
+              float b = __uint_as_float(u[x + 1]) - (kDkv ? st[q * 32 + x + 1].y : delta);
+              const float wa = v[q * 32 + x], wb = v[q * 32 + x + 1];
+              // where nothing is seen the difference may be anything
+              a = masked && wa == 0.f ? 0.f : wa * a;
+              b = masked && wb == 0.f ? 0.f : wb * b;
+              pk[x / 2] = pack2<kBf16>(a, b);
+            }
+            tmem_st_32x32b_x16_issue(dp_col + q * 16, pk);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_a(sm.ds_full());
+          if constexpr (kDkv) mbar_arrive_a(sm.walk_empty(step % kStages));  // the statistics have been read
+        }
+      }
+    }
+    const bool any = g.steps > 0, live = mine < w.len;
+    if (any) {
+      if (!wait(sm.sum_full(), item)) return;
+      ++item;
+      tc_fence_after();
+    }
+    const int64_t token = w.start + mine;
+    constexpr int kChunks = DH / 32;
+    if constexpr (kDkv) {
+      uint4 *dv = row_of(p.dv, token, w.head), *dk = row_of(p.dk, token, w.head);
+#pragma unroll
+      for (int q = 0; q < kChunks; ++q) {  // two warpgroups: one writes dV, one dK
+        if (S::kGroups == 1 || wg == 0)
+          store_sums<kBf16>(tmem + lanes + S::kSum0 + q * 32, dv, q * 32, p.d, 1.f, live, any);
+        if (S::kGroups == 1 || wg == 1)
+          store_sums<kBf16>(tmem + lanes + S::kSum1 + q * 32, dk, q * 32, p.d, p.scale, live, any);
+      }
+    } else {
+      uint4* dq = row_of(p.dq, token, w.head);
+#pragma unroll
+      for (int q = 0; q < kChunks; ++q)
+        if (S::kGroups == 1 || q / (kChunks / 2) == wg)
+          store_sums<kBf16>(tmem + lanes + S::kSum0 + q * 32, dq, q * 32, p.d, p.scale, live, any);
+    }
+    tc_fence_before();  // the next item's first products overwrite the sums after its p_full / ds_full
+  }
+}
+
+template <int DH, int BC, bool kDkv, bool kBf16, bool kCap, bool kBias>
+__global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH, BC, kDkv>::kBlocks)
+    attn_bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ AttnParams p) {
+  using S = BwdShape<DH, BC, kDkv>;
+  extern __shared__ uint8_t raw[];
+  const BwdSmem<S, BC> sm(raw, kDkv);
+  constexpr int kMathWarps = 4 * S::kGroups;
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    mbar_init(sm.at(sm.own_full()), 1);
+    mbar_init(sm.at(sm.own_empty()), 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(sm.at(sm.walk_full(s)), kDkv ? 2 : 1);                // the loader, and the statistics' warp
+      mbar_init(sm.at(sm.walk_empty(s)), kDkv ? 1 + kMathWarps : 1);  // the products, and the statistics' readers
+    }
+    mbar_init(sm.at(sm.s_full()), 1);
+    mbar_init(sm.at(sm.dp_full()), 1);
+    mbar_init(sm.at(sm.p_full()), kMathWarps);
+    mbar_init(sm.at(sm.ds_full()), kMathWarps);
+    mbar_init(sm.at(sm.sum_full()), 1);
+    for (int r = 0; r < kRing; ++r) {
+      mbar_init(sm.at(sm.info_full(r)), 1);
+      mbar_init(sm.at(sm.info_empty(r)), kMathWarps + (kDkv ? 2 : 1));
+    }
+    mbar_init(sm.at(sm.done()), 1);
+    *sm.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMathWarps + 1) {
+    tmem_alloc(sm.tmem_slot, S::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *sm.tmem_slot;
+  if (warp >= kMathWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsOther));
+    if (warp == kMathWarps) bwd_loader<S, BC, kDkv>(p, sm, m);
+    else if (warp == kMathWarps + 1) bwd_products<S, DH, BC, kDkv, kBf16>(p, sm, tmem);
+    else if (kDkv && warp == kMathWarps + 2) bwd_stats<S, BC>(p, sm);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsMath));
+    bwd_math<S, DH, BC, kDkv, kBf16, kCap, kBias>(p, sm, tmem);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMathWarps + 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kTmemCols);
+  }
+}
+
+// (lse in log2 units, <dO, out>) of every row and head, [heads][T]. A row is
+// read by L lanes of 16 bytes each. A row that sees nothing gets lse2 =
+// +infinity, so that its weights are 0.
+template <bool kBf16>
+__global__ void __launch_bounds__(256) attn_stats_kernel(const AttnParams p, int L) {
+  const int64_t id = blockIdx.x * int64_t(256) + threadIdx.x;
+  const int64_t row = id / L;  // heads run fastest, as in memory
+  const int part = static_cast<int>(id % L);
+  check_docs(p, id, gridDim.x * int64_t(256));
+  const bool live = row < static_cast<int64_t>(p.T) * p.heads;
+  const int64_t t = live ? row / p.heads : 0;
+  const int h = live ? static_cast<int>(row % p.heads) : 0;
+  float s = 0.f;
+  if (live && part * 8 < p.d) {
+    const uint4 a = row_of(p.dO, t, h)[part], b = row_of(p.out, t, h)[part];
+    const uint32_t *x = &a.x, *y = &b.x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float2 f, g;
+      if constexpr (kBf16) {
+        f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(x + k));
+        g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(y + k));
+      } else {
+        f = __half22float2(*reinterpret_cast<const __half2*>(x + k));
+        g = __half22float2(*reinterpret_cast<const __half2*>(y + k));
+      }
+      s = fmaf(f.x, g.x, fmaf(f.y, g.y, s));
+    }
+  }
+  for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (live && part == 0) {
+    const float lse = p.lse[static_cast<int64_t>(h) * p.T + t];
+    reinterpret_cast<float2*>(p.delta)[static_cast<int64_t>(h) * p.T + t] =
+        make_float2(lse == -INFINITY ? INFINITY : lse * kLog2e, s);
+  }
+}
+
+template <int DH, int BC, bool kDkv, bool kBf16, bool kCap, bool kBias>
+cudaError_t bwd_launch(const BwdMaps& m, const AttnParams& p, int sm_count, cudaStream_t stream) {
+  using S = BwdShape<DH, BC, kDkv>;
+  auto kern = attn_bwd_kernel<DH, BC, kDkv, kBf16, kCap, kBias>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t items = (p.T / kTile + p.B) * (kDkv ? p.kv_heads : p.heads);
+  const int64_t most = static_cast<int64_t>(sm_count) * S::kBlocks;
+  kern<<<static_cast<int>(items < most ? items : most), S::kThreads, S::kSmem, stream>>>(m, p);
+  return cudaGetLastError();
+}
+
+template <int DH, int BC, bool kDkv, bool kBf16>
+cudaError_t bwd_variant(const BwdMaps& m, const AttnParams& p, int sm_count, cudaStream_t stream) {
+  if (p.cap > 0.f)
+    return p.slopes ? bwd_launch<DH, BC, kDkv, kBf16, true, true>(m, p, sm_count, stream)
+                    : bwd_launch<DH, BC, kDkv, kBf16, true, false>(m, p, sm_count, stream);
+  return p.slopes ? bwd_launch<DH, BC, kDkv, kBf16, false, true>(m, p, sm_count, stream)
+                  : bwd_launch<DH, BC, kDkv, kBf16, false, false>(m, p, sm_count, stream);
+}
+
+template <int DH, int BC>
+cudaError_t bwd_both(const BwdMaps& dkv, const BwdMaps& dq, const AttnParams& p, int is_bf16, int sm_count,
+                     cudaStream_t stream) {
+  cudaError_t e = is_bf16 ? bwd_variant<DH, BC, true, true>(dkv, p, sm_count, stream)
+                          : bwd_variant<DH, BC, true, false>(dkv, p, sm_count, stream);
+  if (e != cudaSuccess) return e;
+  return is_bf16 ? bwd_variant<DH, BC, false, true>(dq, p, sm_count, stream)
+                 : bwd_variant<DH, BC, false, false>(dq, p, sm_count, stream);
 }
 
 }  // namespace
 
-template <typename T>
-static void launch_bwd_typed(const AttnParams& p, cudaStream_t stream) {
-  const dim3 rows((p.T + kWarps - 1) / kWarps, p.heads), keys(rows.x, p.kv_heads);
-  bwd_delta<T><<<rows, kWarps * 32, 0, stream>>>(p);
-  bwd_dq_rows<T><<<rows, kWarps * 32, 0, stream>>>(p);
-  bwd_dkv_rows<T><<<keys, kWarps * 32, 0, stream>>>(p);
-}
-
 maxsim_status launch_attn_bwd(const AttnParams& p, int is_bf16, cudaStream_t stream) {
-  if (is_bf16) launch_bwd_typed<__nv_bfloat16>(p, stream);
-  else launch_bwd_typed<__half>(p, stream);
-  return cudaGetLastError() == cudaSuccess ? MAXSIM_OK : MAXSIM_ERR_CUDA;
+  const DeviceInfo* dev = device_info();
+  if (!dev) return MAXSIM_ERR_CUDA;
+  alignas(64) BwdMaps dkv, dq;
+  if (!attn_tmap(&dkv.own_a, p.k, p.T, p.kv_heads, p.d, is_bf16, kBoxRows) ||
+      !attn_tmap(&dkv.own_b, p.v, p.T, p.kv_heads, p.d, is_bf16, kBoxRows) ||
+      !attn_tmap(&dkv.walk_a, p.q, p.T, p.heads, p.d, is_bf16, kBoxRows) ||
+      !attn_tmap(&dkv.walk_b, p.dO, p.T, p.heads, p.d, is_bf16, kBoxRows))
+    return MAXSIM_ERR_CUDA;
+  dq.own_a = dkv.walk_a;
+  dq.own_b = dkv.walk_b;
+  dq.walk_a = dkv.own_a;
+  dq.walk_b = dkv.own_b;
+  int L = 1;
+  while (L * 8 < p.d) L *= 2;
+  const int64_t blocks = (static_cast<int64_t>(p.T) * p.heads * L + 255) / 256;
+  if (blocks > 0x7fffffff) return MAXSIM_ERR_UNSUPPORTED;
+  if (is_bf16) attn_stats_kernel<true><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p, L);
+  else attn_stats_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p, L);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess)
+    e = p.d <= 64 ? bwd_both<64, 64>(dkv, dq, p, is_bf16, dev->sm_count, stream)
+                  : bwd_both<128, 128>(dkv, dq, p, is_bf16, dev->sm_count, stream);
+  return e == cudaSuccess ? MAXSIM_OK : MAXSIM_ERR_CUDA;
 }
 
 }  // namespace msim
