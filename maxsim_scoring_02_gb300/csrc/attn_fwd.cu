@@ -41,9 +41,9 @@ struct FwdShape {
   static constexpr int kThreads = NQ * 128 + 128;  // softmax warpgroups; loader, issuer and two idle warps
   static constexpr int kBlocks = NQ == 1 ? 2 : 1;  // resident on an SM
   // Registers a thread: at launch (ptxas fills the launch bounds), and after
-  // the softmax threads, which hold a row's 128 scores, took over the others'.
+  // the softmax threads took over some of the others'.
   static constexpr int kRegsLaunch = NQ == 1 ? 128 : 168;
-  static constexpr int kRegsSoftmax = NQ == 1 ? 200 : 224, kRegsOther = 56;
+  static constexpr int kRegsSoftmax = NQ == 1 ? 160 : 200, kRegsOther = NQ == 1 ? 96 : 104;
   static_assert(NQ * kRegsSoftmax + kRegsOther <= (NQ + 1) * kRegsLaunch, "register split");
   static constexpr uint32_t kTmemCols = NQ == 1 ? 256 : 512;
   static constexpr uint32_t kO0 = NQ * kTile;  // TMEM columns: S of each tile, then O of each tile
@@ -264,6 +264,110 @@ __device__ void fwd_products(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uin
 }
 
 // -------------------------------------------------------------- softmax
+// What a softmax thread keeps of its row.
+struct RowState {
+  float m, sum;  // maximum in the units of the scores held, sum of the weights
+};
+struct ScoreConst {
+  float c, to_log2, cap2, in_cap;  // c brings held scores to log2 units
+};
+
+// A group of 32 scores brought to the units that maxima are taken in; `far` is
+// the row less the group's first key, `lim` how many of its keys are seen.
+template <bool kCap, bool kBias, bool kEdge>
+__device__ __forceinline__ void finish_scores(uint32_t (&u)[32], const ScoreConst& k, float slope2, float far, int lim) {
+#pragma unroll
+  for (int x = 0; x < 32; ++x) {
+    float z = __uint_as_float(u[x]);
+    if constexpr (kCap) z = k.cap2 * fast_tanh(z * k.in_cap);
+    if constexpr (kBias) {
+      if constexpr (!kCap) z *= k.to_log2;
+      z = fmaf(-slope2, fabsf(far - static_cast<float>(x)), z);
+    }
+    if constexpr (kEdge) z = x < lim ? z : -INFINITY;
+    u[x] = __float_as_uint(z);
+  }
+}
+__device__ __forceinline__ float group_max(const uint32_t (&u)[32], float m) {
+  float t[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int x = 0; x < 32; x += 2) t[x / 2 % 4] = max3(t[x / 2 % 4], __uint_as_float(u[x]), __uint_as_float(u[x + 1]));
+  return fmaxf(max3(t[0], t[1], t[2]), t[3]);
+}
+// Weights of a group to TMEM; their sum is added to part.
+template <bool kBf16>
+__device__ __forceinline__ void group_weights(uint32_t p_col, const uint32_t (&u)[32], Pair scale, Pair shift, Pair (&part)[2]) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int x = 0; x < 32; x += 2) {
+    float a, b;
+    fma2(Pair(__uint_as_float(u[x]), __uint_as_float(u[x + 1])), scale, shift).get(a, b);
+    a = fast_exp2(a);
+    b = fast_exp2(b);
+    part[x / 2 % 2] = add2(part[x / 2 % 2], Pair(a, b));
+    pk[x / 2] = pack2<kBf16>(a, b);
+  }
+  tmem_st_32x32b_x16_issue(p_col, pk);
+}
+
+// One tile of scores of this thread's row: weights to TMEM, m and sum brought
+// up to date (and O with them). The scores are read twice, 32 at a time with the
+// next group on its way, rather than kept: 128 registers of them spilled.
+// Bent scores are written back between. kEdge: the tile has fewer than 128
+// columns, or some of them are hidden from the row (those from `lim` on).
+template <int DH, bool kBf16, bool kCap, bool kBias, bool kEdge>
+__device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, const ScoreConst& k, float slope2,
+                                             float far, int cols, int lim, bool first, RowState& st) {
+  uint32_t u[2][32];
+  float now = st.m;
+  tmem_ld_32x32b_x32_issue(s_col, u[0]);
+  tmem_wait_ld_regs(u[0]);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (kEdge && q * 32 >= cols) break;
+    if (q + 1 < 4 && (!kEdge || (q + 1) * 32 < cols)) tmem_ld_32x32b_x32_issue(s_col + (q + 1) * 32, u[(q + 1) & 1]);
+    finish_scores<kCap, kBias, kEdge>(u[q & 1], k, slope2, far - q * 32, lim - q * 32);
+    now = group_max(u[q & 1], now);
+    if constexpr (kCap) tmem_st_32x32b_x32_issue(s_col + q * 32, u[q & 1]);
+    tmem_wait_ld_regs(u[(q + 1) & 1]);
+  }
+  if constexpr (kCap) tmem_wait_st();
+  tmem_ld_32x32b_x32_issue(s_col, u[0]);
+  // The first tile sets the maximum; later ones raise it when it has grown a lot.
+  if (first) {
+    st.m = now;
+  } else if (__any_sync(0xffffffffu, (now - st.m) * k.c > kRaise)) {
+    const float keep = now == -INFINITY ? 1.f : fast_exp2((st.m - now) * k.c);
+    st.sum *= keep;
+    st.m = now;
+#pragma unroll 1
+    for (int q = 0; q < DH / 16; ++q) {
+      uint32_t o[16];
+      tmem_ld_32x32b_x16(o_col + q * 16, o);
+#pragma unroll
+      for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
+      tmem_st_32x32b_x16_issue(o_col + q * 16, o);
+    }
+  }
+  const float down = st.m == -INFINITY ? 0.f : -st.m * k.c;
+  const Pair scale(k.c, k.c), shift(down, down);
+  Pair part[2] = {Pair(0.f, 0.f), Pair(0.f, 0.f)};
+  tmem_wait_ld_regs(u[0]);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (kEdge && q * 32 >= cols) break;
+    if (q + 1 < 4 && (!kEdge || (q + 1) * 32 < cols)) tmem_ld_32x32b_x32_issue(s_col + (q + 1) * 32, u[(q + 1) & 1]);
+    if constexpr (!kCap && (kBias || kEdge))
+      finish_scores<kCap, kBias, kEdge>(u[q & 1], k, slope2, far - q * 32, lim - q * 32);
+    group_weights<kBf16>(s_col + q * 16, u[q & 1], scale, shift, part);
+    tmem_wait_ld_regs(u[(q + 1) & 1]);
+  }
+  float lo, hi;
+  add2(part[0], part[1]).get(lo, hi);
+  st.sum += lo + hi;
+  tmem_wait_st();
+}
+
 template <int DH, int NQ, bool kBf16, bool kCap, bool kBias>
 __device__ void fwd_softmax(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint32_t tmem) {
   using S = FwdShape<DH, NQ>;
@@ -271,14 +375,15 @@ __device__ void fwd_softmax(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint
   const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;  // this warp's 32 TMEM lanes
   const uint32_t s_col = tmem + lanes + t * kTile, o_col = tmem + lanes + S::kO0 + t * DH;
   // scores are brought to log2 units by c, or are there already once bent or biased
-  const float to_log2 = p.scale * kLog2e;
-  const float c = kCap || kBias ? 1.f : to_log2;
-  const float cap2 = p.cap * kLog2e, in_cap = kCap ? 2.f * kLog2e * p.scale / p.cap : 0.f;
+  const ScoreConst k = {kCap || kBias ? 1.f : p.scale * kLog2e, p.scale * kLog2e, p.cap * kLog2e,
+                        kCap ? 2.f * kLog2e * p.scale / p.cap : 0.f};
   uint32_t sn = 0, on = 0;
-  const auto wait = [&](uint32_t bar, uint32_t ph) { return mbar_wait_inl_a(bar, ph & 1, sm.abort_flag, p.status); };
+  const auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait_inl_a(bar, ph & 1, sm.abort_flag, p.status));
+  };
   for (uint32_t n = 0;; ++n) {
     const int r = n % kRing;
-    if (!__all_sync(0xffffffffu, wait(sm.info_full(r), n / kRing))) return;
+    if (!wait(sm.info_full(r), n / kRing)) return;
     const Work w = sm.info[r];
     __syncwarp();
     if (lane == 0) mbar_arrive_a(sm.info_empty(r));
@@ -288,81 +393,24 @@ __device__ void fwd_softmax(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint
     const int keys = tile_keys(w, p.mask, t), nk = tiles_of(keys);
     const int end = row_end(w, p.mask, min(row, w.len - 1)), all_see = row_end(w, p.mask, first);
     const float slope2 = kBias ? p.slopes[w.head] * kLog2e : 0.f;
-    float m = -INFINITY, sum = 0.f;  // m is in the units of the scores held in v
-    for (int j = 0; j < nk; ++j) {
-      const int cols = min(kTile, keys - j * kTile);
-      if (!__all_sync(0xffffffffu, wait(sm.s_full(t), sn))) return;
-      ++sn;
+    RowState st = {-INFINITY, 0.f};
+    for (int j = 0; j < nk; ++j, ++sn) {
+      if (!wait(sm.s_full(t), sn)) return;
       tc_fence_after();
-      uint32_t u[4][32];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q * 32 < cols) tmem_ld_32x32b_x32_issue(s_col + q * 32, u[q]);
-      tmem_wait_ld_regs(u[0]);
-#pragma unroll
-      for (int q = 1; q < 4; ++q) reg_order(u[q]);
-      const bool masked = (j + 1) * kTile > all_see;
-      const int lim = end - j * kTile;
-      float top[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        top[q] = -INFINITY;
-        if (q * 32 >= cols) continue;
-#pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          float z = __uint_as_float(u[q][x]);
-          if constexpr (kCap) z = cap2 * fast_tanh(z * in_cap);
-          if constexpr (kBias) {
-            if constexpr (!kCap) z *= to_log2;
-            z = fmaf(-slope2, fabsf(static_cast<float>(row - (j * kTile + q * 32 + x))), z);
-          }
-          if (masked) z = q * 32 + x < lim ? z : -INFINITY;
-          u[q][x] = __float_as_uint(z);
-          top[q] = fmaxf(top[q], z);
-        }
-      }
-      const float now = fmaxf(fmaxf(m, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
-      // The first tile sets the maximum; later ones raise it when it has grown a lot.
-      if (j == 0) {
-        m = now;
-      } else if (__any_sync(0xffffffffu, (now - m) * c > kRaise)) {
-        const float keep = now == -INFINITY ? 1.f : fast_exp2((m - now) * c);
-        sum *= keep;
-        m = now;
-#pragma unroll
-        for (int q = 0; q < DH / 32; ++q) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32_issue(o_col + q * 32, o);
-          tmem_wait_ld_regs(o);
-#pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
-          tmem_st_32x32b_x32_issue(o_col + q * 32, o);
-        }
-      }
-      const float shift = m == -INFINITY ? 0.f : -m * c;
-      float part[4] = {};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (q * 32 >= cols) continue;
-        uint32_t pk[16];
-#pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          const float a = fast_exp2(fmaf(__uint_as_float(u[q][x]), c, shift));
-          const float b = fast_exp2(fmaf(__uint_as_float(u[q][x + 1]), c, shift));
-          part[x / 2 % 4] += a + b;
-          pk[x / 2] = pack2<kBf16>(a, b);
-        }
-        tmem_st_32x32b_x16_issue(s_col + q * 16, pk);
-      }
-      sum += (part[0] + part[1]) + (part[2] + part[3]);
-      tmem_wait_st();
+      const float far = static_cast<float>(row - j * kTile);
+      if ((j + 1) * kTile <= all_see)
+        softmax_tile<DH, kBf16, kCap, kBias, false>(s_col, o_col, k, slope2, far, kTile, kTile, j == 0, st);
+      else
+        softmax_tile<DH, kBf16, kCap, kBias, true>(s_col, o_col, k, slope2, far, min(kTile, keys - j * kTile),
+                                                   end - j * kTile, j == 0, st);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_a(sm.p_full(t));
     }
-    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // a row that sees nothing is 0
+    const bool some = st.sum > 0.f || st.sum != st.sum;  // a row that sees nothing is 0
+    const float inv = some ? 1.f / st.sum : 0.f;
     if (nk > 0) {
-      if (!__all_sync(0xffffffffu, wait(sm.o_full(t), on))) return;
+      if (!wait(sm.o_full(t), on)) return;
       ++on;
       tc_fence_after();
     }
@@ -388,7 +436,7 @@ __device__ void fwd_softmax(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint
       }
     }
     if (p.lse && row < w.len)
-      p.lse[static_cast<int64_t>(w.head) * p.T + token] = sum > 0.f || sum != sum ? (m * c + log2f(sum)) * kLn2 : -INFINITY;
+      p.lse[static_cast<int64_t>(w.head) * p.T + token] = some ? (st.m * k.c + log2f(st.sum)) * kLn2 : -INFINITY;
   }
 }
 
