@@ -4,25 +4,35 @@
 // and delta = <dO, out>. The other two make each score again and own what they
 // write, so there are no atomics and results do not depend on scheduling:
 //
-//   attn_dkv_kernel: 128 keys of one document and key-value head, walking
-//     over the query heads that share it and over the rows that see the keys:
-//       S^T = K Q^T, dP^T = V dO^T          (both operands in shared memory)
-//       P^T = 2^(S^T c - lse2), dS^T = P^T (dP^T - delta) bend
-//       dV += P^T dO, dK += dS^T Q          (A from TMEM, B as it lies in memory)
-//   attn_dq_kernel: 128 rows of one document and head, walking over the keys:
-//       S = Q K^T, dP = dO V^T, dS as above, dQ += dS K
+//   dQ:  128 rows of one document and head, walking over the keys:
+//       S = Q K^T, dP = dO V^T               (both operands in shared memory)
+//       P = 2^(S c - lse2), dS = P (dP - delta) bend
+//       dQ += dS K, R += P bend K            (A from TMEM, B as it lies in memory)
+//   dK and dV:  128 keys of one document and key-value head, walking over the
+//     query heads that share it and over the rows that see the keys:
+//       S^T = K Q^T, dP^T = V dO^T, P^T and dS^T as above
+//       dV += P^T dO, dK += dS^T Q
 //
-// Seven products of 128 x 128 x d for a tile where five would do if dQ were
-// added up in memory by all key blocks, in an order that changes results.
+// delta made from `out` carries that tensor's rounding to 16 bits, which would
+// add as much error to dQ and dK as all other roundings together. Its exact
+// value is sum_j P_ij dP_ij, known at the end of a row: the dQ kernel gathers
+// off = sum_j P_ij (dP_ij - delta) in fp32 on the way, takes off * R from dQ
+// (the same as if delta + off had been used all along) and leaves delta + off
+// for the other kernel. (Error against fp64 on capped pages of 1024 tokens:
+// 0.0032 without, 0.0024 with.)
+//
+// Eight products of 128 x 128 x d for a tile where five would do if dQ were
+// added up in memory by all key blocks, in an order that changes results, and
+// delta were taken as it is.
 //
 // A tile passes through two phases of the arithmetic warps, P and dS. While
-// they are at dS of tile i the tensor cores make dV of tile i and S of tile
-// i + 1, while they are at P of tile i + 1 dK of tile i and dP of tile i + 1:
-// single buffers of S and dP are enough, because the tensor cores run in
-// order. P lies over S and dS over dP, each warpgroup's half in its own
+// they are at dS of tile i the tensor cores make the product with P of tile i and S of tile
+// i + 1, while they are at P of tile i + 1 that with dS of tile i and dP of
+// tile i + 1: single buffers of S and dP are enough, because the tensor cores
+// run in order. P lies over S and dS over dP, each warpgroup's half in its own
 // columns. P and dS are rounded to the inputs' type for their products, as the
-// tensor cores take nothing wider at this rate; sums are fp32. `scale` is applied to
-// the sums.
+// tensor cores take nothing wider at this rate; sums are fp32. `scale` is
+// applied to the sums.
 #include "attn_common.cuh"
 
 namespace msim {
@@ -44,15 +54,18 @@ struct BwdShape {
   static constexpr int kThreads = kGroups * 128 + 128;
   static constexpr int kBlocks = BC == 64 ? 2 : 1;
   static constexpr int kRegsLaunch = BC == 64 ? 128 : 168;
-  static constexpr int kRegsMath = BC == 64 ? 200 : 224, kRegsOther = 56;
-  static_assert(kGroups * kRegsMath + kRegsOther <= (kGroups + 1) * kRegsLaunch, "register split");
+  // Registers of the arithmetic threads once they took over some of the
+  // others'; dQ of capped scores also keeps the cap's derivatives.
+  static constexpr int math_regs(bool cap) { return cap && !kDkv ? (BC == 64 ? 200 : 224) : (BC == 64 ? 168 : 208); }
+  static constexpr int other_regs(bool cap) { return (kGroups + 1) * kRegsLaunch - kGroups * math_regs(cap); }
+  static_assert(other_regs(true) >= 56 && other_regs(true) % 8 == 0 && other_regs(false) % 8 == 0, "register split");
   // TMEM columns: S, dP, then the sums
   static constexpr uint32_t kDp = BC, kSum0 = 2 * BC, kSum1 = 2 * BC + DH;
-  static constexpr uint32_t kNeed = kDkv ? 2 * BC + 2 * DH : 2 * BC + DH;
+  static constexpr uint32_t kNeed = 2 * BC + 2 * DH;
   static constexpr uint32_t kTmemCols = kNeed <= 256 ? 256 : 512;
-  static constexpr int kBars = 2 + 2 * kStages + 5 + 2 * kRing + 1;
+  static constexpr int kBars = 2 + 2 * kStages + 5 + 2 * kRing + 2;
   static constexpr uint32_t kSmem = 1024 + 2 * kOwnBytes + 2 * kStages * kBytes + 8 * kBars +
-                                    (kDkv ? kStages * BC * 8 : 0) + kRing * sizeof(Work) + 16 + 16;
+                                    kStages * BC * 8 + kRing * sizeof(Work) + 16 + 16;
 };
 
 // own_a, own_b: the 128 rows that the block keeps (K and V, or Q and dO);
@@ -61,19 +74,19 @@ template <class S, int BC>
 struct BwdSmem {
   uint32_t own_a, own_b, walk_a, walk_b, bars;
   uint64_t* bar;
-  float2* stats;  // kStages x BC: (lse2, delta) of the walked rows
+  float* stats;   // kStages x (BC times -lse2, BC times -delta) of the walked rows
   Work* info;
   uint32_t* tmem_slot;
   int* abort_flag;
-  __device__ __forceinline__ explicit BwdSmem(uint8_t* raw, bool dkv) {
+  __device__ __forceinline__ explicit BwdSmem(uint8_t* raw) {
     uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     own_a = smem_u32(base);
     own_b = own_a + S::kOwnBytes;
     walk_a = own_b + S::kOwnBytes;
     walk_b = walk_a + kStages * S::kBytes;
     uint8_t* end = base + 2 * S::kOwnBytes + 2 * kStages * S::kBytes;
-    stats = reinterpret_cast<float2*>(end);
-    bar = reinterpret_cast<uint64_t*>(end + (dkv ? kStages * BC * 8 : 0));
+    stats = reinterpret_cast<float*>(end);
+    bar = reinterpret_cast<uint64_t*>(end + kStages * BC * 8);
     bars = smem_u32(bar);
     info = reinterpret_cast<Work*>(bar + S::kBars);
     tmem_slot = reinterpret_cast<uint32_t*>(info + kRing);
@@ -91,6 +104,7 @@ struct BwdSmem {
   __device__ __forceinline__ uint32_t info_full(int r) const { return s_full() + 40 + 8 * r; }
   __device__ __forceinline__ uint32_t info_empty(int r) const { return info_full(kRing + r); }
   __device__ __forceinline__ uint32_t done() const { return info_full(2 * kRing); }
+  __device__ __forceinline__ uint32_t rest_full() const { return done() + 8; }
   __device__ __forceinline__ uint64_t* at(uint32_t b) const { return bar + (b - bars) / 8; }
 };
 
@@ -199,12 +213,15 @@ __device__ void bwd_stats(const AttnParams& p, const BwdSmem<S, BC>& sm) {
 #pragma unroll
         for (int x = 0; x < BC / 32; ++x) {
           const int i = from + x * 32 + lane;
-          v[x] = i < g.end ? row[i] : make_float2(INFINITY, 0.f);
+          v[x] = i < g.end ? row[i] : make_float2(-INFINITY, 0.f);
         }
         if (!__all_sync(0xffffffffu, mbar_wait_inl_a(sm.walk_empty(s), ((step / kStages) & 1) ^ 1, sm.abort_flag, p.status)))
           return;
 #pragma unroll
-        for (int x = 0; x < BC / 32; ++x) sm.stats[s * BC + x * 32 + lane] = v[x];
+        for (int x = 0; x < BC / 32; ++x) {
+          sm.stats[s * 2 * BC + x * 32 + lane] = v[x].x;
+          sm.stats[(s * 2 + 1) * BC + x * 32 + lane] = v[x].y;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive_a(sm.walk_full(s));
       }
@@ -281,7 +298,7 @@ __device__ void bwd_products(const AttnParams& p, const BwdSmem<S, BC>& sm, uint
       const uint32_t u = step + i, s = u % kStages, s1 = (u + 1) % kStages;
       if (!(ok = wait(sm.p_full(), u))) break;
       tc_fence_after();
-      if constexpr (kDkv) add(S::kSum0, 0, sm.walk_b + s * S::kBytes, cols, i == 0);
+      add(S::kSum0, 0, (kDkv ? sm.walk_b : sm.walk_a) + s * S::kBytes, cols, i == 0);
       if (i + 1 < total) {
         if (!(ok = ready(i + 1, next))) break;
         tc_fence_after();
@@ -290,7 +307,7 @@ __device__ void bwd_products(const AttnParams& p, const BwdSmem<S, BC>& sm, uint
       }
       if (!(ok = wait(sm.ds_full(), u))) break;
       tc_fence_after();
-      add(kDkv ? S::kSum1 : S::kSum0, S::kDp, sm.walk_a + s * S::kBytes, cols, i == 0);
+      add(S::kSum1, S::kDp, sm.walk_a + s * S::kBytes, cols, i == 0);
       umma_commit_el(sm.walk_empty(s));
       if (i + 1 < total) {
         score(S::kDp, sm.own_b, sm.walk_b + s1 * S::kBytes, next);
@@ -310,27 +327,151 @@ __device__ void bwd_products(const AttnParams& p, const BwdSmem<S, BC>& sm, uint
 }
 
 // ----------------------------------------------------------- arithmetic
-// 32 columns of fp32 sums, times f, as 16-bit values of a row.
+// 32 columns of fp32 sums, times f (plus others, times f2), as 16-bit values of a row.
 template <bool kBf16>
-__device__ __forceinline__ void store_sums(uint32_t col, uint4* dst, int first, int d, float f, bool live, bool any) {
-  uint32_t o[32];
-  if (any) {
-    tmem_ld_32x32b_x32_issue(col, o);
-    tmem_wait_ld_regs(o);
-  }
+__device__ __forceinline__ void store_sums(uint32_t col, uint32_t col2, uint4* dst, int first, int d, float f, float f2,
+                                           bool live, bool any) {
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    uint4 y = make_uint4(0, 0, 0, 0);
+  for (int half = 0; half < 2; ++half) {
+    uint32_t o[16], o2[16];
     if (any) {
-      const float* v = reinterpret_cast<const float*>(o) + x * 8;
-      y = make_uint4(pack2<kBf16>(v[0] * f, v[1] * f), pack2<kBf16>(v[2] * f, v[3] * f),
-                     pack2<kBf16>(v[4] * f, v[5] * f), pack2<kBf16>(v[6] * f, v[7] * f));
+      tmem_ld_32x32b_x16(col + half * 16, o);
+      if (col2) tmem_ld_32x32b_x16(col2 + half * 16, o2);
     }
-    if (live && first + x * 8 < d) dst[first / 8 + x] = y;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      uint4 y = make_uint4(0, 0, 0, 0);
+      if (any) {
+        float v[8];
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          v[z] = __uint_as_float(o[x * 8 + z]) * f;
+          if (col2) v[z] = fmaf(__uint_as_float(o2[x * 8 + z]), f2, v[z]);
+        }
+        y = make_uint4(pack2<kBf16>(v[0], v[1]), pack2<kBf16>(v[2], v[3]), pack2<kBf16>(v[4], v[5]),
+                       pack2<kBf16>(v[6], v[7]));
+      }
+      if (live && first + half * 16 + x * 8 < d) dst[first / 8 + half * 2 + x] = y;
+    }
   }
 }
 __device__ __forceinline__ uint4* row_of(const HeadsView& v, int64_t token, int head) {
   return reinterpret_cast<uint4*>(static_cast<uint16_t*>(v.data) + token * v.token_stride + head * v.head_stride);
+}
+
+struct MathConst {
+  float c, to_log2, cap2, in_cap;  // c brings held scores to log2 units
+};
+
+// This thread's 64 columns of a tile of scores: weights into e (times bend in
+// the dK and dV kernel) and, in 16 bits, to TMEM. nl: minus the rows' lse2, of
+// the walked rows in shared memory or of this thread's own row. kEdge: columns
+// outside [lo, hi) have weight 0, those from `used` on are not looked at.
+template <bool kDkv, bool kBf16, bool kCap, bool kBias, bool kEdge>
+__device__ __forceinline__ void make_weights(uint32_t s_col, const MathConst& k, const float* nl, float own_nl,
+                                             float slope2, float far, int used, int lo, int hi, float (&e)[64],
+                                             float (&bend)[kCap && !kDkv ? 64 : 1]) {
+  uint32_t u[2][32];
+  tmem_ld_32x32b_x32_issue(s_col, u[0]);
+  if (!kEdge || used > 32) tmem_ld_32x32b_x32_issue(s_col + 32, u[1]);
+  tmem_wait_ld_regs(u[0]);
+  reg_order(u[1]);
+  const Pair scale(k.c, k.c);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    if (kEdge && q * 32 >= used) break;
+    uint32_t pk[16];
+#pragma unroll
+    for (int x = 0; x < 32; x += 4) {
+      float4 n;
+      if constexpr (kDkv) n = *reinterpret_cast<const float4*>(nl + q * 32 + x);
+      else n = make_float4(own_nl, own_nl, own_nl, own_nl);
+      float z[4], d[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        z[y] = __uint_as_float(u[q][x + y]);
+        if constexpr (kCap) {
+          const float t = fast_tanh(z[y] * k.in_cap);
+          z[y] = k.cap2 * t;
+          d[y] = fmaf(-t, t, 1.f);
+        }
+        if constexpr (kBias) {
+          if constexpr (!kCap) z[y] *= k.to_log2;
+          z[y] = fmaf(-slope2, fabsf(far - static_cast<float>(q * 32 + x + y)), z[y]);
+        }
+      }
+      fma2(Pair(z[0], z[1]), scale, Pair(n.x, n.y)).get(z[0], z[1]);
+      fma2(Pair(z[2], z[3]), scale, Pair(n.z, n.w)).get(z[2], z[3]);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        z[y] = fast_exp2(z[y]);
+        if constexpr (kEdge) z[y] = static_cast<unsigned>(q * 32 + x + y - lo) < static_cast<unsigned>(hi - lo) ? z[y] : 0.f;
+      }
+      float w[4] = {z[0], z[1], z[2], z[3]};  // what goes to TMEM: the weights for dV, weights * bend for their product with K
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        if constexpr (kCap) {
+          if (kEdge && z[y] == 0.f) d[y] = 0.f;
+          if constexpr (kDkv) z[y] *= d[y];
+          else {
+            bend[q * 32 + x + y] = d[y];
+            w[y] *= d[y];
+          }
+        }
+        e[q * 32 + x + y] = z[y];
+      }
+      pk[x / 2] = pack2<kBf16>(w[0], w[1]);
+      pk[x / 2 + 1] = pack2<kBf16>(w[2], w[3]);
+    }
+    tmem_st_32x32b_x16_issue(s_col + q * 16, pk);
+  }
+  tmem_wait_st();
+}
+
+// dS of the same columns to TMEM. nd: minus delta, as nl. `rest` gathers the
+// sum over the row of e (dP - delta), which exact arithmetic makes 0.
+template <bool kDkv, bool kBf16, bool kCap, bool kEdge>
+__device__ __forceinline__ void make_ds(uint32_t dp_col, const float* nd, float own_nd, int used, const float (&e)[64],
+                                        const float (&bend)[kCap && !kDkv ? 64 : 1], Pair& rest) {
+  uint32_t u[2][32];
+  tmem_ld_32x32b_x32_issue(dp_col, u[0]);
+  tmem_wait_ld_regs(u[0]);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    if (kEdge && q * 32 >= used) break;
+    if (q == 0 && (!kEdge || used > 32)) tmem_ld_32x32b_x32_issue(dp_col + 32, u[1]);
+    uint32_t pk[16];
+#pragma unroll
+    for (int x = 0; x < 32; x += 4) {
+      float4 n;
+      if constexpr (kDkv) n = *reinterpret_cast<const float4*>(nd + q * 32 + x);
+      else n = make_float4(own_nd, own_nd, own_nd, own_nd);
+      const float* w = e + q * 32 + x;
+      float d[4];
+      Pair a = add2(Pair(__uint_as_float(u[q][x]), __uint_as_float(u[q][x + 1])), Pair(n.x, n.y));
+      Pair b = add2(Pair(__uint_as_float(u[q][x + 2]), __uint_as_float(u[q][x + 3])), Pair(n.z, n.w));
+      a = mul2(a, Pair(w[0], w[1]));
+      b = mul2(b, Pair(w[2], w[3]));
+      a.get(d[0], d[1]);
+      b.get(d[2], d[3]);
+      if constexpr (kEdge) {  // where nothing is seen the difference may be anything
+#pragma unroll
+        for (int y = 0; y < 4; ++y) d[y] = w[y] == 0.f ? 0.f : d[y];
+      }
+      if constexpr (!kDkv) {
+        rest = add2(rest, add2(Pair(d[0], d[1]), Pair(d[2], d[3])));
+        if constexpr (kCap) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) d[y] *= bend[q * 32 + x + y];
+        }
+      }
+      pk[x / 2] = pack2<kBf16>(d[0], d[1]);
+      pk[x / 2 + 1] = pack2<kBf16>(d[2], d[3]);
+    }
+    tmem_st_32x32b_x16_issue(dp_col + q * 16, pk);
+    if (q == 0) tmem_wait_ld_regs(u[1]);
+  }
+  tmem_wait_st();
 }
 
 template <class S, int DH, int BC, bool kDkv, bool kBf16, bool kCap, bool kBias>
@@ -338,9 +479,9 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
   const int wg = threadIdx.x >> 7, lane = threadIdx.x & 31, group = p.heads / p.kv_heads;
   const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;
   const uint32_t s_col = tmem + lanes + wg * 64, dp_col = s_col + S::kDp;
-  const float c = kCap || kBias ? 1.f : p.scale * kLog2e;
-  const float to_log2 = p.scale * kLog2e, cap2 = p.cap * kLog2e, in_cap = kCap ? 2.f * kLog2e * p.scale / p.cap : 0.f;
-  uint32_t step = 0, item = 0;
+  const MathConst k = {kCap || kBias ? 1.f : p.scale * kLog2e, p.scale * kLog2e, p.cap * kLog2e,
+                       kCap ? 2.f * kLog2e * p.scale / p.cap : 0.f};
+  uint32_t step = 0, item = 0, rows_done = 0;
   const auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
     return __all_sync(0xffffffffu, mbar_wait_inl_a(bar, ph & 1, sm.abort_flag, p.status));
   };
@@ -355,8 +496,9 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
     const int mine = w.row0 + static_cast<int>(threadIdx.x & 127);  // this thread's key, or row
     // columns [lo, hi) of the document that meet this thread's row, and the
     // columns from `clear` up to `clear_end` that meet every row of the block
-    int lo, hi, clear, clear_end;
-    float lse2 = 0.f, delta = 0.f;
+    int lo = 0, hi = 0, clear, clear_end;
+    float own_nl = -INFINITY, own_nd = 0.f;
+    float2* own_stats = nullptr;
     if constexpr (kDkv) {
       lo = mine < w.keys ? (p.mask == MAXSIM_MASK_FULL || mine < w.prefix ? 0 : mine) : w.len;
       hi = w.len;
@@ -364,86 +506,39 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
       clear = last < w.keys ? (p.mask == MAXSIM_MASK_FULL || last < w.prefix ? 0 : last) : w.len;
       clear_end = w.len;
     } else {
-      lo = 0;
-      hi = row_end(w, p.mask, min(mine, w.len - 1));
       clear = 0;
       clear_end = w.row0 + kTile <= w.len ? row_end(w, p.mask, w.row0) : 0;
       if (mine < w.len) {
-        const float2 st = reinterpret_cast<const float2*>(p.delta)[static_cast<int64_t>(w.head) * p.T + w.start + mine];
-        lse2 = st.x;
-        delta = st.y;
-      } else {
-        hi = 0;
+        hi = row_end(w, p.mask, mine);
+        own_stats = reinterpret_cast<float2*>(p.delta) + static_cast<int64_t>(w.head) * p.T + w.start + mine;
+        const float2 st = *own_stats;
+        own_nl = st.x;
+        own_nd = st.y;
       }
     }
+    Pair rest(0.f, 0.f);
     for (int h = 0; h < g.heads; ++h) {
       const float slope2 = kBias ? p.slopes[kDkv ? w.head * group + h : w.head] * kLog2e : 0.f;
       for (int j = 0; j < g.steps; ++j, ++step) {
         const int from = g.begin + j * BC + wg * 64, used = min(64, g.end - from);  // this warpgroup's columns
-        const bool masked = from < clear || g.begin + (j + 1) * BC > clear_end;
-        const float2* st = sm.stats + (step % kStages) * BC + wg * 64;
-        float v[64];  // weights, then weights * bend
+        const bool edge = from < clear || g.begin + (j + 1) * BC > clear_end;
+        const float* nl = sm.stats + (step % kStages) * 2 * BC + wg * 64;
+        const float far = static_cast<float>(mine - from);
+        float e[64], bend[kCap && !kDkv ? 64 : 1];
         if (!wait(sm.s_full(), step)) return;
         // the statistics came with the walked tile, whose products have been made from it
         if (kDkv && !wait(sm.walk_full(step % kStages), step / kStages)) return;
         tc_fence_after();
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (q * 32 < used) {
-            uint32_t u[32];
-            tmem_ld_32x32b_x32_issue(s_col + q * 32, u);
-            tmem_wait_ld_regs(u);
-            uint32_t pk[16];
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const int col = from + q * 32 + x;
-              float z = __uint_as_float(u[x]), bend = 1.f;
-              if constexpr (kCap) {
-                const float t = fast_tanh(z * in_cap);
-                z = cap2 * t;
-                bend = fmaf(-t, t, 1.f);
-              }
-              if constexpr (kBias) {
-                if constexpr (!kCap) z *= to_log2;
-                z = fmaf(-slope2, fabsf(static_cast<float>(mine - col)), z);
-              }
-              float e = fast_exp2(fmaf(z, c, -(kDkv ? st[q * 32 + x].x : lse2)));
-              if (masked) e = col >= lo && col < hi ? e : 0.f;
-              v[q * 32 + x] = kCap ? (masked && e == 0.f ? 0.f : e * bend) : e;
-              if constexpr (kDkv) {
-                if (x & 1) pk[x / 2] = pack2<kBf16>(__uint_as_float(u[x - 1]), e);
-                else u[x] = __float_as_uint(e);
-              }
-            }
-            if constexpr (kDkv) tmem_st_32x32b_x16_issue(s_col + q * 16, pk);
-          }
-        }
-        if constexpr (kDkv) tmem_wait_st();
+        if (!edge) make_weights<kDkv, kBf16, kCap, kBias, false>(s_col, k, nl, own_nl, slope2, far, 64, 0, 64, e, bend);
+        else if (used > 0)
+          make_weights<kDkv, kBf16, kCap, kBias, true>(s_col, k, nl, own_nl, slope2, far, used, lo - from, hi - from, e, bend);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_a(sm.p_full());
         if (!wait(sm.dp_full(), step)) return;
         tc_fence_after();
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (q * 32 < used) {
-            uint32_t u[32], pk[16];
-            tmem_ld_32x32b_x32_issue(dp_col + q * 32, u);
-            tmem_wait_ld_regs(u);
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-              float a = __uint_as_float(u[x]) - (kDkv ? st[q * 32 + x].y : delta);
-              float b = __uint_as_float(u[x + 1]) - (kDkv ? st[q * 32 + x + 1].y : delta);
-              const float wa = v[q * 32 + x], wb = v[q * 32 + x + 1];
-              // where nothing is seen the difference may be anything
-              a = masked && wa == 0.f ? 0.f : wa * a;
-              b = masked && wb == 0.f ? 0.f : wb * b;
-              pk[x / 2] = pack2<kBf16>(a, b);
-            }
-            tmem_st_32x32b_x16_issue(dp_col + q * 16, pk);
-          }
-        }
-        tmem_wait_st();
+        if (!edge) make_ds<kDkv, kBf16, kCap, false>(dp_col, nl + BC, own_nd, 64, e, bend, rest);
+        else if (used > 0) make_ds<kDkv, kBf16, kCap, true>(dp_col, nl + BC, own_nd, used, e, bend, rest);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -453,6 +548,22 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
       }
     }
     const bool any = g.steps > 0, live = mine < w.len;
+    float off = 0.f;
+    if constexpr (!kDkv) {
+      float a, b;
+      rest.get(a, b);
+      off = a + b;
+      if constexpr (S::kGroups == 2) {  // the other warpgroup has the other columns' part
+        float* both = sm.stats + (rows_done & 1) * 256;  // read before anyone arrives for the row after next
+        both[threadIdx.x] = off;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_a(sm.rest_full());
+        if (!wait(sm.rest_full(), rows_done)) return;
+        ++rows_done;
+        off = both[threadIdx.x & 127] + both[128 + (threadIdx.x & 127)];
+      }
+      if (live && any && wg == 0) own_stats->y = own_nd - off;
+    }
     if (any) {
       if (!wait(sm.sum_full(), item)) return;
       ++item;
@@ -465,16 +576,17 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
 #pragma unroll
       for (int q = 0; q < kChunks; ++q) {  // two warpgroups: one writes dV, one dK
         if (S::kGroups == 1 || wg == 0)
-          store_sums<kBf16>(tmem + lanes + S::kSum0 + q * 32, dv, q * 32, p.d, 1.f, live, any);
+          store_sums<kBf16>(tmem + lanes + S::kSum0 + q * 32, 0, dv, q * 32, p.d, 1.f, 0.f, live, any);
         if (S::kGroups == 1 || wg == 1)
-          store_sums<kBf16>(tmem + lanes + S::kSum1 + q * 32, dk, q * 32, p.d, p.scale, live, any);
+          store_sums<kBf16>(tmem + lanes + S::kSum1 + q * 32, 0, dk, q * 32, p.d, p.scale, 0.f, live, any);
       }
     } else {
       uint4* dq = row_of(p.dq, token, w.head);
 #pragma unroll
       for (int q = 0; q < kChunks; ++q)
         if (S::kGroups == 1 || q / (kChunks / 2) == wg)
-          store_sums<kBf16>(tmem + lanes + S::kSum0 + q * 32, dq, q * 32, p.d, p.scale, live, any);
+          store_sums<kBf16>(tmem + lanes + S::kSum1 + q * 32, tmem + lanes + S::kSum0 + q * 32, dq, q * 32, p.d, p.scale,
+                            -off * p.scale, live, any);
     }
     tc_fence_before();  // the next item's first products overwrite the sums after its p_full / ds_full
   }
@@ -485,7 +597,7 @@ __global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH,
     attn_bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ AttnParams p) {
   using S = BwdShape<DH, BC, kDkv>;
   extern __shared__ uint8_t raw[];
-  const BwdSmem<S, BC> sm(raw, kDkv);
+  const BwdSmem<S, BC> sm(raw);
   constexpr int kMathWarps = 4 * S::kGroups;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
@@ -505,6 +617,7 @@ __global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH,
       mbar_init(sm.at(sm.info_empty(r)), kMathWarps + (kDkv ? 2 : 1));
     }
     mbar_init(sm.at(sm.done()), 1);
+    mbar_init(sm.at(sm.rest_full()), kMathWarps);
     *sm.abort_flag = 0;
     fence_mbar_init();
   }
@@ -517,12 +630,12 @@ __global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH,
   tc_fence_after();
   const uint32_t tmem = *sm.tmem_slot;
   if (warp >= kMathWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsOther));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::other_regs(kCap)));
     if (warp == kMathWarps) bwd_loader<S, BC, kDkv>(p, sm, m);
     else if (warp == kMathWarps + 1) bwd_products<S, DH, BC, kDkv, kBf16>(p, sm, tmem);
     else if (kDkv && warp == kMathWarps + 2) bwd_stats<S, BC>(p, sm);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsMath));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::math_regs(kCap)));
     bwd_math<S, DH, BC, kDkv, kBf16, kCap, kBias>(p, sm, tmem);
   }
   tc_fence_before();
@@ -534,9 +647,8 @@ __global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH,
   }
 }
 
-// (lse in log2 units, <dO, out>) of every row and head, [heads][T]. A row is
-// read by L lanes of 16 bytes each. A row that sees nothing gets lse2 =
-// +infinity, so that its weights are 0.
+// Minus lse in log2 units, and minus <dO, out>, of every row and head,
+// [heads][T]. A row is read by L lanes of 16 bytes each.
 template <bool kBf16>
 __global__ void __launch_bounds__(256) attn_stats_kernel(const AttnParams p, int L) {
   const int64_t id = blockIdx.x * int64_t(256) + threadIdx.x;
@@ -567,7 +679,7 @@ __global__ void __launch_bounds__(256) attn_stats_kernel(const AttnParams p, int
   if (live && part == 0) {
     const float lse = p.lse[static_cast<int64_t>(h) * p.T + t];
     reinterpret_cast<float2*>(p.delta)[static_cast<int64_t>(h) * p.T + t] =
-        make_float2(lse == -INFINITY ? INFINITY : lse * kLog2e, s);
+        make_float2(lse == -INFINITY ? -INFINITY : -lse * kLog2e, -s);
   }
 }
 
@@ -595,11 +707,11 @@ cudaError_t bwd_variant(const BwdMaps& m, const AttnParams& p, int sm_count, cud
 template <int DH, int BC>
 cudaError_t bwd_both(const BwdMaps& dkv, const BwdMaps& dq, const AttnParams& p, int is_bf16, int sm_count,
                      cudaStream_t stream) {
-  cudaError_t e = is_bf16 ? bwd_variant<DH, BC, true, true>(dkv, p, sm_count, stream)
-                          : bwd_variant<DH, BC, true, false>(dkv, p, sm_count, stream);
-  if (e != cudaSuccess) return e;
-  return is_bf16 ? bwd_variant<DH, BC, false, true>(dq, p, sm_count, stream)
-                 : bwd_variant<DH, BC, false, false>(dq, p, sm_count, stream);
+  const cudaError_t e = is_bf16 ? bwd_variant<DH, BC, false, true>(dq, p, sm_count, stream)
+                                : bwd_variant<DH, BC, false, false>(dq, p, sm_count, stream);
+  if (e != cudaSuccess) return e;  // the other kernel takes the first one's deltas
+  return is_bf16 ? bwd_variant<DH, BC, true, true>(dkv, p, sm_count, stream)
+                 : bwd_variant<DH, BC, true, false>(dkv, p, sm_count, stream);
 }
 
 }  // namespace

@@ -26,7 +26,7 @@ using HeadsView = maxsim_heads;
 struct AttnParams {
   HeadsView q, k, v, out, dO, dq, dk, dv;
   float* lse;    // [heads, T] natural log of the softmax denominators, or null
-  float* delta;  // [heads, T] pairs (lse in log2 units, <dO, out>), backward only
+  float* delta;  // [heads, T] pairs (-lse in log2 units, -<dO, out>), backward only
   const int64_t* offsets;
   const int32_t* key_len;
   const int32_t* prefix_len;
