@@ -40,7 +40,6 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kBoxRows = 64;
-constexpr int kRing = 2;
 constexpr int kStages = 2;
 
 // DH: head size in shared memory; BC: columns of a score tile (rows of Q or
@@ -136,8 +135,7 @@ struct BwdMaps {
 // ---------------------------------------------------------------- loads
 template <class S, int BC, bool kDkv>
 __device__ void bwd_loader(const AttnParams& p, const BwdSmem<S, BC>& sm, const BwdMaps& m) {
-  const int lane = threadIdx.x & 31, group = p.heads / p.kv_heads;
-  Walk walk;
+  const int group = p.heads / p.kv_heads;
   uint32_t item = 0, step = 0;
   bool ok = true;
   const auto load = [&](uint32_t dst, uint32_t panel, const CUtensorMap* map, uint32_t bar, int head, int token, int boxes) {
@@ -146,43 +144,33 @@ __device__ void bwd_loader(const AttnParams& p, const BwdSmem<S, BC>& sm, const 
         tma_load_3d_a(dst + pn * panel + b * (kBoxRows * 128), map, bar, pn * 64, head, token + b * kBoxRows);
   };
   for (uint32_t n = 0; ok; ++n) {
-    const Work w = walk.next(p, kTile, kDkv ? p.kv_heads : p.heads, !kDkv && p.mask != MAXSIM_MASK_FULL);
-    if (lane == 0) {
-      const int r = n % kRing;
-      ok = mbar_wait_inl_a(sm.info_empty(r), ((n / kRing) & 1) ^ 1, sm.abort_flag, p.status);
-      if (ok) {
-        sm.info[r] = w;
-        mbar_arrive_a(sm.info_full(r));
-        const Range g = w.live ? range_of<kDkv, BC>(p, w) : Range{0, 0, 0, 0};
-        if (g.steps > 0) {
-          ok = mbar_wait_inl_a(sm.own_empty(), (item & 1) ^ 1, sm.abort_flag, p.status);
-          if (ok) {
-            const int boxes = (min(kTile, w.len - w.row0) + kBoxRows - 1) / kBoxRows;
-            mbar_arrive_expect_tx_a(sm.own_full(), 2 * boxes * S::kPanels * (kBoxRows * 128));
-            load(sm.own_a, S::kOwnPanel, &m.own_a, sm.own_full(), w.head, w.start + w.row0, boxes);
-            load(sm.own_b, S::kOwnPanel, &m.own_b, sm.own_full(), w.head, w.start + w.row0, boxes);
-            ++item;
-          }
-          for (int h = 0; ok && h < g.heads; ++h) {
-            const int head = kDkv ? w.head * group + h : w.head / group;
-            for (int j = 0; j < g.steps; ++j) {
-              const int s = step % kStages, from = g.begin + j * BC;
-              ok = mbar_wait_inl_a(sm.walk_empty(s), ((step / kStages) & 1) ^ 1, sm.abort_flag, p.status);
-              if (!ok) break;
-              const int boxes = (min(BC, g.end - from) + kBoxRows - 1) / kBoxRows;
-              mbar_arrive_expect_tx_a(sm.walk_full(s), 2 * boxes * S::kPanels * (kBoxRows * 128));
-              load(sm.walk_a + s * S::kBytes, S::kPanel, &m.walk_a, sm.walk_full(s), head, w.start + from, boxes);
-              load(sm.walk_b + s * S::kBytes, S::kPanel, &m.walk_b, sm.walk_full(s), head, w.start + from, boxes);
-              ++step;
-            }
-          }
-        }
+    const int r = n % kRing;
+    if (!(ok = mbar_wait_inl_a(sm.info_full(r), (n / kRing) & 1, sm.abort_flag, p.status))) break;
+    const Work w = sm.info[r];
+    mbar_arrive_a(sm.info_empty(r));
+    if (!w.live) break;
+    const Range g = range_of<kDkv, BC>(p, w);
+    if (g.steps <= 0) continue;
+    if (!(ok = mbar_wait_inl_a(sm.own_empty(), (item & 1) ^ 1, sm.abort_flag, p.status))) break;
+    const int own_boxes = (min(kTile, w.len - w.row0) + kBoxRows - 1) / kBoxRows;
+    mbar_arrive_expect_tx_a(sm.own_full(), 2 * own_boxes * S::kPanels * (kBoxRows * 128));
+    load(sm.own_a, S::kOwnPanel, &m.own_a, sm.own_full(), w.head, w.start + w.row0, own_boxes);
+    load(sm.own_b, S::kOwnPanel, &m.own_b, sm.own_full(), w.head, w.start + w.row0, own_boxes);
+    ++item;
+    for (int h = 0; ok && h < g.heads; ++h) {
+      const int head = kDkv ? w.head * group + h : w.head / group;
+      for (int j = 0; j < g.steps; ++j) {
+        const int s = step % kStages, from = g.begin + j * BC;
+        if (!(ok = mbar_wait_inl_a(sm.walk_empty(s), ((step / kStages) & 1) ^ 1, sm.abort_flag, p.status))) break;
+        const int boxes = (min(BC, g.end - from) + kBoxRows - 1) / kBoxRows;
+        mbar_arrive_expect_tx_a(sm.walk_full(s), 2 * boxes * S::kPanels * (kBoxRows * 128));
+        load(sm.walk_a + s * S::kBytes, S::kPanel, &m.walk_a, sm.walk_full(s), head, w.start + from, boxes);
+        load(sm.walk_b + s * S::kBytes, S::kPanel, &m.walk_b, sm.walk_full(s), head, w.start + from, boxes);
+        ++step;
       }
     }
-    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-    if (!w.live) break;
   }
-  if (!ok && lane == 0) {  // after an abort: wait (bounded) for the copies in flight
+  if (!ok) {  // after an abort: wait (bounded) for the copies in flight
     if (item > 0) mbar_wait_drain(sm.at(sm.own_full()), (item - 1) & 1, p.status);
     for (uint32_t f = step > kStages ? step - kStages : 0; f < step; ++f)
       mbar_wait_drain(sm.at(sm.walk_full(f % kStages)), (f / kStages) & 1, p.status);
@@ -614,7 +602,7 @@ __global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH,
     mbar_init(sm.at(sm.sum_full()), 1);
     for (int r = 0; r < kRing; ++r) {
       mbar_init(sm.at(sm.info_full(r)), 1);
-      mbar_init(sm.at(sm.info_empty(r)), kMathWarps + (kDkv ? 2 : 1));
+      mbar_init(sm.at(sm.info_empty(r)), kMathWarps + (kDkv ? 3 : 2));
     }
     mbar_init(sm.at(sm.done()), 1);
     mbar_init(sm.at(sm.rest_full()), kMathWarps);
@@ -631,7 +619,9 @@ __global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH,
   const uint32_t tmem = *sm.tmem_slot;
   if (warp >= kMathWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::other_regs(kCap)));
-    if (warp == kMathWarps) bwd_loader<S, BC, kDkv>(p, sm, m);
+    if (warp == kMathWarps) {
+      if ((threadIdx.x & 31) == 0) bwd_loader<S, BC, kDkv>(p, sm, m);
+    } else if (warp == kMathWarps + 3) plan_work(p, sm, kTile, kDkv ? p.kv_heads : p.heads, !kDkv && p.mask != MAXSIM_MASK_FULL);
     else if (warp == kMathWarps + 1) bwd_products<S, DH, BC, kDkv, kBf16>(p, sm, tmem);
     else if (kDkv && warp == kMathWarps + 2) bwd_stats<S, BC>(p, sm);
   } else {
@@ -737,7 +727,7 @@ maxsim_status launch_attn_bwd(const AttnParams& p, int is_bf16, cudaStream_t str
   else attn_stats_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p, L);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = p.d <= 64 ? bwd_both<64, 64>(dkv, dq, p, is_bf16, dev->sm_count, stream)
+    e = p.d <= 64 ? bwd_both<64, 128>(dkv, dq, p, is_bf16, dev->sm_count, stream)
                   : bwd_both<128, 128>(dkv, dq, p, is_bf16, dev->sm_count, stream);
   return e == cudaSuccess ? MAXSIM_OK : MAXSIM_ERR_CUDA;
 }

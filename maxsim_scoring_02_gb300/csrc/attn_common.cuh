@@ -97,16 +97,23 @@ __device__ __forceinline__ int64_t slot_base(const AttnParams& p, int64_t b, int
   return (s < 0 ? 0 : s > p.T ? p.T : s) / rows + b;
 }
 
-// The last document in [lo, hi) whose slots begin at or before `slot`; a whole
-// warp looks at 32 places at a time.
-__device__ __forceinline__ int64_t slot_doc(const AttnParams& p, int64_t slot, int rows, int64_t lo, int64_t hi) {
+// The last document whose slots begin at or before `slot`, for each lane's own
+// slot: 32 places are looked at together, the rest of the way alone.
+__device__ __forceinline__ int64_t slot_doc(const AttnParams& p, int64_t slot, int rows) {
   const int lane = threadIdx.x & 31;
+  int64_t lo = 0, hi = p.B;
+  const int64_t step = (hi + 31) / 32;
+  const int64_t mine = lane * step < p.B ? slot_base(p, lane * step, rows) : INT64_MAX;
+  int at = 0;
+#pragma unroll
+  for (int k = 16; k; k >>= 1)
+    if (__shfl_sync(0xffffffffu, mine, at + k) <= slot) at += k;
+  lo = at * step;
+  hi = lo + step < hi ? lo + step : hi;
   while (hi - lo > 1) {
-    const int64_t step = (hi - lo + 31) / 32, m = lo + lane * step;
-    const bool at = lane == 0 || (m < hi && slot_base(p, m, rows) <= slot);
-    const unsigned set = __ballot_sync(0xffffffffu, at);
-    lo += (31 - __clz(set)) * step;
-    hi = lo + step < hi ? lo + step : hi;
+    const int64_t m = lo + (hi - lo) / 2;
+    if (slot_base(p, m, rows) <= slot) lo = m;
+    else hi = m;
   }
   return lo;
 }
@@ -119,50 +126,54 @@ struct Work {
   int live;                      // 0: no work is left
 };
 
-// Walks over (slot, head) pairs: block c takes items c, 2G - 1 - c, 2G + c, ...
-// of G blocks, so that early (heavy) and late (light) items of one document
-// even out; with `reverse` the last rows, which see most keys, come first.
-struct Walk {
-  int64_t round = 0, slot_old = -1, doc_old = 0;
+constexpr int kRing = 4;  // pieces of work that are planned ahead
 
-  // The next slot that holds rows, for the whole warp. Slots of a document lie
-  // together, and every later document is at least one slot further, so the
-  // search starts from the last one found.
-  __device__ __forceinline__ Work next(const AttnParams& p, int rows, int heads, int reverse) {
-    const int64_t slots = p.T / rows + p.B, items = slots * heads, G = gridDim.x;
-    Work w;
-    w.live = 0;
-    for (;; ++round) {
-      const int64_t item = round * G + ((round & 1) ? G - 1 - static_cast<int64_t>(blockIdx.x) : blockIdx.x);
-      if (round * G >= items) break;
-      if (item >= items) continue;
-      const int64_t s = item / heads, slot = reverse ? slots - 1 - s : s;
-      int64_t lo = 0, hi = p.B;
-      if (slot_old >= 0) {
-        const int64_t far = slot > slot_old ? slot - slot_old : slot_old - slot;
-        lo = doc_old - far > 0 && slot < slot_old ? doc_old - far : slot < slot_old ? 0 : doc_old;
-        hi = slot < slot_old ? doc_old + 1 : doc_old + far + 1 < p.B ? doc_old + far + 1 : p.B;
-      }
-      const int64_t b = slot_doc(p, slot, rows, lo, hi);
-      slot_old = slot;
-      doc_old = b;
-      bool bad;
-      const Doc c = load_doc(p, b, bad);
-      const int64_t row0 = (slot - slot_base(p, b, rows)) * rows;
-      if (row0 < 0 || row0 >= c.len) continue;
-      w.start = c.start;
-      w.len = c.len;
-      w.keys = c.keys;
-      w.prefix = c.prefix;
-      w.row0 = static_cast<int>(row0);
-      w.head = static_cast<int>(item % heads);
-      w.live = 1;
-      ++round;
-      break;
+// One warp finds the block's pieces of work, 32 at a time, since each takes a
+// chain of dependent reads, and hands them to the other roles through a ring.
+// Block c of G takes (slot, head) pairs c, 2G - 1 - c, 2G + c, ..., so that
+// early (heavy) and late (light) ones of a document even out; with `reverse`
+// the last rows, which see most keys, come first.
+template <class Smem>
+__device__ void plan_work(const AttnParams& p, const Smem& sm, int rows, int heads, int reverse) {
+  const int lane = threadIdx.x & 31;
+  const int64_t slots = p.T / rows + p.B, items = slots * heads, G = gridDim.x;
+  uint32_t n = 0;
+  const auto put = [&](const Work& w, bool me) -> bool {
+    const int r = n % kRing;
+    if (!__all_sync(0xffffffffu, mbar_wait_inl_a(sm.info_empty(r), ((n / kRing) & 1) ^ 1, sm.abort_flag, p.status)))
+      return false;
+    if (me) {
+      sm.info[r] = w;
+      mbar_arrive_a(sm.info_full(r));  // releases the write
     }
-    return w;
+    __syncwarp();
+    ++n;
+    return true;
+  };
+  Work w;
+  for (int64_t round0 = 0; round0 * G < items; round0 += 32) {
+    const int64_t round = round0 + lane;
+    int64_t item = round * G + ((round & 1) ? G - 1 - static_cast<int64_t>(blockIdx.x) : blockIdx.x);
+    w.live = item < items;
+    if (!w.live) item = items - 1;
+    const int64_t s = item / heads, slot = reverse ? slots - 1 - s : s;
+    const int64_t b = slot_doc(p, slot, rows);
+    bool bad;
+    const Doc c = load_doc(p, b, bad);
+    const int64_t row0 = (slot - slot_base(p, b, rows)) * rows;
+    w.start = c.start;
+    w.len = c.len;
+    w.keys = c.keys;
+    w.prefix = c.prefix;
+    w.row0 = static_cast<int>(row0);
+    w.head = static_cast<int>(item - s * heads);
+    w.live = w.live && row0 >= 0 && row0 < c.len;  // else the slot is empty
+    for (unsigned set = __ballot_sync(0xffffffffu, w.live != 0); set; set &= set - 1)
+      if (!put(w, lane == __ffs(set) - 1)) return;
   }
-};
+  w.live = 0;
+  put(w, lane == 0);
+}
 
 __device__ __forceinline__ int row_end(const Work& c, int mask, int i) {
   if (mask == MAXSIM_MASK_FULL) return c.keys;

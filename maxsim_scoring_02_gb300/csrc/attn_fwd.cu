@@ -29,7 +29,6 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kBoxRows = 64;
-constexpr int kRing = 2;
 constexpr float kRaise = 8.f;  // log2 of how far a weight may exceed 1
 
 template <int DH, int NQ>
@@ -38,7 +37,8 @@ struct FwdShape {
   static constexpr uint32_t kPanelBytes = kTile * 128;
   static constexpr uint32_t kTileBytes = kPanels * kPanelBytes;
   static constexpr int kStages = NQ == 1 ? (DH == 64 ? 2 : 1) : (DH == 64 ? 4 : 2);
-  static constexpr int kThreads = NQ * 128 + 128;  // softmax warpgroups; loader, issuer and two idle warps
+  static constexpr int kQStages = NQ == 1 && DH == 64 ? 2 : 1;
+  static constexpr int kThreads = NQ * 128 + 128;  // softmax warpgroups; loader, issuer, planner and an idle warp
   static constexpr int kBlocks = NQ == 1 ? 2 : 1;  // resident on an SM
   // Registers a thread: at launch (ptxas fills the launch bounds), and after
   // the softmax threads took over some of the others'.
@@ -47,9 +47,10 @@ struct FwdShape {
   static_assert(NQ * kRegsSoftmax + kRegsOther <= (NQ + 1) * kRegsLaunch, "register split");
   static constexpr uint32_t kTmemCols = NQ == 1 ? 256 : 512;
   static constexpr uint32_t kO0 = NQ * kTile;  // TMEM columns: S of each tile, then O of each tile
-  // barriers: q_full, q_empty, k_full, k_empty, v_full, v_empty, s_full, p_full, o_full, info_full, info_empty, done
-  static constexpr int kBars = 2 + 4 * kStages + 3 * NQ + 2 * kRing + 1;
-  static constexpr uint32_t kSmem = 1024 + (NQ + 2 * kStages) * kTileBytes + 8 * kBars + kRing * sizeof(Work) + 16;
+  // barriers: k_full, k_empty, v_full, v_empty, s_full, p_full, o_full, info_full, info_empty, done, q_full, q_empty
+  static constexpr int kBars = 4 * kStages + 3 * NQ + 2 * kRing + 1 + 2 * kQStages;
+  static constexpr uint32_t kTiles = NQ * kQStages + 2 * kStages;
+  static constexpr uint32_t kSmem = 1024 + kTiles * kTileBytes + 8 * kBars + kRing * sizeof(Work) + 16;
 };
 
 template <int DH, int NQ>
@@ -63,17 +64,15 @@ struct FwdSmem {
   __device__ __forceinline__ explicit FwdSmem(uint8_t* raw) {
     uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     q = smem_u32(base);
-    k = q + NQ * S::kTileBytes;
+    k = q + NQ * S::kQStages * S::kTileBytes;
     v = k + S::kStages * S::kTileBytes;
-    bar = reinterpret_cast<uint64_t*>(base + (NQ + 2 * S::kStages) * S::kTileBytes);
+    bar = reinterpret_cast<uint64_t*>(base + S::kTiles * S::kTileBytes);
     bars = smem_u32(bar);
     info = reinterpret_cast<Work*>(bar + S::kBars);
     tmem_slot = reinterpret_cast<uint32_t*>(info + kRing);
     abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   }
-  __device__ __forceinline__ uint32_t q_full() const { return bars; }
-  __device__ __forceinline__ uint32_t q_empty() const { return bars + 8; }
-  __device__ __forceinline__ uint32_t k_full(int s) const { return bars + 16 + 8 * s; }
+  __device__ __forceinline__ uint32_t k_full(int s) const { return bars + 8 * s; }
   __device__ __forceinline__ uint32_t k_empty(int s) const { return k_full(S::kStages + s); }
   __device__ __forceinline__ uint32_t v_full(int s) const { return k_full(2 * S::kStages + s); }
   __device__ __forceinline__ uint32_t v_empty(int s) const { return k_full(3 * S::kStages + s); }
@@ -83,6 +82,8 @@ struct FwdSmem {
   __device__ __forceinline__ uint32_t info_full(int r) const { return s_full(3 * NQ + r); }
   __device__ __forceinline__ uint32_t info_empty(int r) const { return s_full(3 * NQ + kRing + r); }
   __device__ __forceinline__ uint32_t done() const { return s_full(3 * NQ + 2 * kRing); }
+  __device__ __forceinline__ uint32_t q_full(int s) const { return done() + 8 + 8 * s; }
+  __device__ __forceinline__ uint32_t q_empty(int s) const { return q_full(S::kQStages + s); }
   __device__ __forceinline__ uint64_t* at(uint32_t b) const { return bar + (b - bars) / 8; }
 };
 
@@ -98,62 +99,51 @@ template <int DH, int NQ>
 __device__ void fwd_loader(const AttnParams& p, const FwdSmem<DH, NQ>& sm, const CUtensorMap* mq, const CUtensorMap* mk,
                            const CUtensorMap* mv) {
   using S = FwdShape<DH, NQ>;
-  const int lane = threadIdx.x & 31, group = p.heads / p.kv_heads;
-  Walk walk;
-  uint32_t item = 0, loads = 0, kv = 0;  // items with keys; key tiles
+  const int group = p.heads / p.kv_heads;
+  uint32_t item = 0, kv = 0;  // items with keys; key tiles
   bool ok = true;
   const auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int head, int token, int rows) {
     const int boxes = (rows + kBoxRows - 1) / kBoxRows;
-    mbar_arrive_expect_tx_a(bar, boxes * S::kPanels * (kBoxRows * 128));
     for (int b = 0; b < boxes; ++b)
       for (int pn = 0; pn < S::kPanels; ++pn)
-        tma_load_3d_a(dst + pn * S::kPanelBytes + b * (kBoxRows * 128), map, bar, pn * 64, head, token + b * kBoxRows);
+        tma_load_3d_a(dst + (b / 2) * S::kTileBytes + pn * S::kPanelBytes + (b % 2) * (kBoxRows * 128), map, bar, pn * 64,
+                      head, token + b * kBoxRows);
   };
+  const auto bytes = [](int rows) -> uint32_t { return (rows + kBoxRows - 1) / kBoxRows * S::kPanels * (kBoxRows * 128); };
   for (uint32_t n = 0; ok; ++n) {
-    const Work w = walk.next(p, NQ * kTile, p.heads, p.mask != MAXSIM_MASK_FULL);
-    if (lane == 0) {
-      const int r = n % kRing;
-      ok = mbar_wait_inl_a(sm.info_empty(r), ((n / kRing) & 1) ^ 1, sm.abort_flag, p.status);
-      if (ok) {
-        sm.info[r] = w;
-        mbar_arrive_a(sm.info_full(r));  // releases the write
-        int keys = 0;
-        for (int t = 0; w.live && t < NQ; ++t) keys = max(keys, tile_keys(w, p.mask, t));
-        const int nk = w.live ? tiles_of(keys) : 0;
-        if (nk > 0) {
-          ok = mbar_wait_inl_a(sm.q_empty(), (item & 1) ^ 1, sm.abort_flag, p.status);
-          if (ok) {
-            // tiles past the last row are not loaded: their products are not made either
-            const int rows = min(NQ * kTile, w.len - w.row0);
-            mbar_arrive_expect_tx_a(sm.q_full(), (rows + kBoxRows - 1) / kBoxRows * S::kPanels * (kBoxRows * 128));
-            for (int b = 0; b * kBoxRows < rows; ++b)
-              for (int pn = 0; pn < S::kPanels; ++pn)
-                tma_load_3d_a(sm.q + (b / 2) * S::kTileBytes + pn * S::kPanelBytes + (b % 2) * (kBoxRows * 128), mq,
-                              sm.q_full(), pn * 64, w.head, w.start + w.row0 + b * kBoxRows);
-            ++item;
-            ++loads;
-          }
-          for (int j = 0; ok && j < nk; ++j, ++kv) {
-            const int s = kv % S::kStages, rows = min(kTile, keys - j * kTile);
-            const uint32_t ph = ((kv / S::kStages) & 1) ^ 1;
-            ok = mbar_wait_inl_a(sm.k_empty(s), ph, sm.abort_flag, p.status);
-            if (!ok) break;
-            load(sm.k + s * S::kTileBytes, mk, sm.k_full(s), w.head / group, w.start + j * kTile, rows);
-            ok = mbar_wait_inl_a(sm.v_empty(s), ph, sm.abort_flag, p.status);
-            if (!ok) {  // K of this stage is in flight without its V
-              mbar_wait_drain(sm.at(sm.k_full(s)), ph ^ 1, p.status);
-              break;
-            }
-            load(sm.v + s * S::kTileBytes, mv, sm.v_full(s), w.head / group, w.start + j * kTile, rows);
-          }
-        }
-      }
-    }
-    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    const int r = n % kRing;
+    if (!(ok = mbar_wait_inl_a(sm.info_full(r), (n / kRing) & 1, sm.abort_flag, p.status))) break;
+    const Work w = sm.info[r];
+    mbar_arrive_a(sm.info_empty(r));
     if (!w.live) break;
+    int keys = 0;
+    for (int t = 0; t < NQ; ++t) keys = max(keys, tile_keys(w, p.mask, t));
+    const int nk = tiles_of(keys);
+    if (nk == 0) continue;
+    const int sq = item % S::kQStages;
+    if (!(ok = mbar_wait_inl_a(sm.q_empty(sq), ((item / S::kQStages) & 1) ^ 1, sm.abort_flag, p.status))) break;
+    // tiles past the last row are not loaded: their products are not made either
+    const int rows = min(NQ * kTile, w.len - w.row0);
+    mbar_arrive_expect_tx_a(sm.q_full(sq), bytes(rows));
+    load(sm.q + sq * NQ * S::kTileBytes, mq, sm.q_full(sq), w.head, w.start + w.row0, rows);
+    ++item;
+    for (int j = 0; j < nk; ++j, ++kv) {
+      const int s = kv % S::kStages, left = min(kTile, keys - j * kTile);
+      const uint32_t ph = ((kv / S::kStages) & 1) ^ 1;
+      if (!(ok = mbar_wait_inl_a(sm.k_empty(s), ph, sm.abort_flag, p.status))) break;
+      mbar_arrive_expect_tx_a(sm.k_full(s), bytes(left));
+      load(sm.k + s * S::kTileBytes, mk, sm.k_full(s), w.head / group, w.start + j * kTile, left);
+      if (!(ok = mbar_wait_inl_a(sm.v_empty(s), ph, sm.abort_flag, p.status))) {
+        mbar_wait_drain(sm.at(sm.k_full(s)), ph ^ 1, p.status);  // K of this stage is in flight without its V
+        break;
+      }
+      mbar_arrive_expect_tx_a(sm.v_full(s), bytes(left));
+      load(sm.v + s * S::kTileBytes, mv, sm.v_full(s), w.head / group, w.start + j * kTile, left);
+    }
   }
-  if (!ok && lane == 0) {  // after an abort: wait (bounded) for the copies in flight
-    if (item > 0) mbar_wait_drain(sm.at(sm.q_full()), (item - 1) & 1, p.status);
+  if (!ok) {  // after an abort: wait (bounded) for the copies in flight
+    for (uint32_t f = item > S::kQStages ? item - S::kQStages : 0; f < item; ++f)
+      mbar_wait_drain(sm.at(sm.q_full(f % S::kQStages)), (f / S::kQStages) & 1, p.status);
     for (uint32_t f = kv > S::kStages ? kv - S::kStages : 0; f < kv; ++f) {
       mbar_wait_drain(sm.at(sm.k_full(f % S::kStages)), (f / S::kStages) & 1, p.status);
       mbar_wait_drain(sm.at(sm.v_full(f % S::kStages)), (f / S::kStages) & 1, p.status);
@@ -185,11 +175,12 @@ __device__ void fwd_products(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uin
     for (int t = 0; t < NQ; ++t) most = max(most, keys[t] = tile_keys(w, p.mask, t));
     const int nk = tiles_of(most);
     if (nk == 0) continue;
+    const int sq = item % S::kQStages;
     // S_t of key tile j (keys kv + j of the stages)
     const auto score = [&](int t, int j) {
       const int cols = (min(kTile, keys[t] - j * kTile) + 15) & ~15;
       const uint32_t id = idesc | static_cast<uint32_t>(cols >> 3) << 17;
-      const uint64_t a = sdesc_k_sw128(sm.q + t * S::kTileBytes);
+      const uint64_t a = sdesc_k_sw128(sm.q + (sq * NQ + t) * S::kTileBytes);
       const uint64_t b = sdesc_k_sw128(sm.k + (kv + j) % S::kStages * S::kTileBytes);
 #pragma unroll
       for (int kk = 0; kk < DH / 16; ++kk) {
@@ -203,14 +194,14 @@ __device__ void fwd_products(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uin
       seen_k = kv + j + 1;
       return wait(sm.k_full((kv + j) % S::kStages), (kv + j) / S::kStages);
     };
-    ok = wait(sm.q_full(), item) && need_k(0);
+    ok = wait(sm.q_full(sq), item / S::kQStages) && need_k(0);
     if (!ok) break;
     tc_fence_after();
 #pragma unroll
     for (int t = 0; t < NQ; ++t)
       if (keys[t] > 0) score(t, 0);
     umma_commit_el(sm.k_empty(kv % S::kStages));
-    if (nk == 1) umma_commit_el(sm.q_empty());
+    if (nk == 1) umma_commit_el(sm.q_empty(sq));
     for (int j = 0; ok && j < nk; ++j) {
       const int s = (kv + j) % S::kStages;
       bool fresh = true;
@@ -252,7 +243,7 @@ __device__ void fwd_products(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uin
       umma_commit_el(sm.v_empty(s));
       if (j + 1 < nk) {
         umma_commit_el(sm.k_empty((kv + j + 1) % S::kStages));
-        if (j + 2 == nk) umma_commit_el(sm.q_empty());
+        if (j + 2 == nk) umma_commit_el(sm.q_empty(sq));
       }
     }
     kv += nk;
@@ -310,30 +301,10 @@ __device__ __forceinline__ void group_weights(uint32_t p_col, const uint32_t (&u
   tmem_st_32x32b_x16_issue(p_col, pk);
 }
 
-// One tile of scores of this thread's row: weights to TMEM, m and sum brought
-// up to date (and O with them). The scores are read twice, 32 at a time with the
-// next group on its way, rather than kept: 128 registers of them spilled.
-// Bent scores are written back between. kEdge: the tile has fewer than 128
-// columns, or some of them are hidden from the row (those from `lim` on).
-template <int DH, bool kBf16, bool kCap, bool kBias, bool kEdge>
-__device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, const ScoreConst& k, float slope2,
-                                             float far, int cols, int lim, bool first, RowState& st) {
-  uint32_t u[2][32];
-  float now = st.m;
-  tmem_ld_32x32b_x32_issue(s_col, u[0]);
-  tmem_wait_ld_regs(u[0]);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (kEdge && q * 32 >= cols) break;
-    if (q + 1 < 4 && (!kEdge || (q + 1) * 32 < cols)) tmem_ld_32x32b_x32_issue(s_col + (q + 1) * 32, u[(q + 1) & 1]);
-    finish_scores<kCap, kBias, kEdge>(u[q & 1], k, slope2, far - q * 32, lim - q * 32);
-    now = group_max(u[q & 1], now);
-    if constexpr (kCap) tmem_st_32x32b_x32_issue(s_col + q * 32, u[q & 1]);
-    tmem_wait_ld_regs(u[(q + 1) & 1]);
-  }
-  if constexpr (kCap) tmem_wait_st();
-  tmem_ld_32x32b_x32_issue(s_col, u[0]);
-  // The first tile sets the maximum; later ones raise it when it has grown a lot.
+// The maximum of a row has become `now`: the first tile sets it, later ones
+// raise it when it has grown a lot, and bring O and the sum to it.
+template <int DH>
+__device__ __forceinline__ void raise_max(uint32_t o_col, const ScoreConst& k, float now, bool first, RowState& st) {
   if (first) {
     st.m = now;
   } else if (__any_sync(0xffffffffu, (now - st.m) * k.c > kRaise)) {
@@ -349,18 +320,77 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, con
       tmem_st_32x32b_x16_issue(o_col + q * 16, o);
     }
   }
+}
+
+// One tile of scores of this thread's row: weights to TMEM, m and sum brought
+// up to date (and O with them). The scores are read twice, 32 at a time with the
+// next group on its way, rather than kept: 128 registers of them spilled (0.70
+// against 0.40 ms for 16411 causal tokens, 8 heads of 128). Bent scores are
+// written back between.
+template <int DH, bool kBf16, bool kCap, bool kBias>
+__device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, const ScoreConst& k, float slope2,
+                                             float far, bool first, RowState& st) {
+  uint32_t u[2][32];
+  float now = st.m;
+  tmem_ld_32x32b_x32_issue(s_col, u[0]);
+  tmem_wait_ld_regs(u[0]);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (q < 3) tmem_ld_32x32b_x32_issue(s_col + (q + 1) * 32, u[(q + 1) & 1]);
+    finish_scores<kCap, kBias, false>(u[q & 1], k, slope2, far - q * 32, 32);
+    now = group_max(u[q & 1], now);
+    if constexpr (kCap) tmem_st_32x32b_x32_issue(s_col + q * 32, u[q & 1]);
+    if (q < 3) tmem_wait_ld_regs(u[(q + 1) & 1]);
+  }
+  if constexpr (kCap) tmem_wait_st();
+  tmem_ld_32x32b_x32_issue(s_col, u[0]);
+  raise_max<DH>(o_col, k, now, first, st);
   const float down = st.m == -INFINITY ? 0.f : -st.m * k.c;
   const Pair scale(k.c, k.c), shift(down, down);
   Pair part[2] = {Pair(0.f, 0.f), Pair(0.f, 0.f)};
   tmem_wait_ld_regs(u[0]);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    if (kEdge && q * 32 >= cols) break;
-    if (q + 1 < 4 && (!kEdge || (q + 1) * 32 < cols)) tmem_ld_32x32b_x32_issue(s_col + (q + 1) * 32, u[(q + 1) & 1]);
-    if constexpr (!kCap && (kBias || kEdge))
-      finish_scores<kCap, kBias, kEdge>(u[q & 1], k, slope2, far - q * 32, lim - q * 32);
+    if (q < 3) tmem_ld_32x32b_x32_issue(s_col + (q + 1) * 32, u[(q + 1) & 1]);
+    if constexpr (kBias && !kCap) finish_scores<kCap, kBias, false>(u[q & 1], k, slope2, far - q * 32, 32);
     group_weights<kBf16>(s_col + q * 16, u[q & 1], scale, shift, part);
-    tmem_wait_ld_regs(u[(q + 1) & 1]);
+    if (q < 3) tmem_wait_ld_regs(u[(q + 1) & 1]);
+  }
+  float lo, hi;
+  add2(part[0], part[1]).get(lo, hi);
+  st.sum += lo + hi;
+  tmem_wait_st();
+}
+
+// The same for a tile of fewer than 128 columns, or some of whose columns are
+// hidden from the row (those from `lim` on): a loop over the groups of 32 that
+// there are, which compares columns only where a row of the warp needs it. Short
+// documents run here, and small code counts.
+template <int DH, bool kBf16, bool kCap, bool kBias>
+__device__ __forceinline__ void softmax_edge(uint32_t s_col, uint32_t o_col, const ScoreConst& k, float slope2,
+                                             float far, int cols, int lim, bool first, RowState& st) {
+  uint32_t u[32];
+  float now = st.m;
+  const int groups = (cols + 31) / 32, whole = __reduce_min_sync(0xffffffffu, lim) / 32;  // groups that all rows see
+#pragma unroll 1
+  for (int q = 0; q < groups; ++q) {
+    tmem_ld_32x32b_x32_issue(s_col + q * 32, u);
+    tmem_wait_ld_regs(u);
+    if (q < whole) finish_scores<kCap, kBias, false>(u, k, slope2, far - q * 32, 32);
+    else finish_scores<kCap, kBias, true>(u, k, slope2, far - q * 32, lim - q * 32);
+    now = group_max(u, now);
+    if (kCap || kBias || q >= whole) tmem_st_32x32b_x32_issue(s_col + q * 32, u);
+  }
+  tmem_wait_st();
+  raise_max<DH>(o_col, k, now, first, st);
+  const float down = st.m == -INFINITY ? 0.f : -st.m * k.c;
+  const Pair scale(k.c, k.c), shift(down, down);
+  Pair part[2] = {Pair(0.f, 0.f), Pair(0.f, 0.f)};
+#pragma unroll 1
+  for (int q = 0; q < groups; ++q) {
+    tmem_ld_32x32b_x32_issue(s_col + q * 32, u);
+    tmem_wait_ld_regs(u);
+    group_weights<kBf16>(s_col + q * 16, u, scale, shift, part);
   }
   float lo, hi;
   add2(part[0], part[1]).get(lo, hi);
@@ -399,10 +429,10 @@ __device__ void fwd_softmax(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint
       tc_fence_after();
       const float far = static_cast<float>(row - j * kTile);
       if ((j + 1) * kTile <= all_see)
-        softmax_tile<DH, kBf16, kCap, kBias, false>(s_col, o_col, k, slope2, far, kTile, kTile, j == 0, st);
+        softmax_tile<DH, kBf16, kCap, kBias>(s_col, o_col, k, slope2, far, j == 0, st);
       else
-        softmax_tile<DH, kBf16, kCap, kBias, true>(s_col, o_col, k, slope2, far, min(kTile, keys - j * kTile),
-                                                   end - j * kTile, j == 0, st);
+        softmax_edge<DH, kBf16, kCap, kBias>(s_col, o_col, k, slope2, far, min(kTile, keys - j * kTile), end - j * kTile,
+                                             j == 0, st);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_a(sm.p_full(t));
@@ -449,8 +479,7 @@ __global__ void __launch_bounds__(FwdShape<DH, NQ>::kThreads, FwdShape<DH, NQ>::
   const FwdSmem<DH, NQ> sm(raw);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    mbar_init(sm.at(sm.q_full()), 1);
-    mbar_init(sm.at(sm.q_empty()), 1);
+    for (int s = 0; s < 2 * S::kQStages; ++s) mbar_init(sm.at(sm.q_full(s)), 1);
     for (int s = 0; s < 4 * S::kStages; ++s) mbar_init(sm.at(sm.k_full(s)), 1);
     for (int t = 0; t < NQ; ++t) {
       mbar_init(sm.at(sm.s_full(t)), 1);
@@ -459,7 +488,7 @@ __global__ void __launch_bounds__(FwdShape<DH, NQ>::kThreads, FwdShape<DH, NQ>::
     }
     for (int r = 0; r < kRing; ++r) {
       mbar_init(sm.at(sm.info_full(r)), 1);
-      mbar_init(sm.at(sm.info_empty(r)), 4 * NQ + 1);  // softmax warps and the issuing warp
+      mbar_init(sm.at(sm.info_empty(r)), 4 * NQ + 2);  // softmax warps, the loader and the issuing warp
     }
     mbar_init(sm.at(sm.done()), 1);
     *sm.abort_flag = 0;
@@ -476,7 +505,9 @@ __global__ void __launch_bounds__(FwdShape<DH, NQ>::kThreads, FwdShape<DH, NQ>::
   const uint32_t tmem = *sm.tmem_slot;
   if (warp >= 4 * NQ) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsOther));
-    if (warp == 4 * NQ) fwd_loader<DH, NQ>(p, sm, &mq, &mk, &mv);
+    if (warp == 4 * NQ) {
+      if ((threadIdx.x & 31) == 0) fwd_loader<DH, NQ>(p, sm, &mq, &mk, &mv);
+    } else if (warp == 4 * NQ + 2) plan_work(p, sm, NQ * kTile, p.heads, p.mask != MAXSIM_MASK_FULL);
     else if (warp == 4 * NQ + 1) fwd_products<DH, NQ, kBf16>(p, sm, tmem);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsSoftmax));
