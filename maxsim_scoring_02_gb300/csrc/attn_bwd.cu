@@ -353,22 +353,22 @@ struct MathConst {
 
 // This thread's 64 columns of a tile of scores: weights into e (times bend in
 // the dK and dV kernel) and, in 16 bits, to TMEM. nl: minus the rows' lse2, of
-// the walked rows in shared memory or of this thread's own row. kEdge: columns
-// outside [lo, hi) have weight 0, those from `used` on are not looked at.
-template <bool kDkv, bool kBf16, bool kCap, bool kBias, bool kEdge>
+// the walked rows in shared memory or of this thread's own row. In an edge tile
+// columns outside [lo, hi) have weight 0 and those from `used` on are not
+// looked at; one code for both, since its size counts.
+template <bool kDkv, bool kBf16, bool kCap, bool kBias>
 __device__ __forceinline__ void make_weights(uint32_t s_col, const MathConst& k, const float* nl, float own_nl,
-                                             float slope2, float far, int used, int lo, int hi, float (&e)[64],
-                                             float (&bend)[kCap && !kDkv ? 64 : 1]) {
+                                             float slope2, float far, bool edge, int used, int lo, int hi,
+                                             float (&e)[64], float (&bend)[kCap && !kDkv ? 64 : 1]) {
   uint32_t u[2][32];
   tmem_ld_32x32b_x32_issue(s_col, u[0]);
-  if (!kEdge || used > 32) tmem_ld_32x32b_x32_issue(s_col + 32, u[1]);
+  tmem_ld_32x32b_x32_issue(s_col + 32, u[1]);
   tmem_wait_ld_regs(u[0]);
   reg_order(u[1]);
   const Pair scale(k.c, k.c);
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    if (kEdge && q * 32 >= used) break;
-    uint32_t pk[16];
+    if (q * 32 >= used) break;
 #pragma unroll
     for (int x = 0; x < 32; x += 4) {
       float4 n;
@@ -393,23 +393,32 @@ __device__ __forceinline__ void make_weights(uint32_t s_col, const MathConst& k,
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         z[y] = fast_exp2(z[y]);
-        if constexpr (kEdge) z[y] = static_cast<unsigned>(q * 32 + x + y - lo) < static_cast<unsigned>(hi - lo) ? z[y] : 0.f;
-      }
-      float w[4] = {z[0], z[1], z[2], z[3]};  // what goes to TMEM: the weights for dV, weights * bend for their product with K
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
         if constexpr (kCap) {
-          if (kEdge && z[y] == 0.f) d[y] = 0.f;
-          if constexpr (kDkv) z[y] *= d[y];
-          else {
-            bend[q * 32 + x + y] = d[y];
-            w[y] *= d[y];
-          }
+          if constexpr (kDkv) u[q][x + y] = __float_as_uint(z[y]), z[y] *= d[y];
+          else bend[q * 32 + x + y] = d[y];
         }
         e[q * 32 + x + y] = z[y];
       }
-      pk[x / 2] = pack2<kBf16>(w[0], w[1]);
-      pk[x / 2 + 1] = pack2<kBf16>(w[2], w[3]);
+    }
+    if (edge) {
+#pragma unroll
+      for (int x = 0; x < 32; ++x)
+        if (static_cast<unsigned>(q * 32 + x - lo) >= static_cast<unsigned>(hi - lo)) {
+          e[q * 32 + x] = 0.f;
+          if constexpr (kCap) {
+            if constexpr (kDkv) u[q][x] = 0;
+            else bend[q * 32 + x] = 0.f;
+          }
+        }
+    }
+    // to TMEM: the weights for dV, weights * bend for their product with K
+    uint32_t pk[16];
+#pragma unroll
+    for (int x = 0; x < 32; x += 2) {
+      const float *a = e + q * 32 + x, *g = bend + (kCap && !kDkv ? q * 32 + x : 0);
+      if constexpr (!kCap) pk[x / 2] = pack2<kBf16>(a[0], a[1]);
+      else if constexpr (kDkv) pk[x / 2] = pack2<kBf16>(__uint_as_float(u[q][x]), __uint_as_float(u[q][x + 1]));
+      else pk[x / 2] = pack2<kBf16>(a[0] * g[0], a[1] * g[1]);
     }
     tmem_st_32x32b_x16_issue(s_col + q * 16, pk);
   }
@@ -418,16 +427,21 @@ __device__ __forceinline__ void make_weights(uint32_t s_col, const MathConst& k,
 
 // dS of the same columns to TMEM. nd: minus delta, as nl. `rest` gathers the
 // sum over the row of e (dP - delta), which exact arithmetic makes 0.
-template <bool kDkv, bool kBf16, bool kCap, bool kEdge>
-__device__ __forceinline__ void make_ds(uint32_t dp_col, const float* nd, float own_nd, int used, const float (&e)[64],
-                                        const float (&bend)[kCap && !kDkv ? 64 : 1], Pair& rest) {
+template <bool kDkv, bool kBf16, bool kCap>
+__device__ __forceinline__ void make_ds(uint32_t dp_col, const float* nd, float own_nd, bool edge, int used,
+                                        const float (&e)[64], const float (&bend)[kCap && !kDkv ? 64 : 1], Pair& rest) {
   uint32_t u[2][32];
   tmem_ld_32x32b_x32_issue(dp_col, u[0]);
   tmem_wait_ld_regs(u[0]);
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    if (kEdge && q * 32 >= used) break;
-    if (q == 0 && (!kEdge || used > 32)) tmem_ld_32x32b_x32_issue(dp_col + 32, u[1]);
+    if (q * 32 >= used) break;
+    if (q == 0) tmem_ld_32x32b_x32_issue(dp_col + 32, u[1]);
+    if (edge) {  // where nothing is seen dP may be anything
+#pragma unroll
+      for (int x = 0; x < 32; ++x)
+        if (e[q * 32 + x] == 0.f) u[q][x] = 0;
+    }
     uint32_t pk[16];
 #pragma unroll
     for (int x = 0; x < 32; x += 4) {
@@ -440,19 +454,14 @@ __device__ __forceinline__ void make_ds(uint32_t dp_col, const float* nd, float 
       Pair b = add2(Pair(__uint_as_float(u[q][x + 2]), __uint_as_float(u[q][x + 3])), Pair(n.z, n.w));
       a = mul2(a, Pair(w[0], w[1]));
       b = mul2(b, Pair(w[2], w[3]));
+      if constexpr (!kDkv) rest = add2(rest, add2(a, b));
+      if constexpr (kCap && !kDkv) {
+        const float* g = bend + q * 32 + x;
+        a = mul2(a, Pair(g[0], g[1]));
+        b = mul2(b, Pair(g[2], g[3]));
+      }
       a.get(d[0], d[1]);
       b.get(d[2], d[3]);
-      if constexpr (kEdge) {  // where nothing is seen the difference may be anything
-#pragma unroll
-        for (int y = 0; y < 4; ++y) d[y] = w[y] == 0.f ? 0.f : d[y];
-      }
-      if constexpr (!kDkv) {
-        rest = add2(rest, add2(Pair(d[0], d[1]), Pair(d[2], d[3])));
-        if constexpr (kCap) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) d[y] *= bend[q * 32 + x + y];
-        }
-      }
       pk[x / 2] = pack2<kBf16>(d[0], d[1]);
       pk[x / 2 + 1] = pack2<kBf16>(d[2], d[3]);
     }
@@ -517,16 +526,14 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
         // the statistics came with the walked tile, whose products have been made from it
         if (kDkv && !wait(sm.walk_full(step % kStages), step / kStages)) return;
         tc_fence_after();
-        if (!edge) make_weights<kDkv, kBf16, kCap, kBias, false>(s_col, k, nl, own_nl, slope2, far, 64, 0, 64, e, bend);
-        else if (used > 0)
-          make_weights<kDkv, kBf16, kCap, kBias, true>(s_col, k, nl, own_nl, slope2, far, used, lo - from, hi - from, e, bend);
+        if (used > 0)
+          make_weights<kDkv, kBf16, kCap, kBias>(s_col, k, nl, own_nl, slope2, far, edge, used, lo - from, hi - from, e, bend);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_a(sm.p_full());
         if (!wait(sm.dp_full(), step)) return;
         tc_fence_after();
-        if (!edge) make_ds<kDkv, kBf16, kCap, false>(dp_col, nl + BC, own_nd, 64, e, bend, rest);
-        else if (used > 0) make_ds<kDkv, kBf16, kCap, true>(dp_col, nl + BC, own_nd, used, e, bend, rest);
+        if (used > 0) make_ds<kDkv, kBf16, kCap>(dp_col, nl + BC, own_nd, edge, used, e, bend, rest);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -727,8 +734,9 @@ maxsim_status launch_attn_bwd(const AttnParams& p, int is_bf16, cudaStream_t str
   else attn_stats_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p, L);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = p.d <= 64 ? bwd_both<64, 128>(dkv, dq, p, is_bf16, dev->sm_count, stream)
-                  : bwd_both<128, 128>(dkv, dq, p, is_bf16, dev->sm_count, stream);
+    e = p.d > 64            ? bwd_both<128, 128>(dkv, dq, p, is_bf16, dev->sm_count, stream)
+        : p.T / p.B >= 128 ? bwd_both<64, 128>(dkv, dq, p, is_bf16, dev->sm_count, stream)
+                           : bwd_both<64, 64>(dkv, dq, p, is_bf16, dev->sm_count, stream);
   return e == cudaSuccess ? MAXSIM_OK : MAXSIM_ERR_CUDA;
 }
 
