@@ -63,7 +63,7 @@ struct BwdShape {
   static constexpr uint32_t kNeed = 2 * BC + 2 * DH;
   static constexpr uint32_t kTmemCols = kNeed <= 256 ? 256 : 512;
   static constexpr int kBars = 2 + 2 * kStages + 5 + 2 * kRing + 2;
-  static constexpr uint32_t kSmem = 1024 + 2 * kOwnBytes + 2 * kStages * kBytes + 8 * kBars +
+  static constexpr uint32_t kSmem = 1024 + 2 * kOwnBytes + 2 * kStages * kBytes + kGroups * 4 * kStageBytes + 8 * kBars +
                                     kStages * BC * 8 + kRing * sizeof(Work) + 16 + 16;
 };
 
@@ -71,7 +71,7 @@ struct BwdShape {
 // walk_a, walk_b: the stages of what it walks over (Q and dO, or K and V).
 template <class S, int BC>
 struct BwdSmem {
-  uint32_t own_a, own_b, walk_a, walk_b, bars;
+  uint32_t own_a, own_b, walk_a, walk_b, stage, bars;
   uint64_t* bar;
   float* stats;   // kStages x (BC times -lse2, BC times -delta) of the walked rows
   Work* info;
@@ -84,6 +84,8 @@ struct BwdSmem {
     walk_a = own_b + S::kOwnBytes;
     walk_b = walk_a + kStages * S::kBytes;
     uint8_t* end = base + 2 * S::kOwnBytes + 2 * kStages * S::kBytes;
+    stage = walk_b + kStages * S::kBytes;
+    end += S::kGroups * 4 * kStageBytes;
     stats = reinterpret_cast<float*>(end);
     bar = reinterpret_cast<uint64_t*>(end + kStages * BC * 8);
     bars = smem_u32(bar);
@@ -315,33 +317,30 @@ __device__ void bwd_products(const AttnParams& p, const BwdSmem<S, BC>& sm, uint
 }
 
 // ----------------------------------------------------------- arithmetic
-// 32 columns of fp32 sums, times f (plus others, times f2), as 16-bit values of a row.
+// 32 columns of this warp's 32 rows of fp32 sums, times f (plus others, times
+// f2), to memory in 16 bits.
 template <bool kBf16>
-__device__ __forceinline__ void store_sums(uint32_t col, uint32_t col2, uint4* dst, int first, int d, float f, float f2,
-                                           bool live, bool any) {
+__device__ __forceinline__ void store_sums(uint32_t col, uint32_t col2, uint32_t stage, uint16_t* dst, int64_t stride,
+                                           int rows, int first, int d, float f, float f2, bool any) {
+  uint32_t y[16] = {};
+  if (any) {
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t o[16], o2[16];
-    if (any) {
+    for (int half = 0; half < 2; ++half) {
+      uint32_t o[16], o2[16];
       tmem_ld_32x32b_x16(col + half * 16, o);
       if (col2) tmem_ld_32x32b_x16(col2 + half * 16, o2);
-    }
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      uint4 y = make_uint4(0, 0, 0, 0);
-      if (any) {
-        float v[8];
-#pragma unroll
-        for (int z = 0; z < 8; ++z) {
-          v[z] = __uint_as_float(o[x * 8 + z]) * f;
-          if (col2) v[z] = fmaf(__uint_as_float(o2[x * 8 + z]), f2, v[z]);
+      for (int x = 0; x < 16; x += 2) {
+        float a = __uint_as_float(o[x]) * f, b = __uint_as_float(o[x + 1]) * f;
+        if (col2) {
+          a = fmaf(__uint_as_float(o2[x]), f2, a);
+          b = fmaf(__uint_as_float(o2[x + 1]), f2, b);
         }
-        y = make_uint4(pack2<kBf16>(v[0], v[1]), pack2<kBf16>(v[2], v[3]), pack2<kBf16>(v[4], v[5]),
-                       pack2<kBf16>(v[6], v[7]));
+        y[half * 8 + x / 2] = pack2<kBf16>(a, b);
       }
-      if (live && first + half * 16 + x * 8 < d) dst[first / 8 + half * 2 + x] = y;
     }
   }
+  store_rows32(stage, y, dst, stride, rows, first, d);
 }
 __device__ __forceinline__ uint4* row_of(const HeadsView& v, int64_t token, int head) {
   return reinterpret_cast<uint4*>(static_cast<uint16_t*>(v.data) + token * v.token_stride + head * v.head_stride);
@@ -564,24 +563,28 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
       ++item;
       tc_fence_after();
     }
-    const int64_t token = w.start + mine;
+    const int row32 = w.row0 + static_cast<int>(threadIdx.x & 96), rows = w.len - row32;  // this warp's rows
+    const int64_t token = w.start + static_cast<int64_t>(row32);
+    const uint32_t stage = sm.stage + (threadIdx.x >> 5) * kStageBytes;
+    const auto base = [&](const HeadsView& v) {
+      return static_cast<uint16_t*>(v.data) + token * v.token_stride + w.head * v.head_stride;
+    };
     constexpr int kChunks = DH / 32;
+    const uint32_t sum0 = tmem + lanes + S::kSum0, sum1 = tmem + lanes + S::kSum1;
     if constexpr (kDkv) {
-      uint4 *dv = row_of(p.dv, token, w.head), *dk = row_of(p.dk, token, w.head);
 #pragma unroll
       for (int q = 0; q < kChunks; ++q) {  // two warpgroups: one writes dV, one dK
         if (S::kGroups == 1 || wg == 0)
-          store_sums<kBf16>(tmem + lanes + S::kSum0 + q * 32, 0, dv, q * 32, p.d, 1.f, 0.f, live, any);
+          store_sums<kBf16>(sum0 + q * 32, 0, stage, base(p.dv), p.dv.token_stride, rows, q * 32, p.d, 1.f, 0.f, any);
         if (S::kGroups == 1 || wg == 1)
-          store_sums<kBf16>(tmem + lanes + S::kSum1 + q * 32, 0, dk, q * 32, p.d, p.scale, 0.f, live, any);
+          store_sums<kBf16>(sum1 + q * 32, 0, stage, base(p.dk), p.dk.token_stride, rows, q * 32, p.d, p.scale, 0.f, any);
       }
     } else {
-      uint4* dq = row_of(p.dq, token, w.head);
 #pragma unroll
       for (int q = 0; q < kChunks; ++q)
         if (S::kGroups == 1 || q / (kChunks / 2) == wg)
-          store_sums<kBf16>(tmem + lanes + S::kSum1 + q * 32, tmem + lanes + S::kSum0 + q * 32, dq, q * 32, p.d, p.scale,
-                            -off * p.scale, live, any);
+          store_sums<kBf16>(sum1 + q * 32, sum0 + q * 32, stage, base(p.dq), p.dq.token_stride, rows, q * 32, p.d,
+                            p.scale, -off * p.scale, any);
     }
     tc_fence_before();  // the next item's first products overwrite the sums after its p_full / ds_full
   }

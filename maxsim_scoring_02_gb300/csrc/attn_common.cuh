@@ -234,6 +234,34 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
+// A warp's 32 rows of 32 columns of 16-bit values (16 words a lane, one row
+// each) to memory. Written as they are, each store would touch 32 lines, 16
+// bytes of each; through 2.5 KB of shared memory (rows 80 bytes apart: no bank
+// conflicts) it touches 8, 64 bytes of each. base: the first row's head.
+constexpr uint32_t kStageBytes = 32 * 80;
+__device__ __forceinline__ void store_rows32(uint32_t stage, const uint32_t (&v)[16], uint16_t* base, int64_t stride,
+                                             int rows, int col0, int d) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 80 + x * 16), "r"(v[x * 4]),
+                 "r"(v[x * 4 + 1]), "r"(v[x * 4 + 2]), "r"(v[x * 4 + 3])
+                 : "memory");
+  __syncwarp();
+  const int col = col0 + (lane & 3) * 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    uint4 y;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                 : "r"(stage + r * 80 + (lane & 3) * 16)
+                 : "memory");
+    if (r < rows && col < d) *reinterpret_cast<uint4*>(base + r * stride + col) = y;
+  }
+  __syncwarp();
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

@@ -50,13 +50,13 @@ struct FwdShape {
   // barriers: k_full, k_empty, v_full, v_empty, s_full, p_full, o_full, info_full, info_empty, done, q_full, q_empty
   static constexpr int kBars = 4 * kStages + 3 * NQ + 2 * kRing + 1 + 2 * kQStages;
   static constexpr uint32_t kTiles = NQ * kQStages + 2 * kStages;
-  static constexpr uint32_t kSmem = 1024 + kTiles * kTileBytes + 8 * kBars + kRing * sizeof(Work) + 16;
+  static constexpr uint32_t kSmem = 1024 + kTiles * kTileBytes + NQ * 4 * kStageBytes + 8 * kBars + kRing * sizeof(Work) + 16;
 };
 
 template <int DH, int NQ>
 struct FwdSmem {
   using S = FwdShape<DH, NQ>;
-  uint32_t q, k, v, bars;
+  uint32_t q, k, v, stage, bars;
   uint64_t* bar;
   Work* info;
   uint32_t* tmem_slot;
@@ -66,7 +66,8 @@ struct FwdSmem {
     q = smem_u32(base);
     k = q + NQ * S::kQStages * S::kTileBytes;
     v = k + S::kStages * S::kTileBytes;
-    bar = reinterpret_cast<uint64_t*>(base + S::kTiles * S::kTileBytes);
+    stage = q + S::kTiles * S::kTileBytes;
+    bar = reinterpret_cast<uint64_t*>(base + S::kTiles * S::kTileBytes + NQ * 4 * kStageBytes);
     bars = smem_u32(bar);
     info = reinterpret_cast<Work*>(bar + S::kBars);
     tmem_slot = reinterpret_cast<uint32_t*>(info + kRing);
@@ -445,25 +446,20 @@ __device__ void fwd_softmax(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint
       tc_fence_after();
     }
     const int64_t token = w.start + row;
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out.data) + token * p.out.token_stride +
-                                          w.head * p.out.head_stride);
+    const int row32 = first + static_cast<int>(threadIdx.x & 96);  // this warp's first row
+    uint16_t* dst = static_cast<uint16_t*>(p.out.data) + (w.start + static_cast<int64_t>(row32)) * p.out.token_stride +
+                    w.head * p.out.head_stride;
 #pragma unroll
     for (int q = 0; q < DH / 32; ++q) {
-      uint32_t o[32];
+      uint32_t o[32], y[16] = {};
       if (nk > 0) {
         tmem_ld_32x32b_x32_issue(o_col + q * 32, o);
         tmem_wait_ld_regs(o);
-      }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        uint4 y = make_uint4(0, 0, 0, 0);
-        if (nk > 0) {
-          const float* f = reinterpret_cast<const float*>(o) + x * 8;
-          y = make_uint4(pack2<kBf16>(f[0] * inv, f[1] * inv), pack2<kBf16>(f[2] * inv, f[3] * inv),
-                         pack2<kBf16>(f[4] * inv, f[5] * inv), pack2<kBf16>(f[6] * inv, f[7] * inv));
-        }
-        if (row < w.len && q * 32 + x * 8 < p.d) dst[q * 4 + x] = y;
+        for (int x = 0; x < 16; ++x)
+          y[x] = pack2<kBf16>(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
       }
+      store_rows32(sm.stage + (threadIdx.x >> 5) * kStageBytes, y, dst, p.out.token_stride, w.len - row32, q * 32, p.d);
     }
     if (p.lse && row < w.len)
       p.lse[static_cast<int64_t>(w.head) * p.T + token] = some ? (st.m * k.c + log2f(st.sum)) * kLn2 : -INFINITY;
