@@ -189,7 +189,7 @@ __device__ void bwd_stats(const AttnParams& p, const BwdSmem<S, BC>& sm) {
   uint32_t step = 0;
   for (uint32_t n = 0;; ++n) {
     const int r = n % kRing;
-    if (!__all_sync(0xffffffffu, mbar_wait_inl_a(sm.info_full(r), (n / kRing) & 1, sm.abort_flag, p.status))) return;
+    if (!mbar_wait_warp(sm.info_full(r), (n / kRing) & 1, sm.abort_flag, p.status)) return;
     const Work w = sm.info[r];
     __syncwarp();
     if (lane == 0) mbar_arrive_a(sm.info_empty(r));
@@ -205,7 +205,7 @@ __device__ void bwd_stats(const AttnParams& p, const BwdSmem<S, BC>& sm) {
           const int i = from + x * 32 + lane;
           v[x] = i < g.end ? row[i] : make_float2(-INFINITY, 0.f);
         }
-        if (!__all_sync(0xffffffffu, mbar_wait_inl_a(sm.walk_empty(s), ((step / kStages) & 1) ^ 1, sm.abort_flag, p.status)))
+        if (!mbar_wait_warp(sm.walk_empty(s), ((step / kStages) & 1) ^ 1, sm.abort_flag, p.status))
           return;
 #pragma unroll
         for (int x = 0; x < BC / 32; ++x) {
@@ -227,7 +227,7 @@ __device__ void bwd_products(const AttnParams& p, const BwdSmem<S, BC>& sm, uint
   const uint32_t idesc_sum = idesc | static_cast<uint32_t>(DH >> 3) << 17 | kIdescBMnMajor;
   uint32_t item = 0, step = 0;
   const auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait_inl_a(bar, ph & 1, sm.abort_flag, p.status));
+    return mbar_wait_warp(bar, ph & 1, sm.abort_flag, p.status);
   };
   // 128 x cols scores of the block's rows and the walked ones of stage s
   const auto score = [&](uint32_t d_col, uint32_t own, uint32_t walked, int cols) {
@@ -479,7 +479,7 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
                        kCap ? 2.f * kLog2e * p.scale / p.cap : 0.f};
   uint32_t step = 0, item = 0, rows_done = 0;
   const auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait_inl_a(bar, ph & 1, sm.abort_flag, p.status));
+    return mbar_wait_warp(bar, ph & 1, sm.abort_flag, p.status);
   };
   for (uint32_t n = 0;; ++n) {
     const int r = n % kRing;
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH,
   extern __shared__ uint8_t raw[];
   const BwdSmem<S, BC> sm(raw);
   constexpr int kMathWarps = 4 * S::kGroups;
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // known to be uniform, and the roles with it
   if (threadIdx.x == 0) {
     mbar_init(sm.at(sm.own_full()), 1);
     mbar_init(sm.at(sm.own_empty()), 1);
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH,
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *sm.tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *sm.tmem_slot, 0);
   if (warp >= kMathWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::other_regs(kCap)));
     if (warp == kMathWarps) {

@@ -140,7 +140,7 @@ __device__ void plan_work(const AttnParams& p, const Smem& sm, int rows, int hea
   uint32_t n = 0;
   const auto put = [&](const Work& w, bool me) -> bool {
     const int r = n % kRing;
-    if (!__all_sync(0xffffffffu, mbar_wait_inl_a(sm.info_empty(r), ((n / kRing) & 1) ^ 1, sm.abort_flag, p.status)))
+    if (!mbar_wait_warp(sm.info_empty(r), ((n / kRing) & 1) ^ 1, sm.abort_flag, p.status))
       return false;
     if (me) {
       sm.info[r] = w;

@@ -161,7 +161,7 @@ __device__ void fwd_products(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uin
   uint32_t item = 0, kv = 0, seen_k = 0;
   uint32_t pn[NQ] = {};  // p_full phases passed
   const auto wait = [&](uint32_t bar, uint32_t ph) {
-    return __all_sync(0xffffffffu, mbar_wait_inl_a(bar, ph & 1, sm.abort_flag, p.status));
+    return mbar_wait_warp(bar, ph & 1, sm.abort_flag, p.status);
   };
   bool ok = true;
   for (uint32_t n = 0; ok; ++n) {
@@ -173,7 +173,7 @@ __device__ void fwd_products(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uin
     if (!w.live) break;
     int keys[NQ], most = 0;
 #pragma unroll
-    for (int t = 0; t < NQ; ++t) most = max(most, keys[t] = tile_keys(w, p.mask, t));
+    for (int t = 0; t < NQ; ++t) most = max(most, keys[t] = __shfl_sync(0xffffffffu, tile_keys(w, p.mask, t), 0));
     const int nk = tiles_of(most);
     if (nk == 0) continue;
     const int sq = item % S::kQStages;
@@ -410,7 +410,7 @@ __device__ void fwd_softmax(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint
                         kCap ? 2.f * kLog2e * p.scale / p.cap : 0.f};
   uint32_t sn = 0, on = 0;
   const auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait_inl_a(bar, ph & 1, sm.abort_flag, p.status));
+    return mbar_wait_warp(bar, ph & 1, sm.abort_flag, p.status);
   };
   for (uint32_t n = 0;; ++n) {
     const int r = n % kRing;
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(FwdShape<DH, NQ>::kThreads, FwdShape<DH, NQ>::
   using S = FwdShape<DH, NQ>;
   extern __shared__ uint8_t raw[];
   const FwdSmem<DH, NQ> sm(raw);
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // known to be uniform, and the roles with it
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2 * S::kQStages; ++s) mbar_init(sm.at(sm.q_full(s)), 1);
     for (int s = 0; s < 4 * S::kStages; ++s) mbar_init(sm.at(sm.k_full(s)), 1);
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(FwdShape<DH, NQ>::kThreads, FwdShape<DH, NQ>::
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *sm.tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *sm.tmem_slot, 0);
   if (warp >= 4 * NQ) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsOther));
     if (warp == 4 * NQ) {

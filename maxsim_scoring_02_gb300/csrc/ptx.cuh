@@ -218,6 +218,28 @@ __device__ __forceinline__ bool mbar_poll_inl_a(uint32_t bar, uint32_t parity, v
   }
 }
 
+// Bounded wait of a whole warp, every lane active: one vote a poll, so that the
+// compiler keeps the warp's control flow and operands uniform around it.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                               unsigned* status) {
+#pragma unroll 1
+  for (uint32_t it = 0; it < kFastSpins; ++it)
+    if (__all_sync(0xffffffffu, mbar_try_wait_a(bar, parity))) return true;
+  const uint64_t t0 = globaltimer_ns(), lim = wait_limit_ns(status);
+#pragma unroll 1
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_a(bar, parity))) return true;
+    if ((it & 63u) == 0) {
+      const bool late = globaltimer_ns() - t0 > lim;
+      if (late) {
+        atomicOr(status, kDevErrTimeout);
+        *abort_flag = 1;
+      }
+      if (__any_sync(0xffffffffu, late || *abort_flag)) return false;
+    }
+  }
+}
+
 // Bounded wait used while draining after an abort: ignores the abort flag.
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity, unsigned* status) {
   const uint64_t t0 = globaltimer_ns();
