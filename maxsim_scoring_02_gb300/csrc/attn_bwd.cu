@@ -249,7 +249,7 @@ __device__ void bwd_products(const AttnParams& p, const BwdSmem<S, BC>& sm, uint
   for (uint32_t n = 0; ok; ++n) {
     const int r = n % kRing;
     if (!wait(sm.info_full(r), n / kRing)) break;
-    const Work w = sm.info[r];
+    const Work w = uniform_work(sm.info[r]);
     __syncwarp();
     if (lane == 0) mbar_arrive_a(sm.info_empty(r));
     if (!w.live) break;

@@ -126,6 +126,19 @@ struct Work {
   int live;                      // 0: no work is left
 };
 
+// A piece of work read from shared memory, known to be the same in all lanes.
+__device__ __forceinline__ Work uniform_work(const Work& a) {
+  Work w;
+  w.start = __shfl_sync(0xffffffffu, a.start, 0);
+  w.len = __shfl_sync(0xffffffffu, a.len, 0);
+  w.keys = __shfl_sync(0xffffffffu, a.keys, 0);
+  w.prefix = __shfl_sync(0xffffffffu, a.prefix, 0);
+  w.row0 = __shfl_sync(0xffffffffu, a.row0, 0);
+  w.head = __shfl_sync(0xffffffffu, a.head, 0);
+  w.live = __shfl_sync(0xffffffffu, a.live, 0);
+  return w;
+}
+
 constexpr int kRing = 4;  // pieces of work that are planned ahead
 
 // One warp finds the block's pieces of work, 32 at a time, since each takes a

@@ -167,13 +167,13 @@ __device__ void fwd_products(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uin
   for (uint32_t n = 0; ok; ++n) {
     const int r = n % kRing;
     if (!wait(sm.info_full(r), n / kRing)) break;
-    const Work w = sm.info[r];
+    const Work w = uniform_work(sm.info[r]);
     __syncwarp();
     if (lane == 0) mbar_arrive_a(sm.info_empty(r));
     if (!w.live) break;
     int keys[NQ], most = 0;
 #pragma unroll
-    for (int t = 0; t < NQ; ++t) most = max(most, keys[t] = __shfl_sync(0xffffffffu, tile_keys(w, p.mask, t), 0));
+    for (int t = 0; t < NQ; ++t) most = max(most, keys[t] = tile_keys(w, p.mask, t));
     const int nk = tiles_of(most);
     if (nk == 0) continue;
     const int sq = item % S::kQStages;
@@ -230,9 +230,15 @@ __device__ void fwd_products(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uin
         tc_fence_after();
         const int steps = (min(kTile, left) + 15) / 16;
         const uint64_t b = sdesc_mn_sw128(sm.v + s * S::kTileBytes, S::kPanelBytes);
-        for (int kk = 0; kk < steps; ++kk)
-          umma_f16_ts_el(tmem + S::kO0 + t * DH, tmem + t * kTile + kk * 8, b + kk * (2048 >> 4),
-                         idesc | static_cast<uint32_t>(DH >> 3) << 17 | kIdescBMnMajor, (j | kk) != 0);
+        const uint32_t ido = idesc | static_cast<uint32_t>(DH >> 3) << 17 | kIdescBMnMajor;
+        if (NQ == 2 && steps == 8) {  // whole tiles of long documents, without the loop's overhead (4 %)
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_f16_ts_el(tmem + S::kO0 + t * DH, tmem + t * kTile + kk * 8, b + kk * (2048 >> 4), ido, (j | kk) != 0);
+        } else {
+          for (int kk = 0; kk < steps; ++kk)
+            umma_f16_ts_el(tmem + S::kO0 + t * DH, tmem + t * kTile + kk * 8, b + kk * (2048 >> 4), ido, (j | kk) != 0);
+        }
         if (left <= kTile) umma_commit_el(sm.o_full(t));
         if (left > kTile) {
           if (!(ok = need_k(j + 1))) break;
