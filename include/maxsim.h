@@ -528,7 +528,7 @@ maxsim_status maxsim_attention_backward(const maxsim_attention_spec *spec, const
  * dtypes[i] (a maxsim_dtype; types may be mixed), aligned to their elements.
  * outs[i] may be grads[i] (in place), and overlaps no other tensor otherwise.
  * *norm (device, fp32) receives the norm before clipping. Squares are added in
- * fp32 within a thread's part of a 64 KB chunk and in fp64 beyond, in an order that depends
+ * fp32 within a thread's part of a 32 KB chunk and in fp64 beyond, in an order that depends
  * only on the sizes; values whose squares leave fp32's range are added in fp64.
  * A NaN makes norm and all outputs NaN; an infinity makes norm infinite, itself
  * NaN and every finite element 0.

@@ -13,6 +13,7 @@ Operator (TileMaxSim deep reading §1; FLASH-MAXSIM, Abstract):
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import operator
@@ -163,6 +164,17 @@ def _ptr(t):
 def _stream(stream):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+# The current stream's handle without a Stream object around it, where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, index):
+    """Handle of ``stream``, or of the current stream of device ``index``."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(index)
+    return (torch.cuda.current_stream(index) if stream is None else stream).cuda_stream
 
 
 def _dev(t, name, dtype=None):
@@ -528,14 +540,13 @@ def allreduce_dq(dQ, group=None):
 
 # --------------------------------------------------------- the token encoder
 
-def _heads(t, name, shape, dtype, device):
-    """A [T, heads, d] CUDA tensor, its last dimension contiguous, as a maxsim_heads."""
+def _heads(t, name, shape, dtype, index):
+    """A [T, heads, d] tensor on CUDA device ``index``, its last dimension
+    contiguous, as a maxsim_heads."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path) on the first tensor's device")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -577,20 +588,21 @@ def maxsim_rotary(x, freq, offsets=None, positions=None, interleaved=False, ampl
         raise ValueError("x must be a [T, heads, d] tensor")
     if x.dtype not in _DTYPE_CODE:
         raise TypeError(f"x must be bf16, fp16 or fp32, got {x.dtype}")
-    src = _heads(x, "x", x.shape, x.dtype, x.device)
+    shape, dtype, index = x.shape, x.dtype, x.get_device()
+    src = _heads(x, "x", shape, dtype, index)
     _dev(freq, "freq", torch.int64)
-    T, heads, d = x.shape
+    T, heads, d = shape
     B = 0
     if offsets is not None:
         B = _dev(offsets, "offsets", torch.int64).numel() - 1
     if positions is not None and _dev(positions, "positions", torch.int32).numel() != T:
         raise ValueError("positions must have one entry a token")
     if out is None:
-        out = torch.empty((T, heads, d), dtype=x.dtype, device=x.device)
-    dst = src if out is x else _heads(out, "out", x.shape, x.dtype, x.device)
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+    dst = src if out is x else _heads(out, "out", shape, dtype, index)
     st = lib.maxsim_rotary(src, T, heads, d, 2 * freq.numel(), freq.data_ptr(), _ptr(offsets), B, _ptr(positions),
-                           1 if interleaved else 0, amplitude, 1 if inverse else 0, _DTYPE_CODE[x.dtype], dst,
-                           _stream(stream))
+                           1 if interleaved else 0, amplitude, 1 if inverse else 0, _DTYPE_CODE[dtype], dst,
+                           _stream_on(stream, index))
     _check(st, "maxsim_rotary")
     return out
 
@@ -632,16 +644,17 @@ def maxsim_attention(q, k, v, offsets, key_len=None, mask="full", prefix_len=Non
     [heads, T] fp32 when requested."""
     lib = load_library()
     spec = _attention_spec(q, k, offsets, key_len, mask, prefix_len, scale, cap, slopes)
-    dtype, device, kv_shape = q.dtype, q.device, (spec.T, spec.kv_heads, spec.d)
+    dtype, index, shape = q.dtype, q.get_device(), q.shape
+    kv_shape = (shape[0], spec.kv_heads, shape[2])
     if out is None:
-        out = torch.empty(q.shape, dtype=dtype, device=device)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
     if lse is None and want_lse:
-        lse = torch.empty((spec.heads, spec.T), dtype=torch.float32, device=device)
-    if lse is not None and _dev(lse, "lse", torch.float32).shape != (spec.heads, spec.T):
+        lse = torch.empty((shape[1], shape[0]), dtype=torch.float32, device=q.device)
+    if lse is not None and _dev(lse, "lse", torch.float32).shape != (shape[1], shape[0]):
         raise ValueError("lse must be [heads, T]")
-    st = lib.maxsim_attention(spec, _heads(q, "q", q.shape, dtype, device), _heads(k, "k", kv_shape, dtype, device),
-                              _heads(v, "v", kv_shape, dtype, device), _heads(out, "out", q.shape, dtype, device),
-                              _ptr(lse), _stream(stream))
+    st = lib.maxsim_attention(spec, _heads(q, "q", shape, dtype, index), _heads(k, "k", kv_shape, dtype, index),
+                              _heads(v, "v", kv_shape, dtype, index), _heads(out, "out", shape, dtype, index),
+                              None if lse is None else lse.data_ptr(), _stream_on(stream, index))
     _check(st, "maxsim_attention")
     return (out, lse) if lse is not None else out
 
@@ -659,22 +672,22 @@ def maxsim_attention_backward(dO, q, k, v, out, lse, offsets, key_len=None, mask
     inputs' dtype (views of one buffer may be given)."""
     lib = load_library()
     spec = _attention_spec(q, k, offsets, key_len, mask, prefix_len, scale, cap, slopes)
-    dtype, device, kv_shape = q.dtype, q.device, (spec.T, spec.kv_heads, spec.d)
-    if _dev(lse, "lse", torch.float32).shape != (spec.heads, spec.T):
+    dtype, device, index, shape = q.dtype, q.device, q.get_device(), q.shape
+    kv_shape = (shape[0], spec.kv_heads, shape[2])
+    if _dev(lse, "lse", torch.float32).shape != (shape[1], shape[0]):
         raise ValueError("lse must be [heads, T]")
-    dq = torch.empty(q.shape, dtype=dtype, device=device) if dq is None else dq
+    dq = torch.empty(shape, dtype=dtype, device=device) if dq is None else dq
     dk = torch.empty(kv_shape, dtype=dtype, device=device) if dk is None else dk
     dv = torch.empty(kv_shape, dtype=dtype, device=device) if dv is None else dv
     if workspace is None:
         nbytes = lib.maxsim_attention_backward_workspace_size(spec)
         workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
     _dev(workspace, "workspace", torch.uint8)
-    views = [_heads(t, name, shape, dtype, device)
-             for t, name, shape in ((dO, "dO", q.shape), (q, "q", q.shape), (k, "k", kv_shape), (v, "v", kv_shape),
-                                    (out, "out", q.shape), (dq, "dq", q.shape), (dk, "dk", kv_shape),
-                                    (dv, "dv", kv_shape))]
+    views = [_heads(t, name, want, dtype, index)
+             for t, name, want in ((dO, "dO", shape), (q, "q", shape), (k, "k", kv_shape), (v, "v", kv_shape),
+                                   (out, "out", shape), (dq, "dq", shape), (dk, "dk", kv_shape), (dv, "dv", kv_shape))]
     st = lib.maxsim_attention_backward(spec, *views[:5], lse.data_ptr(), *views[5:], workspace.data_ptr(),
-                                       workspace.numel(), _stream(stream))
+                                       workspace.numel(), _stream_on(stream, index))
     _check(st, "maxsim_attention_backward")
     return dq, dk, dv
 
@@ -684,6 +697,14 @@ def maxsim_clip_grad_norm_workspace_size(n_tensors):
     return int(load_library().maxsim_clip_grad_norm_workspace_size(n_tensors))
 
 
+def _sizes(tensors):
+    return list(map(torch.Tensor.numel, tensors))
+
+
+def _dtypes(tensors):
+    return list(map(operator.attrgetter("dtype"), tensors))
+
+
 def maxsim_clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, stream=None):
     """Global 2-norm of the tensors ``grads`` (contiguous, bf16/fp16/fp32, types
     may be mixed), which are scaled by min(1, max_norm / (norm + 1e-6)): in
@@ -691,40 +712,36 @@ def maxsim_clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, 
     norm before clipping, [1] fp32 on the device."""
     lib = load_library()
     grads = list(grads)
-    n = len(grads)
     outs = grads if out is None else list(out)
-    if not all(isinstance(t, torch.Tensor) for t in grads) or (out is not None and not all(
-            isinstance(t, torch.Tensor) for t in outs)):
-        raise TypeError("grads and out must be lists of torch.Tensor")
-    dtypes = list(map(operator.attrgetter("dtype"), grads))
-    sizes = list(map(torch.Tensor.numel, grads))
-    places = set(map(torch.Tensor.get_device, grads))
-    whole = all(map(torch.Tensor.is_contiguous, grads))
-    if out is not None:
-        if len(outs) != n or list(map(torch.Tensor.numel, outs)) != sizes or \
-                list(map(operator.attrgetter("dtype"), outs)) != dtypes:
-            raise ValueError("out must have a tensor of the same size and type for each of grads")
-        places |= set(map(torch.Tensor.get_device, outs))
-        whole = whole and all(map(torch.Tensor.is_contiguous, outs))
+    n = len(grads)
+    # one pass in C for each attribute: lists have hundreds of tensors
+    sizes, dtypes, sides = _sizes(grads), _dtypes(grads), (grads,) if out is None else (grads, outs)
+    if out is not None and (_sizes(outs) != sizes or _dtypes(outs) != dtypes):
+        raise ValueError("out must have a tensor of the same size and type for each of grads")
+    places = set()
+    for side in sides:
+        places.update(map(torch.Tensor.get_device, side))
+        if not all(map(torch.Tensor.is_contiguous, side)):
+            raise ValueError("all tensors must be contiguous")
     if len(places) > 1 or -1 in places:
         raise ValueError("all tensors must be on one CUDA device (the library has no CPU path)")
-    if not whole:
-        raise ValueError("all tensors must be contiguous")
     try:
-        codes = [_DTYPE_CODE[t] for t in dtypes]
+        codes = array.array("i", map(_DTYPE_CODE.__getitem__, dtypes))
     except KeyError as e:
         raise TypeError(f"gradients must be bf16, fp16 or fp32, got {e.args[0]}") from None
-    device = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+    index = places.pop() if places else torch.cuda.current_device()
+    device = torch.device("cuda", index)
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=device)
     _dev(norm, "norm", torch.float32)
     if workspace is None:
         workspace = torch.empty(lib.maxsim_clip_grad_norm_workspace_size(n), dtype=torch.uint8, device=device)
     _dev(workspace, "workspace", torch.uint8)
-    pointers = (ctypes.c_void_p * n)(*map(torch.Tensor.data_ptr, grads))
-    targets = pointers if out is None else (ctypes.c_void_p * n)(*map(torch.Tensor.data_ptr, outs))
-    st = lib.maxsim_clip_grad_norm(pointers, targets, (ctypes.c_int64 * n)(*sizes), (ctypes.c_int32 * n)(*codes), n,
-                                   max_norm, norm.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                   _stream(stream))
+    pointers = array.array("Q", map(torch.Tensor.data_ptr, grads))
+    targets = pointers if out is None else array.array("Q", map(torch.Tensor.data_ptr, outs))
+    counts = array.array("q", sizes)
+    st = lib.maxsim_clip_grad_norm(pointers.buffer_info()[0], targets.buffer_info()[0], counts.buffer_info()[0],
+                                   codes.buffer_info()[0], n, max_norm, norm.data_ptr(), workspace.data_ptr(),
+                                   workspace.numel(), _stream_on(stream, index))
     _check(st, "maxsim_clip_grad_norm")
     return norm

@@ -40,13 +40,15 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kBoxRows = 64;
-constexpr int kStages = 2;
 
 // DH: head size in shared memory; BC: columns of a score tile (rows of Q or
 // keys that are walked over), 64 for each arithmetic warpgroup.
 template <int DH, int BC, bool kDkv>
 struct BwdShape {
   static constexpr int kGroups = BC / 64;
+  // Heads of 64 leave TMEM for a second buffer of S, which is then made a tile
+  // ahead, and shared memory for the tiles that takes.
+  static constexpr int kSBufs = DH == 64 && BC == 128 ? 2 : 1, kStages = 2 * kSBufs;
   static constexpr int kPanels = DH / 64;
   static constexpr uint32_t kOwnPanel = kTile * 128, kOwnBytes = kPanels * kOwnPanel;
   static constexpr uint32_t kPanel = BC * 128, kBytes = kPanels * kPanel;
@@ -59,11 +61,10 @@ struct BwdShape {
   static constexpr int other_regs(bool cap) { return (kGroups + 1) * kRegsLaunch - kGroups * math_regs(cap); }
   static_assert(other_regs(true) >= 56 && other_regs(true) % 8 == 0 && other_regs(false) % 8 == 0, "register split");
   // TMEM columns: S, dP, then the sums
-  static constexpr uint32_t kDp = BC, kSum0 = 2 * BC, kSum1 = 2 * BC + DH;
-  static constexpr uint32_t kNeed = 2 * BC + 2 * DH;
+  static constexpr uint32_t kDp = kSBufs * BC, kSum0 = kDp + BC, kSum1 = kSum0 + DH, kNeed = kSum1 + DH;
   static constexpr uint32_t kTmemCols = kNeed <= 256 ? 256 : 512;
-  static constexpr int kBars = 2 + 2 * kStages + 5 + 2 * kRing + 2;
-  static constexpr uint32_t kSmem = 1024 + 2 * kOwnBytes + 2 * kStages * kBytes + kGroups * 4 * kStageBytes + 8 * kBars +
+  static constexpr int kBars = 2 + 2 * kStages + 3 + 2 * kSBufs + 2 * kRing + 2;
+  static constexpr uint32_t kSmem = 1024 + 2 * kOwnBytes + 2 * kStages * kBytes + kGroups * 4 * kStageBytes<32> + 8 * kBars +
                                     kStages * BC * 8 + kRing * sizeof(Work) + 16 + 16;
 };
 
@@ -73,7 +74,7 @@ template <class S, int BC>
 struct BwdSmem {
   uint32_t own_a, own_b, walk_a, walk_b, stage, bars;
   uint64_t* bar;
-  float* stats;   // kStages x (BC times -lse2, BC times -delta) of the walked rows
+  float* stats;   // S::kStages x (BC times -lse2, BC times -delta) of the walked rows
   Work* info;
   uint32_t* tmem_slot;
   int* abort_flag;
@@ -82,12 +83,12 @@ struct BwdSmem {
     own_a = smem_u32(base);
     own_b = own_a + S::kOwnBytes;
     walk_a = own_b + S::kOwnBytes;
-    walk_b = walk_a + kStages * S::kBytes;
-    uint8_t* end = base + 2 * S::kOwnBytes + 2 * kStages * S::kBytes;
-    stage = walk_b + kStages * S::kBytes;
-    end += S::kGroups * 4 * kStageBytes;
+    walk_b = walk_a + S::kStages * S::kBytes;
+    uint8_t* end = base + 2 * S::kOwnBytes + 2 * S::kStages * S::kBytes;
+    stage = walk_b + S::kStages * S::kBytes;
+    end += S::kGroups * 4 * kStageBytes<32>;
     stats = reinterpret_cast<float*>(end);
-    bar = reinterpret_cast<uint64_t*>(end + kStages * BC * 8);
+    bar = reinterpret_cast<uint64_t*>(end + S::kStages * BC * 8);
     bars = smem_u32(bar);
     info = reinterpret_cast<Work*>(bar + S::kBars);
     tmem_slot = reinterpret_cast<uint32_t*>(info + kRing);
@@ -96,13 +97,15 @@ struct BwdSmem {
   __device__ __forceinline__ uint32_t own_full() const { return bars; }
   __device__ __forceinline__ uint32_t own_empty() const { return bars + 8; }
   __device__ __forceinline__ uint32_t walk_full(int s) const { return bars + 16 + 8 * s; }
-  __device__ __forceinline__ uint32_t walk_empty(int s) const { return bars + 16 + 8 * (kStages + s); }
-  __device__ __forceinline__ uint32_t s_full() const { return walk_full(2 * kStages); }
-  __device__ __forceinline__ uint32_t dp_full() const { return s_full() + 8; }
-  __device__ __forceinline__ uint32_t p_full() const { return s_full() + 16; }   // P written (dkv), S read (dq)
-  __device__ __forceinline__ uint32_t ds_full() const { return s_full() + 24; }
-  __device__ __forceinline__ uint32_t sum_full() const { return s_full() + 32; }
-  __device__ __forceinline__ uint32_t info_full(int r) const { return s_full() + 40 + 8 * r; }
+  __device__ __forceinline__ uint32_t walk_empty(int s) const { return walk_full(S::kStages + s); }
+  __device__ __forceinline__ uint32_t s_full(int b) const { return walk_full(2 * S::kStages + b); }
+  __device__ __forceinline__ uint32_t dp_full() const { return s_full(S::kSBufs); }
+  // one for each buffer of S: with S made ahead, a warp with nothing to do in tile
+  // i may be at tile i + 1 before the others have arrived for tile i
+  __device__ __forceinline__ uint32_t p_full(int b) const { return dp_full() + 8 + 8 * b; }
+  __device__ __forceinline__ uint32_t ds_full() const { return p_full(S::kSBufs); }
+  __device__ __forceinline__ uint32_t sum_full() const { return ds_full() + 8; }
+  __device__ __forceinline__ uint32_t info_full(int r) const { return ds_full() + 16 + 8 * r; }
   __device__ __forceinline__ uint32_t info_empty(int r) const { return info_full(kRing + r); }
   __device__ __forceinline__ uint32_t done() const { return info_full(2 * kRing); }
   __device__ __forceinline__ uint32_t rest_full() const { return done() + 8; }
@@ -162,8 +165,8 @@ __device__ void bwd_loader(const AttnParams& p, const BwdSmem<S, BC>& sm, const 
     for (int h = 0; ok && h < g.heads; ++h) {
       const int head = kDkv ? w.head * group + h : w.head / group;
       for (int j = 0; j < g.steps; ++j) {
-        const int s = step % kStages, from = g.begin + j * BC;
-        if (!(ok = mbar_wait_inl_a(sm.walk_empty(s), ((step / kStages) & 1) ^ 1, sm.abort_flag, p.status))) break;
+        const int s = step % S::kStages, from = g.begin + j * BC;
+        if (!(ok = mbar_wait_inl_a(sm.walk_empty(s), ((step / S::kStages) & 1) ^ 1, sm.abort_flag, p.status))) break;
         const int boxes = (min(BC, g.end - from) + kBoxRows - 1) / kBoxRows;
         mbar_arrive_expect_tx_a(sm.walk_full(s), 2 * boxes * S::kPanels * (kBoxRows * 128));
         load(sm.walk_a + s * S::kBytes, S::kPanel, &m.walk_a, sm.walk_full(s), head, w.start + from, boxes);
@@ -174,8 +177,8 @@ __device__ void bwd_loader(const AttnParams& p, const BwdSmem<S, BC>& sm, const 
   }
   if (!ok) {  // after an abort: wait (bounded) for the copies in flight
     if (item > 0) mbar_wait_drain(sm.at(sm.own_full()), (item - 1) & 1, p.status);
-    for (uint32_t f = step > kStages ? step - kStages : 0; f < step; ++f)
-      mbar_wait_drain(sm.at(sm.walk_full(f % kStages)), (f / kStages) & 1, p.status);
+    for (uint32_t f = step > S::kStages ? step - S::kStages : 0; f < step; ++f)
+      mbar_wait_drain(sm.at(sm.walk_full(f % S::kStages)), (f / S::kStages) & 1, p.status);
   }
 }
 
@@ -198,14 +201,14 @@ __device__ void bwd_stats(const AttnParams& p, const BwdSmem<S, BC>& sm) {
     for (int h = 0; h < g.heads; ++h) {
       const float2* row = src + static_cast<int64_t>(w.head * group + h) * p.T + w.start;
       for (int j = 0; j < g.steps; ++j, ++step) {
-        const int s = step % kStages, from = g.begin + j * BC;
+        const int s = step % S::kStages, from = g.begin + j * BC;
         float2 v[BC / 32];
 #pragma unroll
         for (int x = 0; x < BC / 32; ++x) {
           const int i = from + x * 32 + lane;
           v[x] = i < g.end ? row[i] : make_float2(-INFINITY, 0.f);
         }
-        if (!mbar_wait_warp(sm.walk_empty(s), ((step / kStages) & 1) ^ 1, sm.abort_flag, p.status))
+        if (!mbar_wait_warp(sm.walk_empty(s), ((step / S::kStages) & 1) ^ 1, sm.abort_flag, p.status))
           return;
 #pragma unroll
         for (int x = 0; x < BC / 32; ++x) {
@@ -260,9 +263,9 @@ __device__ void bwd_products(const AttnParams& p, const BwdSmem<S, BC>& sm, uint
     // Waits for walked tile step + i, zeroes the rows behind its last one (up to
     // a multiple of 16): their weights are 0, and 0 * NaN would reach the sums.
     const auto ready = [&](int i, int& cols) -> bool {
-      const int s = (step + i) % kStages, used = min(BC, g.end - g.begin - at * BC);
+      const int s = (step + i) % S::kStages, used = min(BC, g.end - g.begin - at * BC);
       if (++at == g.steps) at = 0;
-      if (!wait(sm.walk_full(s), (step + i) / kStages)) return false;
+      if (!wait(sm.walk_full(s), (step + i) / S::kStages)) return false;
       cols = (used + 15) & ~15;
       if (used != cols) {
         const uint32_t vec = (cols - used) * 8;
@@ -276,25 +279,26 @@ __device__ void bwd_products(const AttnParams& p, const BwdSmem<S, BC>& sm, uint
       }
       return true;
     };
-    int cols = 0, next = 0;
-    ok = wait(sm.own_full(), item) && ready(0, cols);
-    if (!ok) break;
-    tc_fence_after();
-    score(0, sm.own_a, sm.walk_a + step % kStages * S::kBytes, cols);
-    umma_commit_el(sm.s_full());
-    score(S::kDp, sm.own_b, sm.walk_b + step % kStages * S::kBytes, cols);
-    umma_commit_el(sm.dp_full());
-    for (int i = 0; i < total; ++i) {
-      const uint32_t u = step + i, s = u % kStages, s1 = (u + 1) % kStages;
-      if (!(ok = wait(sm.p_full(), u))) break;
+    // cols: columns of tiles i, i + 1 and i + 2. S runs kSBufs tiles ahead of P.
+    int cols = 0, next = 0, after = 0;
+    const auto make_s = [&](int i, int& c) -> bool {
+      if (!ready(i, c)) return false;
       tc_fence_after();
-      add(S::kSum0, 0, (kDkv ? sm.walk_b : sm.walk_a) + s * S::kBytes, cols, i == 0);
-      if (i + 1 < total) {
-        if (!(ok = ready(i + 1, next))) break;
-        tc_fence_after();
-        score(0, sm.own_a, sm.walk_a + s1 * S::kBytes, next);
-        umma_commit_el(sm.s_full());
-      }
+      score((step + i) % S::kSBufs * BC, sm.own_a, sm.walk_a + (step + i) % S::kStages * S::kBytes, c);
+      umma_commit_el(sm.s_full((step + i) % S::kSBufs));
+      return true;
+    };
+    ok = wait(sm.own_full(), item) && make_s(0, cols);
+    if (!ok) break;
+    score(S::kDp, sm.own_b, sm.walk_b + step % S::kStages * S::kBytes, cols);
+    umma_commit_el(sm.dp_full());
+    if (S::kSBufs == 2 && total > 1 && !(ok = make_s(1, next))) break;
+    for (int i = 0; i < total; ++i) {
+      const uint32_t u = step + i, s = u % S::kStages, s1 = (u + 1) % S::kStages;
+      if (!(ok = wait(sm.p_full(u % S::kSBufs), u / S::kSBufs))) break;
+      tc_fence_after();
+      add(S::kSum0, u % S::kSBufs * BC, (kDkv ? sm.walk_b : sm.walk_a) + s * S::kBytes, cols, i == 0);
+      if (S::kSBufs == 1 && i + 1 < total && !(ok = make_s(i + 1, next))) break;
       if (!(ok = wait(sm.ds_full(), u))) break;
       tc_fence_after();
       add(S::kSum1, S::kDp, sm.walk_a + s * S::kBytes, cols, i == 0);
@@ -304,7 +308,9 @@ __device__ void bwd_products(const AttnParams& p, const BwdSmem<S, BC>& sm, uint
         umma_commit_el(sm.dp_full());
         if (i + 2 == total) umma_commit_el(sm.own_empty());
       }
+      if (S::kSBufs == 2 && i + 2 < total && !(ok = make_s(i + 2, after))) break;
       cols = next;
+      next = after;
     }
     if (!ok) break;
     if (total == 1) umma_commit_el(sm.own_empty());
@@ -340,7 +346,7 @@ __device__ __forceinline__ void store_sums(uint32_t col, uint32_t col2, uint32_t
       }
     }
   }
-  store_rows32(stage, y, dst, stride, rows, first, d);
+  store_rows<32>(stage, y, dst, stride, rows, first, d);
 }
 __device__ __forceinline__ uint4* row_of(const HeadsView& v, int64_t token, int head) {
   return reinterpret_cast<uint4*>(static_cast<uint16_t*>(v.data) + token * v.token_stride + head * v.head_stride);
@@ -518,18 +524,19 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
       for (int j = 0; j < g.steps; ++j, ++step) {
         const int from = g.begin + j * BC + wg * 64, used = min(64, g.end - from);  // this warpgroup's columns
         const bool edge = from < clear || g.begin + (j + 1) * BC > clear_end;
-        const float* nl = sm.stats + (step % kStages) * 2 * BC + wg * 64;
+        const float* nl = sm.stats + (step % S::kStages) * 2 * BC + wg * 64;
         const float far = static_cast<float>(mine - from);
         float e[64], bend[kCap && !kDkv ? 64 : 1];
-        if (!wait(sm.s_full(), step)) return;
+        const uint32_t s_now = s_col + step % S::kSBufs * BC;
+        if (!wait(sm.s_full(step % S::kSBufs), step / S::kSBufs)) return;
         // the statistics came with the walked tile, whose products have been made from it
-        if (kDkv && !wait(sm.walk_full(step % kStages), step / kStages)) return;
+        if (kDkv && !wait(sm.walk_full(step % S::kStages), step / S::kStages)) return;
         tc_fence_after();
         if (used > 0)
-          make_weights<kDkv, kBf16, kCap, kBias>(s_col, k, nl, own_nl, slope2, far, edge, used, lo - from, hi - from, e, bend);
+          make_weights<kDkv, kBf16, kCap, kBias>(s_now, k, nl, own_nl, slope2, far, edge, used, lo - from, hi - from, e, bend);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_a(sm.p_full());
+        if (lane == 0) mbar_arrive_a(sm.p_full(step % S::kSBufs));
         if (!wait(sm.dp_full(), step)) return;
         tc_fence_after();
         if (used > 0) make_ds<kDkv, kBf16, kCap>(dp_col, nl + BC, own_nd, edge, used, e, bend, rest);
@@ -537,7 +544,7 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
         __syncwarp();
         if (lane == 0) {
           mbar_arrive_a(sm.ds_full());
-          if constexpr (kDkv) mbar_arrive_a(sm.walk_empty(step % kStages));  // the statistics have been read
+          if constexpr (kDkv) mbar_arrive_a(sm.walk_empty(step % S::kStages));  // the statistics have been read
         }
       }
     }
@@ -565,7 +572,7 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
     }
     const int row32 = w.row0 + static_cast<int>(threadIdx.x & 96), rows = w.len - row32;  // this warp's rows
     const int64_t token = w.start + static_cast<int64_t>(row32);
-    const uint32_t stage = sm.stage + (threadIdx.x >> 5) * kStageBytes;
+    const uint32_t stage = sm.stage + (threadIdx.x >> 5) * kStageBytes<32>;
     const auto base = [&](const HeadsView& v) {
       return static_cast<uint16_t*>(v.data) + token * v.token_stride + w.head * v.head_stride;
     };
@@ -601,13 +608,15 @@ __global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH,
   if (threadIdx.x == 0) {
     mbar_init(sm.at(sm.own_full()), 1);
     mbar_init(sm.at(sm.own_empty()), 1);
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < S::kStages; ++s) {
       mbar_init(sm.at(sm.walk_full(s)), kDkv ? 2 : 1);                // the loader, and the statistics' warp
       mbar_init(sm.at(sm.walk_empty(s)), kDkv ? 1 + kMathWarps : 1);  // the products, and the statistics' readers
     }
-    mbar_init(sm.at(sm.s_full()), 1);
+    for (int b = 0; b < S::kSBufs; ++b) {
+      mbar_init(sm.at(sm.s_full(b)), 1);
+      mbar_init(sm.at(sm.p_full(b)), kMathWarps);
+    }
     mbar_init(sm.at(sm.dp_full()), 1);
-    mbar_init(sm.at(sm.p_full()), kMathWarps);
     mbar_init(sm.at(sm.ds_full()), kMathWarps);
     mbar_init(sm.at(sm.sum_full()), 1);
     for (int r = 0; r < kRing; ++r) {

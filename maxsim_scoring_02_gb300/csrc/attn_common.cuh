@@ -247,30 +247,37 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-// A warp's 32 rows of 32 columns of 16-bit values (16 words a lane, one row
-// each) to memory. Written as they are, each store would touch 32 lines, 16
-// bytes of each; through 2.5 KB of shared memory (rows 80 bytes apart: no bank
-// conflicts) it touches 8, 64 bytes of each. base: the first row's head.
-constexpr uint32_t kStageBytes = 32 * 80;
-__device__ __forceinline__ void store_rows32(uint32_t stage, const uint32_t (&v)[16], uint16_t* base, int64_t stride,
-                                             int rows, int col0, int d) {
+// A warp's 32 rows of kCols columns of 16-bit values (kCols / 2 words a lane,
+// one row each) to memory. Written as they are, each store would touch 32 lines,
+// 16 bytes of each; through shared memory it touches a few, kCols * 2 bytes of
+// each. Rows lie 80 bytes apart, or 128 with their 16-byte parts exchanged by
+// the row's number: no bank conflicts either way. base: the first row's head.
+template <int kCols>
+constexpr uint32_t kStageBytes = 32 * (kCols == 32 ? 80 : 128);
+template <int kCols>
+__device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t (&v)[kCols / 2], uint16_t* base,
+                                           int64_t stride, int rows, int col0, int d) {
+  constexpr int kParts = kCols / 8, kPitch = kCols == 32 ? 80 : 128;
   const int lane = threadIdx.x & 31;
+  const auto at = [&](int r, int part) -> uint32_t { return stage + r * kPitch + (kCols == 32 ? part : part ^ (r & 7)) * 16; };
 #pragma unroll
-  for (int x = 0; x < 4; ++x)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 80 + x * 16), "r"(v[x * 4]),
-                 "r"(v[x * 4 + 1]), "r"(v[x * 4 + 2]), "r"(v[x * 4 + 3])
+  for (int x = 0; x < kParts; ++x)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(lane, x)), "r"(v[x * 4]), "r"(v[x * 4 + 1]),
+                 "r"(v[x * 4 + 2]), "r"(v[x * 4 + 3])
                  : "memory");
   __syncwarp();
-  const int col = col0 + (lane & 3) * 8;
+  const int part = lane % kParts, col = col0 + part * 8;
+  uint4 y[kParts];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = i * 8 + (lane >> 2);
-    uint4 y;
+  for (int i = 0; i < kParts; ++i)
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
-                 : "r"(stage + r * 80 + (lane & 3) * 16)
+                 : "=r"(y[i].x), "=r"(y[i].y), "=r"(y[i].z), "=r"(y[i].w)
+                 : "r"(at(i * (32 / kParts) + lane / kParts, part))
                  : "memory");
-    if (r < rows && col < d) *reinterpret_cast<uint4*>(base + r * stride + col) = y;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    const int r = i * (32 / kParts) + lane / kParts;
+    if (r < rows && col < d) *reinterpret_cast<uint4*>(base + r * stride + col) = y[i];
   }
   __syncwarp();
 }

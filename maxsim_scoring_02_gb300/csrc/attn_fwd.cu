@@ -37,6 +37,7 @@ struct FwdShape {
   static constexpr uint32_t kPanelBytes = kTile * 128;
   static constexpr uint32_t kTileBytes = kPanels * kPanelBytes;
   static constexpr int kStages = NQ == 1 ? (DH == 64 ? 2 : 1) : (DH == 64 ? 4 : 2);
+  static constexpr int kStoreCols = NQ == 1 ? 32 : 64;  // of an output row at a time (two blocks an SM leave no more room)
   static constexpr int kQStages = NQ == 1 && DH == 64 ? 2 : 1;
   static constexpr int kThreads = NQ * 128 + 128;  // softmax warpgroups; loader, issuer, planner and an idle warp
   static constexpr int kBlocks = NQ == 1 ? 2 : 1;  // resident on an SM
@@ -50,7 +51,7 @@ struct FwdShape {
   // barriers: k_full, k_empty, v_full, v_empty, s_full, p_full, o_full, info_full, info_empty, done, q_full, q_empty
   static constexpr int kBars = 4 * kStages + 3 * NQ + 2 * kRing + 1 + 2 * kQStages;
   static constexpr uint32_t kTiles = NQ * kQStages + 2 * kStages;
-  static constexpr uint32_t kSmem = 1024 + kTiles * kTileBytes + NQ * 4 * kStageBytes + 8 * kBars + kRing * sizeof(Work) + 16;
+  static constexpr uint32_t kSmem = 1024 + kTiles * kTileBytes + NQ * 4 * kStageBytes<kStoreCols> + 8 * kBars + kRing * sizeof(Work) + 16;
 };
 
 template <int DH, int NQ>
@@ -67,7 +68,7 @@ struct FwdSmem {
     k = q + NQ * S::kQStages * S::kTileBytes;
     v = k + S::kStages * S::kTileBytes;
     stage = q + S::kTiles * S::kTileBytes;
-    bar = reinterpret_cast<uint64_t*>(base + S::kTiles * S::kTileBytes + NQ * 4 * kStageBytes);
+    bar = reinterpret_cast<uint64_t*>(base + S::kTiles * S::kTileBytes + NQ * 4 * kStageBytes<S::kStoreCols>);
     bars = smem_u32(bar);
     info = reinterpret_cast<Work*>(bar + S::kBars);
     tmem_slot = reinterpret_cast<uint32_t*>(info + kRing);
@@ -455,17 +456,21 @@ __device__ void fwd_softmax(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint
     const int row32 = first + static_cast<int>(threadIdx.x & 96);  // this warp's first row
     uint16_t* dst = static_cast<uint16_t*>(p.out.data) + (w.start + static_cast<int64_t>(row32)) * p.out.token_stride +
                     w.head * p.out.head_stride;
+    constexpr int kCols = S::kStoreCols;
 #pragma unroll
-    for (int q = 0; q < DH / 32; ++q) {
-      uint32_t o[32], y[16] = {};
+    for (int q = 0; q < DH / kCols; ++q) {
+      uint32_t o[2][32], y[kCols / 2] = {};
       if (nk > 0) {
-        tmem_ld_32x32b_x32_issue(o_col + q * 32, o);
-        tmem_wait_ld_regs(o);
+        tmem_ld_32x32b_x32_issue(o_col + q * kCols, o[0]);
+        if constexpr (kCols == 64) tmem_ld_32x32b_x32_issue(o_col + q * kCols + 32, o[1]);
+        tmem_wait_ld_regs(o[0]);
+        if constexpr (kCols == 64) reg_order(o[1]);
 #pragma unroll
-        for (int x = 0; x < 16; ++x)
-          y[x] = pack2<kBf16>(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
+        for (int x = 0; x < kCols / 2; ++x)
+          y[x] = pack2<kBf16>(__uint_as_float(o[x / 16][2 * x % 32]) * inv, __uint_as_float(o[x / 16][2 * x % 32 + 1]) * inv);
       }
-      store_rows32(sm.stage + (threadIdx.x >> 5) * kStageBytes, y, dst, p.out.token_stride, w.len - row32, q * 32, p.d);
+      store_rows<kCols>(sm.stage + (threadIdx.x >> 5) * kStageBytes<kCols>, y, dst, p.out.token_stride, w.len - row32,
+                        q * kCols, p.d);
     }
     if (p.lse && row < w.len)
       p.lse[static_cast<int64_t>(w.head) * p.T + token] = some ? (st.m * k.c + log2f(st.sum)) * kLn2 : -INFINITY;

@@ -3,7 +3,7 @@
 //   norm = sqrt(sum over all tensors of g^2);  g *= min(1, max_norm / (norm + 1e-6))
 //
 // Two kernels read the tensors' table from their launch parameters. The first
-// sums squares: every block walks over 64 KB chunks, a thread adds its own
+// sums squares: every block walks over 32 KB chunks, a thread adds its own
 // squares in fp32 within a chunk and in fp64 across chunks, and each block
 // writes one partial. Squares that leave fp32's range (a chunk whose sum is
 // not finite, or tiny with something nonzero in it) are added again in fp64.
@@ -24,9 +24,9 @@ namespace msim {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVecs = 16;                                // 16-byte vectors of a thread in a chunk
-constexpr int kChunkBytes = kThreads * kVecs * 16;       // 64 KB
-constexpr int kBlocksPerSm = 4;
+constexpr int kVecs = 8;                                 // 16-byte vectors of a thread in a chunk
+constexpr int kChunkBytes = kThreads * kVecs * 16;       // 32 KB
+constexpr int kBlocksPerSm = 6;
 constexpr int kMaxClipBlocks = 1024;                     // partials of one launch
 
 template <int N>
@@ -101,7 +101,7 @@ __device__ __forceinline__ double chunk_squares(const T* g, const Chunk& k) {
   for (int u = 0; u < kVecs; ++u) {
     const int64_t i = u * kThreads + threadIdx.x;
     if (i < vecs) {
-      const uint4 w = v[i];
+      const uint4 w = __ldg(v + i);
       any |= w.x | w.y | w.z | w.w;
       const T* e = reinterpret_cast<const T*>(&w);
 #pragma unroll
@@ -159,11 +159,11 @@ __device__ __forceinline__ void scale_chunk(const T* g, T* o, const Chunk& k, fl
     for (int u = 0; u < kVecs; ++u) {
       const int64_t i = u * kThreads + threadIdx.x;
       if (i < vecs) {
-        uint4 w = v[i];
+        uint4 w = __ldcs(v + i);
         T* e = reinterpret_cast<T*>(&w);
 #pragma unroll
         for (int x = 0; x < E; ++x) e[x] = static_cast<T>(up(e[x]) * f);
-        d[i] = w;
+        __stcs(d + i, w);
       }
     }
     for (int64_t i = k.a + threadIdx.x; i < k.body; i += kThreads) o[i] = static_cast<T>(up(g[i]) * f);

@@ -37,7 +37,7 @@ struct RotaryParams {
   unsigned* status;
   int64_t B;
   int T, heads, d, r;
-  int per_token;      // threads of one token: V pairs each, then V copied elements each
+  int per_token;      // threads of one token: V pairs each, then up to 2 V copied elements each
   int heads_each;     // heads walked by one thread
   float amplitude, sign;
 };
@@ -70,7 +70,7 @@ __device__ __forceinline__ int position_of(const RotaryParams& p, int t) {
 
 // V: pairs of a thread. Half layout: two vectors of V elements r/2 apart.
 // Interleaved: two neighbouring vectors that hold V pairs.
-template <typename T, int V, bool kInterleaved>
+template <typename T, int V, bool kInterleaved, bool kCopies>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) {
   const int64_t id = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
   const int t = static_cast<int>(id / p.per_token), part = static_cast<int>(id % p.per_token);
@@ -80,26 +80,31 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) 
   T* dst = static_cast<T*>(p.out) + t * p.o_token;
   using W = Vec<T, V>;
   const int rotating = p.r / 2 / V;
-  if (part >= rotating) {  // elements that are only copied
-    const int c = p.r + (part - rotating) * V;
-    for (int h = h0; h < h1; ++h)
-      *reinterpret_cast<W*>(dst + h * p.o_head + c) = *reinterpret_cast<const W*>(src + h * p.x_head + c);
-    return;
-  }
-  const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(position_of(p, t)));
+  const bool turns = !kCopies || part < rotating;  // else two vectors that are only copied
   float cs[V], sn[V];
+  if (turns) {
+    const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(position_of(p, t)));
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-    const int turn = static_cast<int>(static_cast<uint32_t>((pos * p.freq[part * V + k]) >> 32));
-    sincospif(static_cast<float>(turn) * (1.f / 2147483648.f), &sn[k], &cs[k]);
-    cs[k] *= p.amplitude;
-    sn[k] *= p.amplitude * p.sign;
+    for (int k = 0; k < V; ++k) {
+      const int turn = static_cast<int>(static_cast<uint32_t>((pos * p.freq[part * V + k]) >> 32));
+      sincospif(static_cast<float>(turn) * (1.f / 2147483648.f), &sn[k], &cs[k]);
+      cs[k] *= p.amplitude;
+      sn[k] *= p.amplitude * p.sign;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) cs[k] = 1.f, sn[k] = 0.f;
   }
-  const int c0 = kInterleaved ? part * 2 * V : part * V, c1 = kInterleaved ? c0 + V : c0 + p.r / 2;
+  const int c0 = !turns ? p.r + (part - rotating) * 2 * V : kInterleaved ? part * 2 * V : part * V;
+  const int c1 = !turns || kInterleaved ? c0 + V : c0 + p.r / 2;
+  const bool second = turns || c1 < p.d;  // the copied vectors may be odd in number
+  // Rotating and copying threads of a warp run the same loop: two vectors a
+  // head each, so loads and stores of both are in flight together.
 #pragma unroll 4
   for (int h = h0; h < h1; ++h) {
     W a = *reinterpret_cast<const W*>(src + h * p.x_head + c0);
-    W b = *reinterpret_cast<const W*>(src + h * p.x_head + c1);
+    W b = *reinterpret_cast<const W*>(src + h * p.x_head + (second ? c1 : c0));
+    const W a0 = a, b0 = b;
     if constexpr (kInterleaved) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {  // pair k sits at elements 2k, 2k + 1 of a and b
@@ -117,22 +122,24 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) 
         b.e[k] = down<T>(x2 * cs[k] + x1 * sn[k]);
       }
     }
-    *reinterpret_cast<W*>(dst + h * p.o_head + c0) = a;
-    *reinterpret_cast<W*>(dst + h * p.o_head + c1) = b;
+    *reinterpret_cast<W*>(dst + h * p.o_head + c0) = turns ? a : a0;
+    if (second) *reinterpret_cast<W*>(dst + h * p.o_head + c1) = turns ? b : b0;
   }
 }
 
 template <typename T, int V>
 void launch_v(RotaryParams& p, int interleaved, int copied, int sm_count, cudaStream_t stream) {
-  p.per_token = p.r / 2 / V + copied / V;
+  p.per_token = p.r / 2 / V + (copied / V + 1) / 2;
   const int64_t blocks = (static_cast<int64_t>(p.T) * p.per_token + kThreads - 1) / kThreads;
   // few tokens: the heads are split over blocks until every SM has a few
   const int64_t want = (4 * static_cast<int64_t>(sm_count) + blocks - 1) / blocks;
   const int parts = static_cast<int>(want < p.heads ? want : p.heads);
   p.heads_each = (p.heads + parts - 1) / parts;
   const dim3 grid(static_cast<unsigned>(blocks), (p.heads + p.heads_each - 1) / p.heads_each);
-  if (interleaved) rotary_kernel<T, V, true><<<grid, kThreads, 0, stream>>>(p);
-  else rotary_kernel<T, V, false><<<grid, kThreads, 0, stream>>>(p);
+  if (interleaved && copied) rotary_kernel<T, V, true, true><<<grid, kThreads, 0, stream>>>(p);
+  else if (interleaved) rotary_kernel<T, V, true, false><<<grid, kThreads, 0, stream>>>(p);
+  else if (copied) rotary_kernel<T, V, false, true><<<grid, kThreads, 0, stream>>>(p);
+  else rotary_kernel<T, V, false, false><<<grid, kThreads, 0, stream>>>(p);
 }
 
 }  // namespace
