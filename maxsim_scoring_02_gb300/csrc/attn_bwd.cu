@@ -64,7 +64,7 @@ struct BwdShape {
   static constexpr uint32_t kDp = kSBufs * BC, kSum0 = kDp + BC, kSum1 = kSum0 + DH, kNeed = kSum1 + DH;
   static constexpr uint32_t kTmemCols = kNeed <= 256 ? 256 : 512;
   static constexpr int kBars = 2 + 2 * kStages + 3 + 2 * kSBufs + 2 * kRing + 2;
-  static constexpr uint32_t kSmem = 1024 + 2 * kOwnBytes + 2 * kStages * kBytes + kGroups * 4 * kStageBytes<32> + 8 * kBars +
+  static constexpr uint32_t kSmem = 2 * kOwnBytes + 2 * kStages * kBytes + kGroups * 4 * kStageBytes<64> + 8 * kBars +
                                     kStages * BC * 8 + kRing * sizeof(Work) + 16 + 16;
 };
 
@@ -79,14 +79,14 @@ struct BwdSmem {
   uint32_t* tmem_slot;
   int* abort_flag;
   __device__ __forceinline__ explicit BwdSmem(uint8_t* raw) {
-    uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint8_t* base = raw;  // on a 1024-byte boundary, as the swizzled tiles need it
     own_a = smem_u32(base);
     own_b = own_a + S::kOwnBytes;
     walk_a = own_b + S::kOwnBytes;
     walk_b = walk_a + S::kStages * S::kBytes;
     uint8_t* end = base + 2 * S::kOwnBytes + 2 * S::kStages * S::kBytes;
     stage = walk_b + S::kStages * S::kBytes;
-    end += S::kGroups * 4 * kStageBytes<32>;
+    end += S::kGroups * 4 * kStageBytes<64>;
     stats = reinterpret_cast<float*>(end);
     bar = reinterpret_cast<uint64_t*>(end + S::kStages * BC * 8);
     bars = smem_u32(bar);
@@ -323,30 +323,32 @@ __device__ void bwd_products(const AttnParams& p, const BwdSmem<S, BC>& sm, uint
 }
 
 // ----------------------------------------------------------- arithmetic
-// 32 columns of this warp's 32 rows of fp32 sums, times f (plus others, times
+// 64 columns of this warp's 32 rows of fp32 sums, times f (plus others, times
 // f2), to memory in 16 bits.
-template <bool kBf16>
+template <bool kBf16, bool kOther>
 __device__ __forceinline__ void store_sums(uint32_t col, uint32_t col2, uint32_t stage, uint16_t* dst, int64_t stride,
                                            int rows, int first, int d, float f, float f2, bool any) {
-  uint32_t y[16] = {};
+  uint32_t y[32] = {};
   if (any) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      uint32_t o[16], o2[16];
-      tmem_ld_32x32b_x16(col + half * 16, o);
-      if (col2) tmem_ld_32x32b_x16(col2 + half * 16, o2);
+      uint32_t o[32], o2[32];
+      tmem_ld_32x32b_x32_issue(col + half * 32, o);
+      if constexpr (kOther) tmem_ld_32x32b_x32_issue(col2 + half * 32, o2);
+      tmem_wait_ld_regs(o);
+      if constexpr (kOther) reg_order(o2);
 #pragma unroll
-      for (int x = 0; x < 16; x += 2) {
+      for (int x = 0; x < 32; x += 2) {
         float a = __uint_as_float(o[x]) * f, b = __uint_as_float(o[x + 1]) * f;
-        if (col2) {
+        if constexpr (kOther) {
           a = fmaf(__uint_as_float(o2[x]), f2, a);
           b = fmaf(__uint_as_float(o2[x + 1]), f2, b);
         }
-        y[half * 8 + x / 2] = pack2<kBf16>(a, b);
+        y[half * 16 + x / 2] = pack2<kBf16>(a, b);
       }
     }
   }
-  store_rows<32>(stage, y, dst, stride, rows, first, d);
+  store_rows<64>(stage, y, dst, stride, rows, first, d);
 }
 __device__ __forceinline__ uint4* row_of(const HeadsView& v, int64_t token, int head) {
   return reinterpret_cast<uint4*>(static_cast<uint16_t*>(v.data) + token * v.token_stride + head * v.head_stride);
@@ -572,26 +574,26 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
     }
     const int row32 = w.row0 + static_cast<int>(threadIdx.x & 96), rows = w.len - row32;  // this warp's rows
     const int64_t token = w.start + static_cast<int64_t>(row32);
-    const uint32_t stage = sm.stage + (threadIdx.x >> 5) * kStageBytes<32>;
+    const uint32_t stage = sm.stage + (threadIdx.x >> 5) * kStageBytes<64>;
     const auto base = [&](const HeadsView& v) {
       return static_cast<uint16_t*>(v.data) + token * v.token_stride + w.head * v.head_stride;
     };
-    constexpr int kChunks = DH / 32;
+    constexpr int kChunks = DH / 64;
     const uint32_t sum0 = tmem + lanes + S::kSum0, sum1 = tmem + lanes + S::kSum1;
     if constexpr (kDkv) {
 #pragma unroll
       for (int q = 0; q < kChunks; ++q) {  // two warpgroups: one writes dV, one dK
         if (S::kGroups == 1 || wg == 0)
-          store_sums<kBf16>(sum0 + q * 32, 0, stage, base(p.dv), p.dv.token_stride, rows, q * 32, p.d, 1.f, 0.f, any);
+          store_sums<kBf16, false>(sum0 + q * 64, 0, stage, base(p.dv), p.dv.token_stride, rows, q * 64, p.d, 1.f, 0.f, any);
         if (S::kGroups == 1 || wg == 1)
-          store_sums<kBf16>(sum1 + q * 32, 0, stage, base(p.dk), p.dk.token_stride, rows, q * 32, p.d, p.scale, 0.f, any);
+          store_sums<kBf16, false>(sum1 + q * 64, 0, stage, base(p.dk), p.dk.token_stride, rows, q * 64, p.d, p.scale, 0.f, any);
       }
     } else {
 #pragma unroll
       for (int q = 0; q < kChunks; ++q)
-        if (S::kGroups == 1 || q / (kChunks / 2) == wg)
-          store_sums<kBf16>(sum1 + q * 32, sum0 + q * 32, stage, base(p.dq), p.dq.token_stride, rows, q * 32, p.d,
-                            p.scale, -off * p.scale, any);
+        if (S::kGroups == 1 || q % 2 == wg)  // (heads of 64: the second warpgroup has none)
+          store_sums<kBf16, true>(sum1 + q * 64, sum0 + q * 64, stage, base(p.dq), p.dq.token_stride, rows, q * 64, p.d,
+                                  p.scale, -off * p.scale, any);
     }
     tc_fence_before();  // the next item's first products overwrite the sums after its p_full / ds_full
   }
@@ -601,7 +603,11 @@ template <int DH, int BC, bool kDkv, bool kBf16, bool kCap, bool kBias>
 __global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH, BC, kDkv>::kBlocks)
     attn_bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ AttnParams p) {
   using S = BwdShape<DH, BC, kDkv>;
-  extern __shared__ uint8_t raw[];
+  extern __shared__ __align__(1024) uint8_t raw[];
+  if (smem_u32(raw) & 1023) {  // cannot be, by the declaration; a tile copied there would fault
+    if (threadIdx.x == 0) atomicOr(p.status, kDevErrTimeout);
+    return;
+  }
   const BwdSmem<S, BC> sm(raw);
   constexpr int kMathWarps = 4 * S::kGroups;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // known to be uniform, and the roles with it
