@@ -365,7 +365,7 @@ struct MathConst {
 // looked at; one code for both, since its size counts.
 template <bool kDkv, bool kBf16, bool kCap, bool kBias>
 __device__ __forceinline__ void make_weights(uint32_t s_col, const MathConst& k, const float* nl, float own_nl,
-                                             float slope2, float far, bool edge, int used, int lo, int hi,
+                                             float slope2, float far, bool live, bool edge, int used, int lo, int hi,
                                              float (&e)[64], float (&bend)[kCap && !kDkv ? 64 : 1]) {
   uint32_t u[2][32];
   tmem_ld_32x32b_x32_issue(s_col, u[0]);
@@ -376,6 +376,7 @@ __device__ __forceinline__ void make_weights(uint32_t s_col, const MathConst& k,
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     if (q * 32 >= used) break;
+    if constexpr (kCap) tanh_group(u[q], k.in_cap, q * 32 + 32 <= used, live);
 #pragma unroll
     for (int x = 0; x < 32; x += 4) {
       float4 n;
@@ -386,9 +387,8 @@ __device__ __forceinline__ void make_weights(uint32_t s_col, const MathConst& k,
       for (int y = 0; y < 4; ++y) {
         z[y] = __uint_as_float(u[q][x + y]);
         if constexpr (kCap) {
-          const float t = fast_tanh(z[y] * k.in_cap);
-          z[y] = k.cap2 * t;
-          d[y] = fmaf(-t, t, 1.f);
+          d[y] = fmaf(-z[y], z[y], 1.f);  // z is the tangent here
+          if constexpr (kBias) z[y] *= k.cap2;
         }
         if constexpr (kBias) {
           if constexpr (!kCap) z[y] *= k.to_log2;
@@ -483,8 +483,8 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
   const int wg = threadIdx.x >> 7, lane = threadIdx.x & 31, group = p.heads / p.kv_heads;
   const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;
   const uint32_t s_col = tmem + lanes + wg * 64, dp_col = s_col + S::kDp;
-  const MathConst k = {kCap || kBias ? 1.f : p.scale * kLog2e, p.scale * kLog2e, p.cap * kLog2e,
-                       kCap ? 2.f * kLog2e * p.scale / p.cap : 0.f};
+  const MathConst k = {kBias ? 1.f : kCap ? p.cap * kLog2e : p.scale * kLog2e, p.scale * kLog2e, p.cap * kLog2e,
+                       kCap ? p.scale / p.cap : 0.f};
   uint32_t step = 0, item = 0, rows_done = 0;
   const auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
     return mbar_wait_warp(bar, ph & 1, sm.abort_flag, p.status);
@@ -535,7 +535,7 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
         if (kDkv && !wait(sm.walk_full(step % S::kStages), step / S::kStages)) return;
         tc_fence_after();
         if (used > 0)
-          make_weights<kDkv, kBf16, kCap, kBias>(s_now, k, nl, own_nl, slope2, far, edge, used, lo - from, hi - from, e, bend);
+          make_weights<kDkv, kBf16, kCap, kBias>(s_now, k, nl, own_nl, slope2, far, mine < w.len, edge, used, lo - from, hi - from, e, bend);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_a(sm.p_full(step % S::kSBufs));

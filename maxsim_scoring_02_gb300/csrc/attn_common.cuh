@@ -238,6 +238,39 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// u = tanh(k u) for 32 values of each lane. `whole`: the same for the warp, all
+// 32 are scores; `live`: this lane's are (others hold what was left there, and
+// must not decide how the rest is rounded). Through exp2 and a reciprocal a value
+// costs two of the special function unit's slots, and the softmax of capped
+// scores waits for that unit. Where no value of the warp exceeds 0.7 (scores up
+// to 0.7 cap), tanh(x) = x p(x^2) with p of degree 5, fitted to tanh on that
+// interval by least squares reweighted towards equal errors: off by 1.3e-8
+// relatively, 7e-8 in fp32 arithmetic.
+__device__ __forceinline__ void tanh_group(uint32_t (&u)[32], float k, bool whole, bool live) {
+  float top = 0.f;
+#pragma unroll
+  for (int x = 0; x < 32; x += 2) top = max3(top, fabsf(__uint_as_float(u[x])), fabsf(__uint_as_float(u[x + 1])));
+  if (__all_sync(0xffffffffu, whole && (!live || top * k <= 0.7f))) {
+    constexpr float c[6] = {1.0f, -0.3333314061164856f, 0.13328571617603302f, -0.05353494733572006f,
+                            0.02004525437951088f, -0.005105282180011272f};
+#pragma unroll
+    for (int x = 0; x < 32; x += 2) {
+      const Pair v = mul2(Pair(__uint_as_float(u[x]), __uint_as_float(u[x + 1])), Pair(k, k)), w = mul2(v, v);
+      Pair r(c[5], c[5]);
+#pragma unroll
+      for (int i = 4; i >= 0; --i) r = fma2(r, w, Pair(c[i], c[i]));
+      float a, b;
+      mul2(v, r).get(a, b);
+      u[x] = __float_as_uint(a);
+      u[x + 1] = __float_as_uint(b);
+    }
+  } else {
+    const float k2 = 2.f * 1.4426950408889634f * k;
+#pragma unroll
+    for (int x = 0; x < 32; ++x) u[x] = __float_as_uint(fast_tanh(__uint_as_float(u[x]) * k2));
+  }
+}
+
 // Two values as 16-bit ones in a word, `lo` in its low half.
 template <bool kBf16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {

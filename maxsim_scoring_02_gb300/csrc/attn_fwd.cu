@@ -266,6 +266,7 @@ __device__ void fwd_products(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uin
 // What a softmax thread keeps of its row.
 struct RowState {
   float m, sum;  // maximum in the units of the scores held, sum of the weights
+  bool live;     // a row of the document: others hold what was left in shared memory, and have no say
 };
 struct ScoreConst {
   float c, to_log2, cap2, in_cap;  // c brings held scores to log2 units
@@ -315,7 +316,7 @@ template <int DH>
 __device__ __forceinline__ void raise_max(uint32_t o_col, const ScoreConst& k, float now, bool first, RowState& st) {
   if (first) {
     st.m = now;
-  } else if (__any_sync(0xffffffffu, (now - st.m) * k.c > kRaise)) {
+  } else if (__any_sync(0xffffffffu, st.live && (now - st.m) * k.c > kRaise)) {
     const float keep = now == -INFINITY ? 1.f : fast_exp2((st.m - now) * k.c);
     st.sum *= keep;
     st.m = now;
@@ -431,7 +432,7 @@ __device__ void fwd_softmax(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint
     const int keys = tile_keys(w, p.mask, t), nk = tiles_of(keys);
     const int end = row_end(w, p.mask, min(row, w.len - 1)), all_see = row_end(w, p.mask, first);
     const float slope2 = kBias ? p.slopes[w.head] * kLog2e : 0.f;
-    RowState st = {-INFINITY, 0.f};
+    RowState st = {-INFINITY, 0.f, row < w.len};
     for (int j = 0; j < nk; ++j, ++sn) {
       if (!wait(sm.s_full(t), sn)) return;
       tc_fence_after();

@@ -239,6 +239,28 @@ def test_another_stream_and_repeats():
     assert torch.equal(o2, out) and torch.equal(l2, lse) and all(torch.equal(a, b) for a, b in zip(g2, grads))
 
 
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_what_ran_before_changes_no_bit(cap, d):
+    """Scores whose maximum grows along the keys, documents that end inside a tile:
+    neither what other calls leave on the chip nor their order shows in a result."""
+    for n in ([300, 1, 77, 513], [40, 17, 90, 9, 33, 64, 21] * 6):
+        q, k, v, dO = _inputs(sum(n), 3, 3, d, "bf16", 103)
+        q = q * 6
+        off = _offsets(n)
+
+        def run():
+            out, lse = m.maxsim_attention(q, k, v, off, cap=cap, want_lse=True)
+            return (out, lse) + tuple(m.maxsim_attention_backward(dO, q, k, v, out, lse, off, cap=cap))
+
+        first = run()
+        for seed in range(4):
+            a, b, c, e = _inputs(2000, 4, 4, 128, "bf16", 200 + seed)
+            o, l = m.maxsim_attention(a * 30, b, c, _offsets([2000]), want_lse=True)
+            m.maxsim_attention_backward(e, a * 30, b, c, o, l, _offsets([2000]))
+            assert all(torch.equal(x, y) for x, y in zip(run(), first))
+
+
 def test_capture_in_a_graph():
     n = [128, 60]
     q, k, v, _ = _inputs(188, 2, 2, 64, "fp16", 99)
