@@ -78,7 +78,8 @@ typedef enum maxsim_dtype {
  * is synchronous).
  *   flags          MAXSIM_DEBUG_STALL_FWD_LOADER: the loader role of the
  *                  tensor-core forward kernel (maxsim_score / _varlen with
- *                  bf16 or fp16 and queries below 256 tokens) issues no copy,
+ *                  bf16 or fp16 and queries below 256 tokens) and of the
+ *                  attention kernels (maxsim_attention / _backward) issues no copy,
  *                  so the kernel's other roles wait on barriers nothing will
  *                  complete; their bounded waits run out, record
  *                  MAXSIM_DEVERR_TIMEOUT and the kernel exits with no copy or
@@ -509,7 +510,8 @@ maxsim_status maxsim_attention(const maxsim_attention_spec *spec, const maxsim_h
  * scheduling. Rows that see nothing and hidden keys have gradient 0. Slopes
  * are constants.
  * Sums are fp32; p and dS are rounded to the inputs' type for their products.
- * Limits as in maxsim_attention, for dO and the gradients too. workspace: at least
+ * Limits as in maxsim_attention, for dO and the gradients too, and T * heads
+ * below 2^35. workspace: at least
  * maxsim_attention_backward_workspace_size(spec) bytes, 16-byte aligned.
  */
 size_t maxsim_attention_backward_workspace_size(const maxsim_attention_spec *spec);

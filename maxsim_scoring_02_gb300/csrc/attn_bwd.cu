@@ -140,6 +140,7 @@ struct BwdMaps {
 // ---------------------------------------------------------------- loads
 template <class S, int BC, bool kDkv>
 __device__ void bwd_loader(const AttnParams& p, const BwdSmem<S, BC>& sm, const BwdMaps& m) {
+  if (debug_faults(p.status) & kDebugStallFwdLoader) return;  // test-only switch (maxsim_debug_set_faults)
   const int group = p.heads / p.kv_heads;
   uint32_t item = 0, step = 0;
   bool ok = true;

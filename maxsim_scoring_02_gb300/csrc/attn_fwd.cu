@@ -101,6 +101,7 @@ template <int DH, int NQ>
 __device__ void fwd_loader(const AttnParams& p, const FwdSmem<DH, NQ>& sm, const CUtensorMap* mq, const CUtensorMap* mk,
                            const CUtensorMap* mv) {
   using S = FwdShape<DH, NQ>;
+  if (debug_faults(p.status) & kDebugStallFwdLoader) return;  // test-only switch (maxsim_debug_set_faults)
   const int group = p.heads / p.kv_heads;
   uint32_t item = 0, kv = 0;  // items with keys; key tiles
   bool ok = true;

@@ -289,6 +289,31 @@ def test_inconsistent_documents_are_reported_and_skipped():
     assert m.maxsim_device_status() == (0, 0)
 
 
+@pytest.mark.parametrize("d,n", [(64, [60, 20, 33]), (64, [400]), (128, [60, 20, 33]), (128, [400])])
+def test_waits_that_run_out_are_reported(d, n):
+    """The loaders bring nothing (a test-only switch): every wait gives up after
+    its bound, the call reports it, and the next one is as if nothing had been."""
+    lib = m.load_library()
+    q, k, v, dO = _inputs(sum(n), 2, 1, d, "bf16", 104)
+    off = _offsets(n)
+    out, lse = m.maxsim_attention(q, k, v, off, want_lse=True)
+    grads = m.maxsim_attention_backward(dO, q, k, v, out, lse, off)
+    torch.cuda.synchronize()
+    assert lib.maxsim_debug_set_faults(1, 50_000_000) == 0
+    try:
+        m.maxsim_attention(q, k, v, off)
+        forward = m.maxsim_device_status()
+        m.maxsim_attention_backward(dO, q, k, v, out, lse, off)
+        backward = m.maxsim_device_status()
+    finally:
+        assert lib.maxsim_debug_set_faults(0, 0) == 0
+    assert forward[0] == backward[0] == 4
+    o2, l2 = m.maxsim_attention(q, k, v, off, want_lse=True)
+    assert torch.equal(o2, out) and torch.equal(l2, lse)
+    assert all(torch.equal(a, b) for a, b in zip(m.maxsim_attention_backward(dO, q, k, v, out, lse, off), grads))
+    assert m.maxsim_device_status() == (0, 0)
+
+
 def test_nothing_to_do():
     q, k, v, dO = _inputs(0, 2, 2, 64, "bf16", 101)
     out, lse = m.maxsim_attention(q, k, v, _offsets([0, 0]), want_lse=True)
