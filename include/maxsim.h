@@ -510,8 +510,7 @@ maxsim_status maxsim_attention(const maxsim_attention_spec *spec, const maxsim_h
  * scheduling. Rows that see nothing and hidden keys have gradient 0. Slopes
  * are constants.
  * Sums are fp32; p and dS are rounded to the inputs' type for their products.
- * Limits as in maxsim_attention, for dO and the gradients too, and T * heads
- * below 2^35. workspace: at least
+ * Limits as in maxsim_attention, for dO and the gradients too. workspace: at least
  * maxsim_attention_backward_workspace_size(spec) bytes, 16-byte aligned.
  */
 size_t maxsim_attention_backward_workspace_size(const maxsim_attention_spec *spec);

@@ -664,38 +664,44 @@ __global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH,
 }
 
 // Minus lse in log2 units, and minus <dO, out>, of every row and head,
-// [heads][T]. A row is read by L lanes of 16 bytes each.
+// [heads][T]. A row is read by L lanes of 16 bytes each; a block takes kTokens
+// tokens with all their heads, which lie together in memory. Bound by HBM
+// (dO and out once).
+constexpr int kTokens = 8;
 template <bool kBf16>
-__global__ void __launch_bounds__(256) attn_stats_kernel(const AttnParams p, int L) {
-  const int64_t id = blockIdx.x * int64_t(256) + threadIdx.x;
-  const int64_t row = id / L;  // heads run fastest, as in memory
-  const int part = static_cast<int>(id % L);
-  check_docs(p, id, gridDim.x * int64_t(256));
-  const bool live = row < static_cast<int64_t>(p.T) * p.heads;
-  const int64_t t = live ? row / p.heads : 0;
-  const int h = live ? static_cast<int>(row % p.heads) : 0;
-  float s = 0.f;
-  if (live && part * 8 < p.d) {
-    const uint4 a = row_of(p.dO, t, h)[part], b = row_of(p.out, t, h)[part];
-    const uint32_t *x = &a.x, *y = &b.x;
+__global__ void __launch_bounds__(256) attn_stats_kernel(const AttnParams p, int log_l) {
+  check_docs(p, blockIdx.x * int64_t(256) + threadIdx.x, gridDim.x * int64_t(256));
+  const int64_t t0 = blockIdx.x * int64_t(kTokens);
+  const unsigned heads = p.heads, rows = static_cast<unsigned>(min(static_cast<int64_t>(kTokens), p.T - t0)) * heads;
+  const int part = threadIdx.x & ((1 << log_l) - 1);
+#pragma unroll 2
+  for (unsigned r0 = 0; r0 < rows; r0 += 256u >> log_l) {
+    const unsigned r = r0 + (threadIdx.x >> log_l);
+    const int64_t t = t0 + r / heads;
+    const int h = static_cast<int>(r % heads);
+    float s = 0.f;
+    if (r < rows && part * 8 < p.d) {
+      const uint4 a = row_of(p.dO, t, h)[part], b = row_of(p.out, t, h)[part];
+      const uint32_t *x = &a.x, *y = &b.x;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float2 f, g;
-      if constexpr (kBf16) {
-        f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(x + k));
-        g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(y + k));
-      } else {
-        f = __half22float2(*reinterpret_cast<const __half2*>(x + k));
-        g = __half22float2(*reinterpret_cast<const __half2*>(y + k));
+      for (int k = 0; k < 4; ++k) {
+        float2 f, g;
+        if constexpr (kBf16) {
+          f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(x + k));
+          g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(y + k));
+        } else {
+          f = __half22float2(*reinterpret_cast<const __half2*>(x + k));
+          g = __half22float2(*reinterpret_cast<const __half2*>(y + k));
+        }
+        s = fmaf(f.x, g.x, fmaf(f.y, g.y, s));
       }
-      s = fmaf(f.x, g.x, fmaf(f.y, g.y, s));
     }
-  }
-  for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (live && part == 0) {
-    const float lse = p.lse[static_cast<int64_t>(h) * p.T + t];
-    reinterpret_cast<float2*>(p.delta)[static_cast<int64_t>(h) * p.T + t] =
-        make_float2(lse == -INFINITY ? -INFINITY : -lse * kLog2e, -s);
+    for (int o = 1 << log_l >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (r < rows && part == 0) {
+      const float lse = p.lse[static_cast<int64_t>(h) * p.T + t];
+      reinterpret_cast<float2*>(p.delta)[static_cast<int64_t>(h) * p.T + t] =
+          make_float2(lse == -INFINITY ? -INFINITY : -lse * kLog2e, -s);
+    }
   }
 }
 
@@ -745,12 +751,11 @@ maxsim_status launch_attn_bwd(const AttnParams& p, int is_bf16, cudaStream_t str
   dq.own_b = dkv.walk_b;
   dq.walk_a = dkv.own_a;
   dq.walk_b = dkv.own_b;
-  int L = 1;
-  while (L * 8 < p.d) L *= 2;
-  const int64_t blocks = (static_cast<int64_t>(p.T) * p.heads * L + 255) / 256;
-  if (blocks > 0x7fffffff) return MAXSIM_ERR_UNSUPPORTED;
-  if (is_bf16) attn_stats_kernel<true><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p, L);
-  else attn_stats_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p, L);
+  int log_l = 0;  // lanes of a row, a power of two
+  while ((8 << log_l) < p.d) ++log_l;
+  const unsigned blocks = static_cast<unsigned>((p.T + static_cast<int64_t>(kTokens) - 1) / kTokens);
+  if (is_bf16) attn_stats_kernel<true><<<blocks, 256, 0, stream>>>(p, log_l);
+  else attn_stats_kernel<false><<<blocks, 256, 0, stream>>>(p, log_l);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
     e = p.d > 64            ? bwd_both<128, 128>(dkv, dq, p, is_bf16, dev->sm_count, stream)
