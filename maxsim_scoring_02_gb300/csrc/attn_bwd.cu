@@ -42,13 +42,15 @@ constexpr int kTile = 128;
 constexpr int kBoxRows = 64;
 
 // DH: head size in shared memory; BC: columns of a score tile (rows of Q or
-// keys that are walked over), 64 for each arithmetic warpgroup.
+// keys that are walked over), 64 for each arithmetic warpgroup. Heads of 64 and
+// fewer take tiles of 64 columns and two blocks an SM, whose phases interleave:
+// against one block with tiles of 128 and S made a tile ahead that is 18 % faster
+// at 150 tokens a document, 4 % at 256 and even at 1024 (12 heads). Heads of 128
+// fill TMEM with one block.
 template <int DH, int BC, bool kDkv>
 struct BwdShape {
   static constexpr int kGroups = BC / 64;
-  // Heads of 64 leave TMEM for a second buffer of S, which is then made a tile
-  // ahead, and shared memory for the tiles that takes.
-  static constexpr int kSBufs = DH == 64 && BC == 128 ? 2 : 1, kStages = 2 * kSBufs;
+  static constexpr int kStages = 2;
   static constexpr int kPanels = DH / 64;
   static constexpr uint32_t kOwnPanel = kTile * 128, kOwnBytes = kPanels * kOwnPanel;
   static constexpr uint32_t kPanel = BC * 128, kBytes = kPanels * kPanel;
@@ -61,9 +63,9 @@ struct BwdShape {
   static constexpr int other_regs(bool cap) { return (kGroups + 1) * kRegsLaunch - kGroups * math_regs(cap); }
   static_assert(other_regs(true) >= 56 && other_regs(true) % 8 == 0 && other_regs(false) % 8 == 0, "register split");
   // TMEM columns: S, dP, then the sums
-  static constexpr uint32_t kDp = kSBufs * BC, kSum0 = kDp + BC, kSum1 = kSum0 + DH, kNeed = kSum1 + DH;
+  static constexpr uint32_t kDp = BC, kSum0 = kDp + BC, kSum1 = kSum0 + DH, kNeed = kSum1 + DH;
   static constexpr uint32_t kTmemCols = kNeed <= 256 ? 256 : 512;
-  static constexpr int kBars = 2 + 2 * kStages + 3 + 2 * kSBufs + 2 * kRing + 2;
+  static constexpr int kBars = 2 + 2 * kStages + 5 + 2 * kRing + 2;
   static constexpr uint32_t kSmem = 2 * kOwnBytes + 2 * kStages * kBytes + kGroups * 4 * kStageBytes<64> + 8 * kBars +
                                     kStages * BC * 8 + kRing * sizeof(Work) + 16 + 16;
 };
@@ -98,14 +100,12 @@ struct BwdSmem {
   __device__ __forceinline__ uint32_t own_empty() const { return bars + 8; }
   __device__ __forceinline__ uint32_t walk_full(int s) const { return bars + 16 + 8 * s; }
   __device__ __forceinline__ uint32_t walk_empty(int s) const { return walk_full(S::kStages + s); }
-  __device__ __forceinline__ uint32_t s_full(int b) const { return walk_full(2 * S::kStages + b); }
-  __device__ __forceinline__ uint32_t dp_full() const { return s_full(S::kSBufs); }
-  // one for each buffer of S: with S made ahead, a warp with nothing to do in tile
-  // i may be at tile i + 1 before the others have arrived for tile i
-  __device__ __forceinline__ uint32_t p_full(int b) const { return dp_full() + 8 + 8 * b; }
-  __device__ __forceinline__ uint32_t ds_full() const { return p_full(S::kSBufs); }
-  __device__ __forceinline__ uint32_t sum_full() const { return ds_full() + 8; }
-  __device__ __forceinline__ uint32_t info_full(int r) const { return ds_full() + 16 + 8 * r; }
+  __device__ __forceinline__ uint32_t s_full() const { return walk_full(2 * S::kStages); }
+  __device__ __forceinline__ uint32_t dp_full() const { return s_full() + 8; }
+  __device__ __forceinline__ uint32_t p_full() const { return s_full() + 16; }
+  __device__ __forceinline__ uint32_t ds_full() const { return s_full() + 24; }
+  __device__ __forceinline__ uint32_t sum_full() const { return s_full() + 32; }
+  __device__ __forceinline__ uint32_t info_full(int r) const { return s_full() + 40 + 8 * r; }
   __device__ __forceinline__ uint32_t info_empty(int r) const { return info_full(kRing + r); }
   __device__ __forceinline__ uint32_t done() const { return info_full(2 * kRing); }
   __device__ __forceinline__ uint32_t rest_full() const { return done() + 8; }
@@ -280,38 +280,36 @@ __device__ void bwd_products(const AttnParams& p, const BwdSmem<S, BC>& sm, uint
       }
       return true;
     };
-    // cols: columns of tiles i, i + 1 and i + 2. S runs kSBufs tiles ahead of P.
-    int cols = 0, next = 0, after = 0;
+    int cols = 0, next = 0;  // columns of tiles i and i + 1
     const auto make_s = [&](int i, int& c) -> bool {
       if (!ready(i, c)) return false;
       tc_fence_after();
-      score((step + i) % S::kSBufs * BC, sm.own_a, sm.walk_a + (step + i) % S::kStages * S::kBytes, c);
-      umma_commit_el(sm.s_full((step + i) % S::kSBufs));
+      score(0, sm.own_a, sm.walk_a + (step + i) % S::kStages * S::kBytes, c);
+      umma_commit_el(sm.s_full());
       return true;
+    };
+    const auto make_dp = [&](int i, int c) {
+      score(S::kDp, sm.own_b, sm.walk_b + (step + i) % S::kStages * S::kBytes, c);
+      umma_commit_el(sm.dp_full());
     };
     ok = wait(sm.own_full(), item) && make_s(0, cols);
     if (!ok) break;
-    score(S::kDp, sm.own_b, sm.walk_b + step % S::kStages * S::kBytes, cols);
-    umma_commit_el(sm.dp_full());
-    if (S::kSBufs == 2 && total > 1 && !(ok = make_s(1, next))) break;
+    make_dp(0, cols);
     for (int i = 0; i < total; ++i) {
-      const uint32_t u = step + i, s = u % S::kStages, s1 = (u + 1) % S::kStages;
-      if (!(ok = wait(sm.p_full(u % S::kSBufs), u / S::kSBufs))) break;
+      const uint32_t u = step + i, s = u % S::kStages;
+      if (!(ok = wait(sm.p_full(), u))) break;
       tc_fence_after();
-      add(S::kSum0, u % S::kSBufs * BC, (kDkv ? sm.walk_b : sm.walk_a) + s * S::kBytes, cols, i == 0);
-      if (S::kSBufs == 1 && i + 1 < total && !(ok = make_s(i + 1, next))) break;
+      add(S::kSum0, 0, (kDkv ? sm.walk_b : sm.walk_a) + s * S::kBytes, cols, i == 0);
+      if (i + 1 < total && !(ok = make_s(i + 1, next))) break;
       if (!(ok = wait(sm.ds_full(), u))) break;
       tc_fence_after();
       add(S::kSum1, S::kDp, sm.walk_a + s * S::kBytes, cols, i == 0);
       umma_commit_el(sm.walk_empty(s));
       if (i + 1 < total) {
-        score(S::kDp, sm.own_b, sm.walk_b + s1 * S::kBytes, next);
-        umma_commit_el(sm.dp_full());
+        make_dp(i + 1, next);
         if (i + 2 == total) umma_commit_el(sm.own_empty());
       }
-      if (S::kSBufs == 2 && i + 2 < total && !(ok = make_s(i + 2, after))) break;
       cols = next;
-      next = after;
     }
     if (!ok) break;
     if (total == 1) umma_commit_el(sm.own_empty());
@@ -530,16 +528,15 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
         const float* nl = sm.stats + (step % S::kStages) * 2 * BC + wg * 64;
         const float far = static_cast<float>(mine - from);
         float e[64], bend[kCap && !kDkv ? 64 : 1];
-        const uint32_t s_now = s_col + step % S::kSBufs * BC;
-        if (!wait(sm.s_full(step % S::kSBufs), step / S::kSBufs)) return;
+        if (!wait(sm.s_full(), step)) return;
         // the statistics came with the walked tile, whose products have been made from it
         if (kDkv && !wait(sm.walk_full(step % S::kStages), step / S::kStages)) return;
         tc_fence_after();
         if (used > 0)
-          make_weights<kDkv, kBf16, kCap, kBias>(s_now, k, nl, own_nl, slope2, far, mine < w.len, edge, used, lo - from, hi - from, e, bend);
+          make_weights<kDkv, kBf16, kCap, kBias>(s_col, k, nl, own_nl, slope2, far, mine < w.len, edge, used, lo - from, hi - from, e, bend);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_a(sm.p_full(step % S::kSBufs));
+        if (lane == 0) mbar_arrive_a(sm.p_full());
         if (!wait(sm.dp_full(), step)) return;
         tc_fence_after();
         if (used > 0) make_ds<kDkv, kBf16, kCap>(dp_col, nl + BC, own_nd, edge, used, e, bend, rest);
@@ -619,10 +616,8 @@ __global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH,
       mbar_init(sm.at(sm.walk_full(s)), kDkv ? 2 : 1);                // the loader, and the statistics' warp
       mbar_init(sm.at(sm.walk_empty(s)), kDkv ? 1 + kMathWarps : 1);  // the products, and the statistics' readers
     }
-    for (int b = 0; b < S::kSBufs; ++b) {
-      mbar_init(sm.at(sm.s_full(b)), 1);
-      mbar_init(sm.at(sm.p_full(b)), kMathWarps);
-    }
+    mbar_init(sm.at(sm.s_full()), 1);
+    mbar_init(sm.at(sm.p_full()), kMathWarps);
     mbar_init(sm.at(sm.dp_full()), 1);
     mbar_init(sm.at(sm.ds_full()), kMathWarps);
     mbar_init(sm.at(sm.sum_full()), 1);
@@ -758,9 +753,8 @@ maxsim_status launch_attn_bwd(const AttnParams& p, int is_bf16, cudaStream_t str
   else attn_stats_kernel<false><<<blocks, 256, 0, stream>>>(p, log_l);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = p.d > 64            ? bwd_both<128, 128>(dkv, dq, p, is_bf16, dev->sm_count, stream)
-        : p.T / p.B >= 128 ? bwd_both<64, 128>(dkv, dq, p, is_bf16, dev->sm_count, stream)
-                           : bwd_both<64, 64>(dkv, dq, p, is_bf16, dev->sm_count, stream);
+    e = p.d > 64 ? bwd_both<128, 128>(dkv, dq, p, is_bf16, dev->sm_count, stream)
+                 : bwd_both<64, 64>(dkv, dq, p, is_bf16, dev->sm_count, stream);
   return e == cudaSuccess ? MAXSIM_OK : MAXSIM_ERR_CUDA;
 }
 

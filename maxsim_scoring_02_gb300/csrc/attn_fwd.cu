@@ -544,11 +544,13 @@ cudaError_t fwd_launch(const CUtensorMap* m, const AttnParams& p, int sm_count, 
 
 template <int DH, int NQ, bool kBf16>
 cudaError_t fwd_variant(const CUtensorMap* m, const AttnParams& p, int sm_count, cudaStream_t stream) {
-  if (p.cap > 0.f)
-    return p.slopes ? fwd_launch<DH, NQ, kBf16, true, true>(m, p, sm_count, stream)
-                    : fwd_launch<DH, NQ, kBf16, true, false>(m, p, sm_count, stream);
-  return p.slopes ? fwd_launch<DH, NQ, kBf16, false, true>(m, p, sm_count, stream)
-                  : fwd_launch<DH, NQ, kBf16, false, false>(m, p, sm_count, stream);
+  if (p.slopes)
+    return p.cap > 0.f ? fwd_launch<DH, NQ, kBf16, true, true>(m, p, sm_count, stream)
+                       : fwd_launch<DH, NQ, kBf16, false, true>(m, p, sm_count, stream);
+  if constexpr (DH == 64 && NQ == 2) return cudaErrorInvalidValue;  // not chosen without slopes
+  else
+    return p.cap > 0.f ? fwd_launch<DH, NQ, kBf16, true, false>(m, p, sm_count, stream)
+                       : fwd_launch<DH, NQ, kBf16, false, false>(m, p, sm_count, stream);
 }
 
 template <int DH>
@@ -575,7 +577,14 @@ maxsim_status launch_attn_fwd(const AttnParams& p, int is_bf16, cudaStream_t str
       !attn_tmap(&m[1], p.k, p.T, p.kv_heads, p.d, is_bf16, kBoxRows) ||
       !attn_tmap(&m[2], p.v, p.T, p.kv_heads, p.d, is_bf16, kBoxRows))
     return MAXSIM_ERR_CUDA;
-  const int nq = p.T / p.B >= 192 ? 2 : 1;
+  // Two tiles of rows a block halve the traffic of K and V, which heads of 128
+  // need (24 documents of 1024 tokens, 16 heads: 159 against 206 us; 300 of 256,
+  // 12 heads: 150 against 178), unless documents fit one tile. Heads of 64 run
+  // better as two blocks of one tile (300 documents of 256 tokens, 12 heads: 100
+  // against 112 us; of 320: 181 against 231; 64 of 1024: 254 against 280), but for the
+  // distance bias, whose arithmetic wants the larger block's registers (160
+  // ragged ones: 146 against 159).
+  const int nq = (p.d > 64 || p.slopes) && p.T / p.B >= 192 ? 2 : 1;
   const cudaError_t e = p.d <= 64 ? fwd_typed<64>(m, p, nq, is_bf16, dev->sm_count, stream)
                                   : fwd_typed<128>(m, p, nq, is_bf16, dev->sm_count, stream);
   return e == cudaSuccess ? MAXSIM_OK : MAXSIM_ERR_CUDA;
