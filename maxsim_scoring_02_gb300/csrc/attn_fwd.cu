@@ -36,9 +36,9 @@ struct FwdShape {
   static constexpr int kPanels = DH / 64;
   static constexpr uint32_t kPanelBytes = kTile * 128;
   static constexpr uint32_t kTileBytes = kPanels * kPanelBytes;
-  static constexpr int kStages = NQ == 1 ? (DH == 64 ? 2 : 1) : (DH == 64 ? 4 : 2);
+  static constexpr int kStages = DH == 64 || NQ == 2 ? 2 : 1;
   static constexpr int kStoreCols = NQ == 1 ? 32 : 64;  // of an output row at a time (two blocks an SM leave no more room)
-  static constexpr int kQStages = NQ == 1 && DH == 64 ? 2 : 1;
+  static constexpr int kQStages = DH == 64 ? 2 : 1;
   static constexpr int kThreads = NQ * 128 + 128;  // softmax warpgroups; loader, issuer, planner and an idle warp
   static constexpr int kBlocks = NQ == 1 ? 2 : 1;  // resident on an SM
   // Registers a thread: at launch (ptxas fills the launch bounds), and after
@@ -332,14 +332,13 @@ __device__ __forceinline__ void raise_max(uint32_t o_col, const ScoreConst& k, f
   }
 }
 
-// One tile of scores of this thread's row: weights to TMEM, m and sum brought
+// One tile of scores, all seen by this thread's row, without a bias: weights to TMEM, m and sum brought
 // up to date (and O with them). The scores are read twice, 32 at a time with the
 // next group on its way, rather than kept: 128 registers of them spilled (0.70
 // against 0.40 ms for 16411 causal tokens, 8 heads of 128). Bent scores are
 // written back between.
-template <int DH, bool kBf16, bool kCap, bool kBias>
-__device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, const ScoreConst& k, float slope2,
-                                             float far, bool first, RowState& st) {
+template <int DH, bool kBf16, bool kCap>
+__device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, const ScoreConst& k, bool first, RowState& st) {
   uint32_t u[2][32];
   float now = st.m;
   tmem_ld_32x32b_x32_issue(s_col, u[0]);
@@ -347,7 +346,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, con
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     if (q < 3) tmem_ld_32x32b_x32_issue(s_col + (q + 1) * 32, u[(q + 1) & 1]);
-    finish_scores<kCap, kBias, false>(u[q & 1], k, slope2, far - q * 32, 32);
+    finish_scores<kCap, false, false>(u[q & 1], k, 0.f, 0.f, 32);
     now = group_max(u[q & 1], now);
     if constexpr (kCap) tmem_st_32x32b_x32_issue(s_col + q * 32, u[q & 1]);
     if (q < 3) tmem_wait_ld_regs(u[(q + 1) & 1]);
@@ -362,7 +361,6 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, con
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     if (q < 3) tmem_ld_32x32b_x32_issue(s_col + (q + 1) * 32, u[(q + 1) & 1]);
-    if constexpr (kBias && !kCap) finish_scores<kCap, kBias, false>(u[q & 1], k, slope2, far - q * 32, 32);
     group_weights<kBf16>(s_col + q * 16, u[q & 1], scale, shift, part);
     if (q < 3) tmem_wait_ld_regs(u[(q + 1) & 1]);
   }
@@ -372,8 +370,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, con
   tmem_wait_st();
 }
 
-// The same for a tile of fewer than 128 columns, or some of whose columns are
-// hidden from the row (those from `lim` on): a loop over the groups of 32 that
+// The same for any tile: of fewer than 128 columns, with some hidden from the row
+// (those from `lim` on), with a distance bias: a loop over the groups of 32 that
 // there are, which compares columns only where a row of the warp needs it. Short
 // documents run here, and small code counts.
 template <int DH, bool kBf16, bool kCap, bool kBias>
@@ -438,8 +436,8 @@ __device__ void fwd_softmax(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint
       if (!wait(sm.s_full(t), sn)) return;
       tc_fence_after();
       const float far = static_cast<float>(row - j * kTile);
-      if ((j + 1) * kTile <= all_see)
-        softmax_tile<DH, kBf16, kCap, kBias>(s_col, o_col, k, slope2, far, j == 0, st);
+      if (!kBias && (j + 1) * kTile <= all_see)  // (a bias in unrolled code: 131 us where the loop takes 119)
+        softmax_tile<DH, kBf16, kCap>(s_col, o_col, k, j == 0, st);
       else
         softmax_edge<DH, kBf16, kCap, kBias>(s_col, o_col, k, slope2, far, min(kTile, keys - j * kTile), end - j * kTile,
                                              j == 0, st);
@@ -544,20 +542,16 @@ cudaError_t fwd_launch(const CUtensorMap* m, const AttnParams& p, int sm_count, 
 
 template <int DH, int NQ, bool kBf16>
 cudaError_t fwd_variant(const CUtensorMap* m, const AttnParams& p, int sm_count, cudaStream_t stream) {
-  if (p.slopes)
-    return p.cap > 0.f ? fwd_launch<DH, NQ, kBf16, true, true>(m, p, sm_count, stream)
-                       : fwd_launch<DH, NQ, kBf16, false, true>(m, p, sm_count, stream);
-  if constexpr (DH == 64 && NQ == 2) return cudaErrorInvalidValue;  // not chosen without slopes
-  else
-    return p.cap > 0.f ? fwd_launch<DH, NQ, kBf16, true, false>(m, p, sm_count, stream)
-                       : fwd_launch<DH, NQ, kBf16, false, false>(m, p, sm_count, stream);
+  if (p.cap > 0.f)
+    return p.slopes ? fwd_launch<DH, NQ, kBf16, true, true>(m, p, sm_count, stream)
+                    : fwd_launch<DH, NQ, kBf16, true, false>(m, p, sm_count, stream);
+  return p.slopes ? fwd_launch<DH, NQ, kBf16, false, true>(m, p, sm_count, stream)
+                  : fwd_launch<DH, NQ, kBf16, false, false>(m, p, sm_count, stream);
 }
 
-template <int DH>
-cudaError_t fwd_typed(const CUtensorMap* m, const AttnParams& p, int nq, int is_bf16, int sm_count, cudaStream_t stream) {
-  if (nq == 1)
-    return is_bf16 ? fwd_variant<DH, 1, true>(m, p, sm_count, stream) : fwd_variant<DH, 1, false>(m, p, sm_count, stream);
-  return is_bf16 ? fwd_variant<DH, 2, true>(m, p, sm_count, stream) : fwd_variant<DH, 2, false>(m, p, sm_count, stream);
+template <int DH, int NQ>
+cudaError_t fwd_typed(const CUtensorMap* m, const AttnParams& p, int is_bf16, int sm_count, cudaStream_t stream) {
+  return is_bf16 ? fwd_variant<DH, NQ, true>(m, p, sm_count, stream) : fwd_variant<DH, NQ, false>(m, p, sm_count, stream);
 }
 
 }  // namespace
@@ -581,12 +575,12 @@ maxsim_status launch_attn_fwd(const AttnParams& p, int is_bf16, cudaStream_t str
   // need (24 documents of 1024 tokens, 16 heads: 159 against 206 us; 300 of 256,
   // 12 heads: 150 against 178), unless documents fit one tile. Heads of 64 run
   // better as two blocks of one tile (300 documents of 256 tokens, 12 heads: 100
-  // against 112 us; of 320: 181 against 231; 64 of 1024: 254 against 280), but for the
-  // distance bias, whose arithmetic wants the larger block's registers (160
-  // ragged ones: 146 against 159).
-  const int nq = (p.d > 64 || p.slopes) && p.T / p.B >= 192 ? 2 : 1;
-  const cudaError_t e = p.d <= 64 ? fwd_typed<64>(m, p, nq, is_bf16, dev->sm_count, stream)
-                                  : fwd_typed<128>(m, p, nq, is_bf16, dev->sm_count, stream);
+  // against 112 us; of 320: 181 against 231; 64 of 1024: 254 against 280; 200 of 512:
+  // 223 against 216; 160 ragged ones with a distance bias: 119 against 131).
+  const int n = dev->sm_count;
+  const cudaError_t e = p.d <= 64              ? fwd_typed<64, 1>(m, p, is_bf16, n, stream)
+                        : p.T / p.B >= 192 ? fwd_typed<128, 2>(m, p, is_bf16, n, stream)
+                                           : fwd_typed<128, 1>(m, p, is_bf16, n, stream);
   return e == cudaSuccess ? MAXSIM_OK : MAXSIM_ERR_CUDA;
 }
 
