@@ -25,6 +25,12 @@
 // added up in memory by all key blocks, in an order that changes results, and
 // delta were taken as it is.
 //
+// Measured: 24 documents of 1024 tokens, 16 heads of 128: 0.65 ms (0.79 PFLOP/s
+// of the five products, 1.27 of the eight made); 64 documents, 12 heads of 64: 0.91
+// ms. Bound by the arithmetic phases beside the products: 960 to 1180 cycles
+// for P and 750 to 850 for dS of a tile whose eight products, in both kernels,
+// take 4130.
+//
 // A tile passes through two phases of the arithmetic warps, P and dS. While
 // they are at dS of tile i the tensor cores make the product with P of tile i and S of tile
 // i + 1, while they are at P of tile i + 1 that with dS of tile i and dP of

@@ -17,6 +17,12 @@
 // the tensor cores take nothing wider at this rate; their sum is made of the
 // unrounded ones, so lse keeps fp32.
 //
+// Bound by the chain of one tile (softmax 1190 cycles, its two products 1033,
+// the way between the warps 500), which two tiles at a time cover to seven
+// tenths: 16411 causal tokens, 8 heads over 2 of 128: 0.36 ms (1.53 PFLOP/s, the
+// tensor cores' burst 1.95); on documents shorter than a tile by the same chain
+// over less work: 2500 passages of 78 tokens, 12 heads of 64: 0.31 ms (HBM 0.59).
+//
 // Keys past a document's last visible one are cut off the products (to a
 // multiple of 16) and the up to 15 rows of V behind them are zeroed in shared
 // memory: 0 * NaN would reach the sum.
