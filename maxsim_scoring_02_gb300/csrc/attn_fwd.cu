@@ -50,7 +50,7 @@ struct FwdShape {
   // Registers a thread: at launch (ptxas fills the launch bounds), and after
   // the softmax threads took over some of the others'.
   static constexpr int kRegsLaunch = NQ == 1 ? 128 : 168;
-  static constexpr int kRegsSoftmax = NQ == 1 ? 160 : 200, kRegsOther = NQ == 1 ? 96 : 104;
+  static constexpr int kRegsSoftmax = NQ == 1 ? 176 : 208, kRegsOther = NQ == 1 ? 80 : 88;
   static_assert(NQ * kRegsSoftmax + kRegsOther <= (NQ + 1) * kRegsLaunch, "register split");
   static constexpr uint32_t kTmemCols = NQ == 1 ? 256 : 512;
   static constexpr uint32_t kO0 = NQ * kTile;  // TMEM columns: S of each tile, then O of each tile
