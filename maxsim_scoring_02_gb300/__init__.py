@@ -540,6 +540,15 @@ def allreduce_dq(dQ, group=None):
 
 # --------------------------------------------------------- the token encoder
 
+def _scratch(nbytes, device, stream):
+    """A workspace of the call's own; its memory is not given to others before
+    ``stream``, where that is not the current one, has passed the call."""
+    workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    if stream is not None:
+        workspace.record_stream(stream)
+    return workspace
+
+
 def _heads(t, name, shape, dtype, index):
     """A [T, heads, d] tensor on CUDA device ``index``, its last dimension
     contiguous, as a maxsim_heads."""
@@ -680,8 +689,7 @@ def maxsim_attention_backward(dO, q, k, v, out, lse, offsets, key_len=None, mask
     dk = torch.empty(kv_shape, dtype=dtype, device=device) if dk is None else dk
     dv = torch.empty(kv_shape, dtype=dtype, device=device) if dv is None else dv
     if workspace is None:
-        nbytes = lib.maxsim_attention_backward_workspace_size(spec)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        workspace = _scratch(lib.maxsim_attention_backward_workspace_size(spec), device, stream)
     _dev(workspace, "workspace", torch.uint8)
     views = [_heads(t, name, want, dtype, index)
              for t, name, want in ((dO, "dO", shape), (q, "q", shape), (k, "k", kv_shape), (v, "v", kv_shape),
@@ -735,7 +743,7 @@ def maxsim_clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, 
         norm = torch.empty(1, dtype=torch.float32, device=device)
     _dev(norm, "norm", torch.float32)
     if workspace is None:
-        workspace = torch.empty(lib.maxsim_clip_grad_norm_workspace_size(n), dtype=torch.uint8, device=device)
+        workspace = _scratch(lib.maxsim_clip_grad_norm_workspace_size(n), device, stream)
     _dev(workspace, "workspace", torch.uint8)
     pointers = array.array("Q", map(torch.Tensor.data_ptr, grads))
     targets = pointers if out is None else array.array("Q", map(torch.Tensor.data_ptr, outs))

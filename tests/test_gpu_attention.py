@@ -237,6 +237,12 @@ def test_another_stream_and_repeats():
             g2 = m.maxsim_attention_backward(dO, q, k, v, o2, l2, off)
     s.synchronize()
     assert torch.equal(o2, out) and torch.equal(l2, lse) and all(torch.equal(a, b) for a, b in zip(g2, grads))
+    torch.cuda.synchronize()
+    o3, l3 = m.maxsim_attention(q, k, v, off, want_lse=True, stream=s)      # the stream as an argument
+    g3 = m.maxsim_attention_backward(dO, q, k, v, o3, l3, off, stream=s)
+    junk = torch.full((1 << 20,), 255, dtype=torch.uint8, device=DEV)       # may not be the workspace's memory
+    s.synchronize()
+    assert torch.equal(o3, out) and all(torch.equal(a, b) for a, b in zip(g3, grads)) and (junk == 255).all()
 
 
 @pytest.mark.parametrize("cap", [0.0, 20.0])
