@@ -230,7 +230,11 @@ __device__ void i8x_converters(const FwdTcParams& p, const I8xSmem& sm, const I8
         if (j >= kN) j -= kN;
         w4[c] = lds_u4(src + ((static_cast<uint32_t>(j) ^ sw) << 4));
       }
-      mbar_arrive_a(br.rawempty + 8 * s);  // the row is in registers (the arrive orders the reads before it)
+      // The row is asked for, not yet in registers: the fence orders the reads
+      // before the copy that the release lets into the stage. (Without it a cold
+      // copy overtook them at d = 192: 33 of 1500 launches scored a document wrongly.)
+      fence_proxy_async_smem();
+      mbar_arrive_a(br.rawempty + 8 * s);
       if (!mbar_wait_a(br.opempty + 8 * o, oph ^ 1u, sm.abort_flag, p.status)) return;
       const uint32_t dst = op0 + static_cast<uint32_t>(o) * kOp;
 #pragma unroll

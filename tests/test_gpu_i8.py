@@ -247,3 +247,20 @@ def test_scores_only_bad_offsets_are_reported():
     st, flags = m.maxsim_device_status()
     assert st == 1 and flags & m.DEVERR_BAD_INPUT
     assert out[1].item() == 0.0 and out[2].item() == 0.0 and out[3].item() == 0.0
+
+
+def test_scores_only_cold_copies_d192():
+    """Documents that span tiles, with L2 cold at every fourth launch: copies
+    into a raw stage must not overtake the reads of what it held."""
+    d = 192
+    L = torch.tensor([255, 256, 257, 1, 0, 2, 5, 31, 32, 33, 127, 128, 129] * 12, dtype=torch.int64)
+    off = workloads.csr_offsets(L)
+    Qi, sq = workloads.quantize_int8(workloads.normalized_tokens((32, d), seed=71, dtype="fp32"))
+    Di, sd = workloads.quantize_int8(workloads.normalized_tokens((int(off[-1]), d), seed=72, dtype="fp32"))
+    first = _check_scores(Qi, sq, Di, sd, off)
+    args = [t.to(DEV) for t in (Qi, sq, Di, sd, off)]
+    flush = torch.empty(200 << 20, dtype=torch.uint8, device=DEV)
+    for i in range(400):
+        if i % 4 == 0:
+            flush.fill_(i % 251)
+        assert torch.equal(m.maxsim_score_i8(*args), first), i
