@@ -17,7 +17,7 @@
 #include <cstdint>
 
 #include "internal.h"
-#include "ptx.cuh"
+#include "attn_ptx.cuh"
 
 namespace msim {
 
