@@ -14,7 +14,10 @@ Operator (TileMaxSim deep reading §1; FLASH-MAXSIM, Abstract):
 from __future__ import annotations
 
 import array
+import contextlib
 import ctypes
+import functools
+import inspect
 import math
 import operator
 import os
@@ -175,6 +178,37 @@ def _stream_on(stream, index):
     if stream is None and _raw_stream is not None:
         return _raw_stream(index)
     return (torch.cuda.current_stream(index) if stream is None else stream).cuda_stream
+
+
+@contextlib.contextmanager
+def _made_on(stream):
+    """Makes ``stream`` current for a call that launches on it, so that memory
+    which the call makes comes from that stream's pool. Memory of another
+    stream's pool may have been given up by work that has yet to run there, and
+    nothing would order that work and the call's. Yields a function that keeps
+    the result's memory from reuse until the caller's stream is done with it."""
+    outer = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        yield lambda t: t.record_stream(outer)
+
+
+def _entry(fn):
+    """An entry point whose last parameter is ``stream``: with one given, the
+    call's workspace and results are made on that stream, too."""
+    names = tuple(inspect.signature(fn).parameters)
+    place = names.index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[place] if len(args) > place else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        with _made_on(stream) as keep:
+            result = fn(*args, **kw)
+            for t in result if isinstance(result, tuple) else (result,):
+                keep(t)
+            return result
+    return call
 
 
 def _dev(t, name, dtype=None):
@@ -539,14 +573,15 @@ def allreduce_dq(dQ, group=None):
 
 
 # --------------------------------------------------------- the token encoder
+#
+# ``stream=None`` is the current stream. With a stream given, the call runs on
+# it, and so does everything that makes its workspace and results; tensors that
+# the caller gives are ordered with that stream by the caller, and the results
+# are read elsewhere once that stream has been waited for.
 
-def _scratch(nbytes, device, stream):
-    """A workspace of the call's own; its memory is not given to others before
-    ``stream``, where that is not the current one, has passed the call."""
-    workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    if stream is not None:
-        workspace.record_stream(stream)
-    return workspace
+def _scratch(nbytes, device):
+    """A workspace of the call's own."""
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
 
 
 def _heads(t, name, shape, dtype, index):
@@ -585,6 +620,7 @@ def maxsim_rotary_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0,
     return freq.to(device), amplitude.value
 
 
+@_entry
 def maxsim_rotary(x, freq, offsets=None, positions=None, interleaved=False, amplitude=1.0, inverse=False, out=None,
                   stream=None):
     """Rotary positions: turns the first 2 * len(freq) dimensions of every head
@@ -642,6 +678,7 @@ def _attention_spec(q, k, offsets, key_len, mask, prefix_len, scale, cap, slopes
                           None if slopes is None else slopes.data_ptr())
 
 
+@_entry
 def maxsim_attention(q, k, v, offsets, key_len=None, mask="full", prefix_len=None, scale=None, cap=0.0, slopes=None,
                      out=None, lse=None, want_lse=False, stream=None):
     """Softmax attention within each CSR-packed document. q [T, heads, d], k and
@@ -674,6 +711,7 @@ def maxsim_attention_backward_workspace_size(q, k, offsets, mask="full", prefix_
     return int(load_library().maxsim_attention_backward_workspace_size(spec))
 
 
+@_entry
 def maxsim_attention_backward(dO, q, k, v, out, lse, offsets, key_len=None, mask="full", prefix_len=None, scale=None,
                               cap=0.0, slopes=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
     """Gradients of maxsim_attention for the gradient dO of its out, from its
@@ -689,7 +727,7 @@ def maxsim_attention_backward(dO, q, k, v, out, lse, offsets, key_len=None, mask
     dk = torch.empty(kv_shape, dtype=dtype, device=device) if dk is None else dk
     dv = torch.empty(kv_shape, dtype=dtype, device=device) if dv is None else dv
     if workspace is None:
-        workspace = _scratch(lib.maxsim_attention_backward_workspace_size(spec), device, stream)
+        workspace = _scratch(lib.maxsim_attention_backward_workspace_size(spec), device)
     _dev(workspace, "workspace", torch.uint8)
     views = [_heads(t, name, want, dtype, index)
              for t, name, want in ((dO, "dO", shape), (q, "q", shape), (k, "k", kv_shape), (v, "v", kv_shape),
@@ -713,6 +751,7 @@ def _dtypes(tensors):
     return list(map(operator.attrgetter("dtype"), tensors))
 
 
+@_entry
 def maxsim_clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, stream=None):
     """Global 2-norm of the tensors ``grads`` (contiguous, bf16/fp16/fp32, types
     may be mixed), which are scaled by min(1, max_norm / (norm + 1e-6)): in
@@ -743,7 +782,7 @@ def maxsim_clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, 
         norm = torch.empty(1, dtype=torch.float32, device=device)
     _dev(norm, "norm", torch.float32)
     if workspace is None:
-        workspace = _scratch(lib.maxsim_clip_grad_norm_workspace_size(n), device, stream)
+        workspace = _scratch(lib.maxsim_clip_grad_norm_workspace_size(n), device)
     _dev(workspace, "workspace", torch.uint8)
     pointers = array.array("Q", map(torch.Tensor.data_ptr, grads))
     targets = pointers if out is None else array.array("Q", map(torch.Tensor.data_ptr, outs))

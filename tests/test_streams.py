@@ -1,0 +1,60 @@
+"""What a call makes, and where: with ``stream=`` its workspace and its results
+come from that stream's memory, not from the current stream's, whose freed
+blocks may still be written by work that has yet to run."""
+import pytest
+import torch
+
+import maxsim_scoring_02_gb300 as m
+from tests import _fake_cuda as fake
+
+BF, F32, I32, I64, U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+
+
+@pytest.fixture
+def cuda(monkeypatch):
+    return fake.Cuda(monkeypatch, m)
+
+
+def _calls(cuda, index=0):
+    """Every entry point that makes something: (call, tensors that it makes)."""
+    t = lambda shape, dtype: cuda.tensor(shape, dtype, index)  # noqa: E731
+    q, k, x = t((6, 4, 64), BF), t((6, 2, 64), BF), t((6, 4, 64), BF)
+    off, lse, freq = t((3,), I64), t((4, 6), F32), t((32,), I64)
+    return {
+        "rotary": (lambda **kw: m.maxsim_rotary(x, freq, offsets=off, **kw), 1),
+        "attention": (lambda **kw: m.maxsim_attention(q, k, k, off, want_lse=True, **kw), 2),
+        "attention_backward": (lambda **kw: m.maxsim_attention_backward(x, q, k, k, x, lse, off, **kw), 4),
+        "clip": (lambda **kw: m.maxsim_clip_grad_norm([t((8,), F32), t((9,), BF)], 1.0, **kw), 2),
+    }
+
+
+ENTRIES = ["rotary", "attention", "attention_backward", "clip"]
+
+
+@pytest.mark.parametrize("name", ENTRIES)
+def test_a_call_on_another_stream_makes_its_memory_there(cuda, name):
+    call, count = _calls(cuda)[name]
+    other, outer = fake.Stream(0, 0x77), cuda.streams[0]
+    result = call(stream=other)
+    result = result if isinstance(result, tuple) else (result,)
+    assert len(cuda.made) == count and all(t.pool is other for t in cuda.made)
+    # results are read by the caller's stream; a workspace is not
+    for t in cuda.made:
+        assert (outer in t.users) == any(t is r for r in result)
+    launches = [c for c in cuda.lib.calls]
+    assert len(launches) == 1 and 0x77 in [getattr(a, "value", a) for a in launches[0][2]]
+    assert cuda.streams[0] is outer
+
+
+@pytest.mark.parametrize("name", ENTRIES)
+def test_a_call_on_the_current_stream(cuda, name):
+    call, count = _calls(cuda)[name]
+    call()
+    assert len(cuda.made) == count and all(t.pool is cuda.streams[0] and not t.users for t in cuda.made)
+
+
+def test_the_stream_may_be_given_by_position(cuda):
+    other = fake.Stream(0, 0x77)
+    x, freq = cuda.tensor((6, 4, 64), BF), cuda.tensor((32,), I64)
+    m.maxsim_rotary(x, freq, None, None, False, 1.0, False, None, other)
+    assert [t.pool for t in cuda.made] == [other]
