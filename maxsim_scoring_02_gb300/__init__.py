@@ -240,7 +240,13 @@ def maxsim_device_status(stream=None):
 
 
 # ------------------------------------------------------------- entry points
+#
+# ``stream=None`` is the current stream. With a stream given, the call runs on
+# it, and so does everything that makes its workspace and results; tensors that
+# the caller gives are ordered with that stream by the caller, and the results
+# are read elsewhere once that stream has been waited for.
 
+@_entry
 def maxsim_score(Q, D, doc_len=None, out=None, argmax_out=None, want_argmax=False, stream=None):
     """Padded layout. Q [nq,d] or [n_queries,nq,d]; D [B,Nd,d] (bf16/fp16/fp32);
     doc_len [B] int32 or None. Returns out [n_queries,B] fp32 (and argmax
@@ -273,6 +279,7 @@ def maxsim_length_order_workspace_size(B, nd, csr=False):
     return int(load_library().maxsim_length_order_workspace_size(B, nd, 1 if csr else 0))
 
 
+@_entry
 def maxsim_length_order(doc_len=None, offsets=None, B=None, nd=None, order=None, stream=None):
     """Length-bucketed document order: int32 [B] permutation sorting documents
     by ceil(L_b / 8), ascending and stable. Give doc_len [B] int32 with nd
@@ -301,6 +308,7 @@ def maxsim_length_order(doc_len=None, offsets=None, B=None, nd=None, order=None,
     return order
 
 
+@_entry
 def maxsim_score_ordered(Q, D, doc_order, doc_len=None, out=None, argmax_out=None, want_argmax=False, stream=None):
     """maxsim_score with the documents walked in doc_order (int32 [B]
     permutation); results land at the documents' own indices."""
@@ -333,6 +341,7 @@ def maxsim_score_streamed_workspace_size(n_queries, nq, nd, d, dtype, chunk_docs
     return load_library().maxsim_score_streamed_workspace_size(n_queries, nq, nd, d, _DTYPE_CODE[dtype], chunk_docs)
 
 
+@_entry
 def maxsim_score_streamed(Q, D_host, doc_len_host=None, chunk_docs=16384, out=None, argmax_out=None,
                           want_argmax=False, workspace=None, stream=None):
     """Padded layout with the documents in HOST memory: D_host [B,Nd,d] and
@@ -372,6 +381,7 @@ def maxsim_score_streamed(Q, D_host, doc_len_host=None, chunk_docs=16384, out=No
     return (out, argmax_out) if argmax_out is not None else out
 
 
+@_entry
 def maxsim_score_varlen(Q, D_packed, offsets, out=None, argmax_out=None, want_argmax=False, stream=None):
     """CSR layout: document b owns rows offsets[b]..offsets[b+1]-1 of D_packed [T,d]."""
     lib = load_library()
@@ -398,6 +408,7 @@ def maxsim_score_pq_workspace_size(nq: int, M: int, K: int) -> int:
     return int(load_library().maxsim_score_pq_workspace_size(nq, M, K))
 
 
+@_entry
 def maxsim_score_pq(Q, codebooks, codes, offsets, out=None, argmax_out=None, want_argmax=False,
                     workspace=None, stream=None):
     """PQ scoring: Q [nq,d] fp32, codebooks [M,K,d/M] fp32, codes [T,M] uint8, CSR offsets."""
@@ -424,6 +435,7 @@ def maxsim_score_pq(Q, codebooks, codes, offsets, out=None, argmax_out=None, wan
     return (out, argmax_out) if argmax_out is not None else out
 
 
+@_entry
 def maxsim_score_pq_noalloc(Q, codebooks, codes, offsets, out=None, argmax_out=None, want_argmax=False,
                             stream=None):
     """PQ scoring with the table kept in the library's fixed device array, for
@@ -447,6 +459,7 @@ def maxsim_score_pq_noalloc(Q, codebooks, codes, offsets, out=None, argmax_out=N
     return (out, argmax_out) if argmax_out is not None else out
 
 
+@_entry
 def maxsim_score_i8(Q, q_scale, D, d_scale, offsets, out=None, maxv_out=None, maxdot_out=None,
                     argmax_out=None, want_details=False, stream=None):
     """INT8 x INT8 scoring with per-token fp32 scales; CSR documents."""
@@ -480,6 +493,7 @@ def maxsim_backward_workspace_size(n_queries, nq, d, B, nd) -> int:
     return int(load_library().maxsim_backward_workspace_size(n_queries, nq, d, B, nd))
 
 
+@_entry
 def maxsim_backward(Q, D, argmax, dS, doc_len=None, dQ=None, dD=None, workspace=None, stream=None):
     """Gradients of sum dS*score through the saved forward argmax (padded layout)."""
     lib = load_library()
@@ -506,6 +520,7 @@ def maxsim_backward(Q, D, argmax, dS, doc_len=None, dQ=None, dD=None, workspace=
     return dQ.view(Q.shape) if Q.dim() == 2 else dQ, dD
 
 
+@_entry
 def maxsim_backward_dq(D, argmax, dS, nq=None, doc_len=None, dQ=None, workspace=None, stream=None):
     """dQ only (frozen document side). D [B,Nd,d]; argmax [n_queries,B,nq]
     int32; dS [n_queries,B] fp32. Returns dQ [n_queries,nq,d] fp32."""
@@ -532,6 +547,7 @@ def maxsim_backward_dq(D, argmax, dS, nq=None, doc_len=None, dQ=None, workspace=
     return dQ
 
 
+@_entry
 def maxsim_backward_dd(Q, argmax, dS, nd, doc_len=None, dD=None, stream=None):
     """dD only (frozen query side). Q [nq,d] or [n_queries,nq,d]; argmax
     [n_queries,B,nq] int32; dS [n_queries,B] fp32. Returns dD [B,nd,d] fp32."""
@@ -573,11 +589,6 @@ def allreduce_dq(dQ, group=None):
 
 
 # --------------------------------------------------------- the token encoder
-#
-# ``stream=None`` is the current stream. With a stream given, the call runs on
-# it, and so does everything that makes its workspace and results; tensors that
-# the caller gives are ordered with that stream by the caller, and the results
-# are read elsewhere once that stream has been waited for.
 
 def _scratch(nbytes, device):
     """A workspace of the call's own."""

@@ -7,7 +7,7 @@ import torch
 import maxsim_scoring_02_gb300 as m
 from tests import _fake_cuda as fake
 
-BF, F32, I32, I64, U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+BF, F32, I8, I32, I64, U8 = torch.bfloat16, torch.float32, torch.int8, torch.int32, torch.int64, torch.uint8
 
 
 @pytest.fixture
@@ -19,16 +19,31 @@ def _calls(cuda, index=0):
     """Every entry point that makes something: (call, tensors that it makes)."""
     t = lambda shape, dtype: cuda.tensor(shape, dtype, index)  # noqa: E731
     q, k, x = t((6, 4, 64), BF), t((6, 2, 64), BF), t((6, 4, 64), BF)
+    Q, D, pq = t((1, 3, 64), BF), t((5, 8, 64), BF), (t((3, 64), F32), t((8, 16, 8), F32), t((9, 8), U8), t((3,), I64))
     off, lse, freq = t((3,), I64), t((4, 6), F32), t((32,), I64)
     return {
         "rotary": (lambda **kw: m.maxsim_rotary(x, freq, offsets=off, **kw), 1),
         "attention": (lambda **kw: m.maxsim_attention(q, k, k, off, want_lse=True, **kw), 2),
         "attention_backward": (lambda **kw: m.maxsim_attention_backward(x, q, k, k, x, lse, off, **kw), 4),
         "clip": (lambda **kw: m.maxsim_clip_grad_norm([t((8,), F32), t((9,), BF)], 1.0, **kw), 2),
+        "score": (lambda **kw: m.maxsim_score(Q, D, want_argmax=True, **kw), 2),
+        "length_order": (lambda **kw: m.maxsim_length_order(doc_len=t((5,), I32), nd=8, **kw), 2),
+        "score_ordered": (lambda **kw: m.maxsim_score_ordered(Q, D, t((5,), I32), want_argmax=True, **kw), 2),
+        "score_streamed": (lambda **kw: m.maxsim_score_streamed(Q, torch.zeros((5, 8, 64), dtype=BF), want_argmax=True, **kw), 3),
+        "score_varlen": (lambda **kw: m.maxsim_score_varlen(Q, t((9, 64), BF), off, want_argmax=True, **kw), 2),
+        "score_pq": (lambda **kw: m.maxsim_score_pq(*pq, want_argmax=True, **kw), 3),
+        "score_pq_noalloc": (lambda **kw: m.maxsim_score_pq_noalloc(*pq, want_argmax=True, **kw), 2),
+        "score_i8": (lambda **kw: m.maxsim_score_i8(t((3, 64), I8), t((3,), F32), t((9, 64), I8), t((9,), F32), off,
+                                                    want_details=True, **kw), 4),
+        "backward": (lambda **kw: m.maxsim_backward(Q, D, t((1, 5, 3), I32), t((1, 5), F32), **kw), 3),
+        "backward_dq": (lambda **kw: m.maxsim_backward_dq(D, t((1, 5, 3), I32), t((1, 5), F32), **kw), 2),
+        "backward_dd": (lambda **kw: m.maxsim_backward_dd(Q, t((1, 5, 3), I32), t((1, 5), F32), 8, **kw), 1),
     }
 
 
-ENTRIES = ["rotary", "attention", "attention_backward", "clip"]
+ENTRIES = ["rotary", "attention", "attention_backward", "clip", "score", "length_order", "score_ordered",
+           "score_streamed", "score_varlen", "score_pq", "score_pq_noalloc", "score_i8", "backward", "backward_dq",
+           "backward_dd"]
 
 
 @pytest.mark.parametrize("name", ENTRIES)
