@@ -180,30 +180,65 @@ def _stream_on(stream, index):
     return (torch.cuda.current_stream(index) if stream is None else stream).cuda_stream
 
 
+_devices = None                               # CUDA devices of this process, once asked for
+_HERE = contextlib.nullcontext(lambda t: t)   # the current device and stream are the call's
+
+
+def _several():
+    global _devices
+    if _devices is None:
+        _devices = torch.cuda.device_count()
+    return _devices > 1
+
+
 @contextlib.contextmanager
-def _made_on(stream):
-    """Makes ``stream`` current for a call that launches on it, so that memory
-    which the call makes comes from that stream's pool. Memory of another
-    stream's pool may have been given up by work that has yet to run there, and
-    nothing would order that work and the call's. Yields a function that keeps
-    the result's memory from reuse until the caller's stream is done with it."""
-    outer = torch.cuda.current_stream()
-    with torch.cuda.stream(stream):
-        yield lambda t: t.record_stream(outer)
+def _moved(index, stream):
+    if stream is None:
+        with torch.cuda.device(index):
+            yield lambda t: t
+    else:
+        if stream.device.index != index:
+            raise ValueError("stream must be one of the tensors' device")
+        outer = torch.cuda.current_stream(index)
+        with torch.cuda.stream(stream):
+            yield lambda t: t.record_stream(outer)
+
+
+def _on(index, stream):
+    """Makes device ``index`` current for a call, and ``stream`` if one is
+    given. The library launches on the current device, where handle 0 is the
+    default stream of whichever that is. Memory that the call makes then comes
+    from its stream's pool: that of another may have been given up by work that
+    has yet to run there, and nothing would order that work and the call's.
+    Gives a function that keeps a result's memory from reuse until the caller's
+    stream is done with it."""
+    if stream is None and (not _several() or index == torch.cuda.current_device()):
+        return _HERE
+    return _moved(index, stream)
 
 
 def _entry(fn):
-    """An entry point whose last parameter is ``stream``: with one given, the
-    call's workspace and results are made on that stream, too."""
+    """An entry point whose last parameter is ``stream``: the call's tensors are
+    on one device, which is current for it, and with a stream given its
+    workspace and results are made there, too."""
     names = tuple(inspect.signature(fn).parameters)
     place = names.index("stream")
 
     @functools.wraps(fn)
     def call(*args, **kw):
         stream = args[place] if len(args) > place else kw.get("stream")
-        if stream is None:
+        if stream is None and not _several():
             return fn(*args, **kw)
-        with _made_on(stream) as keep:
+        index, first = None, None
+        for name, t in (*zip(names, args), *kw.items()):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                if index is None:
+                    index, first = t.get_device(), name
+                elif t.get_device() != index:
+                    raise ValueError(f"{name} must be on the same device as {first}")
+        if index is None:
+            return fn(*args, **kw)  # whose checks say what is wrong
+        with _on(index, stream) as keep:
             result = fn(*args, **kw)
             for t in result if isinstance(result, tuple) else (result,):
                 keep(t)
@@ -241,7 +276,8 @@ def maxsim_device_status(stream=None):
 
 # ------------------------------------------------------------- entry points
 #
-# ``stream=None`` is the current stream. With a stream given, the call runs on
+# All CUDA tensors of a call are on one device, which need not be the current
+# one. ``stream=None`` is that device's current stream. With a stream given, the call runs on
 # it, and so does everything that makes its workspace and results; tensors that
 # the caller gives are ordered with that stream by the caller, and the results
 # are read elsewhere once that stream has been waited for.
@@ -762,7 +798,6 @@ def _dtypes(tensors):
     return list(map(operator.attrgetter("dtype"), tensors))
 
 
-@_entry
 def maxsim_clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, stream=None):
     """Global 2-norm of the tensors ``grads`` (contiguous, bf16/fp16/fp32, types
     may be mixed), which are scaled by min(1, max_norm / (norm + 1e-6)): in
@@ -787,19 +822,27 @@ def maxsim_clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, 
         codes = array.array("i", map(_DTYPE_CODE.__getitem__, dtypes))
     except KeyError as e:
         raise TypeError(f"gradients must be bf16, fp16 or fp32, got {e.args[0]}") from None
-    index = places.pop() if places else torch.cuda.current_device()
-    device = torch.device("cuda", index)
-    if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device=device)
-    _dev(norm, "norm", torch.float32)
-    if workspace is None:
-        workspace = _scratch(lib.maxsim_clip_grad_norm_workspace_size(n), device)
-    _dev(workspace, "workspace", torch.uint8)
+    beside = [t for t in (norm, workspace) if t is not None]
+    places.update(_dev(t, "norm and workspace").get_device() for t in beside)
+    if len(places) > 1:
+        raise ValueError("norm and workspace must be on the tensors' device")
+    if not places:
+        places.add(torch.cuda.current_device() if stream is None else stream.device.index)
+    index = places.pop()
     pointers = array.array("Q", map(torch.Tensor.data_ptr, grads))
     targets = pointers if out is None else array.array("Q", map(torch.Tensor.data_ptr, outs))
     counts = array.array("q", sizes)
-    st = lib.maxsim_clip_grad_norm(pointers.buffer_info()[0], targets.buffer_info()[0], counts.buffer_info()[0],
-                                   codes.buffer_info()[0], n, max_norm, norm.data_ptr(), workspace.data_ptr(),
-                                   workspace.numel(), _stream_on(stream, index))
+    with _on(index, stream) as keep:
+        device = torch.device("cuda", index)
+        if norm is None:
+            norm = torch.empty(1, dtype=torch.float32, device=device)
+        _dev(norm, "norm", torch.float32)
+        if workspace is None:
+            workspace = _scratch(lib.maxsim_clip_grad_norm_workspace_size(n), device)
+        _dev(workspace, "workspace", torch.uint8)
+        st = lib.maxsim_clip_grad_norm(pointers.buffer_info()[0], targets.buffer_info()[0], counts.buffer_info()[0],
+                                       codes.buffer_info()[0], n, max_norm, norm.data_ptr(), workspace.data_ptr(),
+                                       workspace.numel(), _stream_on(stream, index))
+        keep(norm)
     _check(st, "maxsim_clip_grad_norm")
     return norm

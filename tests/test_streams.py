@@ -1,6 +1,9 @@
-"""What a call makes, and where: with ``stream=`` its workspace and its results
-come from that stream's memory, not from the current stream's, whose freed
-blocks may still be written by work that has yet to run."""
+"""Where a call runs and what it makes there: on its tensors' device, whichever
+is current; and with ``stream=`` its workspace and its results come from that
+stream's memory, not from the current stream's, whose freed blocks may still be
+written by work that has yet to run."""
+import inspect
+
 import pytest
 import torch
 
@@ -73,3 +76,67 @@ def test_the_stream_may_be_given_by_position(cuda):
     x, freq = cuda.tensor((6, 4, 64), BF), cuda.tensor((32,), I64)
     m.maxsim_rotary(x, freq, None, None, False, 1.0, False, None, other)
     assert [t.pool for t in cuda.made] == [other]
+
+
+@pytest.mark.parametrize("name", ENTRIES)
+def test_a_call_runs_on_its_tensors_device(cuda, name):
+    call, count = _calls(cuda, 1)[name]
+    call()
+    assert [device for _, device, _ in cuda.lib.calls] == [1] and cuda.device == 0
+    assert len(cuda.made) == count and all(t.index == 1 and t.pool is cuda.streams[1] for t in cuda.made)
+    other = fake.Stream(1, 0x99)
+    call(stream=other)
+    assert cuda.lib.calls[-1][1] == 1 and 0x99 in [getattr(a, "value", a) for a in cuda.lib.calls[-1][2]]
+
+
+@pytest.mark.parametrize("name", ENTRIES)
+def test_a_stream_of_another_device_is_refused(cuda, name):
+    call, _ = _calls(cuda, 1)[name]
+    with pytest.raises(ValueError):
+        call(stream=fake.Stream(0, 0x77))
+    assert not cuda.lib.calls
+
+
+ARGUMENTS = {
+    "maxsim_rotary": dict(x=((6, 4, 64), BF), freq=((32,), I64), offsets=((3,), I64), out=((6, 4, 64), BF)),
+    "maxsim_attention": dict(q=((6, 4, 64), BF), k=((6, 2, 64), BF), v=((6, 2, 64), BF), offsets=((3,), I64),
+                             key_len=((2,), I32), prefix_len=((2,), I32), slopes=((4,), F32), out=((6, 4, 64), BF),
+                             lse=((4, 6), F32)),
+    "maxsim_attention_backward": dict(dO=((6, 4, 64), BF), q=((6, 4, 64), BF), k=((6, 2, 64), BF), v=((6, 2, 64), BF),
+                                      out=((6, 4, 64), BF), lse=((4, 6), F32), offsets=((3,), I64),
+                                      key_len=((2,), I32), prefix_len=((2,), I32), slopes=((4,), F32),
+                                      dq=((6, 4, 64), BF), dk=((6, 2, 64), BF), dv=((6, 2, 64), BF),
+                                      workspace=((64,), U8)),
+    "maxsim_score": dict(Q=((1, 3, 64), BF), D=((5, 8, 64), BF), doc_len=((5,), I32), out=((1, 5), F32)),
+    "maxsim_backward": dict(Q=((1, 3, 64), BF), D=((5, 8, 64), BF), argmax=((1, 5, 3), I32), dS=((1, 5), F32)),
+}
+
+
+@pytest.mark.parametrize("name", ARGUMENTS)
+def test_tensors_of_two_devices_are_refused(cuda, name):
+    f, shapes = getattr(m, name), ARGUMENTS[name]
+    how = {"mask": "prefix"} if "prefix_len" in shapes else {}
+    every = lambda odd: {k: cuda.tensor(*v, 0 if k == odd else 1) for k, v in shapes.items()}  # noqa: E731
+    f(**every(None), **how)
+    assert len(cuda.lib.calls) == 1
+    for odd in shapes:
+        with pytest.raises(ValueError):
+            f(**every(odd), **how)
+    assert len(cuda.lib.calls) == 1
+
+
+def test_clipping_refuses_tensors_of_two_devices(cuda):
+    g = [cuda.tensor((8,), F32, 1), cuda.tensor((9,), F32, 1)]
+    for kw in ({"norm": cuda.tensor((1,), F32, 0)}, {"workspace": cuda.tensor((64,), U8, 0)},
+               {"out": [cuda.tensor((8,), F32, 0), cuda.tensor((9,), F32, 0)]}):
+        with pytest.raises(ValueError):
+            m.maxsim_clip_grad_norm(g, 1.0, **kw)
+    with pytest.raises(ValueError):
+        m.maxsim_clip_grad_norm([g[0], cuda.tensor((9,), F32, 0)], 1.0)
+    assert not cuda.lib.calls
+
+
+def test_every_entry_point_with_a_stream_is_covered():
+    with_stream = {n[len("maxsim_"):] for n in dir(m) if n.startswith("maxsim_") and n != "maxsim_device_status"
+                   and "stream" in inspect.signature(getattr(m, n)).parameters}
+    assert with_stream == {"clip_grad_norm" if n == "clip" else n for n in ENTRIES}
