@@ -181,7 +181,7 @@ def _stream_on(stream, index):
 
 
 _devices = None                               # CUDA devices of this process, once asked for
-_HERE = contextlib.nullcontext(lambda t: t)   # the current device and stream are the call's
+_STAY = contextlib.nullcontext(lambda t: t)   # the current device and stream are the call's
 
 
 def _several():
@@ -213,7 +213,7 @@ def _on(index, stream):
     Gives a function that keeps a result's memory from reuse until the caller's
     stream is done with it."""
     if stream is None and (not _several() or index == torch.cuda.current_device()):
-        return _HERE
+        return _STAY
     return _moved(index, stream)
 
 
