@@ -26,8 +26,8 @@ bool fits(const maxsim_heads* v) {
          v->head_stride < kMaxStride;
 }
 
-// Checks of a spec that both directions share. MAXSIM_OK with T == 0 or B == 0
-// means that there is nothing to do.
+// Checks of a spec that both directions share. MAXSIM_OK with T == 0 means that
+// there is nothing to do.
 maxsim_status check_spec(const maxsim_attention_spec* s) {
   if (!s || s->T < 0 || s->B < 0 || s->heads < 1 || s->kv_heads < 1 || s->d < 1 || !known(s->dtype))
     return MAXSIM_ERR_INVALID_ARG;
@@ -38,7 +38,8 @@ maxsim_status check_spec(const maxsim_attention_spec* s) {
   if (s->dtype == MAXSIM_FP32 || s->d % 8 != 0 || s->d > 128 || s->heads > 65535 || s->T >= INT_MAX - 256 ||
       s->B >= INT_MAX)
     return MAXSIM_ERR_UNSUPPORTED;
-  if (s->T == 0 || s->B == 0) return MAXSIM_OK;
+  if (s->T == 0) return MAXSIM_OK;
+  if (s->B == 0) return MAXSIM_ERR_INVALID_ARG;  // tokens, and no document that holds them
   if (!s->offsets || !multiple(s->offsets, 8) || !multiple(s->key_len, 4) || !multiple(s->prefix_len, 4) ||
       !multiple(s->slopes, 4) || (s->mask == MAXSIM_MASK_PREFIX && !s->prefix_len))
     return MAXSIM_ERR_INVALID_ARG;
@@ -132,7 +133,7 @@ maxsim_status maxsim_rotary(const maxsim_heads* x, int64_t T, int heads, int d, 
 maxsim_status maxsim_attention(const maxsim_attention_spec* spec, const maxsim_heads* q, const maxsim_heads* k,
                                const maxsim_heads* v, const maxsim_heads* out, float* lse, void* stream) {
   maxsim_status st = check_spec(spec);
-  if (st != MAXSIM_OK || spec->T == 0 || spec->B == 0) return st;
+  if (st != MAXSIM_OK || spec->T == 0) return st;
   if (!fits(q) || !fits(k) || !fits(v) || !fits(out) || !multiple(lse, 4)) return MAXSIM_ERR_INVALID_ARG;
   const DeviceInfo* dev = device_info();
   if (!dev) return MAXSIM_ERR_CUDA;
@@ -157,7 +158,7 @@ maxsim_status maxsim_attention_backward(const maxsim_attention_spec* spec, const
                                         const maxsim_heads* dk, const maxsim_heads* dv, void* workspace,
                                         size_t workspace_bytes, void* stream) {
   maxsim_status st = check_spec(spec);
-  if (st != MAXSIM_OK || spec->T == 0 || spec->B == 0) return st;
+  if (st != MAXSIM_OK || spec->T == 0) return st;
   if (!fits(dO) || !fits(q) || !fits(k) || !fits(v) || !fits(out) || !fits(dq) || !fits(dk) || !fits(dv) || !lse ||
       !multiple(lse, 4))
     return MAXSIM_ERR_INVALID_ARG;
