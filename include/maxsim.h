@@ -381,7 +381,9 @@ maxsim_status maxsim_backward_dd(const void *Q, int n_queries, int nq, int d,
  * maxsim_heads is a [T, heads, d] view of device memory with d contiguous
  * elements and any token and head strides (in elements), so that q, k and v may
  * lie side by side in one projection's output. The struct itself is on the
- * host.
+ * host. In a view that is written no two rows may share an element (one of its
+ * strides steps over all that the other one reaches, and both are at least d);
+ * others return MAXSIM_ERR_INVALID_ARG.
  */
 typedef struct maxsim_heads {
     void *data;

@@ -26,6 +26,17 @@ bool fits(const maxsim_heads* v) {
          v->head_stride < kMaxStride;
 }
 
+// No two rows of a view that is written share an element: the longer stride
+// steps over all that the shorter one reaches.
+bool apart(const maxsim_heads* v, int64_t T, int heads, int d) {
+  if ((heads > 1 && v->head_stride < d) || (T > 1 && v->token_stride < d)) return false;
+  if (heads == 1 || T == 1) return true;
+  const bool tokens_outside = v->head_stride <= v->token_stride;
+  const int64_t near = tokens_outside ? v->head_stride : v->token_stride, n = tokens_outside ? heads : T;
+  const int64_t far = tokens_outside ? v->token_stride : v->head_stride;
+  return (far - d) / near >= n - 1;  // far >= (n - 1) * near + d
+}
+
 // Checks of a spec that both directions share. MAXSIM_OK with T == 0 means that
 // there is nothing to do.
 maxsim_status check_spec(const maxsim_attention_spec* s) {
@@ -124,6 +135,7 @@ maxsim_status maxsim_rotary(const maxsim_heads* x, int64_t T, int heads, int d, 
       x->token_stride >= kMaxStride || x->head_stride >= kMaxStride || out->token_stride >= kMaxStride ||
       out->head_stride >= kMaxStride)
     return MAXSIM_ERR_INVALID_ARG;
+  if (!apart(out, T, heads, d)) return MAXSIM_ERR_INVALID_ARG;
   if (x->data == out->data && (x->token_stride != out->token_stride || x->head_stride != out->head_stride))
     return MAXSIM_ERR_INVALID_ARG;
   return launch_rotary(*x, T, heads, d, rot_dim, freq, offsets, B, positions, interleaved, amplitude, inverse, dtype,
@@ -135,6 +147,7 @@ maxsim_status maxsim_attention(const maxsim_attention_spec* spec, const maxsim_h
   maxsim_status st = check_spec(spec);
   if (st != MAXSIM_OK || spec->T == 0) return st;
   if (!fits(q) || !fits(k) || !fits(v) || !fits(out) || !multiple(lse, 4)) return MAXSIM_ERR_INVALID_ARG;
+  if (!apart(out, spec->T, spec->heads, spec->d)) return MAXSIM_ERR_INVALID_ARG;
   const DeviceInfo* dev = device_info();
   if (!dev) return MAXSIM_ERR_CUDA;
   AttnParams p = params_of(spec);
@@ -161,6 +174,9 @@ maxsim_status maxsim_attention_backward(const maxsim_attention_spec* spec, const
   if (st != MAXSIM_OK || spec->T == 0) return st;
   if (!fits(dO) || !fits(q) || !fits(k) || !fits(v) || !fits(out) || !fits(dq) || !fits(dk) || !fits(dv) || !lse ||
       !multiple(lse, 4))
+    return MAXSIM_ERR_INVALID_ARG;
+  if (!apart(dq, spec->T, spec->heads, spec->d) || !apart(dk, spec->T, spec->kv_heads, spec->d) ||
+      !apart(dv, spec->T, spec->kv_heads, spec->d))
     return MAXSIM_ERR_INVALID_ARG;
   if (!workspace || !multiple(workspace, 16) || workspace_bytes < maxsim_attention_backward_workspace_size(spec))
     return MAXSIM_ERR_WORKSPACE;

@@ -38,3 +38,36 @@ def test_tokens_without_a_document_are_refused(lib):
     """Nothing would be written, and the results would be what the memory held."""
     assert _forward(lib, B=0) == INVALID and _backward(lib, B=0) == INVALID
     assert _forward(lib, T=0, B=0) == 0 and _backward(lib, T=0, B=0) == 0
+
+
+# (token stride, head stride) of 100 tokens with 4 heads of 64 (2 of them for keys)
+APART = [(256, 64), (64, 6400), (64, 6408), (512, 128), (264, 64), (288, 72)]
+SHARED = [(64, 64), (248, 64), (64, 6328), (128, 64), (256, 56), (8, 6400), (256, 256), (96, 64)]
+
+
+
+@pytest.mark.parametrize("token,head", SHARED)
+def test_results_whose_rows_share_elements_are_refused(lib, token, head):
+    """Which block wrote such an element last would decide its value."""
+    bad, good = _heads(token=token, head=head), _heads()
+    assert _forward(lib, [good, good, good, bad]) == INVALID
+    for i in (5, 6, 7):
+        views = [good] * 8
+        views[i] = bad
+        if i == 5 or (token, head) not in ((128, 64), (248, 64)):   # two key-value heads of 64 lie within 128
+            assert _backward(lib, views) == INVALID, i
+    assert lib.maxsim_rotary(_heads(0x8000), 100, 4, 64, 64, 0x1000, None, 0, None, 0, 1.0, 0, 0, bad, None) == INVALID
+
+
+def test_rotary_results_without_a_stride_are_refused(lib):
+    for bad in (_heads(token=0), _heads(head=0)):
+        assert lib.maxsim_rotary(_heads(0x8000), 100, 4, 64, 64, 0x1000, None, 0, None, 0, 1.0, 0, 0, bad, None) == INVALID
+
+
+def test_rows_that_lie_apart_pass_that_check(lib):
+    """Past it comes the workspace's check, which these calls fail."""
+    for token, head in APART:
+        v = _heads(token=token, head=head)
+        assert lib.maxsim_attention_backward(_spec(), *[_heads()] * 5, 0x1000, v, v, v, None, 0, None) == 5
+    one = _heads(token=8, head=64)
+    assert lib.maxsim_attention_backward(_spec(T=1), *[_heads()] * 5, 0x1000, one, one, one, None, 0, None) == 5
