@@ -465,7 +465,8 @@ maxsim_status maxsim_rotary(const maxsim_heads *x, int64_t T, int heads, int d, 
  *
  * Scores, softmax statistics and sums are fp32 on tensor-core products of the
  * inputs; the weights are rounded to the inputs' type for their product with
- * v. Keys at or past key_len[b], and other documents, never reach a row, even
+ * v. A capped score is within 2^-22 of the cap for caps up to 128, within 2^-20 of
+ * itself for greater ones. Keys at or past key_len[b], and other documents, never reach a row, even
  * if they hold NaN or infinity. (A key that is hidden from a row only by the
  * order of tokens has weight 0 there, so its v must be finite.)
  *

@@ -368,7 +368,7 @@ struct MathConst {
 // the walked rows in shared memory or of this thread's own row. In an edge tile
 // columns outside [lo, hi) have weight 0 and those from `used` on are not
 // looked at; one code for both, since its size counts.
-template <bool kDkv, bool kBf16, bool kCap, bool kBias>
+template <bool kDkv, bool kBf16, Cap kCap, bool kBias>
 __device__ __forceinline__ void make_weights(uint32_t s_col, const MathConst& k, const float* nl, float own_nl,
                                              float slope2, float far, bool live, bool edge, int used, int lo, int hi,
                                              float (&e)[64], float (&bend)[kCap && !kDkv ? 64 : 1]) {
@@ -381,7 +381,7 @@ __device__ __forceinline__ void make_weights(uint32_t s_col, const MathConst& k,
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     if (q * 32 >= used) break;
-    if constexpr (kCap) tanh_group(u[q], k.in_cap, q * 32 + 32 <= used, live);
+    if constexpr (kCap != kNoCap) tanh_group<kCap == kWide>(u[q], k.in_cap, q * 32 + 32 <= used, live);
 #pragma unroll
     for (int x = 0; x < 32; x += 4) {
       float4 n;
@@ -391,12 +391,12 @@ __device__ __forceinline__ void make_weights(uint32_t s_col, const MathConst& k,
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         z[y] = __uint_as_float(u[q][x + y]);
-        if constexpr (kCap) {
+        if constexpr (kCap != kNoCap) {
           d[y] = fmaf(-z[y], z[y], 1.f);  // z is the tangent here
           if constexpr (kBias) z[y] *= k.cap2;
         }
         if constexpr (kBias) {
-          if constexpr (!kCap) z[y] *= k.to_log2;
+          if constexpr (kCap == kNoCap) z[y] *= k.to_log2;
           z[y] = fmaf(-slope2, fabsf(far - static_cast<float>(q * 32 + x + y)), z[y]);
         }
       }
@@ -405,7 +405,7 @@ __device__ __forceinline__ void make_weights(uint32_t s_col, const MathConst& k,
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         z[y] = fast_exp2(z[y]);
-        if constexpr (kCap) {
+        if constexpr (kCap != kNoCap) {
           if constexpr (kDkv) u[q][x + y] = __float_as_uint(z[y]), z[y] *= d[y];
           else bend[q * 32 + x + y] = d[y];
         }
@@ -417,7 +417,7 @@ __device__ __forceinline__ void make_weights(uint32_t s_col, const MathConst& k,
       for (int x = 0; x < 32; ++x)
         if (static_cast<unsigned>(q * 32 + x - lo) >= static_cast<unsigned>(hi - lo)) {
           e[q * 32 + x] = 0.f;
-          if constexpr (kCap) {
+          if constexpr (kCap != kNoCap) {
             if constexpr (kDkv) u[q][x] = 0;
             else bend[q * 32 + x] = 0.f;
           }
@@ -428,7 +428,7 @@ __device__ __forceinline__ void make_weights(uint32_t s_col, const MathConst& k,
 #pragma unroll
     for (int x = 0; x < 32; x += 2) {
       const float *a = e + q * 32 + x, *g = bend + (kCap && !kDkv ? q * 32 + x : 0);
-      if constexpr (!kCap) pk[x / 2] = pack2<kBf16>(a[0], a[1]);
+      if constexpr (kCap == kNoCap) pk[x / 2] = pack2<kBf16>(a[0], a[1]);
       else if constexpr (kDkv) pk[x / 2] = pack2<kBf16>(__uint_as_float(u[q][x]), __uint_as_float(u[q][x + 1]));
       else pk[x / 2] = pack2<kBf16>(a[0] * g[0], a[1] * g[1]);
     }
@@ -439,7 +439,7 @@ __device__ __forceinline__ void make_weights(uint32_t s_col, const MathConst& k,
 
 // dS of the same columns to TMEM. nd: minus delta, as nl. `rest` gathers the
 // sum over the row of e (dP - delta), which exact arithmetic makes 0.
-template <bool kDkv, bool kBf16, bool kCap>
+template <bool kDkv, bool kBf16, Cap kCap>
 __device__ __forceinline__ void make_ds(uint32_t dp_col, const float* nd, float own_nd, bool edge, int used,
                                         const float (&e)[64], const float (&bend)[kCap && !kDkv ? 64 : 1], Pair& rest) {
   uint32_t u[2][32];
@@ -483,7 +483,7 @@ __device__ __forceinline__ void make_ds(uint32_t dp_col, const float* nd, float 
   tmem_wait_st();
 }
 
-template <class S, int DH, int BC, bool kDkv, bool kBf16, bool kCap, bool kBias>
+template <class S, int DH, int BC, bool kDkv, bool kBf16, Cap kCap, bool kBias>
 __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t tmem) {
   const int wg = threadIdx.x >> 7, lane = threadIdx.x & 31, group = p.heads / p.kv_heads;
   const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;
@@ -527,7 +527,7 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
     }
     Pair rest(0.f, 0.f);
     for (int h = 0; h < g.heads; ++h) {
-      const float slope2 = kBias ? p.slopes[kDkv ? w.head * group + h : w.head] * kLog2e : 0.f;
+      const float slope2 = kBias && p.slopes ? p.slopes[kDkv ? w.head * group + h : w.head] * kLog2e : 0.f;
       for (int j = 0; j < g.steps; ++j, ++step) {
         const int from = g.begin + j * BC + wg * 64, used = min(64, g.end - from);  // this warpgroup's columns
         const bool edge = from < clear || g.begin + (j + 1) * BC > clear_end;
@@ -603,7 +603,7 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
   }
 }
 
-template <int DH, int BC, bool kDkv, bool kBf16, bool kCap, bool kBias>
+template <int DH, int BC, bool kDkv, bool kBf16, Cap kCap, bool kBias>
 __global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH, BC, kDkv>::kBlocks)
     attn_bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ AttnParams p) {
   using S = BwdShape<DH, BC, kDkv>;
@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(256) attn_stats_kernel(const AttnParams p, int
   }
 }
 
-template <int DH, int BC, bool kDkv, bool kBf16, bool kCap, bool kBias>
+template <int DH, int BC, bool kDkv, bool kBf16, Cap kCap, bool kBias>
 cudaError_t bwd_launch(const BwdMaps& m, const AttnParams& p, int sm_count, cudaStream_t stream) {
   using S = BwdShape<DH, BC, kDkv>;
   auto kern = attn_bwd_kernel<DH, BC, kDkv, kBf16, kCap, kBias>;
@@ -720,11 +720,13 @@ cudaError_t bwd_launch(const BwdMaps& m, const AttnParams& p, int sm_count, cuda
 
 template <int DH, int BC, bool kDkv, bool kBf16>
 cudaError_t bwd_variant(const BwdMaps& m, const AttnParams& p, int sm_count, cudaStream_t stream) {
+  if (p.cap > kWideCap)  // (rare: one kernel, whose slopes may be missing)
+    return bwd_launch<DH, BC, kDkv, kBf16, kWide, true>(m, p, sm_count, stream);
   if (p.cap > 0.f)
-    return p.slopes ? bwd_launch<DH, BC, kDkv, kBf16, true, true>(m, p, sm_count, stream)
-                    : bwd_launch<DH, BC, kDkv, kBf16, true, false>(m, p, sm_count, stream);
-  return p.slopes ? bwd_launch<DH, BC, kDkv, kBf16, false, true>(m, p, sm_count, stream)
-                  : bwd_launch<DH, BC, kDkv, kBf16, false, false>(m, p, sm_count, stream);
+    return p.slopes ? bwd_launch<DH, BC, kDkv, kBf16, kNarrow, true>(m, p, sm_count, stream)
+                    : bwd_launch<DH, BC, kDkv, kBf16, kNarrow, false>(m, p, sm_count, stream);
+  return p.slopes ? bwd_launch<DH, BC, kDkv, kBf16, kNoCap, true>(m, p, sm_count, stream)
+                  : bwd_launch<DH, BC, kDkv, kBf16, kNoCap, false>(m, p, sm_count, stream);
 }
 
 template <int DH, int BC>

@@ -238,27 +238,56 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// tanh(x) = x p(x^2) for |x| <= 0.7, with p of degree 5, fitted to tanh on that
+// interval by least squares reweighted towards equal errors: off by 1.3e-8
+// relatively, 7e-8 in fp32 arithmetic.
+constexpr float kTanhReach = 0.7f;
+__device__ __forceinline__ constexpr float tanh_fit(int i) {
+  constexpr float c[6] = {1.0f, -0.3333314061164856f, 0.13328571617603302f, -0.05353494733572006f,
+                          0.02004525437951088f, -0.005105282180011272f};
+  return c[i];
+}
+
+// How scores are capped. fast_tanh may be off by 2^-22, so all scores by that part
+// of the cap: up to 3e-5 for caps of 128. Beyond, where scores are small against
+// their cap and that error would reach them, the tangent is made right relatively,
+// to 2^-20 (kWide, in kernels of their own: in those for usual caps the additional
+// code cost 2 %; 24 documents of 1024 tokens, 16 heads of 128: forward 433 us where
+// narrow caps take 308, backward 1022 and 876).
+enum Cap { kNoCap, kNarrow, kWide };
+constexpr float kWideCap = 128.f;
+
+// Both forms are made and one is taken: a branch for each value took four times as long.
+__device__ __forceinline__ float close_tanh(float x) {
+  const float w = x * x, far = fast_tanh(2.f * 1.4426950408889634f * x);
+  float r = tanh_fit(5);
+#pragma unroll
+  for (int i = 4; i >= 0; --i) r = fmaf(r, w, tanh_fit(i));
+  float y;
+  asm("{\n\t.reg .pred p;\n\tsetp.le.f32 p, %1, %2;\n\tselp.f32 %0, %3, %4, p;\n\t}"
+      : "=f"(y)
+      : "f"(fabsf(x)), "f"(kTanhReach), "f"(x * r), "f"(far));
+  return y;
+}
+
 // u = tanh(k u) for 32 values of each lane. `whole`: the same for the warp, all
 // 32 are scores; `live`: this lane's are (others hold what was left there, and
 // must not decide how the rest is rounded). Through exp2 and a reciprocal a value
 // costs two of the special function unit's slots, and the softmax of capped
-// scores waits for that unit. Where no value of the warp exceeds 0.7 (scores up
-// to 0.7 cap), tanh(x) = x p(x^2) with p of degree 5, fitted to tanh on that
-// interval by least squares reweighted towards equal errors: off by 1.3e-8
-// relatively, 7e-8 in fp32 arithmetic.
+// scores waits for that unit: where no value of the warp exceeds 0.7 (scores up
+// to 0.7 cap) the polynomial makes all of them.
+template <bool kClose>
 __device__ __forceinline__ void tanh_group(uint32_t (&u)[32], float k, bool whole, bool live) {
   float top = 0.f;
 #pragma unroll
   for (int x = 0; x < 32; x += 2) top = max3(top, fabsf(__uint_as_float(u[x])), fabsf(__uint_as_float(u[x + 1])));
-  if (__all_sync(0xffffffffu, whole && (!live || top * k <= 0.7f))) {
-    constexpr float c[6] = {1.0f, -0.3333314061164856f, 0.13328571617603302f, -0.05353494733572006f,
-                            0.02004525437951088f, -0.005105282180011272f};
+  if (__all_sync(0xffffffffu, whole && (!live || top * k <= kTanhReach))) {
 #pragma unroll
     for (int x = 0; x < 32; x += 2) {
       const Pair v = mul2(Pair(__uint_as_float(u[x]), __uint_as_float(u[x + 1])), Pair(k, k)), w = mul2(v, v);
-      Pair r(c[5], c[5]);
+      Pair r(tanh_fit(5), tanh_fit(5));
 #pragma unroll
-      for (int i = 4; i >= 0; --i) r = fma2(r, w, Pair(c[i], c[i]));
+      for (int i = 4; i >= 0; --i) r = fma2(r, w, Pair(tanh_fit(i), tanh_fit(i)));
       float a, b;
       mul2(v, r).get(a, b);
       u[x] = __float_as_uint(a);
@@ -267,7 +296,10 @@ __device__ __forceinline__ void tanh_group(uint32_t (&u)[32], float k, bool whol
   } else {
     const float k2 = 2.f * 1.4426950408889634f * k;
 #pragma unroll
-    for (int x = 0; x < 32; ++x) u[x] = __float_as_uint(fast_tanh(__uint_as_float(u[x]) * k2));
+    for (int x = 0; x < 32; ++x) {
+      const float z = __uint_as_float(u[x]);
+      u[x] = __float_as_uint(kClose ? close_tanh(z * k) : fast_tanh(z * k2));
+    }
   }
 }
 

@@ -281,14 +281,15 @@ struct ScoreConst {
 
 // A group of 32 scores brought to the units that maxima are taken in; `far` is
 // the row less the group's first key, `lim` how many of its keys are seen.
-template <bool kCap, bool kBias, bool kEdge>
+template <Cap kCap, bool kBias, bool kEdge>
 __device__ __forceinline__ void finish_scores(uint32_t (&u)[32], const ScoreConst& k, float slope2, float far, int lim) {
 #pragma unroll
   for (int x = 0; x < 32; ++x) {
     float z = __uint_as_float(u[x]);
-    if constexpr (kCap) z = k.cap2 * fast_tanh(z * k.in_cap);
+    if constexpr (kCap == kNarrow) z = k.cap2 * fast_tanh(z * k.in_cap);
+    if constexpr (kCap == kWide) z = k.cap2 * close_tanh(z * k.in_cap);
     if constexpr (kBias) {
-      if constexpr (!kCap) z *= k.to_log2;
+      if constexpr (kCap == kNoCap) z *= k.to_log2;
       z = fmaf(-slope2, fabsf(far - static_cast<float>(x)), z);
     }
     if constexpr (kEdge) z = x < lim ? z : -INFINITY;
@@ -343,7 +344,7 @@ __device__ __forceinline__ void raise_max(uint32_t o_col, const ScoreConst& k, f
 // next group on its way, rather than kept: 128 registers of them spilled (0.70
 // against 0.40 ms for 16411 causal tokens, 8 heads of 128). Bent scores are
 // written back between.
-template <int DH, bool kBf16, bool kCap>
+template <int DH, bool kBf16, Cap kCap>
 __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, const ScoreConst& k, bool first, RowState& st) {
   uint32_t u[2][32];
   float now = st.m;
@@ -354,10 +355,10 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, con
     if (q < 3) tmem_ld_32x32b_x32_issue(s_col + (q + 1) * 32, u[(q + 1) & 1]);
     finish_scores<kCap, false, false>(u[q & 1], k, 0.f, 0.f, 32);
     now = group_max(u[q & 1], now);
-    if constexpr (kCap) tmem_st_32x32b_x32_issue(s_col + q * 32, u[q & 1]);
+    if constexpr (kCap != kNoCap) tmem_st_32x32b_x32_issue(s_col + q * 32, u[q & 1]);
     if (q < 3) tmem_wait_ld_regs(u[(q + 1) & 1]);
   }
-  if constexpr (kCap) tmem_wait_st();
+  if constexpr (kCap != kNoCap) tmem_wait_st();
   tmem_ld_32x32b_x32_issue(s_col, u[0]);
   raise_max<DH>(o_col, k, now, first, st);
   const float down = st.m == -INFINITY ? 0.f : -st.m * k.c;
@@ -380,7 +381,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, con
 // (those from `lim` on), with a distance bias: a loop over the groups of 32 that
 // there are, which compares columns only where a row of the warp needs it. Short
 // documents run here, and small code counts.
-template <int DH, bool kBf16, bool kCap, bool kBias>
+template <int DH, bool kBf16, Cap kCap, bool kBias>
 __device__ __forceinline__ void softmax_edge(uint32_t s_col, uint32_t o_col, const ScoreConst& k, float slope2,
                                              float far, int cols, int lim, bool first, RowState& st) {
   uint32_t u[32];
@@ -393,7 +394,7 @@ __device__ __forceinline__ void softmax_edge(uint32_t s_col, uint32_t o_col, con
     if (q < whole) finish_scores<kCap, kBias, false>(u, k, slope2, far - q * 32, 32);
     else finish_scores<kCap, kBias, true>(u, k, slope2, far - q * 32, lim - q * 32);
     now = group_max(u, now);
-    if (kCap || kBias || q >= whole) tmem_st_32x32b_x32_issue(s_col + q * 32, u);
+    if (kCap != kNoCap || kBias || q >= whole) tmem_st_32x32b_x32_issue(s_col + q * 32, u);
   }
   tmem_wait_st();
   raise_max<DH>(o_col, k, now, first, st);
@@ -412,7 +413,7 @@ __device__ __forceinline__ void softmax_edge(uint32_t s_col, uint32_t o_col, con
   tmem_wait_st();
 }
 
-template <int DH, int NQ, bool kBf16, bool kCap, bool kBias>
+template <int DH, int NQ, bool kBf16, Cap kCap, bool kBias>
 __device__ void fwd_softmax(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint32_t tmem) {
   using S = FwdShape<DH, NQ>;
   const int t = threadIdx.x >> 7, lane = threadIdx.x & 31;
@@ -420,7 +421,7 @@ __device__ void fwd_softmax(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint
   const uint32_t s_col = tmem + lanes + t * kTile, o_col = tmem + lanes + S::kO0 + t * DH;
   // scores are brought to log2 units by c, or are there already once bent or biased
   const ScoreConst k = {kCap || kBias ? 1.f : p.scale * kLog2e, p.scale * kLog2e, p.cap * kLog2e,
-                        kCap ? 2.f * kLog2e * p.scale / p.cap : 0.f};
+                        kCap == kWide ? p.scale / p.cap : kCap ? 2.f * kLog2e * p.scale / p.cap : 0.f};
   uint32_t sn = 0, on = 0;
   const auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
     return mbar_wait_warp(bar, ph & 1, sm.abort_flag, p.status);
@@ -436,7 +437,7 @@ __device__ void fwd_softmax(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint
     if (first >= w.len) continue;
     const int keys = tile_keys(w, p.mask, t), nk = tiles_of(keys);
     const int end = row_end(w, p.mask, min(row, w.len - 1)), all_see = row_end(w, p.mask, first);
-    const float slope2 = kBias ? p.slopes[w.head] * kLog2e : 0.f;
+    const float slope2 = kBias && p.slopes ? p.slopes[w.head] * kLog2e : 0.f;
     RowState st = {-INFINITY, 0.f, row < w.len};
     for (int j = 0; j < nk; ++j, ++sn) {
       if (!wait(sm.s_full(t), sn)) return;
@@ -483,7 +484,7 @@ __device__ void fwd_softmax(const AttnParams& p, const FwdSmem<DH, NQ>& sm, uint
   }
 }
 
-template <int DH, int NQ, bool kBf16, bool kCap, bool kBias>
+template <int DH, int NQ, bool kBf16, Cap kCap, bool kBias>
 __global__ void __launch_bounds__(FwdShape<DH, NQ>::kThreads, FwdShape<DH, NQ>::kBlocks)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnParams p) {
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(FwdShape<DH, NQ>::kThreads, FwdShape<DH, NQ>::
   }
 }
 
-template <int DH, int NQ, bool kBf16, bool kCap, bool kBias>
+template <int DH, int NQ, bool kBf16, Cap kCap, bool kBias>
 cudaError_t fwd_launch(const CUtensorMap* m, const AttnParams& p, int sm_count, cudaStream_t stream) {
   using S = FwdShape<DH, NQ>;
   auto kern = attn_fwd_kernel<DH, NQ, kBf16, kCap, kBias>;
@@ -548,11 +549,13 @@ cudaError_t fwd_launch(const CUtensorMap* m, const AttnParams& p, int sm_count, 
 
 template <int DH, int NQ, bool kBf16>
 cudaError_t fwd_variant(const CUtensorMap* m, const AttnParams& p, int sm_count, cudaStream_t stream) {
+  if (p.cap > kWideCap)  // (rare: one kernel, whose slopes may be missing)
+    return fwd_launch<DH, NQ, kBf16, kWide, true>(m, p, sm_count, stream);
   if (p.cap > 0.f)
-    return p.slopes ? fwd_launch<DH, NQ, kBf16, true, true>(m, p, sm_count, stream)
-                    : fwd_launch<DH, NQ, kBf16, true, false>(m, p, sm_count, stream);
-  return p.slopes ? fwd_launch<DH, NQ, kBf16, false, true>(m, p, sm_count, stream)
-                  : fwd_launch<DH, NQ, kBf16, false, false>(m, p, sm_count, stream);
+    return p.slopes ? fwd_launch<DH, NQ, kBf16, kNarrow, true>(m, p, sm_count, stream)
+                    : fwd_launch<DH, NQ, kBf16, kNarrow, false>(m, p, sm_count, stream);
+  return p.slopes ? fwd_launch<DH, NQ, kBf16, kNoCap, true>(m, p, sm_count, stream)
+                  : fwd_launch<DH, NQ, kBf16, kNoCap, false>(m, p, sm_count, stream);
 }
 
 template <int DH, int NQ>
