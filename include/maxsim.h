@@ -472,7 +472,7 @@ maxsim_status maxsim_rotary(const maxsim_heads *x, int64_t T, int heads, int d, 
  *
  * Limits: dtype BF16 or FP16 (FP32 returns MAXSIM_ERR_UNSUPPORTED); d a
  * multiple of 8, 8 <= d <= 128; heads a multiple of kv_heads, heads <= 65535;
- * T < 2^31 - 256; B < 2^31, and not 0 unless T is; scale > 0; all views 16-byte aligned with strides that are
+ * T < 2^31 - 256; B < 2^31, and not 0 unless T is; scale, and a cap > 0, from 2^-60 to 2^60; all views 16-byte aligned with strides that are
  * multiples of 8 elements, positive and below 2^39. out may overlap no input.
  * Inconsistent offsets, a key_len outside [0, length] (clamped) or a negative
  * prefix_len (taken as 0) set MAXSIM_DEVERR_BAD_INPUT; a document whose offsets

@@ -14,6 +14,8 @@ namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 constexpr int64_t kMaxStride = int64_t(1) << 39;
+constexpr float kLargest = 0x1p60f;  // of scale and cap, and of their reciprocals: the kernels' constants made of them
+                                     // (scale / cap, cap log2(e)) then neither overflow nor lose bits
 
 bool multiple(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
@@ -48,6 +50,8 @@ maxsim_status check_spec(const maxsim_attention_spec* s) {
   if (s->heads % s->kv_heads != 0) return MAXSIM_ERR_INVALID_ARG;
   if (s->dtype == MAXSIM_FP32 || s->d % 8 != 0 || s->d > 128 || s->heads > 65535 || s->T >= INT_MAX - 256 ||
       s->B >= INT_MAX)
+    return MAXSIM_ERR_UNSUPPORTED;
+  if (s->scale > kLargest || s->scale < 1.f / kLargest || (s->cap > 0.f && (s->cap > kLargest || s->cap < 1.f / kLargest)))
     return MAXSIM_ERR_UNSUPPORTED;
   if (s->T == 0) return MAXSIM_OK;
   if (s->B == 0) return MAXSIM_ERR_INVALID_ARG;  // tokens, and no document that holds them

@@ -5,7 +5,7 @@ import pytest
 import maxsim_scoring_02_gb300 as m
 from maxsim_scoring_02_gb300 import build as mbuild
 
-INVALID = 1
+INVALID, UNSUPPORTED = 1, 2
 
 
 @pytest.fixture(scope="module")
@@ -32,6 +32,18 @@ def _forward(lib, views=None, **change):
 def _backward(lib, views=None, **change):
     views = views or [_heads()] * 8
     return lib.maxsim_attention_backward(_spec(**change), *views[:5], 0x1000, *views[5:], 0x1000, 1 << 30, None)
+
+
+@pytest.mark.parametrize("change", [{"cap": 3e38}, {"cap": 2.0 ** 61}, {"cap": 1e-39}, {"cap": 2.0 ** -61},
+                                    {"scale": 2.0 ** 61}, {"scale": 3e38}, {"scale": 1e-39}])
+def test_scales_and_caps_out_of_the_kernels_range_are_refused(lib, change):
+    """3e38 log2(e) is infinite and scale / 1e-39 too: a score of 0 became NaN."""
+    assert _forward(lib, **change) == UNSUPPORTED and _backward(lib, **change) == UNSUPPORTED
+
+
+def test_the_ends_of_the_range_are_taken(lib):
+    for change in ({"cap": 2.0 ** 60}, {"cap": 2.0 ** -60}, {"scale": 2.0 ** 60}, {"scale": 2.0 ** -60}, {"cap": -1.0}):
+        assert lib.maxsim_attention_backward(_spec(**change), *[_heads()] * 5, 0x1000, *[_heads()] * 3, None, 0, None) == 5
 
 
 def test_tokens_without_a_document_are_refused(lib):

@@ -66,3 +66,10 @@ def test_wide_caps_that_scores_reach(run, d):
     """Scores of 0.3 caps on average: most tiles hold small ones and bent ones."""
     run([140, 3, 290], 2, 2, d, "bf16", 7, times=60.0, cap=200.0)
     run([500], 2, 1, d, "fp16", 9, times=60.0, cap=200.0, mask="causal", slopes=True)
+
+
+@pytest.mark.parametrize("cap", [2.0 ** 60, 2.0 ** -60])
+def test_the_widest_and_the_narrowest_cap(run, cap):
+    """Scores as they are, and scores that are all but equal."""
+    run([140, 3, 290], 2, 2, 64, "bf16", 11, cap=cap)
+    run([300], 2, 1, 128, "bf16", 13, cap=cap, mask="causal")
