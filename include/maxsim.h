@@ -512,7 +512,10 @@ maxsim_status maxsim_attention(const maxsim_attention_spec *spec, const maxsim_h
  * the block that owns the row: no atomics, results do not depend on
  * scheduling. Rows that see nothing and hidden keys have gradient 0. Slopes
  * are constants.
- * Sums are fp32; p and dS are rounded to the inputs' type for their products.
+ * Sums are fp32; p and dS are rounded to the inputs' type for their products. In
+ * FP16 both are held times a power of two that suits the document's largest dO
+ * and v, so that neither small gradients nor long documents lose bits; p_ij
+ * (dP_ij - <dO_i, out_i>) must stay below 65504 in size.
  * Limits as in maxsim_attention, for dO and the gradients too. workspace: at least
  * maxsim_attention_backward_workspace_size(spec) bytes, 16-byte aligned.
  */

@@ -78,6 +78,10 @@ AttnParams params_of(const maxsim_attention_spec* s) {
   return p;
 }
 
+size_t delta_bytes(const maxsim_attention_spec* s) {
+  return static_cast<size_t>(s->T) * s->heads * 2 * sizeof(float);
+}
+
 }  // namespace
 
 extern "C" {
@@ -166,7 +170,7 @@ maxsim_status maxsim_attention(const maxsim_attention_spec* spec, const maxsim_h
 
 size_t maxsim_attention_backward_workspace_size(const maxsim_attention_spec* spec) {
   if (check_spec(spec) != MAXSIM_OK) return 0;
-  return static_cast<size_t>(spec->T) * spec->heads * 2 * sizeof(float);
+  return delta_bytes(spec) + (spec->dtype == MAXSIM_FP16 ? static_cast<size_t>(spec->T) * sizeof(float2) : 0);
 }
 
 maxsim_status maxsim_attention_backward(const maxsim_attention_spec* spec, const maxsim_heads* dO,
@@ -198,6 +202,7 @@ maxsim_status maxsim_attention_backward(const maxsim_attention_spec* spec, const
   p.dk = *dk;
   p.dv = *dv;
   p.delta = static_cast<float*>(workspace);
+  if (spec->dtype == MAXSIM_FP16) p.shifts = reinterpret_cast<float2*>(static_cast<char*>(workspace) + delta_bytes(spec));
   return launch_attn_bwd(p, spec->dtype == MAXSIM_BF16, static_cast<cudaStream_t>(stream));
 }
 

@@ -39,6 +39,14 @@
 // columns. P and dS are rounded to the inputs' type for their products, as the
 // tensor cores take nothing wider at this rate; sums are fp32. `scale` is
 // applied to the sums.
+//
+// fp16 holds 2^-14 to 2^16 in full, but a weight among 16K keys is 2^-14 on
+// average and dS less by dO's size (dO of 1e-3 there: dS off by 4 %, dQ by 1.5 %). So
+// both are held times a power of two made of the document's greatest |dO_i| |v_j|,
+// which two small kernels find: it is added to the lse2 that scores are taken
+// from, and taken off the sums, so it is exact and costs the large kernels nothing
+// (the small ones read v once: 24 documents of 1024 tokens, 16 heads of 128, 0.70 ms
+// where bf16 takes 0.65).
 #include "attn_common.cuh"
 
 namespace msim {
@@ -192,7 +200,7 @@ __device__ void bwd_loader(const AttnParams& p, const BwdSmem<S, BC>& sm, const 
 // The walked rows' (lse2, delta), which every arithmetic thread needs: one
 // warp brings them to shared memory beside the tiles. Its arrival is part of
 // walk_full, so it also keeps an abort's drain from waiting for ever.
-template <class S, int BC>
+template <class S, int BC, bool kBf16>
 __device__ void bwd_stats(const AttnParams& p, const BwdSmem<S, BC>& sm) {
   const int lane = threadIdx.x & 31, group = p.heads / p.kv_heads;
   const float2* src = reinterpret_cast<const float2*>(p.delta);
@@ -205,6 +213,7 @@ __device__ void bwd_stats(const AttnParams& p, const BwdSmem<S, BC>& sm) {
     if (lane == 0) mbar_arrive_a(sm.info_empty(r));
     if (!w.live) return;
     const Range g = range_of<true, BC>(p, w);
+    const float shift = kBf16 ? 0.f : p.shifts[w.start].x;
     for (int h = 0; h < g.heads; ++h) {
       const float2* row = src + static_cast<int64_t>(w.head * group + h) * p.T + w.start;
       for (int j = 0; j < g.steps; ++j, ++step) {
@@ -219,7 +228,7 @@ __device__ void bwd_stats(const AttnParams& p, const BwdSmem<S, BC>& sm) {
           return;
 #pragma unroll
         for (int x = 0; x < BC / 32; ++x) {
-          sm.stats[s * 2 * BC + x * 32 + lane] = v[x].x;
+          sm.stats[s * 2 * BC + x * 32 + lane] = kBf16 ? v[x].x : v[x].x + shift;
           sm.stats[(s * 2 + 1) * BC + x * 32 + lane] = v[x].y;
         }
         __syncwarp();
@@ -344,10 +353,18 @@ __device__ __forceinline__ void store_sums(uint32_t col, uint32_t col2, uint32_t
       if constexpr (kOther) reg_order(o2);
 #pragma unroll
       for (int x = 0; x < 32; x += 2) {
-        float a = __uint_as_float(o[x]) * f, b = __uint_as_float(o[x + 1]) * f;
-        if constexpr (kOther) {
-          a = fmaf(__uint_as_float(o2[x]), f2, a);
-          b = fmaf(__uint_as_float(o2[x + 1]), f2, b);
+        float a, b;
+        if constexpr (kBf16) {
+          a = __uint_as_float(o[x]) * f;
+          b = __uint_as_float(o[x + 1]) * f;
+          if constexpr (kOther) {
+            a = fmaf(__uint_as_float(o2[x]), f2, a);
+            b = fmaf(__uint_as_float(o2[x + 1]), f2, b);
+          }
+        } else {
+          Pair v = mul2(Pair(__uint_as_float(o[x]), __uint_as_float(o[x + 1])), Pair(f, f));
+          if constexpr (kOther) v = fma2(Pair(__uint_as_float(o2[x]), __uint_as_float(o2[x + 1])), Pair(f2, f2), v);
+          v.get(a, b);
         }
         y[half * 16 + x / 2] = pack2<kBf16>(a, b);
       }
@@ -521,7 +538,7 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
         hi = row_end(w, p.mask, mine);
         own_stats = reinterpret_cast<float2*>(p.delta) + static_cast<int64_t>(w.head) * p.T + w.start + mine;
         const float2 st = *own_stats;
-        own_nl = st.x;
+        own_nl = kBf16 ? st.x : st.x + p.shifts[w.start + mine].x;
         own_nd = st.y;
       }
     }
@@ -555,6 +572,7 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
       }
     }
     const bool any = g.steps > 0, live = mine < w.len;
+    const float unshift = kBf16 || !any ? 1.f : p.shifts[w.start + w.row0].y;
     float off = 0.f;
     if constexpr (!kDkv) {
       float a, b;
@@ -569,6 +587,7 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
         ++rows_done;
         off = both[threadIdx.x & 127] + both[128 + (threadIdx.x & 127)];
       }
+      off *= unshift;
       if (live && any && wg == 0) own_stats->y = own_nd - off;
     }
     if (any) {
@@ -584,7 +603,7 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
     };
     constexpr int kChunks = DH / 64;
     const uint32_t sum0 = tmem + lanes + S::kSum0, sum1 = tmem + lanes + S::kSum1;
-    if constexpr (kDkv) {
+    if constexpr (kDkv && kBf16) {
 #pragma unroll
       for (int q = 0; q < kChunks; ++q) {  // two warpgroups: one writes dV, one dK
         if (S::kGroups == 1 || wg == 0)
@@ -592,12 +611,24 @@ __device__ void bwd_math(const AttnParams& p, const BwdSmem<S, BC>& sm, uint32_t
         if (S::kGroups == 1 || wg == 1)
           store_sums<kBf16, false>(sum1 + q * 64, 0, stage, base(p.dk), p.dk.token_stride, rows, q * 64, p.d, p.scale, 0.f, any);
       }
+    } else if constexpr (kDkv) {
+      // The same with a factor for dV too: one rolled code for both, with packed
+      // products, since its size counts (2500 passages, 12 heads of 64: 1.54 ms, and
+      // 1.62 written as above; bf16 at 400 documents of 150: 0.49 above, 0.51 here).
+#pragma unroll 1
+      for (int x = 0; x < 2 * kChunks / S::kGroups; ++x) {
+        const bool is_dk = S::kGroups == 2 ? wg == 1 : x >= kChunks;
+        const int q = x % kChunks;
+        const HeadsView to = is_dk ? p.dk : p.dv;
+        store_sums<kBf16, false>((is_dk ? sum1 : sum0) + q * 64, 0, stage, base(to), to.token_stride, rows, q * 64, p.d,
+                                 is_dk ? p.scale * unshift : unshift, 0.f, any);
+      }
     } else {
 #pragma unroll
       for (int q = 0; q < kChunks; ++q)
         if (S::kGroups == 1 || q % 2 == wg)  // (heads of 64: the second warpgroup has none)
           store_sums<kBf16, true>(sum1 + q * 64, sum0 + q * 64, stage, base(p.dq), p.dq.token_stride, rows, q * 64, p.d,
-                                  p.scale, -off * p.scale, any);
+                                  p.scale * unshift, -off * p.scale * unshift, any);
     }
     tc_fence_before();  // the next item's first products overwrite the sums after its p_full / ds_full
   }
@@ -650,7 +681,7 @@ __global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH,
       if ((threadIdx.x & 31) == 0) bwd_loader<S, BC, kDkv>(p, sm, m);
     } else if (warp == kMathWarps + 3) plan_work(p, sm, kTile, kDkv ? p.kv_heads : p.heads, !kDkv && p.mask != MAXSIM_MASK_FULL);
     else if (warp == kMathWarps + 1) bwd_products<S, DH, BC, kDkv, kBf16>(p, sm, tmem);
-    else if (kDkv && warp == kMathWarps + 2) bwd_stats<S, BC>(p, sm);
+    else if (kDkv && warp == kMathWarps + 2) bwd_stats<S, BC, kBf16>(p, sm);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::math_regs(kCap)));
     bwd_math<S, DH, BC, kDkv, kBf16, kCap, kBias>(p, sm, tmem);
@@ -664,45 +695,116 @@ __global__ void __launch_bounds__(BwdShape<DH, BC, kDkv>::kThreads, BwdShape<DH,
   }
 }
 
+// A row's 16 bytes of this lane, as floats.
+template <bool kBf16>
+__device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
+  const uint32_t* x = &w.x;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float2 y;
+    if constexpr (kBf16) y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(x + k));
+    else y = __half22float2(*reinterpret_cast<const __half2*>(x + k));
+    f[2 * k] = y.x;
+    f[2 * k + 1] = y.y;
+  }
+}
+
 // Minus lse in log2 units, and minus <dO, out>, of every row and head,
 // [heads][T]. A row is read by L lanes of 16 bytes each; a block takes kTokens
 // tokens with all their heads, which lie together in memory. Bound by HBM
-// (dO and out once).
+// (dO and out once). In fp16 it reads v beside them, for the greatest |dO|^2 and
+// |v|^2 among a token's heads; ones that are not finite are left out, as their
+// results are not finite in any range.
 constexpr int kTokens = 8;
 template <bool kBf16>
 __global__ void __launch_bounds__(256) attn_stats_kernel(const AttnParams p, int log_l) {
   check_docs(p, blockIdx.x * int64_t(256) + threadIdx.x, gridDim.x * int64_t(256));
   const int64_t t0 = blockIdx.x * int64_t(kTokens);
-  const unsigned heads = p.heads, rows = static_cast<unsigned>(min(static_cast<int64_t>(kTokens), p.T - t0)) * heads;
+  const unsigned tokens = static_cast<unsigned>(min(static_cast<int64_t>(kTokens), p.T - t0));
+  const unsigned heads = p.heads, kv_heads = p.kv_heads, rows = tokens * heads, keys = tokens * kv_heads;
   const int part = threadIdx.x & ((1 << log_l) - 1);
+  __shared__ unsigned reach[2 * kTokens];
+  if constexpr (!kBf16) {
+    if (threadIdx.x < 2 * kTokens) reach[threadIdx.x] = 0;
+    __syncthreads();
+  }
 #pragma unroll 2
   for (unsigned r0 = 0; r0 < rows; r0 += 256u >> log_l) {
     const unsigned r = r0 + (threadIdx.x >> log_l);
     const int64_t t = t0 + r / heads;
     const int h = static_cast<int>(r % heads);
-    float s = 0.f;
+    float s = 0.f, size = 0.f, size_v = 0.f;
     if (r < rows && part * 8 < p.d) {
+      uint4 v = {};
+      if constexpr (!kBf16)
+        if (r < keys) v = row_of(p.v, t0 + r / kv_heads, static_cast<int>(r % kv_heads))[part];
+      float f[8], g[8];
       const uint4 a = row_of(p.dO, t, h)[part], b = row_of(p.out, t, h)[part];
-      const uint32_t *x = &a.x, *y = &b.x;
+      unpack8<kBf16>(a, f);
+      unpack8<kBf16>(b, g);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float2 f, g;
-        if constexpr (kBf16) {
-          f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(x + k));
-          g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(y + k));
-        } else {
-          f = __half22float2(*reinterpret_cast<const __half2*>(x + k));
-          g = __half22float2(*reinterpret_cast<const __half2*>(y + k));
+      for (int k = 0; k < 8; k += 2) s = fmaf(f[k], g[k], fmaf(f[k + 1], g[k + 1], s));
+      if constexpr (!kBf16) {
+        unpack8<kBf16>(v, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          size = fmaf(f[k], f[k], size);
+          size_v = fmaf(g[k], g[k], size_v);
         }
-        s = fmaf(f.x, g.x, fmaf(f.y, g.y, s));
       }
     }
-    for (int o = 1 << log_l >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int o = 1 << log_l >> 1; o; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      if constexpr (!kBf16) {
+        size += __shfl_xor_sync(0xffffffffu, size, o);
+        size_v += __shfl_xor_sync(0xffffffffu, size_v, o);
+      }
+    }
     if (r < rows && part == 0) {
       const float lse = p.lse[static_cast<int64_t>(h) * p.T + t];
       reinterpret_cast<float2*>(p.delta)[static_cast<int64_t>(h) * p.T + t] =
           make_float2(lse == -INFINITY ? -INFINITY : -lse * kLog2e, -s);
+      if (!kBf16 && size < INFINITY) atomicMax(&reach[r / heads], __float_as_uint(size));
+      if (!kBf16 && size_v < INFINITY && r < keys) atomicMax(&reach[kTokens + r / kv_heads], __float_as_uint(size_v));
     }
+  }
+  if constexpr (!kBf16) {
+    __syncthreads();
+    if (threadIdx.x < tokens)
+      p.shifts[t0 + threadIdx.x] = make_float2(__uint_as_float(reach[threadIdx.x]), __uint_as_float(reach[kTokens + threadIdx.x]));
+  }
+}
+
+// P and dS = P (dP - delta) are held in fp16 times 2^shift. |dP| <= |dO_i| |v_j| and
+// |delta| <= |dO_i| |out_i|, with out_i among the visible v_j: twice the greatest
+// product bounds dS, and times 2^shift that stays below 2^15. From 0, what they are
+// without, to 14, which brings a weight of 1 to the upper end. Each token gets its
+// document's (shift, 2^-shift), in place of its own |dO|^2 and |v|^2.
+__global__ void __launch_bounds__(128) attn_shift_kernel(const AttnParams p) {
+  for (int64_t b = blockIdx.x; b < p.B; b += gridDim.x) {
+    bool bad;
+    const Doc c = load_doc(p, b, bad);
+    float2* of = p.shifts + c.start;
+    unsigned a = 0, v = 0;  // (floats >= 0 compare as their bits)
+#pragma unroll 4
+    for (int i = threadIdx.x; i < c.len; i += 128) {
+      const float2 x = of[i];
+      a = max(a, __float_as_uint(x.x));
+      if (i < c.keys) v = max(v, __float_as_uint(x.y));
+    }
+    a = __reduce_max_sync(0xffffffffu, a);
+    v = __reduce_max_sync(0xffffffffu, v);
+    __shared__ uint2 all[4];
+    if ((threadIdx.x & 31) == 0) all[threadIdx.x >> 5] = make_uint2(a, v);
+    __syncthreads();
+    a = max(max(all[0].x, all[1].x), max(all[2].x, all[3].x));
+    v = max(max(all[0].y, all[1].y), max(all[2].y, all[3].y));
+    const float both = __uint_as_float(a) * __uint_as_float(v);         // of the squares: below 2^80
+    const int x = static_cast<int>(__float_as_uint(both) >> 23) - 127;  // both < 2^(x+1)
+    const int shift = max(0, min(14, 14 - ((x + 2) >> 1)));
+    for (int i = threadIdx.x; i < c.len; i += 128)
+      of[i] = make_float2(static_cast<float>(shift), __uint_as_float(static_cast<unsigned>(127 - shift) << 23));
+    __syncthreads();
   }
 }
 
@@ -757,8 +859,13 @@ maxsim_status launch_attn_bwd(const AttnParams& p, int is_bf16, cudaStream_t str
   int log_l = 0;  // lanes of a row, a power of two
   while ((8 << log_l) < p.d) ++log_l;
   const unsigned blocks = static_cast<unsigned>((p.T + static_cast<int64_t>(kTokens) - 1) / kTokens);
-  if (is_bf16) attn_stats_kernel<true><<<blocks, 256, 0, stream>>>(p, log_l);
-  else attn_stats_kernel<false><<<blocks, 256, 0, stream>>>(p, log_l);
+  if (is_bf16) {
+    attn_stats_kernel<true><<<blocks, 256, 0, stream>>>(p, log_l);
+  } else {
+    attn_stats_kernel<false><<<blocks, 256, 0, stream>>>(p, log_l);
+    const int64_t most = 16 * static_cast<int64_t>(dev->sm_count);
+    attn_shift_kernel<<<static_cast<int>(p.B < most ? p.B : most), 128, 0, stream>>>(p);
+  }
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
     e = p.d > 64 ? bwd_both<128, 128>(dkv, dq, p, is_bf16, dev->sm_count, stream)

@@ -27,6 +27,7 @@ struct AttnParams {
   HeadsView q, k, v, out, dO, dq, dk, dv;
   float* lse;    // [heads, T] natural log of the softmax denominators, or null
   float* delta;  // [heads, T] pairs (-lse in log2 units, -<dO, out>), backward only
+  float2* shifts;  // [T] (shift, 2^-shift): P and dS are held times 2^shift; backward in fp16 only
   const int64_t* offsets;
   const int32_t* key_len;
   const int32_t* prefix_len;
