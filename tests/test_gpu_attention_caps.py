@@ -73,3 +73,46 @@ def test_the_widest_and_the_narrowest_cap(run, cap):
     """Scores as they are, and scores that are all but equal."""
     run([140, 3, 290], 2, 2, 64, "bf16", 11, cap=cap)
     run([300], 2, 1, 128, "bf16", 13, cap=cap, mask="causal")
+
+
+# Documents of 192 tokens and more on average run two tiles of rows a block at
+# d = 128; a group of 32 x 32 scores that all lie within 0.7 caps takes the
+# polynomial in the backward, which N(0,1) scores do at a cap of 30 and hardly
+# ever at 2.5.
+SHAPES = {"one tile": [140, 3, 290], "two tiles": [300, 1, 77, 513], "long": [1030]}
+MASKS = ["full", "causal", "prefix"]
+
+
+def _mask(lengths, mask):
+    if mask != "prefix":
+        return {"mask": mask}
+    return {"mask": mask, "prefix_len": [(5 * n + 3) // 7 + (i % 2) * 200 for i, n in enumerate(lengths)]}
+
+
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_usual_caps_and_small_scores(run, d, shape, mask):
+    n = SHAPES[shape]
+    run(n, 2, 2, d, "bf16", 15, cap=30.0, **_mask(n, mask))
+    run(n, 2, 1, d, "fp16", 17, cap=30.0, **_mask(n, mask))
+
+
+@pytest.mark.parametrize("cap", [30.0, 10.0, 2.5])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_caps_that_scores_reach(run, d, shape, cap):
+    """Queries four times as large: few scores beyond 0.7 caps, many, nearly all."""
+    run(SHAPES[shape], 2, 1, d, "bf16", 19, times=4.0, cap=cap)
+    run(SHAPES[shape], 2, 2, d, "fp16", 21, times=4.0, cap=cap, mask="causal")
+
+
+@pytest.mark.parametrize("cap", [0.0, 2.5, 30.0])
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_caps_with_a_distance_bias(run, d, shape, mask, cap):
+    n = SHAPES[shape]
+    run(n, 4, 2, d, "bf16", 23, cap=cap, slopes=True, **_mask(n, mask))
+    hidden = [max(0, x - 40) if i % 2 else x for i, x in enumerate(n)]
+    run(n, 2, 2, d, "fp16", 25, cap=cap, slopes=True, key_len=hidden, **_mask(n, mask))
