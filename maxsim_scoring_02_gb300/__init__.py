@@ -217,32 +217,39 @@ def _on(index, stream):
     return _moved(index, stream)
 
 
-def _entry(fn):
-    """An entry point whose last parameter is ``stream``: the call's tensors are
-    on one device, which is current for it, and with a stream given its
-    workspace and results are made there, too."""
-    names = tuple(inspect.signature(fn).parameters)
-    place = names.index("stream")
+def _elsewhere(fn, names, values):
+    """Calls an entry point with its tensors' device and its stream current."""
+    index, first = None, None
+    for name, t in zip(names, values):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            if index is None:
+                index, first = t.get_device(), name
+            elif t.get_device() != index:
+                raise ValueError(f"{name} must be on the same device as {first}")
+    if index is None:
+        return fn(*values)  # whose checks say what is wrong
+    with _on(index, values[names.index("stream")]) as keep:
+        result = fn(*values)
+        for t in result if isinstance(result, tuple) else (result,):
+            keep(t)
+        return result
 
-    @functools.wraps(fn)
-    def call(*args, **kw):
-        stream = args[place] if len(args) > place else kw.get("stream")
-        if stream is None and not _several():
-            return fn(*args, **kw)
-        index, first = None, None
-        for name, t in (*zip(names, args), *kw.items()):
-            if isinstance(t, torch.Tensor) and t.is_cuda:
-                if index is None:
-                    index, first = t.get_device(), name
-                elif t.get_device() != index:
-                    raise ValueError(f"{name} must be on the same device as {first}")
-        if index is None:
-            return fn(*args, **kw)  # whose checks say what is wrong
-        with _on(index, stream) as keep:
-            result = fn(*args, **kw)
-            for t in result if isinstance(result, tuple) else (result,):
-                keep(t)
-            return result
+
+def _entry(fn):
+    """An entry point with a ``stream`` parameter: the call's tensors are on one
+    device, which is current for it, and with a stream given its workspace and
+    results are made there, too. The common call, on the one device's current
+    stream, only passes through a function with fn's own parameters (packing
+    and unpacking them cost up to a microsecond)."""
+    params = inspect.signature(fn).parameters
+    names = tuple(params)
+    scope = {"fn": fn, "names": names, "several": _several, "elsewhere": _elsewhere}
+    exec(f"def call({', '.join(n if p.default is p.empty else n + '=None' for n, p in params.items())}):\n"
+         f"    if stream is None and not several():\n"
+         f"        return fn({', '.join(names)})\n"
+         f"    return elsewhere(fn, names, ({', '.join(names)},))\n", scope)
+    call = functools.wraps(fn)(scope["call"])
+    call.__defaults__ = fn.__defaults__
     return call
 
 
@@ -816,19 +823,20 @@ def maxsim_clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, 
         places.update(map(torch.Tensor.get_device, side))
         if not all(map(torch.Tensor.is_contiguous, side)):
             raise ValueError("all tensors must be contiguous")
+    if norm is not None:
+        places.add(_dev(norm, "norm", torch.float32).get_device())
+    if workspace is not None:
+        places.add(_dev(workspace, "workspace", torch.uint8).get_device())
     if len(places) > 1 or -1 in places:
         raise ValueError("all tensors must be on one CUDA device (the library has no CPU path)")
     try:
         codes = array.array("i", map(_DTYPE_CODE.__getitem__, dtypes))
     except KeyError as e:
         raise TypeError(f"gradients must be bf16, fp16 or fp32, got {e.args[0]}") from None
-    beside = [t for t in (norm, workspace) if t is not None]
-    places.update(_dev(t, "norm and workspace").get_device() for t in beside)
-    if len(places) > 1:
-        raise ValueError("norm and workspace must be on the tensors' device")
-    if not places:
-        places.add(torch.cuda.current_device() if stream is None else stream.device.index)
-    index = places.pop()
+    if places:
+        index = places.pop()
+    else:
+        index = torch.cuda.current_device() if stream is None else stream.device.index
     pointers = array.array("Q", map(torch.Tensor.data_ptr, grads))
     targets = pointers if out is None else array.array("Q", map(torch.Tensor.data_ptr, outs))
     counts = array.array("q", sizes)
@@ -836,10 +844,8 @@ def maxsim_clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, 
         device = torch.device("cuda", index)
         if norm is None:
             norm = torch.empty(1, dtype=torch.float32, device=device)
-        _dev(norm, "norm", torch.float32)
         if workspace is None:
             workspace = _scratch(lib.maxsim_clip_grad_norm_workspace_size(n), device)
-        _dev(workspace, "workspace", torch.uint8)
         st = lib.maxsim_clip_grad_norm(pointers.buffer_info()[0], targets.buffer_info()[0], counts.buffer_info()[0],
                                        codes.buffer_info()[0], n, max_norm, norm.data_ptr(), workspace.data_ptr(),
                                        workspace.numel(), _stream_on(stream, index))
