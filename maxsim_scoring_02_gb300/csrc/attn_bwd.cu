@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(256) attn_stats_kernel(const AttnParams p, int
   check_docs(p, blockIdx.x * int64_t(256) + threadIdx.x, gridDim.x * int64_t(256));
   const int64_t t0 = blockIdx.x * int64_t(kTokens);
   const unsigned tokens = static_cast<unsigned>(min(static_cast<int64_t>(kTokens), p.T - t0));
-  const unsigned heads = p.heads, kv_heads = p.kv_heads, rows = tokens * heads, keys = tokens * kv_heads;
+  const unsigned heads = p.heads, rows = tokens * heads;
   const int part = threadIdx.x & ((1 << log_l) - 1);
   __shared__ unsigned reach[2 * kTokens];
   if constexpr (!kBf16) {
@@ -733,11 +733,11 @@ __global__ void __launch_bounds__(256) attn_stats_kernel(const AttnParams p, int
     const unsigned r = r0 + (threadIdx.x >> log_l);
     const int64_t t = t0 + r / heads;
     const int h = static_cast<int>(r % heads);
+    const bool keyed = !kBf16 && h < p.kv_heads;  // the row reads v of the head of its own number
     float s = 0.f, size = 0.f, size_v = 0.f;
     if (r < rows && part * 8 < p.d) {
       uint4 v = {};
-      if constexpr (!kBf16)
-        if (r < keys) v = row_of(p.v, t0 + r / kv_heads, static_cast<int>(r % kv_heads))[part];
+      if (keyed) v = row_of(p.v, t, h)[part];
       float f[8], g[8];
       const uint4 a = row_of(p.dO, t, h)[part], b = row_of(p.out, t, h)[part];
       unpack8<kBf16>(a, f);
@@ -746,11 +746,18 @@ __global__ void __launch_bounds__(256) attn_stats_kernel(const AttnParams p, int
       for (int k = 0; k < 8; k += 2) s = fmaf(f[k], g[k], fmaf(f[k + 1], g[k + 1], s));
       if constexpr (!kBf16) {
         unpack8<kBf16>(v, g);
+        Pair x(0.f, 0.f), y(0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          size = fmaf(f[k], f[k], size);
-          size_v = fmaf(g[k], g[k], size_v);
+        for (int k = 0; k < 8; k += 2) {
+          const Pair a2(f[k], f[k + 1]), v2(g[k], g[k + 1]);
+          x = fma2(a2, a2, x);
+          y = fma2(v2, v2, y);
         }
+        float lo, hi;
+        x.get(lo, hi);
+        size = lo + hi;
+        y.get(lo, hi);
+        size_v = lo + hi;
       }
     }
     for (int o = 1 << log_l >> 1; o; o >>= 1) {
@@ -765,7 +772,7 @@ __global__ void __launch_bounds__(256) attn_stats_kernel(const AttnParams p, int
       reinterpret_cast<float2*>(p.delta)[static_cast<int64_t>(h) * p.T + t] =
           make_float2(lse == -INFINITY ? -INFINITY : -lse * kLog2e, -s);
       if (!kBf16 && size < INFINITY) atomicMax(&reach[r / heads], __float_as_uint(size));
-      if (!kBf16 && size_v < INFINITY && r < keys) atomicMax(&reach[kTokens + r / kv_heads], __float_as_uint(size_v));
+      if (keyed && size_v < INFINITY) atomicMax(&reach[kTokens + r / heads], __float_as_uint(size_v));
     }
   }
   if constexpr (!kBf16) {
