@@ -399,11 +399,15 @@ typedef struct maxsim_heads {
  *   NONE    theta_i
  *   LINEAR  theta_i / s (positions are interpolated)
  *   NTK     theta_i with base * s^(rot_dim / (rot_dim - 2))
- *   YARN    theta_i for pairs that turn often within original_length
- *           positions, theta_i / s for those that turn less than once, a
- *           linear ramp over i between them ("YaRN: Efficient Context Window
- *           Extension of Large Language Models", 3.2, with 32 turns and 1)
- * *amplitude receives 1, or 0.1 ln s + 1 for YARN (ibid., 3.4).
+ *   YARN    theta_i for pairs that turn more than 32 times within
+ *           original_length positions, theta_i / s for those that turn less
+ *           than once, and between them theta_i (1 - c) + theta_i / s c with c
+ *           linear in the pair's number i: 0 at the number (a real one, rounded
+ *           down) that turns 32 times, 1 at the one (rounded up) that turns
+ *           once. Checkpoints that were extended this way want this ramp; the
+ *           one of "YaRN: Efficient Context Window Extension of Large Language
+ *           Models", 3.2, is linear in the number of turns instead.
+ * *amplitude receives 1, or 0.1 ln s + 1 for YARN (that paper's 3.4).
  * rot_dim even and >= 2 (>= 4 for NTK), base > 1, s >= 1, original_length >= 1
  * for YARN; otherwise MAXSIM_ERR_INVALID_ARG.
  */
@@ -512,11 +516,18 @@ maxsim_status maxsim_attention(const maxsim_attention_spec *spec, const maxsim_h
  * the block that owns the row: no atomics, results do not depend on
  * scheduling. Rows that see nothing and hidden keys have gradient 0. Slopes
  * are constants.
+ * lse and out have to be those of this call's keys alone: the rounding of
+ * <dO_i, out_i> is mended by sum_j p_ij = 1 and sum_j p_ij dP_ij = <dO_i, out_i>,
+ * so an lse merged over shards of the keys gives wrong dQ and dK.
+ * dO, q, k and v must be finite where a row and a key that only the order of
+ * tokens hides from one another lie in one document.
  * Sums are fp32; p and dS are rounded to the inputs' type for their products. In
  * FP16 both are held times a power of two that suits the document's largest dO
  * and v, so that neither small gradients nor long documents lose bits; p_ij
  * (dP_ij - <dO_i, out_i>) must stay below 65504 in size.
- * Limits as in maxsim_attention, for dO and the gradients too. workspace: at least
+ * Limits as in maxsim_attention, for dO and the gradients too; heads / kv_heads
+ * times a document's length below about 10^8 (the block that owns 128 keys walks
+ * over that many rows, and waits are bounded by 2 s). workspace: at least
  * maxsim_attention_backward_workspace_size(spec) bytes, 16-byte aligned.
  */
 size_t maxsim_attention_backward_workspace_size(const maxsim_attention_spec *spec);
@@ -533,7 +544,9 @@ maxsim_status maxsim_attention_backward(const maxsim_attention_spec *spec, const
  * The four arrays are on the HOST and are read before the call returns;
  * grads[i] and outs[i] are device pointers to sizes[i] contiguous elements of
  * dtypes[i] (a maxsim_dtype; types may be mixed), aligned to their elements.
- * outs[i] may be grads[i] (in place), and overlaps no other tensor otherwise.
+ * outs[i] may be grads[i] (in place), and overlaps no other tensor otherwise. An
+ * outs[i] that lies differently from grads[i] against 16-byte boundaries is
+ * written element by element (twice the time for a whole encoder's gradients).
  * *norm (device, fp32) receives the norm before clipping. Squares are added in
  * fp32 within a thread's part of a 32 KB chunk and in fp64 beyond, in an order that depends
  * only on the sizes; values whose squares leave fp32's range are added in fp64.

@@ -581,8 +581,11 @@ maxsim_status launch_attn_fwd(const AttnParams& p, int is_bf16, cudaStream_t str
       !attn_tmap(&m[2], p.v, p.T, p.kv_heads, p.d, is_bf16, kBoxRows))
     return MAXSIM_ERR_CUDA;
   // Two tiles of rows a block halve the traffic of K and V, which heads of 128
-  // need (24 documents of 1024 tokens, 16 heads: 159 against 206 us; 300 of 256,
-  // 12 heads: 150 against 178), unless documents fit one tile. Heads of 64 run
+  // need (24 documents of 1024 tokens, 16 heads: 159 against 197 us; 300 of 256,
+  // 12 heads: 150 against 178), unless documents fit one tile. The number of pieces
+  // is not looked at: where few leave SMs idle, tiles of their own gain little (one
+  // document of 1024, 16 heads: 17.3 against 16.4 us; two: 18.1 against 20.5; one of
+  // 4096, 4 heads: 49.3 against 47.5). Heads of 64 run
   // better as two blocks of one tile (300 documents of 256 tokens, 12 heads: 100
   // against 112 us; of 320: 181 against 231; 64 of 1024: 254 against 280; 200 of 512:
   // 223 against 216; 160 ragged ones with a distance bias: 119 against 131).

@@ -12,7 +12,9 @@
 // chunks from the last to the first: what the first kernel read last is still
 // in L2. Bound by HBM: one read for the norm, one read and one write: 264 M fp32
 // elements 497 us for both (6.4 TB/s), 516 with six blocks an SM and streaming
-// accesses, 562 with four and 64 KB chunks.
+// accesses, 562 with four and 64 KB chunks. An output that lies differently from
+// its input against 16-byte boundaries is written element by element: 196 tensors,
+// 132.8 M bf16 elements 304 us for both where vectors take 140.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
