@@ -182,28 +182,28 @@ def run(state):
 
 def _own_dropout(s):
     import maxsim_scoring_02_gb300 as m
-    return m.maxsim_dropout(s["x"], s["p"], s["rng"], residual=s["res"])
+    return m.encoder_dropout(s["x"], s["p"], s["rng"], residual=s["res"])
 
 
 def _own_norm(s):
     import maxsim_scoring_02_gb300 as m
     drop = {"p": s["p"], "rng": s["rng"]} if s["p"] else {}
     if s["fmt"] != "none":
-        got = m.maxsim_rms_norm(s["x"], s["weight"], residual=s["res"], fmt=s["fmt"], want_sum=s["residual"], **drop)
+        got = m.encoder_rms_norm(s["x"], s["weight"], residual=s["res"], fmt=s["fmt"], want_sum=s["residual"], **drop)
         return (_values(got[0], got[1]),) + tuple(got[1:])
     if not s["train"]:
-        return m.maxsim_rms_norm(s["x"], s["weight"], residual=s["res"], want_sum=s["residual"], **drop)
-    y, total = m.maxsim_rms_norm(s["x"], s["weight"], residual=s["res"], want_sum=True, **drop)
-    dx, dres, dw = m.maxsim_rms_norm_backward(s["dy"], total, s["weight"], dsum=s["dsum"], **drop)
+        return m.encoder_rms_norm(s["x"], s["weight"], residual=s["res"], want_sum=s["residual"], **drop)
+    y, total = m.encoder_rms_norm(s["x"], s["weight"], residual=s["res"], want_sum=True, **drop)
+    dx, dres, dw = m.encoder_rms_norm_backward(s["dy"], total, s["weight"], dsum=s["dsum"], **drop)
     return y, total, dx, dres, dw
 
 
 def _own_loss(s):
     import maxsim_scoring_02_gb300 as m
-    loss, lse = m.maxsim_cross_entropy(s["x"], s["weight"], s["targets"], scale=s["scale"])
+    loss, lse = m.encoder_cross_entropy(s["x"], s["weight"], s["targets"], scale=s["scale"])
     if not s["train"]:
         return loss, lse
-    dx, dw = m.maxsim_cross_entropy_backward(s["dloss"], s["x"], s["weight"], s["targets"], lse, scale=s["scale"])
+    dx, dw = m.encoder_cross_entropy_backward(s["dloss"], s["x"], s["weight"], s["targets"], lse, scale=s["scale"])
     return loss, lse, dx, dw
 
 
