@@ -560,6 +560,163 @@ maxsim_status maxsim_clip_grad_norm(const void *const *grads, void *const *outs,
                                     const int32_t *dtypes, int n_tensors, float max_norm, float *norm,
                                     void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Operators on rows of hidden states: what a layer of the encoder has between its
+ * attention and its projections, and the loss that it is pretrained with.
+ * maxsim_rows is a [T, d] view of device memory with d contiguous elements and any
+ * row stride (in elements): a view that is read may have rows that coincide (a
+ * stride of 0), one that is written may not. The struct itself is on the host.
+ */
+typedef struct maxsim_rows {
+    void *data;
+    int64_t row_stride;
+} maxsim_rows;
+
+/*
+ * maxsim_dropout -- dropout from a counter-based generator, and the residual's
+ * addition:
+ *   out[t, j] = residual[t, j] + (lot(t, j) >= limit ? x[t, j] * f : 0)
+ *   limit = round(65536 p),  f = 65536 / (65536 - limit)
+ * The mask is never stored: lot(t, j) is made from the place. Philox4x32-10 with
+ * the two words of rng[0] (low, high) as its key turns the counter (j / 8, t, low
+ * and high word of rng[1]) into four words: eight lots of 16 bits for columns
+ * 8 (j / 8) .. + 7, low half first. The gradient of x is the call on the gradient
+ * of out without a residual.
+ *
+ *   x, residual, out  [T, d] views of dtype BF16, FP16 or FP32, aligned to their
+ *                     elements; residual may be NULL. out may be x or residual
+ *                     (same stride), or other columns of their rows; other overlap
+ *                     returns MAXSIM_ERR_INVALID_ARG.
+ *   p                 0 <= p < 1 - 2^-17; the chance is limit / 65536
+ *   rng               [2] int64 on the DEVICE (NULL where limit is 0): a seed, and
+ *                     a number that differs between the calls that share it. A
+ *                     captured call reads them when it is replayed.
+ *
+ * A dropped element is 0 (or the residual) even where x is not finite. Arithmetic is
+ * fp32, rounded once. Limits: T < 2^31 - 256, row strides below 2^38. Views whose
+ * rows do not all begin on 16-byte boundaries, or whose d is not a multiple of 8, are
+ * moved element by element.
+ */
+maxsim_status maxsim_dropout(const maxsim_rows *x, const maxsim_rows *residual, int64_t T, int32_t d,
+                             float p, const int64_t *rng, maxsim_dtype dtype, const maxsim_rows *out,
+                             void *stream);
+
+/*
+ * maxsim_rms_norm -- root-mean-square norm of rows, with dropout and the
+ * residual's addition before it:
+ *   h = residual + dropped(x) as maxsim_dropout makes it, in the rows' dtype
+ *   y[t, j] = h[t, j] * weight[j] / sqrt(mean_j h[t, j]^2 + eps)
+ * and out is y in the rows' dtype, or in 8 bits with a scale a row:
+ *   scale[t] = max(max_j |y[t, j]|, 1e-30) / 127 (INT8) or / 448 (E4M3)
+ *   out[t, j] = y[t, j] / scale[t], rounded to nearest, ties to even
+ * INT8 rows and their scales are documents or queries of maxsim_score_i8. A row
+ * with a y that is not finite gets a scale that is none, too.
+ *
+ *   x, residual  [T, d] views of dtype; residual may be NULL
+ *   sum          [T, d] view that receives h, or NULL; maxsim_rms_norm_backward
+ *                needs it. It may be x or residual.
+ *   out          [T, d] view of dtype (SAME; it may be x or residual) or of bytes
+ *   scale        [T] fp32; 8-bit formats only
+ *   spec         weight [d] of weight_dtype (FP32 or dtype), or NULL (all 1);
+ *                p and rng as in maxsim_dropout (p = 0: no dropout)
+ *
+ * Overlaps as in maxsim_dropout; sum and out may not be the same. Sums are fp32, and
+ * fp64 where squares leave fp32's range. Limits: d <= 16384, T < 2^31 - 256, eps
+ * from 2^-60 to 2^60.
+ */
+typedef enum maxsim_norm_format {
+    MAXSIM_NORM_SAME = 0,
+    MAXSIM_NORM_INT8 = 1,
+    MAXSIM_NORM_E4M3 = 2
+} maxsim_norm_format;
+
+typedef struct maxsim_norm_spec {
+    int64_t T;
+    int32_t d;
+    maxsim_dtype dtype, weight_dtype;
+    maxsim_norm_format format;
+    float eps;
+    float p;
+    const int64_t *rng;  /* [2], device, or NULL */
+    const void *weight;  /* [d], device, or NULL */
+} maxsim_norm_spec;
+
+maxsim_status maxsim_rms_norm(const maxsim_norm_spec *spec, const maxsim_rows *x, const maxsim_rows *residual,
+                              const maxsim_rows *sum, const maxsim_rows *out, float *scale, void *stream);
+
+/*
+ * maxsim_rms_norm_backward -- gradients of maxsim_rms_norm (format SAME), from
+ * its sum h and the gradient dy of its out:
+ *   g = dy * weight,  rstd = 1 / sqrt(mean h^2 + eps)
+ *   dresidual = rstd * (g - h * mean(g h) rstd^2) + dsum
+ *   dx = dropout of dresidual with the call's p and rng
+ *   dweight[j] = sum_t dy[t, j] h[t, j] rstd[t]
+ *   dy, h        [T, d] views of dtype
+ *   dsum         the gradient that reaches the sum from elsewhere, or NULL
+ *   dx, dresidual  [T, d] views of dtype, each or NULL; either may be dy, h or
+ *                dsum (same stride). Without dropout they are the same numbers.
+ *   dweight      [d] of weight_dtype, or NULL
+ * dweight is added up in an order that depends on T, d and the number of SMs alone,
+ * without atomics. workspace: at least maxsim_rms_norm_backward_workspace_size(spec)
+ * bytes, 16-byte aligned, where dweight is given. With T = 0 dweight is 0.
+ */
+size_t maxsim_rms_norm_backward_workspace_size(const maxsim_norm_spec *spec);
+maxsim_status maxsim_rms_norm_backward(const maxsim_norm_spec *spec, const maxsim_rows *dy, const maxsim_rows *h,
+                                       const maxsim_rows *dsum, const maxsim_rows *dx,
+                                       const maxsim_rows *dresidual, void *dweight, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
+/*
+ * maxsim_cross_entropy -- softmax cross entropy over a vocabulary, whose logits
+ * are never written to memory:
+ *   z[t, v] = scale * <x_t, w_v>,  lse[t] = ln sum_v exp z[t, v]
+ *   loss[t] = lse[t] - z[t, targets[t]], or 0 where targets[t] < 0 (no target)
+ * A target >= V counts as none and sets MAXSIM_DEVERR_BAD_INPUT.
+ *   x            [T, d] view, weight [V, d] view (dtype BF16 or FP16)
+ *   loss, lse    [T] fp32
+ * Products are fp32 sums on the tensor cores, statistics fp32. A logit that is not
+ * finite makes its row's lse and loss NaN (minus infinity: a weight of 0).
+ * workspace: at least maxsim_cross_entropy_workspace_size(spec) bytes, 16-byte
+ * aligned.
+ * Limits: FP32 returns MAXSIM_ERR_UNSUPPORTED; d a multiple of 8, d <= 65536;
+ * V >= 1; T, V < 2^31 - 256; scale from 2^-60 to 2^60; views 16-byte aligned with
+ * strides that are multiples of 8 and at least d.
+ */
+typedef struct maxsim_loss_spec {
+    int64_t T, V;
+    int32_t d;
+    maxsim_dtype dtype;
+    float scale;
+    const int64_t *targets;  /* [T], device */
+} maxsim_loss_spec;
+
+size_t maxsim_cross_entropy_workspace_size(const maxsim_loss_spec *spec);
+maxsim_status maxsim_cross_entropy(const maxsim_loss_spec *spec, const maxsim_rows *x, const maxsim_rows *weight,
+                                   float *loss, float *lse, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/*
+ * maxsim_cross_entropy_backward -- gradients of maxsim_cross_entropy, from its
+ * lse and the gradient dloss [T] fp32 of its loss:
+ *   dz[t, v] = dloss[t] * scale * (exp(z[t, v] - lse[t]) - (v == targets[t]))
+ *   dx = dz W [T, d],  dweight = dz^T x [V, d], in the inputs' dtype
+ * dx or dweight may be NULL (a frozen side). Rows without a target have gradient 0;
+ * x has to be finite there, too (0 * infinity is NaN in dweight).
+ * The logits are made again, a piece of the vocabulary at a time: the workspace
+ * holds one piece's dz in the inputs' type (256 MB, or 256 columns where T is above
+ * 524288), times a power of two so that small dloss lose no bits, and fp32 sums of
+ * dx where the vocabulary has several pieces or few rows. Sums are added in an
+ * order that depends on the sizes and the number of SMs alone.
+ * workspace: at least maxsim_cross_entropy_backward_workspace_size(spec) bytes,
+ * 256-byte aligned. dx and dweight may overlap no input and not one another. With
+ * T = 0 dweight is 0. Limits as in maxsim_cross_entropy, for the gradients too.
+ */
+size_t maxsim_cross_entropy_backward_workspace_size(const maxsim_loss_spec *spec);
+maxsim_status maxsim_cross_entropy_backward(const maxsim_loss_spec *spec, const float *dloss, const maxsim_rows *x,
+                                            const maxsim_rows *weight, const float *lse, const maxsim_rows *dx,
+                                            const maxsim_rows *dweight, void *workspace, size_t workspace_bytes,
+                                            void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -33,6 +33,9 @@ __all__ = [
     "maxsim_version", "allreduce_dq",
     "maxsim_rotary_frequencies", "maxsim_rotary", "maxsim_attention", "maxsim_attention_backward",
     "maxsim_attention_backward_workspace_size", "maxsim_clip_grad_norm", "maxsim_clip_grad_norm_workspace_size",
+    "encoder_dropout", "encoder_rms_norm", "encoder_rms_norm_backward", "encoder_rms_norm_backward_workspace_size",
+    "encoder_cross_entropy", "encoder_cross_entropy_workspace_size", "encoder_cross_entropy_backward",
+    "encoder_cross_entropy_backward_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -59,10 +62,14 @@ EXPORTS = (
     "maxsim_rotary_frequencies", "maxsim_rotary", "maxsim_attention",
     "maxsim_attention_backward_workspace_size", "maxsim_attention_backward",
     "maxsim_clip_grad_norm_workspace_size", "maxsim_clip_grad_norm",
+    "maxsim_dropout", "maxsim_rms_norm", "maxsim_rms_norm_backward_workspace_size", "maxsim_rms_norm_backward",
+    "maxsim_cross_entropy_workspace_size", "maxsim_cross_entropy",
+    "maxsim_cross_entropy_backward_workspace_size", "maxsim_cross_entropy_backward",
 )
 
 ROTARY_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 MASKS = {"full": 0, "causal": 1, "prefix": 2}
+NORM_FORMATS = {None: (0, None), "int8": (1, torch.int8), "e4m3": (2, torch.float8_e4m3fn)}
 
 
 class _Heads(ctypes.Structure):
@@ -76,6 +83,24 @@ class _AttentionSpec(ctypes.Structure):
                 ("d", ctypes.c_int32), ("dtype", ctypes.c_int), ("mask", ctypes.c_int), ("scale", ctypes.c_float),
                 ("cap", ctypes.c_float), ("offsets", ctypes.c_void_p), ("key_len", ctypes.c_void_p),
                 ("prefix_len", ctypes.c_void_p), ("slopes", ctypes.c_void_p)]
+
+
+class _Rows(ctypes.Structure):
+    """maxsim_rows: a [T, d] view, its stride in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64)]
+
+
+class _NormSpec(ctypes.Structure):
+    """maxsim_norm_spec."""
+    _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int32), ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int),
+                ("format", ctypes.c_int), ("eps", ctypes.c_float), ("p", ctypes.c_float), ("rng", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p)]
+
+
+class _LossSpec(ctypes.Structure):
+    """maxsim_loss_spec."""
+    _fields_ = [("T", ctypes.c_int64), ("V", ctypes.c_int64), ("d", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("scale", ctypes.c_float), ("targets", ctypes.c_void_p)]
 
 
 class MaxSimError(RuntimeError):
@@ -154,6 +179,23 @@ def load_library():
     lib.maxsim_clip_grad_norm_workspace_size.argtypes = [I32]
     lib.maxsim_clip_grad_norm.restype = I32
     lib.maxsim_clip_grad_norm.argtypes = [P, P, P, P, I32, F32, P, P, SZ, P]
+    RP, NP, LP = ctypes.POINTER(_Rows), ctypes.POINTER(_NormSpec), ctypes.POINTER(_LossSpec)
+    lib.maxsim_dropout.restype = I32
+    lib.maxsim_dropout.argtypes = [RP, RP, I64, I32, F32, P, I32, RP, P]
+    lib.maxsim_rms_norm.restype = I32
+    lib.maxsim_rms_norm.argtypes = [NP, RP, RP, RP, RP, P, P]
+    lib.maxsim_rms_norm_backward_workspace_size.restype = SZ
+    lib.maxsim_rms_norm_backward_workspace_size.argtypes = [NP]
+    lib.maxsim_rms_norm_backward.restype = I32
+    lib.maxsim_rms_norm_backward.argtypes = [NP, RP, RP, RP, RP, RP, P, P, SZ, P]
+    lib.maxsim_cross_entropy_workspace_size.restype = SZ
+    lib.maxsim_cross_entropy_workspace_size.argtypes = [LP]
+    lib.maxsim_cross_entropy.restype = I32
+    lib.maxsim_cross_entropy.argtypes = [LP, RP, RP, P, P, P, SZ, P]
+    lib.maxsim_cross_entropy_backward_workspace_size.restype = SZ
+    lib.maxsim_cross_entropy_backward_workspace_size.argtypes = [LP]
+    lib.maxsim_cross_entropy_backward.restype = I32
+    lib.maxsim_cross_entropy_backward.argtypes = [LP, P, RP, RP, P, RP, RP, P, SZ, P]
     _lib = lib
     return lib
 
@@ -852,3 +894,238 @@ def maxsim_clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, 
         keep(norm)
     _check(st, "maxsim_clip_grad_norm")
     return norm
+
+
+# ------------------------------------------------- rows of hidden states, and the loss
+#
+# The C entry points are maxsim_dropout, maxsim_rms_norm and maxsim_cross_entropy, with
+# their gradients.
+
+def _rows(t, name, shape, dtype, index):
+    """A [T, d] tensor on CUDA device ``index``, its rows contiguous, as a maxsim_rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path) on the first tensor's device")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    row, last = t.stride()
+    if last != 1 and shape[1] != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if shape[0] <= 1 or shape[1] == 0:  # the stride of a dimension of one element says nothing
+        row = (shape[1] + 7) // 8 * 8
+    return _Rows(t.data_ptr(), row)
+
+
+def _shape_of_rows(x, name, dtypes, said):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError(f"{name} must be a [T, d] tensor")
+    if x.dtype not in dtypes:
+        raise TypeError(f"{name} must be {said}, got {x.dtype}")
+    return x.shape, x.dtype, x.get_device()
+
+
+def _rng(p, rng):
+    """The device's pointer to a call's seed and number."""
+    if rng is None:
+        if p:
+            raise ValueError("p > 0 needs rng, an int64 tensor of a seed and a call's number")
+        return None
+    if _dev(rng, "rng", torch.int64).numel() != 2:
+        raise ValueError("rng must have two entries: a seed and a call's number")
+    return rng.data_ptr()
+
+
+@_entry
+def encoder_dropout(x, p, rng, residual=None, out=None, stream=None):
+    """Dropout of x [T, d] (bf16/fp16/fp32; any row stride), plus ``residual``:
+    an element is dropped with chance p (a multiple of 2^-16), others are divided by
+    1 - p. The mask is made from ``rng``, [2] int64 on the device (a seed, and a
+    number that differs between calls), and an element's row and column, and is
+    not stored: the same call on the gradient of the result, without a residual,
+    gives that of x. ``out`` may be x or residual."""
+    lib = load_library()
+    shape, dtype, index = _shape_of_rows(x, "x", _DTYPE_CODE, "bf16, fp16 or fp32")
+    src = _rows(x, "x", shape, dtype, index)
+    res = None if residual is None else _rows(residual, "residual", shape, dtype, index)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+    st = lib.maxsim_dropout(src, res, shape[0], shape[1], p, _rng(p, rng), _DTYPE_CODE[dtype],
+                            _rows(out, "out", shape, dtype, index), _stream_on(stream, index))
+    _check(st, "maxsim_dropout")
+    return out
+
+
+def _norm_spec(x, name, weight, eps, p, rng, fmt):
+    shape, dtype, index = _shape_of_rows(x, name, _DTYPE_CODE, "bf16, fp16 or fp32")
+    code = _DTYPE_CODE[dtype]
+    wcode = FP32
+    if weight is not None:
+        if _dev(weight, "weight").dtype not in (torch.float32, dtype):
+            raise TypeError(f"weight must be fp32 or {dtype}, got {weight.dtype}")
+        if weight.numel() != shape[1]:
+            raise ValueError("weight must have one entry a column")
+        wcode = _DTYPE_CODE[weight.dtype]
+    if fmt not in NORM_FORMATS:
+        raise ValueError(f"fmt must be one of {tuple(NORM_FORMATS)}")
+    spec = _NormSpec(shape[0], shape[1], code, wcode, NORM_FORMATS[fmt][0], eps, p, _rng(p, rng),
+                     None if weight is None else weight.data_ptr())
+    return spec, shape, dtype, index
+
+
+@_entry
+def encoder_rms_norm(x, weight=None, residual=None, eps=1e-6, p=0.0, rng=None, fmt=None, out=None, sum_out=None,
+                     want_sum=False, scale=None, stream=None):
+    """Root-mean-square norm of the rows h = residual + dropout(x) (p and rng as in
+    encoder_dropout; both parts are optional): y = h * weight / sqrt(mean(h^2) +
+    eps). x [T, d] and residual bf16/fp16/fp32 with any row stride; weight [d]
+    fp32 or of x's type. ``fmt`` None: y in x's type; "int8" or "e4m3": y / scale in
+    8 bits, with scale [T] fp32 (int8 rows and scales are what maxsim_score_i8
+    takes). Returns out, then scale with a ``fmt``, then h with ``want_sum`` or
+    ``sum_out`` (which may be x or residual): one tensor, or a tuple."""
+    lib = load_library()
+    spec, shape, dtype, index = _norm_spec(x, "x", weight, eps, p, rng, fmt)
+    src = _rows(x, "x", shape, dtype, index)
+    res = None if residual is None else _rows(residual, "residual", shape, dtype, index)
+    otype = NORM_FORMATS[fmt][1] or dtype
+    if out is None:
+        out = torch.empty(shape, dtype=otype, device=x.device)
+    if sum_out is None and want_sum:
+        sum_out = torch.empty(shape, dtype=dtype, device=x.device)
+    if fmt is None:
+        if scale is not None:
+            raise ValueError("scale goes with an 8-bit fmt")
+    elif scale is None:
+        scale = torch.empty(shape[0], dtype=torch.float32, device=x.device)
+    elif _dev(scale, "scale", torch.float32).numel() != shape[0]:
+        raise ValueError("scale must have one entry a row")
+    st = lib.maxsim_rms_norm(spec, src, res, None if sum_out is None else _rows(sum_out, "sum_out", shape, dtype, index),
+                             _rows(out, "out", shape, otype, index), None if scale is None else scale.data_ptr(),
+                             _stream_on(stream, index))
+    _check(st, "maxsim_rms_norm")
+    if fmt is None:
+        return out if sum_out is None else (out, sum_out)
+    return (out, scale) if sum_out is None else (out, scale, sum_out)
+
+
+def encoder_rms_norm_backward_workspace_size(h, weight=None):
+    """Device bytes of the workspace of encoder_rms_norm_backward."""
+    spec = _norm_spec(h, "h", weight, 1e-6, 0.0, None, None)[0]
+    return int(load_library().maxsim_rms_norm_backward_workspace_size(spec))
+
+
+@_entry
+def encoder_rms_norm_backward(dy, h, weight=None, dsum=None, eps=1e-6, p=0.0, rng=None, dx=None, dresidual=None,
+                              dweight=None, workspace=None, stream=None):
+    """Gradients of encoder_rms_norm for the gradient dy of its out, from its sum h
+    and the same weight, eps, p and rng; ``dsum`` is the gradient that reaches h
+    from elsewhere. Returns dx, dresidual and dweight (None without a weight). Without
+    dropout dx and dresidual are one tensor, unless both are given."""
+    lib = load_library()
+    spec, shape, dtype, index = _norm_spec(h, "h", weight, eps, p, rng, None)
+    device = h.device
+    views = [_rows(dy, "dy", shape, dtype, index), _rows(h, "h", shape, dtype, index),
+             None if dsum is None else _rows(dsum, "dsum", shape, dtype, index)]
+    if not p and (dx is None or dresidual is None):
+        dx = dx if dx is not None else dresidual if dresidual is not None else torch.empty(shape, dtype=dtype, device=device)
+        dresidual, second = dx, None
+    else:
+        dx = torch.empty(shape, dtype=dtype, device=device) if dx is None else dx
+        dresidual = torch.empty(shape, dtype=dtype, device=device) if dresidual is None else dresidual
+        second = _rows(dresidual, "dresidual", shape, dtype, index)
+    if weight is not None:
+        if dweight is None:
+            dweight = torch.empty(shape[1], dtype=weight.dtype, device=device)
+        if _dev(dweight, "dweight", weight.dtype).numel() != shape[1]:
+            raise ValueError("dweight must have one entry a column")
+        if workspace is None:
+            workspace = _scratch(lib.maxsim_rms_norm_backward_workspace_size(spec), device)
+    elif dweight is not None:
+        raise ValueError("dweight goes with a weight")
+    if workspace is not None:
+        _dev(workspace, "workspace", torch.uint8)
+    st = lib.maxsim_rms_norm_backward(spec, *views, _rows(dx, "dx", shape, dtype, index), second,
+                                      None if dweight is None else dweight.data_ptr(),
+                                      None if workspace is None else workspace.data_ptr(),
+                                      0 if workspace is None else workspace.numel(), _stream_on(stream, index))
+    _check(st, "maxsim_rms_norm_backward")
+    return dx, dresidual, dweight
+
+
+_LOSS_TYPES = {torch.bfloat16: BF16, torch.float16: FP16}
+
+
+def _loss_spec(x, weight, targets, scale):
+    shape, dtype, index = _shape_of_rows(x, "x", _LOSS_TYPES, "bf16 or fp16")
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2 or weight.shape[1] != shape[1]:
+        raise ValueError("weight must be [V, d], with x's d")
+    if _dev(targets, "targets", torch.int64).numel() != shape[0]:
+        raise ValueError("targets must have one entry a row")
+    spec = _LossSpec(shape[0], weight.shape[0], shape[1], _LOSS_TYPES[dtype], scale, targets.data_ptr())
+    return spec, _rows(x, "x", shape, dtype, index), _rows(weight, "weight", weight.shape, dtype, index), index
+
+
+def encoder_cross_entropy_workspace_size(x, weight, targets):
+    """Device bytes of the workspace of encoder_cross_entropy."""
+    return int(load_library().maxsim_cross_entropy_workspace_size(_loss_spec(x, weight, targets, 1.0)[0]))
+
+
+def encoder_cross_entropy_backward_workspace_size(x, weight, targets):
+    """Device bytes of the workspace of encoder_cross_entropy_backward."""
+    return int(load_library().maxsim_cross_entropy_backward_workspace_size(_loss_spec(x, weight, targets, 1.0)[0]))
+
+
+def _row_values(t, name, n):
+    if _dev(t, name, torch.float32).numel() != n:
+        raise ValueError(f"{name} must have one entry a row")
+    return t
+
+
+@_entry
+def encoder_cross_entropy(x, weight, targets, scale=1.0, loss=None, lse=None, workspace=None, stream=None):
+    """Softmax cross entropy of the logits scale * x @ weight.T, which are never
+    stored: x [T, d], weight [V, d] (bf16/fp16; d a multiple of 8), targets [T]
+    int64, negative where a row has none. Returns loss [T] fp32 (0 without a
+    target) and lse [T] fp32, the logarithms of the softmax's denominators, which
+    the backward needs."""
+    lib = load_library()
+    spec, xv, wv, index = _loss_spec(x, weight, targets, scale)
+    n = spec.T
+    loss = torch.empty(n, dtype=torch.float32, device=x.device) if loss is None else _row_values(loss, "loss", n)
+    lse = torch.empty(n, dtype=torch.float32, device=x.device) if lse is None else _row_values(lse, "lse", n)
+    if workspace is None:
+        workspace = _scratch(lib.maxsim_cross_entropy_workspace_size(spec), x.device)
+    _dev(workspace, "workspace", torch.uint8)
+    st = lib.maxsim_cross_entropy(spec, xv, wv, loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                                  workspace.numel(), _stream_on(stream, index))
+    _check(st, "maxsim_cross_entropy")
+    return loss, lse
+
+
+@_entry
+def encoder_cross_entropy_backward(dloss, x, weight, targets, lse, scale=1.0, dx=None, dweight=None, want_dx=True,
+                                   want_dweight=True, workspace=None, stream=None):
+    """Gradients of encoder_cross_entropy for the gradient dloss [T] fp32 of its
+    loss, from its lse; the other arguments as in that call. Returns dx [T, d]
+    and dweight [V, d] in the inputs' type; a side that is not wanted, nor given, is
+    None and costs nothing."""
+    lib = load_library()
+    spec, xv, wv, index = _loss_spec(x, weight, targets, scale)
+    n, dtype, device = spec.T, x.dtype, x.device
+    _row_values(dloss, "dloss", n)
+    _row_values(lse, "lse", n)
+    if dx is None and want_dx:
+        dx = torch.empty(x.shape, dtype=dtype, device=device)
+    if dweight is None and want_dweight:
+        dweight = torch.empty(weight.shape, dtype=dtype, device=device)
+    if workspace is None:
+        workspace = _scratch(lib.maxsim_cross_entropy_backward_workspace_size(spec), device)
+    _dev(workspace, "workspace", torch.uint8)
+    st = lib.maxsim_cross_entropy_backward(
+        spec, dloss.data_ptr(), xv, wv, lse.data_ptr(), None if dx is None else _rows(dx, "dx", x.shape, dtype, index),
+        None if dweight is None else _rows(dweight, "dweight", weight.shape, dtype, index), workspace.data_ptr(),
+        workspace.numel(), _stream_on(stream, index))
+    _check(st, "maxsim_cross_entropy_backward")
+    return dx, dweight

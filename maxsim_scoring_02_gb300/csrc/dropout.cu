@@ -1,0 +1,92 @@
+// dropout.cu -- dropout of rows from a counter-based generator, and the residual's
+// addition; its gradient is the same call on the gradient.
+//
+//   out = residual + (lot >= limit ? x * factor : 0)
+//
+// The mask is never stored: rows.cuh makes an element's lot from its place. Bound by
+// HBM where a thread's ten rounds of integer products hide behind its loads.
+#include "rows.cuh"
+
+namespace msim {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnits = 2;  // groups of 8 columns of a thread
+
+struct DropoutParams {
+  const void *x, *res;
+  void* out;
+  int64_t x_stride, res_stride, out_stride;
+  Drop drop;
+  Divisor parts;   // groups (whole) or runs of 256 columns (else) of a row
+  uint32_t count;  // of them in this launch
+  int row0, d;
+};
+
+template <typename T, bool kWhole>
+__global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p) {
+  const Key key = load_key(p.drop);
+  const int lane = threadIdx.x & 31;
+  // a warp's lanes share a run of 256 columns where rows are not whole
+  const uint32_t per = kWhole ? kThreads : kThreads / 32, mine = kWhole ? threadIdx.x : threadIdx.x >> 5;
+  alignas(16) T x[kUnits][8], r[kUnits][8];
+  uint32_t row[kUnits], part[kUnits];
+  bool live[kUnits];
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const uint32_t n = (blockIdx.x * kUnits + u) * per + mine;
+    live[u] = n < p.count;
+    const uint32_t q = p.parts.of(live[u] ? n : 0);
+    part[u] = (live[u] ? n : 0) - q * p.parts.d;
+    row[u] = p.row0 + q;
+    const Cols<kWhole> c(part[u], lane, p.d);
+    load8<T, kWhole>(static_cast<const T*>(p.x) + row[u] * p.x_stride, c, x[u]);
+    if (p.res) load8<T, kWhole>(static_cast<const T*>(p.res) + row[u] * p.res_stride, c, r[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    const Cols<kWhole> c(part[u], lane, p.d);
+    const uint32_t keep = p.drop.limit ? kept<kWhole>(key, c, row[u], p.drop.limit) : 0xFFu;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float add = p.res ? up(r[u][j]) : 0.f;
+      v[j] = keep >> j & 1 ? fmaf(up(x[u][j]), p.drop.factor, add) : add;
+    }
+    if (live[u]) store8<T, kWhole>(static_cast<T*>(p.out) + row[u] * p.out_stride, c, v);
+  }
+}
+
+template <typename T>
+maxsim_status run(DropoutParams p, int T_, bool whole, cudaStream_t stream) {
+  const uint32_t parts = whole ? p.d / 8 : (p.d + 255) / 256, per = whole ? kThreads : kThreads / 32;
+  const int most = static_cast<int>((INT_MAX - 8192) / parts);  // rows of a launch: its parts are counted in 31 bits
+  for (int64_t row0 = 0; row0 < T_; row0 += most) {
+    const int rows = T_ - row0 < most ? static_cast<int>(T_ - row0) : most;
+    p.row0 = static_cast<int>(row0);
+    p.count = static_cast<uint32_t>(rows) * parts;
+    const int grid = static_cast<int>((p.count + per * kUnits - 1) / (per * kUnits));
+    if (whole) dropout_kernel<T, true><<<grid, kThreads, 0, stream>>>(p);
+    else dropout_kernel<T, false><<<grid, kThreads, 0, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return MAXSIM_ERR_CUDA;
+  }
+  return MAXSIM_OK;
+}
+
+}  // namespace
+
+maxsim_status launch_dropout(const maxsim_rows& x, const maxsim_rows* residual, int T, int d, const Drop& drop, int dtype,
+                             const maxsim_rows& out, cudaStream_t stream) {
+  const int e = dtype == MAXSIM_FP32 ? 4 : 2;
+  const bool whole = whole_rows(&x, d, e) && whole_rows(residual, d, e) && whole_rows(&out, d, e);
+  DropoutParams p = {x.data, residual ? residual->data : nullptr, out.data, x.row_stride,
+                     residual ? residual->row_stride : 0, out.row_stride, drop,
+                     Divisor(whole ? d / 8 : (d + 255) / 256), 0, 0, d};
+  switch (dtype) {
+    case MAXSIM_BF16: return run<__nv_bfloat16>(p, T, whole, stream);
+    case MAXSIM_FP16: return run<__half>(p, T, whole, stream);
+    default: return run<float>(p, T, whole, stream);
+  }
+}
+
+}  // namespace msim

@@ -117,6 +117,16 @@ struct AttnParams;
 maxsim_status launch_attn_fwd(const AttnParams& p, int is_bf16, cudaStream_t stream);
 maxsim_status launch_attn_bwd(const AttnParams& p, int is_bf16, cudaStream_t stream);
 
+// Dropout, root-mean-square norms (norm.cuh has the parameters); whole: every row
+// begins on a 16-byte boundary (rows.cuh). The cross entropy is in loss.cuh.
+struct Drop;
+struct NormParams;
+maxsim_status launch_dropout(const maxsim_rows& x, const maxsim_rows* residual, int T, int d, const Drop& drop, int dtype,
+                             const maxsim_rows& out, cudaStream_t stream);
+maxsim_status launch_norm(const NormParams& p, int dtype, bool whole, cudaStream_t stream);
+size_t norm_bwd_workspace_bytes(int T, int d);
+maxsim_status launch_norm_bwd(const NormParams& p, int dtype, bool whole, void* dweight, cudaStream_t stream);
+
 // Encodes a TMA tensor map through the driver entry point (no libcuda link).
 // dtype_code: 0 fp16, 1 bf16, 2 uint8, 3 fp32; swizzle: 0 none, 1 128-byte,
 // 2 64-byte. Returns false if the driver call is unavailable or rejects the

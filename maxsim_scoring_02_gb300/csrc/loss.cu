@@ -1,0 +1,725 @@
+// loss.cu -- softmax cross entropy over a vocabulary, whose logits are never kept,
+// and its gradients.
+//
+//   z = scale x W^T,  lse = ln sum_v exp z_v,  loss = lse - z_target
+//   dz = dloss scale (softmax - onehot),  dx = dz W,  dW = dz^T x
+//
+// Four matrix products, all by one kernel on tcgen05: two SMs form a pair that owns
+// tiles of 256 x 256 (cta_group::2: each SM holds 128 rows of A and half of B's, so a
+// tile costs each of them half the operand traffic of one that works alone), K in
+// steps of 64 through six stages that TMA fills, two accumulators of 256 TMEM columns,
+// so that eight warps empty one while the other is made.
+//   kStats   z tile -> its rows' maxima and sums, 128 columns apart: [V / 128, T] pairs
+//   kGrad    z tile again -> dz in 16 bits, a piece of the vocabulary at a time
+//   kSums    the piece's dz -> dx (+= over pieces) and dW, in one launch: dx has few
+//            and long tiles, dW many short ones that even out the pairs' work
+// A piece's dz is bounded by 256 MB; logits live in TMEM and registers alone. Making
+// them again costs a fourth product instead of T x V numbers kept between the calls.
+// dz is held times a power of two that brings the largest dloss to 1 (to 2^14 in fp16,
+// whose range ends there): small gradients keep their bits.
+// Bound by the tensor cores (and by the power limit in long runs).
+#include <cmath>
+
+#include "attn_common.cuh"
+#include "loss.cuh"
+
+namespace msim {
+namespace {
+
+constexpr int kEpiWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kThreads = 384;
+// Registers: launched with 168 a thread; the control warpgroup gives up 112 for the two that empty accumulators.
+constexpr int kRegsCtl = 56, kRegsEpi = 224, kRegsLaunch = 168;
+static_assert(2 * 128 * kRegsEpi + 128 * kRegsCtl <= kThreads * kRegsLaunch, "register split");
+constexpr int kTile = 256, kHalf = 128, kStep = 64;
+constexpr int kBox = 64;                       // every operand is loaded in boxes of 64 x 64 elements
+constexpr int kBoxBytes = kBox * 128;
+constexpr int kStages = 6, kStageBytes = 4 * kBoxBytes;  // two boxes of A, two of B
+constexpr int kAcc = 2;
+constexpr int kStageOut = 32 * 128;            // a warp's way out: 32 rows of 128 bytes
+constexpr int kBars = 3 * kStages + 2 * kAcc + 1;
+constexpr int kSmallBytes = kBars * 8 + 16;
+constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kEpiWarps * kStageOut + kSmallBytes;
+constexpr int kGroupM = 32;                    // row tiles that share a pass over the vocabulary
+
+constexpr uint32_t kIdescAMnMajor = 1u << 15;  // flag of the instruction descriptor: A has its M dimension contiguous
+
+enum Mode { kStats, kGrad, kSums };
+
+struct Maps {
+  CUtensorMap x, w, dz;    // operands: [T, d], [V, d], [T, columns of the piece]
+  CUtensorMap out0, out1;  // kGrad: dz; kSums: dx (or its fp32 sums), dW
+};
+
+struct Params {
+  LossShape s;
+  int first, columns;       // the piece
+  int tiles_m, tiles_n;     // of z
+  int dx_m, dx_n, splits;   // kSums: dx tiles, and parts of their K
+  int dw_m, dw_n, rounds;   // dW tiles; how many of them are worth one of dx
+  int dx_wide, dx_adds;     // dx goes to fp32 sums; they are added to
+  const int64_t* targets;
+  const float *lse, *coef, *gain;
+  float2* parts;
+  float* hit;               // [T] the target's product
+  float z2;                 // scale * log2(e)
+  unsigned* status;
+};
+
+struct Smem {
+  uint8_t *stages, *out;
+  uint64_t* bars;
+  uint32_t* tmem_slot;
+  volatile int* abort_flag;
+  uint32_t full, empty, full2, accfull, accempty, done;
+};
+__device__ __forceinline__ Smem carve(uint8_t* raw) {
+  Smem s;
+  const uintptr_t base = (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023);
+  s.stages = reinterpret_cast<uint8_t*>(base);
+  s.out = s.stages + kStages * kStageBytes;
+  s.bars = reinterpret_cast<uint64_t*>(s.out + kEpiWarps * kStageOut);
+  s.tmem_slot = reinterpret_cast<uint32_t*>(s.bars + kBars);
+  s.abort_flag = reinterpret_cast<volatile int*>(s.tmem_slot + 1);
+  s.full = smem_u32(s.bars);
+  s.empty = s.full + 8 * kStages;
+  s.full2 = s.empty + 8 * kStages;
+  s.accfull = s.full2 + 8 * kStages;
+  s.accempty = s.accfull + 8 * kAcc;
+  s.done = s.accempty + 8 * kAcc;
+  return s;
+}
+
+// One tile of a pair. A is K-major in z and dx, B in z alone; the others have their
+// M or N dimension contiguous.
+struct Tile {
+  int m0, n0, n;    // n: the product's N, a multiple of 32
+  int k0, steps;    // of 64
+  int kind;         // 0 z, 1 dx, 2 dW
+  int split;
+};
+
+__device__ __forceinline__ int width(int left) { return left >= kTile ? kTile : (left + 31) & ~31; }
+
+template <int kMode>
+__device__ __forceinline__ bool tile_of(const Params& p, int i, Tile& t) {
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  t.split = 0;
+  t.k0 = 0;
+  if constexpr (kMode != kSums) {
+    const int64_t at = static_cast<int64_t>(i) * pairs + pair;
+    if (at >= static_cast<int64_t>(p.tiles_m) * p.tiles_n) return false;
+    const int64_t per = static_cast<int64_t>(kGroupM) * p.tiles_n;
+    const int group = static_cast<int>(at / per), in = static_cast<int>(at - group * per);
+    const int rows = min(kGroupM, p.tiles_m - group * kGroupM);
+    const int n = in / rows;
+    t.kind = 0;
+    t.m0 = (group * kGroupM + in - n * rows) * kTile;
+    t.n0 = n * kTile;  // within the piece
+    t.n = width(p.columns - t.n0);
+    t.steps = (p.s.d + kStep - 1) / kStep;
+    return true;
+  } else {
+    // dx tiles in turn; then dW tiles, of which pairs with one dx tile less have `rounds` more
+    const int n_dx = p.dx_m * p.dx_n * p.splits, n_dw = p.dw_m * p.dw_n;
+    const int whole = n_dx / pairs, rest = n_dx - whole * pairs;
+    const int mine = whole + (pair < rest);
+    if (i < mine) {
+      const int at = i * pairs + pair, per = p.dx_m * p.dx_n;
+      t.kind = 1;
+      t.split = at / per;
+      const int in = at - t.split * per, m = in / p.dx_n;
+      t.m0 = m * kTile;
+      t.n0 = (in - m * p.dx_n) * kTile;
+      t.n = width(p.s.d - t.n0);
+      const int steps = (p.columns + kStep - 1) / kStep;
+      t.k0 = static_cast<int>(static_cast<int64_t>(steps) * t.split / p.splits);
+      t.steps = static_cast<int>(static_cast<int64_t>(steps) * (t.split + 1) / p.splits) - t.k0;
+      return true;
+    }
+    int k = i - mine;
+    const int extra = rest ? p.rounds : 0, light = pairs - rest;
+    int64_t at;
+    if (pair >= rest && k < extra) {
+      at = static_cast<int64_t>(k) * light + (pair - rest);
+    } else {
+      if (pair >= rest) k -= extra;
+      at = static_cast<int64_t>(extra) * light + static_cast<int64_t>(k) * pairs + pair;
+    }
+    if (at >= n_dw) return false;
+    const int m = static_cast<int>(at / p.dw_n);
+    t.kind = 2;
+    t.m0 = m * kTile;
+    t.n0 = static_cast<int>(at - static_cast<int64_t>(m) * p.dw_n) * kTile;
+    t.n = width(p.s.d - t.n0);
+    t.steps = (p.s.T + kStep - 1) / kStep;
+    return true;
+  }
+}
+
+// ------------------------------------------------------------------ producer
+template <int kMode>
+__device__ void produce(const Params& p, const Smem& sm, const Maps& maps, uint32_t rank) {
+  if (debug_faults(p.status) & kDebugStallFwdLoader) return;
+  const uint32_t stage0 = smem_u32(sm.stages);
+  uint32_t fills = 0;
+  int s = 0;
+  uint32_t ph = 0;
+  Tile t;
+  bool ok = true;
+  for (int i = 0; ok && tile_of<kMode>(p, i, t); ++i) {
+    const CUtensorMap* a = t.kind == 0 ? &maps.x : &maps.dz;
+    const CUtensorMap* b = t.kind == 2 ? &maps.x : &maps.w;
+    const int am = t.m0 + static_cast<int>(rank) * kHalf, bn = t.n0 + static_cast<int>(rank) * (t.n / 2);
+    const int boxes_b = t.n / 2 > kBox ? 2 : 1;
+    for (int k = 0; k < t.steps; ++k) {
+      if (!mbar_wait_inl_a(sm.empty + 8 * s, ph ^ 1u, sm.abort_flag, p.status)) {
+        ok = false;
+        break;
+      }
+      const uint32_t bar = sm.full + 8 * s, to = stage0 + static_cast<uint32_t>(s) * kStageBytes;
+      const int kk = (t.k0 + k) * kStep;
+      mbar_arrive_expect_tx_a(bar, (2 + boxes_b) * kBoxBytes);
+      // K-major: x along K, y along M or N. Else x along M or N, y along K.
+      for (int h = 0; h < 2; ++h) {
+        if (t.kind == 2) tma_load_2d_nohint_a(to + h * kBoxBytes, a, bar, am + h * kBox, kk);
+        else tma_load_2d_nohint_a(to + h * kBoxBytes, a, bar, kk, am + h * kBox);
+      }
+      for (int h = 0; h < boxes_b; ++h) {
+        const uint32_t dst = to + (2 + h) * kBoxBytes;
+        if (t.kind == 0) tma_load_2d_nohint_a(dst, b, bar, kk, p.first + bn + h * kBox);
+        else tma_load_2d_nohint_a(dst, b, bar, bn + h * kBox, (t.kind == 1 ? p.first : 0) + kk);
+      }
+      ++fills;
+      if (++s == kStages) s = 0, ph ^= 1u;
+    }
+  }
+  if (!ok)  // copies in flight land before the block ends
+    for (uint32_t f = fills > kStages ? fills - kStages : 0; f < fills; ++f)
+      mbar_wait_drain(sm.bars + (f % kStages), (f / kStages) & 1u, p.status);
+}
+
+// ------------------------------------------------- products (even CTA, one thread)
+template <int kMode>
+__device__ void multiply(const Params& p, const Smem& sm, uint32_t tmem_base) {
+  const uint32_t stage0 = smem_u32(sm.stages);
+  const uint64_t kmajor = sdesc_k_sw128(stage0), mnmajor = sdesc_mn_sw128(stage0, kBoxBytes);
+  const uint16_t both = 3;
+  int s = 0, a = 0;
+  uint32_t ph = 0, aph = 0;
+  Tile t;
+  bool ok = true;
+  for (int i = 0; ok && tile_of<kMode>(p, i, t); ++i) {
+    if (t.steps == 0) continue;
+    if (!mbar_poll_inl_a(sm.accempty + 8 * a, aph ^ 1u, sm.abort_flag, p.status)) break;
+    tc_fence_after();
+    const bool a_mn = t.kind == 2, b_mn = t.kind != 0;
+    const uint32_t idesc = idesc_f16(p.s.is_bf16, kTile, t.n) | (a_mn ? kIdescAMnMajor : 0u) | (b_mn ? kIdescBMnMajor : 0u);
+    const uint64_t ad0 = a_mn ? mnmajor : kmajor, bd0 = (b_mn ? mnmajor : kmajor) + ((2 * kBoxBytes) >> 4);
+    const uint64_t a_step = a_mn ? 2048 >> 4 : 2, b_step = b_mn ? 2048 >> 4 : 2;
+    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(a * kTile);
+    for (int k = 0; k < t.steps; ++k) {
+      if (!mbar_poll_inl_a(sm.full + 8 * s, ph, sm.abort_flag, p.status) ||
+          !mbar_poll_inl_a(sm.full2 + 8 * s, ph, sm.abort_flag, p.status)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint64_t at = static_cast<uint64_t>((s * kStageBytes) >> 4);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        umma_f16_pair(d_tmem, ad0 + at + x * a_step, bd0 + at + x * b_step, idesc, (k | x) != 0 ? 1u : 0u);
+      umma_commit_pair(sm.empty + 8 * s, both);
+      if (++s == kStages) s = 0, ph ^= 1u;
+    }
+    if (!ok) break;
+    umma_commit_pair(sm.accfull + 8 * a, both);
+    if (++a == kAcc) a = 0, aph ^= 1u;
+  }
+  umma_commit_pair(sm.done, 1);  // TMEM is freed only after the last product
+  mbar_wait_drain(sm.bars + kBars - 1, 0, p.status);
+}
+
+// The odd CTA's operands have arrived: the even one's issuer hears of it.
+template <int kMode>
+__device__ void relay(const Params& p, const Smem& sm) {
+  const uint32_t to = mapa_shared(sm.full2, 0);
+  int s = 0;
+  uint32_t ph = 0;
+  Tile t;
+  for (int i = 0; tile_of<kMode>(p, i, t); ++i)
+    for (int k = 0; k < t.steps; ++k) {
+      if (!mbar_wait_inl_a(sm.full + 8 * s, ph, sm.abort_flag, p.status)) return;
+      mbar_arrive_cluster(to + 8 * s);
+      if (++s == kStages) s = 0, ph ^= 1u;
+    }
+}
+
+// ------------------------------------------------------------------ epilogue
+// A warp's 32 rows of 128 bytes, 16-byte parts exchanged as TMA's 128-byte swizzle does.
+__device__ __forceinline__ void put_row(uint32_t stage, int lane, const uint32_t (&w)[32]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((c ^ (lane & 7)) * 16)),
+                 "r"(w[4 * c]), "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                 : "memory");
+}
+__device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+template <bool kAdd>
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, uint32_t from, int x, int y, int z) {
+  if constexpr (kAdd)
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(from), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(from), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// The warp's staged rows go out at column x of row y.
+__device__ __forceinline__ void send(const CUtensorMap* map, uint32_t stage, int lane, int x, int y, int z, bool adds) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (adds) store_tile<true>(map, stage, x, y, z);
+    else store_tile<false>(map, stage, x, y, z);
+  }
+}
+
+// Thread = row (TMEM lane); warps w and w + 4 share a lane quarter and take half of the columns each.
+template <int kMode, bool kBf16>
+__device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32_t tmem_base, uint32_t rank) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3, half = warp >> 2;
+  const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16, accempty_r = mapa_shared(sm.accempty, 0);
+  const uint32_t stage = smem_u32(sm.out) + warp * kStageOut;
+  int a = 0;
+  uint32_t aph = 0;
+  Tile t;
+  for (int i = 0; tile_of<kMode>(p, i, t); ++i) {
+    if (t.steps == 0) continue;
+    const int row0 = t.m0 + static_cast<int>(rank) * kHalf + quarter * 32, row = row0 + lane;
+    const int col0 = half * kHalf;  // within the tile
+    const int chunks = min(4, max(0, (t.n - col0 + 31) / 32));
+    // what the row needs, asked for before the wait
+    int target = -1;
+    float lse2 = 0.f, coef = 0.f, gain = 1.f;
+    if constexpr (kMode != kSums) {
+      if (row < p.s.T) {
+        const int64_t g = p.targets[row] - p.first - t.n0 - col0;
+        target = g >= 0 && g < kHalf ? static_cast<int>(g) : -1;
+        if constexpr (kMode == kGrad) {
+          lse2 = p.lse[row] * kLog2e;
+          coef = p.coef[row];
+        }
+      }
+    } else {
+      gain = t.kind == 1 && p.dx_wide ? 1.f : *p.gain;
+    }
+    __syncwarp();
+    if (!mbar_wait_warp(sm.accfull + 8 * a, aph, sm.abort_flag, p.status)) break;
+    tc_fence_after();
+    uint32_t v[4][32];
+    const uint32_t at = tmem_base + lanes + static_cast<uint32_t>(a * kTile + col0);
+    if (chunks > 0) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < chunks) tmem_ld_32x32b_x32_issue(at + 32 * c, v[c]);
+      tmem_wait_ld_regs(v[0]);
+#pragma unroll
+      for (int c = 1; c < 4; ++c) reg_order(v[c]);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      if (rank == 0) mbar_arrive_a(sm.accempty + 8 * a);
+      else mbar_arrive_remote(accempty_r + 8 * a);
+    }
+    if (++a == kAcc) a = 0, aph ^= 1u;
+    if constexpr (kMode == kStats) {
+      const int valid = p.columns - t.n0 - col0;  // of this warp's columns
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c >= chunks) continue;
+        if (c * 32 + 32 > valid)
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (c * 32 + x >= valid) v[c][x] = __float_as_uint(-INFINITY);
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) top = max3(top, __uint_as_float(v[c][x]), __uint_as_float(v[c][x + 1]));
+      }
+      const float m2 = top * p.z2;
+      float sum[4] = {};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c >= chunks) continue;
+#pragma unroll
+        for (int x = 0; x < 32; ++x) sum[x & 3] += fast_exp2(fmaf(__uint_as_float(v[c][x]), p.z2, -m2));
+        if (__any_sync(0xffffffffu, (target >> 5) == c)) {
+          float z = 0.f;
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (target == c * 32 + x) z = __uint_as_float(v[c][x]);
+          if ((target >> 5) == c) p.hit[row] = z;
+        }
+      }
+      if (row < p.s.T && valid > 0)
+        p.parts[static_cast<int64_t>((t.n0 + col0) / kHalf) * p.s.T + row] =
+            make_float2(m2, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+    } else if constexpr (kMode == kGrad) {
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        if (c >= chunks) continue;
+        uint32_t w[32];
+#pragma unroll
+        for (int x = 0; x < 64; x += 2) {
+          float e[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float q = fast_exp2(fmaf(__uint_as_float(v[c + (x + y) / 32][(x + y) % 32]), p.z2, -lse2));
+            e[y] = q * coef;
+          }
+          w[x / 2] = pack2<kBf16>(e[0], e[1]);
+        }
+        if (__any_sync(0xffffffffu, (target >> 6) == c / 2)) {
+#pragma unroll
+          for (int x = 0; x < 64; ++x)
+            if (target == c * 32 + x) {
+              const float q = fast_exp2(fmaf(__uint_as_float(v[c + x / 32][x % 32]), p.z2, -lse2));
+              const uint32_t one = pack2<kBf16>((q - 1.f) * coef, 0.f) & 0xFFFFu;
+              w[x / 2] = x & 1 ? (w[x / 2] & 0xFFFFu) | one << 16 : (w[x / 2] & 0xFFFF0000u) | one;
+            }
+        }
+        if (lane == 0) store_wait_read();
+        __syncwarp();
+        put_row(stage, lane, w);
+        if (row0 < p.s.T && t.n0 + col0 + c * 32 < p.columns)
+          send(&maps.out0, stage, lane, t.n0 + col0 + c * 32, row0, 0, false);
+      }
+    } else {
+      const bool dx = t.kind == 1;
+      const int rows = dx ? p.s.T : p.columns;
+      const int y = dx ? row0 : p.first + row0;
+      if (dx && p.dx_wide) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c >= chunks) continue;
+          if (lane == 0) store_wait_read();
+          __syncwarp();
+          put_row(stage, lane, v[c]);
+          if (row0 < rows && t.n0 + col0 + c * 32 < p.s.d)
+            send(&maps.out0, stage, lane, t.n0 + col0 + c * 32, y, t.split, p.dx_adds);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          if (c >= chunks) continue;
+          uint32_t w[32];
+#pragma unroll
+          for (int x = 0; x < 64; x += 2)
+            w[x / 2] = pack2<kBf16>(__uint_as_float(v[c + x / 32][x % 32]) * gain,
+                                    __uint_as_float(v[c + x / 32][x % 32 + 1]) * gain);
+          if (lane == 0) store_wait_read();
+          __syncwarp();
+          put_row(stage, lane, w);
+          if (row0 < rows && t.n0 + col0 + c * 32 < p.s.d)
+            send(dx ? &maps.out0 : &maps.out1, stage, lane, t.n0 + col0 + c * 32, y, 0, false);
+        }
+      }
+    }
+  }
+  if (kMode != kStats && lane == 0) store_wait();
+}
+
+template <int kMode, bool kBf16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    loss_kernel(const __grid_constant__ Maps maps, const Params p) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  const Smem sm = carve(raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(sm.bars + s, 1);                // full: this CTA's copies
+      mbar_init(sm.bars + kStages + s, 1);      // empty: the products' commit, to both CTAs
+      mbar_init(sm.bars + 2 * kStages + s, 1);  // full2: the odd CTA's copies, on the even one
+    }
+    for (int i = 0; i < kAcc; ++i) {
+      mbar_init(sm.bars + 3 * kStages + i, 1);                     // accfull
+      mbar_init(sm.bars + 3 * kStages + kAcc + i, 2 * kEpiWarps);  // accempty: the warps of both CTAs, on the even one
+    }
+    mbar_init(sm.bars + kBars - 1, 1);
+    *sm.abort_flag = 0;
+    fence_mbar_init_cluster();
+  }
+  if (warp == kMmaWarp) tmem_alloc_pair(sm.tmem_slot, 512);
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *sm.tmem_slot;
+  if (warp >= kEpiWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+    if (warp == kProducerWarp && lane == 0) {
+      produce<kMode>(p, sm, maps, rank);
+    } else if (warp == kMmaWarp && lane == 0) {
+      if (rank == 0) multiply<kMode>(p, sm, tmem_base);
+      else relay<kMode>(p, sm);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+    finish<kMode, kBf16>(p, sm, maps, tmem_base, rank);
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();  // neither CTA leaves while the other may still signal it
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// ------------------------------------------------------------- small kernels
+// A row's parts become its lse and loss: 32 rows a block, eight warps along the parts.
+__global__ void __launch_bounds__(256) join_kernel(const float2* parts, int n, int T, int64_t V, const int64_t* targets,
+                                                   const float* hit, float scale, float* loss, float* lse,
+                                                   unsigned* status) {
+  __shared__ float2 s[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x * 32 + lane;
+  float top = -INFINITY, sum = 0.f;
+  if (row < T)
+    for (int i = warp; i < n; i += 8) {
+      const float2 q = parts[static_cast<int64_t>(i) * T + row];
+      const float m = fmaxf(top, q.x);
+      sum = sum * exp2f(top - m) + q.y * exp2f(q.x - m);  // the first: exp2(-inf) = 0
+      top = m;
+    }
+  s[warp][lane] = make_float2(top, sum);
+  __syncthreads();
+  if (warp || row >= T) return;
+  for (int w = 0; w < 8; ++w) top = fmaxf(top, s[w][lane].x);
+  sum = 0.f;
+  for (int w = 0; w < 8; ++w)
+    if (w < n) sum += s[w][lane].y * exp2f(s[w][lane].x - top);
+  const float l = (top + log2f(sum)) * kLn2;
+  lse[row] = l;
+  const int64_t t = targets[row];
+  if (t >= V) atomicOr(status, kDevErrBadInput);
+  loss[row] = t >= 0 && t < V ? l - hit[row] * scale : 0.f;
+}
+
+// coef[t] = dloss[t] 2^-e (0 where the row has no target), gain = scale 2^e, with e
+// the exponent of the largest |dloss|. fp16: 2^14 more in coef, and less in gain.
+__global__ void __launch_bounds__(1024) coef_kernel(const float* dloss, const int64_t* targets, int T, int64_t V,
+                                                    float scale, int more, float* coef, float* gain, unsigned* status) {
+  __shared__ float s[32];
+  float top = 0.f;
+  for (int i = threadIdx.x; i < T; i += 1024) {
+    const int64_t t = targets[i];
+    if (t >= V) atomicOr(status, kDevErrBadInput);
+    if (t >= 0 && t < V) top = fmaxf(top, fabsf(dloss[i]));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = top;
+  __syncthreads();
+  for (int w = 0; w < 32; ++w) top = fmaxf(top, s[w]);
+  const int e = top > 0.f && top < INFINITY ? ilogbf(top) : 0;
+  for (int i = threadIdx.x; i < T; i += 1024) {
+    const int64_t t = targets[i];
+    coef[i] = t >= 0 && t < V ? ldexpf(dloss[i], more - e) : 0.f;
+  }
+  if (threadIdx.x == 0) *gain = ldexpf(scale, e - more);
+}
+
+// dx: the parts' fp32 sums, times the gain.
+template <typename T>
+__global__ void __launch_bounds__(256) dx_kernel(const float* sums, int splits, int64_t n, int d, const float* gain,
+                                                 T* dx, int64_t stride) {
+  const int64_t i = (blockIdx.x * int64_t(256) + threadIdx.x) * 8;
+  if (i >= n) return;
+  float a[8] = {};
+  for (int s = 0; s < splits; ++s) {
+    const float4* q = reinterpret_cast<const float4*>(sums + s * n + i);
+    const float4 u = q[0], v = q[1];
+    a[0] += u.x, a[1] += u.y, a[2] += u.z, a[3] += u.w, a[4] += v.x, a[5] += v.y, a[6] += v.z, a[7] += v.w;
+  }
+  const int64_t row = i / d;
+  alignas(16) T o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = static_cast<T>(a[j] * *gain);
+  *reinterpret_cast<uint4*>(dx + row * stride + (i - row * d)) = *reinterpret_cast<uint4*>(o);
+}
+
+// ---------------------------------------------------------------------- host
+constexpr int64_t kPieceBytes = int64_t(256) << 20;
+
+int up_to(int64_t v, int to) { return static_cast<int>((v + to - 1) / to); }
+size_t padded(size_t bytes) { return (bytes + 255) & ~size_t(255); }
+
+// Columns of a piece: at most 256 MB of dz, in whole tiles, one tile at least.
+int piece_columns(const LossShape& s) {
+  const int64_t most = kPieceBytes / (2 * static_cast<int64_t>(s.T)) / kTile * kTile;
+  const int64_t all = static_cast<int64_t>(up_to(s.V, kTile)) * kTile;
+  return static_cast<int>(most < kTile ? kTile : most < all ? most : all);
+}
+
+// How dx's tiles are cut along the vocabulary: no part longer than a pair's share
+// of the launch, with an epilogue counted as eight steps.
+int split_count(const LossShape& s, int columns, int pairs) {
+  const int64_t steps = up_to(columns, kStep), dx = static_cast<int64_t>(up_to(s.T, kTile)) * up_to(s.d, kTile);
+  const int64_t dw = static_cast<int64_t>(up_to(columns, kTile)) * up_to(s.d, kTile);
+  int64_t share = (dx * (steps + 8) + dw * (up_to(s.T, kStep) + 8)) / pairs;
+  if (share < 16) share = 16;
+  const int64_t n = (steps + share - 1) / share;
+  return static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
+}
+
+bool map2(CUtensorMap* m, const LossShape& s, const void* data, int64_t stride, int64_t inner, int64_t rows) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(inner), static_cast<uint64_t>(rows)};
+  const uint64_t strides[1] = {static_cast<uint64_t>(stride) * 2};
+  const uint32_t box[2] = {kBox, kBox};
+  return encode_tmap(m, s.is_bf16 ? 1 : 0, 2, const_cast<void*>(data), dims, strides, box, 1);
+}
+bool map_out(CUtensorMap* m, int type, int esize, void* data, int64_t stride, int64_t inner, int64_t rows, int64_t depth) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(inner), static_cast<uint64_t>(rows), static_cast<uint64_t>(depth)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(stride) * esize, depth > 1 ? static_cast<uint64_t>(stride) * rows * esize : static_cast<uint64_t>(stride) * esize};
+  const uint32_t box[3] = {static_cast<uint32_t>(128 / esize), 32, 1};
+  return encode_tmap(m, type, 3, data, dims, strides, box, 1);
+}
+
+template <int kMode>
+cudaError_t launch(const Maps& maps, const Params& p, int pairs, cudaStream_t stream) {
+  const auto go = [&](auto kernel) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<2 * pairs, kThreads, kSmemBytes, stream>>>(maps, p);
+    return cudaGetLastError();
+  };
+  return p.s.is_bf16 ? go(loss_kernel<kMode, true>) : go(loss_kernel<kMode, false>);
+}
+
+struct Space {  // of the backward's workspace
+  size_t coef, dz, sums, bytes;
+  int columns, splits;
+  bool wide;
+};
+Space plan(const LossShape& s, int pairs) {
+  Space w;
+  w.columns = piece_columns(s);
+  w.splits = split_count(s, w.columns < s.V ? w.columns : static_cast<int>(s.V), pairs);
+  w.wide = w.splits > 1 || w.columns < s.V;
+  w.coef = 256;
+  w.dz = w.coef + padded(static_cast<size_t>(s.T) * 4);
+  w.sums = w.dz + padded(static_cast<size_t>(s.T) * w.columns * 2);
+  w.bytes = w.sums + (w.wide ? padded(static_cast<size_t>(w.splits) * s.T * s.d * 4) : 0);
+  return w;
+}
+
+}  // namespace
+
+size_t loss_workspace_bytes(const LossShape& s) {
+  return padded(static_cast<size_t>(s.T) * 4) + static_cast<size_t>(up_to(s.V, kHalf)) * s.T * sizeof(float2);
+}
+
+maxsim_status launch_loss(const LossShape& s, const maxsim_rows& x, const maxsim_rows& w, const int64_t* targets,
+                          float* loss, float* lse, void* workspace, cudaStream_t stream) {
+  const DeviceInfo* dev = device_info();
+  if (!dev) return MAXSIM_ERR_CUDA;
+  alignas(64) Maps maps = {};
+  if (!map2(&maps.x, s, x.data, x.row_stride, s.d, s.T) || !map2(&maps.w, s, w.data, w.row_stride, s.d, s.V))
+    return MAXSIM_ERR_CUDA;
+  Params p = {};
+  p.s = s;
+  p.columns = static_cast<int>(s.V);
+  p.tiles_m = up_to(s.T, kTile);
+  p.tiles_n = up_to(s.V, kTile);
+  p.targets = targets;
+  p.hit = static_cast<float*>(workspace);
+  p.parts = reinterpret_cast<float2*>(static_cast<char*>(workspace) + padded(static_cast<size_t>(s.T) * 4));
+  p.z2 = s.scale * kLog2e;
+  p.status = dev->status;
+  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+  const int most = dev->sm_count / 2, pairs = tiles < most ? static_cast<int>(tiles) : most;
+  if (launch<kStats>(maps, p, pairs, stream) != cudaSuccess) return MAXSIM_ERR_CUDA;
+  join_kernel<<<up_to(s.T, 32), 256, 0, stream>>>(p.parts, up_to(s.V, kHalf), s.T, s.V, targets, p.hit, s.scale, loss,
+                                                  lse, dev->status);
+  return cudaGetLastError() == cudaSuccess ? MAXSIM_OK : MAXSIM_ERR_CUDA;
+}
+
+size_t loss_bwd_workspace_bytes(const LossShape& s) {
+  const DeviceInfo* dev = device_info();
+  return plan(s, dev ? dev->sm_count / 2 : 76).bytes;
+}
+
+maxsim_status launch_loss_bwd(const LossShape& s, const float* dloss, const maxsim_rows& x, const maxsim_rows& w,
+                              const int64_t* targets, const float* lse, const maxsim_rows* dx, const maxsim_rows* dw,
+                              void* workspace, cudaStream_t stream) {
+  const DeviceInfo* dev = device_info();
+  if (!dev) return MAXSIM_ERR_CUDA;
+  const int most = dev->sm_count / 2;
+  const Space at = plan(s, most);
+  char* base = static_cast<char*>(workspace);
+  float *gain = reinterpret_cast<float*>(base), *coef = reinterpret_cast<float*>(base + at.coef);
+  float* sums = reinterpret_cast<float*>(base + at.sums);
+  coef_kernel<<<1, 1024, 0, stream>>>(dloss, targets, s.T, s.V, s.scale, s.is_bf16 ? 0 : 14, coef, gain, dev->status);
+  if (cudaGetLastError() != cudaSuccess) return MAXSIM_ERR_CUDA;
+  for (int64_t first = 0; first < s.V; first += at.columns) {
+    const int columns = s.V - first < at.columns ? static_cast<int>(s.V - first) : at.columns;
+    alignas(64) Maps maps = {};
+    if (!map2(&maps.x, s, x.data, x.row_stride, s.d, s.T) || !map2(&maps.w, s, w.data, w.row_stride, s.d, s.V) ||
+        !map2(&maps.dz, s, base + at.dz, at.columns, columns, s.T) ||
+        !map_out(&maps.out0, s.is_bf16 ? 1 : 0, 2, base + at.dz, at.columns, columns, s.T, 1))
+      return MAXSIM_ERR_CUDA;
+    Params p = {};
+    p.s = s;
+    p.first = static_cast<int>(first);
+    p.columns = columns;
+    p.tiles_m = up_to(s.T, kTile);
+    p.tiles_n = up_to(columns, kTile);
+    p.targets = targets;
+    p.lse = lse;
+    p.coef = coef;
+    p.gain = gain;
+    p.z2 = s.scale * kLog2e;
+    p.status = dev->status;
+    int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+    if (launch<kGrad>(maps, p, tiles < most ? static_cast<int>(tiles) : most, stream) != cudaSuccess)
+      return MAXSIM_ERR_CUDA;
+    p.splits = at.splits;
+    if (dx) {
+      p.dx_m = up_to(s.T, kTile);
+      p.dx_n = up_to(s.d, kTile);
+      p.dx_wide = at.wide;
+      p.dx_adds = first > 0;
+      if (!(at.wide ? map_out(&maps.out0, 3, 4, sums, s.d, s.d, s.T, at.splits)
+                    : map_out(&maps.out0, s.is_bf16 ? 1 : 0, 2, dx->data, dx->row_stride, s.d, s.T, 1)))
+        return MAXSIM_ERR_CUDA;
+    }
+    if (dw) {
+      p.dw_m = up_to(columns, kTile);
+      p.dw_n = up_to(s.d, kTile);
+      const int dx_cost = up_to(columns, kStep) / at.splits + 8, dw_cost = up_to(s.T, kStep) + 8;
+      p.rounds = (dx_cost + dw_cost / 2) / dw_cost;
+      if (!map_out(&maps.out1, s.is_bf16 ? 1 : 0, 2, dw->data, dw->row_stride, s.d, s.V, 1)) return MAXSIM_ERR_CUDA;
+    }
+    tiles = static_cast<int64_t>(p.dx_m) * p.dx_n * p.splits + static_cast<int64_t>(p.dw_m) * p.dw_n;
+    if (tiles && launch<kSums>(maps, p, tiles < most ? static_cast<int>(tiles) : most, stream) != cudaSuccess)
+      return MAXSIM_ERR_CUDA;
+  }
+  if (dx && at.wide) {
+    const int64_t n = static_cast<int64_t>(s.T) * s.d;
+    const int grid = static_cast<int>((n / 8 + 255) / 256);
+    if (s.is_bf16)
+      dx_kernel<<<grid, 256, 0, stream>>>(sums, at.splits, n, s.d, gain, static_cast<__nv_bfloat16*>(dx->data), dx->row_stride);
+    else
+      dx_kernel<<<grid, 256, 0, stream>>>(sums, at.splits, n, s.d, gain, static_cast<__half*>(dx->data), dx->row_stride);
+    if (cudaGetLastError() != cudaSuccess) return MAXSIM_ERR_CUDA;
+  }
+  return MAXSIM_OK;
+}
+
+}  // namespace msim
