@@ -36,7 +36,7 @@ constexpr int kBoxBytes = kBox * 128;
 constexpr int kStages = 6, kStageBytes = 4 * kBoxBytes;  // two boxes of A, two of B
 constexpr int kAcc = 2;
 constexpr int kStageOut = 32 * 128;            // a warp's way out: 32 rows of 128 bytes
-constexpr int kBars = 3 * kStages + 2 * kAcc + 1;
+constexpr int kBars = 2 * kStages + 2 * kAcc + 1;
 constexpr int kSmallBytes = kBars * 8 + 16;
 constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kEpiWarps * kStageOut + kSmallBytes;
 constexpr int kGroupM = 32;                    // row tiles that share a pass over the vocabulary
@@ -70,7 +70,7 @@ struct Smem {
   uint64_t* bars;
   uint32_t* tmem_slot;
   volatile int* abort_flag;
-  uint32_t full, empty, full2, accfull, accempty, done;
+  uint32_t full, empty, accfull, accempty, done;
 };
 __device__ __forceinline__ Smem carve(uint8_t* raw) {
   Smem s;
@@ -82,8 +82,7 @@ __device__ __forceinline__ Smem carve(uint8_t* raw) {
   s.abort_flag = reinterpret_cast<volatile int*>(s.tmem_slot + 1);
   s.full = smem_u32(s.bars);
   s.empty = s.full + 8 * kStages;
-  s.full2 = s.empty + 8 * kStages;
-  s.accfull = s.full2 + 8 * kStages;
+  s.accfull = s.empty + 8 * kStages;
   s.accempty = s.accfull + 8 * kAcc;
   s.done = s.accempty + 8 * kAcc;
   return s;
@@ -157,10 +156,21 @@ __device__ __forceinline__ bool tile_of(const Params& p, int i, Tile& t) {
 }
 
 // ------------------------------------------------------------------ producer
+constexpr uint64_t kSettleNs = 1000000;
+
+// A load into this CTA that completes on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
 template <int kMode>
 __device__ void produce(const Params& p, const Smem& sm, const Maps& maps, uint32_t rank) {
   if (debug_faults(p.status) & kDebugStallFwdLoader) return;
-  const uint32_t stage0 = smem_u32(sm.stages);
+  const uint32_t stage0 = smem_u32(sm.stages), full_even = mapa_shared(sm.full, 0);
   uint32_t fills = 0;
   int s = 0;
   uint32_t ph = 0;
@@ -176,26 +186,34 @@ __device__ void produce(const Params& p, const Smem& sm, const Maps& maps, uint3
         ok = false;
         break;
       }
-      const uint32_t bar = sm.full + 8 * s, to = stage0 + static_cast<uint32_t>(s) * kStageBytes;
+      const uint32_t bar = full_even + 8 * s, to = stage0 + static_cast<uint32_t>(s) * kStageBytes;
       const int kk = (t.k0 + k) * kStep;
-      mbar_arrive_expect_tx_a(bar, (2 + boxes_b) * kBoxBytes);
+      if (rank == 0) mbar_arrive_expect_tx_a(sm.full + 8 * s, 2 * (2 + boxes_b) * kBoxBytes);
       // K-major: x along K, y along M or N. Else x along M or N, y along K.
       for (int h = 0; h < 2; ++h) {
-        if (t.kind == 2) tma_load_2d_nohint_a(to + h * kBoxBytes, a, bar, am + h * kBox, kk);
-        else tma_load_2d_nohint_a(to + h * kBoxBytes, a, bar, kk, am + h * kBox);
+        if (t.kind == 2) tma_load_pair(to + h * kBoxBytes, a, bar, am + h * kBox, kk);
+        else tma_load_pair(to + h * kBoxBytes, a, bar, kk, am + h * kBox);
       }
       for (int h = 0; h < boxes_b; ++h) {
         const uint32_t dst = to + (2 + h) * kBoxBytes;
-        if (t.kind == 0) tma_load_2d_nohint_a(dst, b, bar, kk, p.first + bn + h * kBox);
-        else tma_load_2d_nohint_a(dst, b, bar, bn + h * kBox, (t.kind == 1 ? p.first : 0) + kk);
+        if (t.kind == 0) tma_load_pair(dst, b, bar, kk, p.first + bn + h * kBox);
+        else tma_load_pair(dst, b, bar, bn + h * kBox, (t.kind == 1 ? p.first : 0) + kk);
       }
       ++fills;
       if (++s == kStages) s = 0, ph ^= 1u;
     }
   }
-  if (!ok)  // copies in flight land before the block ends
+  if (ok || !fills) return;
+  // Given up: copies in flight land before the block ends. The even CTA waits for
+  // those that it announced; the odd one, whose copies signal there, for a
+  // thousand times what a copy takes.
+  if (rank == 0) {
     for (uint32_t f = fills > kStages ? fills - kStages : 0; f < fills; ++f)
       mbar_wait_drain(sm.bars + (f % kStages), (f / kStages) & 1u, p.status);
+  }
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < kSettleNs) {
+  }
 }
 
 // ------------------------------------------------- products (even CTA, one thread)
@@ -218,8 +236,7 @@ __device__ void multiply(const Params& p, const Smem& sm, uint32_t tmem_base) {
     const uint64_t a_step = a_mn ? 2048 >> 4 : 2, b_step = b_mn ? 2048 >> 4 : 2;
     const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(a * kTile);
     for (int k = 0; k < t.steps; ++k) {
-      if (!mbar_poll_inl_a(sm.full + 8 * s, ph, sm.abort_flag, p.status) ||
-          !mbar_poll_inl_a(sm.full2 + 8 * s, ph, sm.abort_flag, p.status)) {
+      if (!mbar_poll_inl_a(sm.full + 8 * s, ph, sm.abort_flag, p.status)) {
         ok = false;
         break;
       }
@@ -237,21 +254,6 @@ __device__ void multiply(const Params& p, const Smem& sm, uint32_t tmem_base) {
   }
   umma_commit_pair(sm.done, 1);  // TMEM is freed only after the last product
   mbar_wait_drain(sm.bars + kBars - 1, 0, p.status);
-}
-
-// The odd CTA's operands have arrived: the even one's issuer hears of it.
-template <int kMode>
-__device__ void relay(const Params& p, const Smem& sm) {
-  const uint32_t to = mapa_shared(sm.full2, 0);
-  int s = 0;
-  uint32_t ph = 0;
-  Tile t;
-  for (int i = 0; tile_of<kMode>(p, i, t); ++i)
-    for (int k = 0; k < t.steps; ++k) {
-      if (!mbar_wait_inl_a(sm.full + 8 * s, ph, sm.abort_flag, p.status)) return;
-      mbar_arrive_cluster(to + 8 * s);
-      if (++s == kStages) s = 0, ph ^= 1u;
-    }
 }
 
 // ------------------------------------------------------------------ epilogue
@@ -444,13 +446,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(sm.bars + s, 1);                // full: this CTA's copies
-      mbar_init(sm.bars + kStages + s, 1);      // empty: the products' commit, to both CTAs
-      mbar_init(sm.bars + 2 * kStages + s, 1);  // full2: the odd CTA's copies, on the even one
+      mbar_init(sm.bars + s, 1);            // full: the copies of both CTAs, on the even one
+      mbar_init(sm.bars + kStages + s, 1);  // empty: the products' commit, to both CTAs
     }
     for (int i = 0; i < kAcc; ++i) {
-      mbar_init(sm.bars + 3 * kStages + i, 1);                     // accfull
-      mbar_init(sm.bars + 3 * kStages + kAcc + i, 2 * kEpiWarps);  // accempty: the warps of both CTAs, on the even one
+      mbar_init(sm.bars + 2 * kStages + i, 1);                     // accfull
+      mbar_init(sm.bars + 2 * kStages + kAcc + i, 2 * kEpiWarps);  // accempty: the warps of both CTAs, on the even one
     }
     mbar_init(sm.bars + kBars - 1, 1);
     *sm.abort_flag = 0;
@@ -467,7 +468,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       produce<kMode>(p, sm, maps, rank);
     } else if (warp == kMmaWarp && lane == 0) {
       if (rank == 0) multiply<kMode>(p, sm, tmem_base);
-      else relay<kMode>(p, sm);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
