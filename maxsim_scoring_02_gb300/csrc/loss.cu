@@ -31,8 +31,8 @@ constexpr int kEpiWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kThreads = 384;
 constexpr int kRegsCtl = 56, kRegsEpi = 224, kRegsLaunch = 168;
 static_assert(2 * 128 * kRegsEpi + 128 * kRegsCtl <= kThreads * kRegsLaunch, "register split");
 constexpr int kTile = 256, kHalf = 128, kStep = 64;
-constexpr int kBox = 64;                       // every operand is loaded in boxes of 64 x 64 elements
-constexpr int kBoxBytes = kBox * 128;
+constexpr int kBox = 64;                       // 64 x 64 elements: a K-major operand comes as one copy of two
+constexpr int kBoxBytes = kBox * 128;          // such boxes, one with M or N contiguous as two copies
 constexpr int kStages = 6, kStageBytes = 4 * kBoxBytes;  // two boxes of A, two of B
 constexpr int kAcc = 2;
 constexpr int kStageOut = 32 * 128;            // a warp's way out: 32 rows of 128 bytes
@@ -46,7 +46,8 @@ constexpr uint32_t kIdescAMnMajor = 1u << 15;  // flag of the instruction descri
 enum Mode { kStats, kGrad, kSums };
 
 struct Maps {
-  CUtensorMap x, w, dz;    // operands: [T, d], [V, d], [T, columns of the piece]
+  CUtensorMap a, b;        // z: x and W; dx: dz and W
+  CUtensorMap a2, b2;      // dW: dz and x
   CUtensorMap out0, out1;  // kGrad: dz; kSums: dx (or its fp32 sums), dW
 };
 
@@ -177,10 +178,9 @@ __device__ void produce(const Params& p, const Smem& sm, const Maps& maps, uint3
   Tile t;
   bool ok = true;
   for (int i = 0; ok && tile_of<kMode>(p, i, t); ++i) {
-    const CUtensorMap* a = t.kind == 0 ? &maps.x : &maps.dz;
-    const CUtensorMap* b = t.kind == 2 ? &maps.x : &maps.w;
+    const CUtensorMap *a = t.kind == 2 ? &maps.a2 : &maps.a, *b = t.kind == 2 ? &maps.b2 : &maps.b;
     const int am = t.m0 + static_cast<int>(rank) * kHalf, bn = t.n0 + static_cast<int>(rank) * (t.n / 2);
-    const int boxes_b = t.n / 2 > kBox ? 2 : 1;
+    const int boxes_b = t.kind == 0 || t.n / 2 > kBox ? 2 : 1;
     for (int k = 0; k < t.steps; ++k) {
       if (!mbar_wait_inl_a(sm.empty + 8 * s, ph ^ 1u, sm.abort_flag, p.status)) {
         ok = false;
@@ -189,15 +189,18 @@ __device__ void produce(const Params& p, const Smem& sm, const Maps& maps, uint3
       const uint32_t bar = full_even + 8 * s, to = stage0 + static_cast<uint32_t>(s) * kStageBytes;
       const int kk = (t.k0 + k) * kStep;
       if (rank == 0) mbar_arrive_expect_tx_a(sm.full + 8 * s, 2 * (2 + boxes_b) * kBoxBytes);
-      // K-major: x along K, y along M or N. Else x along M or N, y along K.
-      for (int h = 0; h < 2; ++h) {
-        if (t.kind == 2) tma_load_pair(to + h * kBoxBytes, a, bar, am + h * kBox, kk);
-        else tma_load_pair(to + h * kBoxBytes, a, bar, kk, am + h * kBox);
+      if (t.kind == 2) {
+        tma_load_pair(to, a, bar, am, kk);
+        tma_load_pair(to + kBoxBytes, a, bar, am + kBox, kk);
+      } else {
+        tma_load_pair(to, a, bar, kk, am);
       }
-      for (int h = 0; h < boxes_b; ++h) {
-        const uint32_t dst = to + (2 + h) * kBoxBytes;
-        if (t.kind == 0) tma_load_pair(dst, b, bar, kk, p.first + bn + h * kBox);
-        else tma_load_pair(dst, b, bar, bn + h * kBox, (t.kind == 1 ? p.first : 0) + kk);
+      if (t.kind == 0) {
+        tma_load_pair(to + 2 * kBoxBytes, b, bar, kk, p.first + bn);
+      } else {
+        const int kb = (t.kind == 1 ? p.first : 0) + kk;
+        tma_load_pair(to + 2 * kBoxBytes, b, bar, bn, kb);
+        if (boxes_b == 2) tma_load_pair(to + 3 * kBoxBytes, b, bar, bn + kBox, kb);
       }
       ++fills;
       if (++s == kStages) s = 0, ph ^= 1u;
@@ -578,10 +581,10 @@ int split_count(const LossShape& s, int columns, int pairs) {
   return static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
 }
 
-bool map2(CUtensorMap* m, const LossShape& s, const void* data, int64_t stride, int64_t inner, int64_t rows) {
+bool map_in(CUtensorMap* m, const LossShape& s, const void* data, int64_t stride, int64_t inner, int64_t rows, uint32_t box_rows) {
   const uint64_t dims[2] = {static_cast<uint64_t>(inner), static_cast<uint64_t>(rows)};
   const uint64_t strides[1] = {static_cast<uint64_t>(stride) * 2};
-  const uint32_t box[2] = {kBox, kBox};
+  const uint32_t box[2] = {kBox, box_rows};
   return encode_tmap(m, s.is_bf16 ? 1 : 0, 2, const_cast<void*>(data), dims, strides, box, 1);
 }
 bool map_out(CUtensorMap* m, int type, int esize, void* data, int64_t stride, int64_t inner, int64_t rows, int64_t depth) {
@@ -630,7 +633,7 @@ maxsim_status launch_loss(const LossShape& s, const maxsim_rows& x, const maxsim
   const DeviceInfo* dev = device_info();
   if (!dev) return MAXSIM_ERR_CUDA;
   alignas(64) Maps maps = {};
-  if (!map2(&maps.x, s, x.data, x.row_stride, s.d, s.T) || !map2(&maps.w, s, w.data, w.row_stride, s.d, s.V))
+  if (!map_in(&maps.a, s, x.data, x.row_stride, s.d, s.T, kHalf) || !map_in(&maps.b, s, w.data, w.row_stride, s.d, s.V, kHalf))
     return MAXSIM_ERR_CUDA;
   Params p = {};
   p.s = s;
@@ -670,8 +673,8 @@ maxsim_status launch_loss_bwd(const LossShape& s, const float* dloss, const maxs
   for (int64_t first = 0; first < s.V; first += at.columns) {
     const int columns = s.V - first < at.columns ? static_cast<int>(s.V - first) : at.columns;
     alignas(64) Maps maps = {};
-    if (!map2(&maps.x, s, x.data, x.row_stride, s.d, s.T) || !map2(&maps.w, s, w.data, w.row_stride, s.d, s.V) ||
-        !map2(&maps.dz, s, base + at.dz, at.columns, columns, s.T) ||
+    if (!map_in(&maps.a, s, x.data, x.row_stride, s.d, s.T, kHalf) ||
+        !map_in(&maps.b, s, w.data, w.row_stride, s.d, s.V, kHalf) ||
         !map_out(&maps.out0, s.is_bf16 ? 1 : 0, 2, base + at.dz, at.columns, columns, s.T, 1))
       return MAXSIM_ERR_CUDA;
     Params p = {};
@@ -688,6 +691,11 @@ maxsim_status launch_loss_bwd(const LossShape& s, const float* dloss, const maxs
     p.status = dev->status;
     int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
     if (launch<kGrad>(maps, p, tiles < most ? static_cast<int>(tiles) : most, stream) != cudaSuccess)
+      return MAXSIM_ERR_CUDA;
+    if (!map_in(&maps.a, s, base + at.dz, at.columns, columns, s.T, kHalf) ||
+        !map_in(&maps.b, s, w.data, w.row_stride, s.d, s.V, kBox) ||
+        !map_in(&maps.a2, s, base + at.dz, at.columns, columns, s.T, kBox) ||
+        !map_in(&maps.b2, s, x.data, x.row_stride, s.d, s.T, kBox))
       return MAXSIM_ERR_CUDA;
     p.splits = at.splits;
     if (dx) {
