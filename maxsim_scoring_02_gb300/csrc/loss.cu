@@ -159,12 +159,44 @@ __device__ __forceinline__ bool tile_of(const Params& p, int i, Tile& t) {
 // ------------------------------------------------------------------ producer
 constexpr uint64_t kSettleNs = 1000000;
 
+// The producer and the issuer are whole warps that stay together, one elected lane
+// of which does the work: their operands are then known to be uniform. As single
+// threads beside 31 waiting ones they took 545 cycles a step, whatever the step held.
+
 // A load into this CTA that completes on a barrier of either CTA of the pair.
-__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+__device__ __forceinline__ void tma_load_pair_el(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx_el(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f16_pair_el(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_pair_el(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+      "h"(mask)
       : "memory");
 }
 
@@ -182,25 +214,25 @@ __device__ void produce(const Params& p, const Smem& sm, const Maps& maps, uint3
     const int am = t.m0 + static_cast<int>(rank) * kHalf, bn = t.n0 + static_cast<int>(rank) * (t.n / 2);
     const int boxes_b = t.kind == 0 || t.n / 2 > kBox ? 2 : 1;
     for (int k = 0; k < t.steps; ++k) {
-      if (!mbar_wait_inl_a(sm.empty + 8 * s, ph ^ 1u, sm.abort_flag, p.status)) {
+      if (!mbar_wait_warp(sm.empty + 8 * s, ph ^ 1u, sm.abort_flag, p.status)) {
         ok = false;
         break;
       }
       const uint32_t bar = full_even + 8 * s, to = stage0 + static_cast<uint32_t>(s) * kStageBytes;
       const int kk = (t.k0 + k) * kStep;
-      if (rank == 0) mbar_arrive_expect_tx_a(sm.full + 8 * s, 2 * (2 + boxes_b) * kBoxBytes);
+      if (rank == 0) mbar_arrive_expect_tx_el(sm.full + 8 * s, 2 * (2 + boxes_b) * kBoxBytes);
       if (t.kind == 2) {
-        tma_load_pair(to, a, bar, am, kk);
-        tma_load_pair(to + kBoxBytes, a, bar, am + kBox, kk);
+        tma_load_pair_el(to, a, bar, am, kk);
+        tma_load_pair_el(to + kBoxBytes, a, bar, am + kBox, kk);
       } else {
-        tma_load_pair(to, a, bar, kk, am);
+        tma_load_pair_el(to, a, bar, kk, am);
       }
       if (t.kind == 0) {
-        tma_load_pair(to + 2 * kBoxBytes, b, bar, kk, p.first + bn);
+        tma_load_pair_el(to + 2 * kBoxBytes, b, bar, kk, p.first + bn);
       } else {
         const int kb = (t.kind == 1 ? p.first : 0) + kk;
-        tma_load_pair(to + 2 * kBoxBytes, b, bar, bn, kb);
-        if (boxes_b == 2) tma_load_pair(to + 3 * kBoxBytes, b, bar, bn + kBox, kb);
+        tma_load_pair_el(to + 2 * kBoxBytes, b, bar, bn, kb);
+        if (boxes_b == 2) tma_load_pair_el(to + 3 * kBoxBytes, b, bar, bn + kBox, kb);
       }
       ++fills;
       if (++s == kStages) s = 0, ph ^= 1u;
@@ -219,7 +251,7 @@ __device__ void produce(const Params& p, const Smem& sm, const Maps& maps, uint3
   }
 }
 
-// ------------------------------------------------- products (even CTA, one thread)
+// ------------------------------------------------- products (even CTA, one warp)
 template <int kMode>
 __device__ void multiply(const Params& p, const Smem& sm, uint32_t tmem_base) {
   const uint32_t stage0 = smem_u32(sm.stages);
@@ -231,7 +263,7 @@ __device__ void multiply(const Params& p, const Smem& sm, uint32_t tmem_base) {
   bool ok = true;
   for (int i = 0; ok && tile_of<kMode>(p, i, t); ++i) {
     if (t.steps == 0) continue;
-    if (!mbar_poll_inl_a(sm.accempty + 8 * a, aph ^ 1u, sm.abort_flag, p.status)) break;
+    if (!mbar_wait_warp(sm.accempty + 8 * a, aph ^ 1u, sm.abort_flag, p.status)) break;
     tc_fence_after();
     const bool a_mn = t.kind == 2, b_mn = t.kind != 0;
     const uint32_t idesc = idesc_f16(p.s.is_bf16, kTile, t.n) | (a_mn ? kIdescAMnMajor : 0u) | (b_mn ? kIdescBMnMajor : 0u);
@@ -239,7 +271,7 @@ __device__ void multiply(const Params& p, const Smem& sm, uint32_t tmem_base) {
     const uint64_t a_step = a_mn ? 2048 >> 4 : 2, b_step = b_mn ? 2048 >> 4 : 2;
     const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(a * kTile);
     for (int k = 0; k < t.steps; ++k) {
-      if (!mbar_poll_inl_a(sm.full + 8 * s, ph, sm.abort_flag, p.status)) {
+      if (!mbar_wait_warp(sm.full + 8 * s, ph, sm.abort_flag, p.status)) {
         ok = false;
         break;
       }
@@ -247,15 +279,15 @@ __device__ void multiply(const Params& p, const Smem& sm, uint32_t tmem_base) {
       const uint64_t at = static_cast<uint64_t>((s * kStageBytes) >> 4);
 #pragma unroll
       for (int x = 0; x < 4; ++x)
-        umma_f16_pair(d_tmem, ad0 + at + x * a_step, bd0 + at + x * b_step, idesc, (k | x) != 0 ? 1u : 0u);
-      umma_commit_pair(sm.empty + 8 * s, both);
+        umma_f16_pair_el(d_tmem, ad0 + at + x * a_step, bd0 + at + x * b_step, idesc, (k | x) != 0 ? 1u : 0u);
+      umma_commit_pair_el(sm.empty + 8 * s, both);
       if (++s == kStages) s = 0, ph ^= 1u;
     }
     if (!ok) break;
-    umma_commit_pair(sm.accfull + 8 * a, both);
+    umma_commit_pair_el(sm.accfull + 8 * a, both);
     if (++a == kAcc) a = 0, aph ^= 1u;
   }
-  umma_commit_pair(sm.done, 1);  // TMEM is freed only after the last product
+  umma_commit_pair_el(sm.done, 1);  // TMEM is freed only after the last product
   mbar_wait_drain(sm.bars + kBars - 1, 0, p.status);
 }
 
@@ -445,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     loss_kernel(const __grid_constant__ Maps maps, const Params p) {
   extern __shared__ __align__(16) uint8_t raw[];
   const Smem sm = carve(raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // known to be the same in all lanes
   const uint32_t rank = cluster_ctarank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -467,11 +499,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *sm.tmem_slot;
   if (warp >= kEpiWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
-    if (warp == kProducerWarp && lane == 0) {
-      produce<kMode>(p, sm, maps, rank);
-    } else if (warp == kMmaWarp && lane == 0) {
-      if (rank == 0) multiply<kMode>(p, sm, tmem_base);
-    }
+    if (warp == kProducerWarp) produce<kMode>(p, sm, maps, rank);
+    else if (warp == kMmaWarp && rank == 0) multiply<kMode>(p, sm, tmem_base);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
     finish<kMode, kBf16>(p, sm, maps, tmem_base, rank);
