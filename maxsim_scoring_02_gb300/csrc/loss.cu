@@ -39,6 +39,10 @@ constexpr int kStageOut = 32 * 128;            // a warp's way out: 32 rows of 1
 constexpr int kBars = 2 * kStages + 2 * kAcc + 1;
 constexpr int kSmallBytes = kBars * 8 + 16;
 constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kEpiWarps * kStageOut + kSmallBytes;
+// The tensor core cuts each sum towards zero, so a logit of d = 2048 is off by some
+// 1e-6 of itself in one direction. kStats adds no more than this many steps there and
+// the parts in registers, with rounding: a quarter of that, and no more time.
+constexpr int kPartSteps = 8;
 constexpr int kGroupM = 32;                    // row tiles that share a pass over the vocabulary
 
 constexpr uint32_t kIdescAMnMajor = 1u << 15;  // flag of the instruction descriptor: A has its M dimension contiguous
@@ -263,29 +267,35 @@ __device__ void multiply(const Params& p, const Smem& sm, uint32_t tmem_base) {
   bool ok = true;
   for (int i = 0; ok && tile_of<kMode>(p, i, t); ++i) {
     if (t.steps == 0) continue;
-    if (!mbar_wait_warp(sm.accempty + 8 * a, aph ^ 1u, sm.abort_flag, p.status)) break;
-    tc_fence_after();
     const bool a_mn = t.kind == 2, b_mn = t.kind != 0;
     const uint32_t idesc = idesc_f16(p.s.is_bf16, kTile, t.n) | (a_mn ? kIdescAMnMajor : 0u) | (b_mn ? kIdescBMnMajor : 0u);
     const uint64_t ad0 = a_mn ? mnmajor : kmajor, bd0 = (b_mn ? mnmajor : kmajor) + ((2 * kBoxBytes) >> 4);
     const uint64_t a_step = a_mn ? 2048 >> 4 : 2, b_step = b_mn ? 2048 >> 4 : 2;
-    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(a * kTile);
-    for (int k = 0; k < t.steps; ++k) {
-      if (!mbar_wait_warp(sm.full + 8 * s, ph, sm.abort_flag, p.status)) {
+    for (int k = 0; ok && k < t.steps;) {
+      const int part = kMode == kStats ? min(t.steps, k + kPartSteps) : t.steps;
+      if (!mbar_wait_warp(sm.accempty + 8 * a, aph ^ 1u, sm.abort_flag, p.status)) {
         ok = false;
         break;
       }
-      tc_fence_after();
-      const uint64_t at = static_cast<uint64_t>((s * kStageBytes) >> 4);
+      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(a * kTile);
+      uint32_t adds = 0;
+      for (; k < part; ++k) {
+        if (!mbar_wait_warp(sm.full + 8 * s, ph, sm.abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t at = static_cast<uint64_t>((s * kStageBytes) >> 4);
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        umma_f16_pair_el(d_tmem, ad0 + at + x * a_step, bd0 + at + x * b_step, idesc, (k | x) != 0 ? 1u : 0u);
-      umma_commit_pair_el(sm.empty + 8 * s, both);
-      if (++s == kStages) s = 0, ph ^= 1u;
+        for (int x = 0; x < 4; ++x, adds = 1)
+          umma_f16_pair_el(d_tmem, ad0 + at + x * a_step, bd0 + at + x * b_step, idesc, adds);
+        umma_commit_pair_el(sm.empty + 8 * s, both);
+        if (++s == kStages) s = 0, ph ^= 1u;
+      }
+      if (!ok) break;
+      umma_commit_pair_el(sm.accfull + 8 * a, both);
+      if (++a == kAcc) a = 0, aph ^= 1u;
     }
-    if (!ok) break;
-    umma_commit_pair_el(sm.accfull + 8 * a, both);
-    if (++a == kAcc) a = 0, aph ^= 1u;
   }
   umma_commit_pair_el(sm.done, 1);  // TMEM is freed only after the last product
   mbar_wait_drain(sm.bars + kBars - 1, 0, p.status);
@@ -356,26 +366,41 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
     } else {
       gain = t.kind == 1 && p.dx_wide ? 1.f : *p.gain;
     }
-    __syncwarp();
-    if (!mbar_wait_warp(sm.accfull + 8 * a, aph, sm.abort_flag, p.status)) break;
-    tc_fence_after();
     uint32_t v[4][32];
-    const uint32_t at = tmem_base + lanes + static_cast<uint32_t>(a * kTile + col0);
-    if (chunks > 0) {
+    bool ok = true;
+    for (int k = 0; k < t.steps; k += kMode == kStats ? kPartSteps : t.steps) {
+      __syncwarp();
+      ok = mbar_wait_warp(sm.accfull + 8 * a, aph, sm.abort_flag, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t at = tmem_base + lanes + static_cast<uint32_t>(a * kTile + col0);
+      if (k == 0) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < chunks) tmem_ld_32x32b_x32_issue(at + 32 * c, v[c]);
-      tmem_wait_ld_regs(v[0]);
+        for (int c = 0; c < 4; ++c)
+          if (c < chunks) tmem_ld_32x32b_x32_issue(at + 32 * c, v[c]);
+        tmem_wait_ld_regs(v[0]);
 #pragma unroll
-      for (int c = 1; c < 4; ++c) reg_order(v[c]);
+        for (int c = 1; c < 4; ++c) reg_order(v[c]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c >= chunks) continue;
+          uint32_t u[32];
+          tmem_ld_32x32b_x32_issue(at + 32 * c, u);
+          tmem_wait_ld_regs(u);
+#pragma unroll
+          for (int x = 0; x < 32; ++x) v[c][x] = __float_as_uint(__uint_as_float(v[c][x]) + __uint_as_float(u[x]));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive_a(sm.accempty + 8 * a);
+        else mbar_arrive_remote(accempty_r + 8 * a);
+      }
+      if (++a == kAcc) a = 0, aph ^= 1u;
     }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) {
-      if (rank == 0) mbar_arrive_a(sm.accempty + 8 * a);
-      else mbar_arrive_remote(accempty_r + 8 * a);
-    }
-    if (++a == kAcc) a = 0, aph ^= 1u;
+    if (!ok) break;
     if constexpr (kMode == kStats) {
       const int valid = p.columns - t.n0 - col0;  // of this warp's columns
       float top = -INFINITY;
@@ -515,32 +540,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------- small kernels
-// A row's parts become its lse and loss: 32 rows a block, eight warps along the parts.
-__global__ void __launch_bounds__(256) join_kernel(const float2* parts, int n, int T, int64_t V, const int64_t* targets,
-                                                   const float* hit, float scale, float* loss, float* lse,
-                                                   unsigned* status) {
-  __shared__ float2 s[8][32];
+// A row's parts become its lse and loss: 32 rows a block, 32 warps along the parts,
+// each with eight loads in flight.
+__global__ void __launch_bounds__(1024) join_kernel(const float2* parts, int n, int T, int64_t V, const int64_t* targets,
+                                                    const float* hit, float scale, float* loss, float* lse,
+                                                    unsigned* status) {
+  __shared__ float2 s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x * 32 + lane;
   float top = -INFINITY, sum = 0.f;
   if (row < T)
-    for (int i = warp; i < n; i += 8) {
-      const float2 q = parts[static_cast<int64_t>(i) * T + row];
-      const float m = fmaxf(top, q.x);
-      sum = sum * exp2f(top - m) + q.y * exp2f(q.x - m);  // the first: exp2(-inf) = 0
+    for (int i = warp; i < n; i += 256) {
+      float2 q[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        q[u] = i + 32 * u < n ? parts[static_cast<int64_t>(i + 32 * u) * T + row] : make_float2(-INFINITY, 0.f);
+      float m = top;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) m = fmaxf(m, q[u].x);
+      sum *= exp2f(top - m);  // the first: exp2(-inf) = 0
+#pragma unroll
+      for (int u = 0; u < 8; ++u) sum += q[u].y * exp2f(q[u].x - m);
       top = m;
     }
   s[warp][lane] = make_float2(top, sum);
   __syncthreads();
-  if (warp || row >= T) return;
-  for (int w = 0; w < 8; ++w) top = fmaxf(top, s[w][lane].x);
-  sum = 0.f;
-  for (int w = 0; w < 8; ++w)
-    if (w < n) sum += s[w][lane].y * exp2f(s[w][lane].x - top);
+  // a warp a row
+  const float2 mine = s[lane][warp];
+  top = mine.x;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  sum = lane < n ? mine.y * exp2f(mine.x - top) : 0.f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  const int mine_row = blockIdx.x * 32 + warp;
+  if (lane || mine_row >= T) return;
   const float l = (top + log2f(sum)) * kLn2;
-  lse[row] = l;
-  const int64_t t = targets[row];
+  lse[mine_row] = l;
+  const int64_t t = targets[mine_row];
   if (t >= V) atomicOr(status, kDevErrBadInput);
-  loss[row] = t >= 0 && t < V ? l - hit[row] * scale : 0.f;
+  loss[mine_row] = t >= 0 && t < V ? l - hit[mine_row] * scale : 0.f;
 }
 
 // coef[t] = dloss[t] 2^-e (0 where the row has no target), gain = scale 2^e, with e
@@ -677,7 +715,7 @@ maxsim_status launch_loss(const LossShape& s, const maxsim_rows& x, const maxsim
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   const int most = dev->sm_count / 2, pairs = tiles < most ? static_cast<int>(tiles) : most;
   if (launch<kStats>(maps, p, pairs, stream) != cudaSuccess) return MAXSIM_ERR_CUDA;
-  join_kernel<<<up_to(s.T, 32), 256, 0, stream>>>(p.parts, up_to(s.V, kHalf), s.T, s.V, targets, p.hit, s.scale, loss,
+  join_kernel<<<up_to(s.T, 32), 1024, 0, stream>>>(p.parts, up_to(s.V, kHalf), s.T, s.V, targets, p.hit, s.scale, loss,
                                                   lse, dev->status);
   return cudaGetLastError() == cudaSuccess ? MAXSIM_OK : MAXSIM_ERR_CUDA;
 }
