@@ -901,6 +901,8 @@ def maxsim_clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, 
 # The C entry points are maxsim_dropout, maxsim_rms_norm and maxsim_cross_entropy, with
 # their gradients.
 
+# Calls on a few rows take as long as their Python: what was just made is not checked.
+
 def _rows(t, name, shape, dtype, index):
     """A [T, d] tensor on CUDA device ``index``, its rows contiguous, as a maxsim_rows."""
     if not isinstance(t, torch.Tensor):
@@ -919,12 +921,27 @@ def _rows(t, name, shape, dtype, index):
     return _Rows(t.data_ptr(), row)
 
 
-def _shape_of_rows(x, name, dtypes, said):
+def _first_rows(x, name, dtypes, said):
+    """The call's first tensor: its shape, type, device and view."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError(f"{name} must be a [T, d] tensor")
-    if x.dtype not in dtypes:
-        raise TypeError(f"{name} must be {said}, got {x.dtype}")
-    return x.shape, x.dtype, x.get_device()
+    dtype, index = x.dtype, x.get_device()
+    if dtype not in dtypes:
+        raise TypeError(f"{name} must be {said}, got {dtype}")
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    shape = x.shape
+    row, last = x.stride()
+    if last != 1 and shape[1] != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if shape[0] <= 1 or shape[1] == 0:
+        row = (shape[1] + 7) // 8 * 8
+    return shape, dtype, index, _Rows(x.data_ptr(), row)
+
+
+def _new_rows(t, d):
+    """A tensor of the call's own."""
+    return _Rows(t.data_ptr(), d if t.shape[0] > 1 else (d + 7) // 8 * 8)
 
 
 def _rng(p, rng):
@@ -947,32 +964,35 @@ def encoder_dropout(x, p, rng, residual=None, out=None, stream=None):
     not stored: the same call on the gradient of the result, without a residual,
     gives that of x. ``out`` may be x or residual."""
     lib = load_library()
-    shape, dtype, index = _shape_of_rows(x, "x", _DTYPE_CODE, "bf16, fp16 or fp32")
-    src = _rows(x, "x", shape, dtype, index)
+    shape, dtype, index, src = _first_rows(x, "x", _DTYPE_CODE, "bf16, fp16 or fp32")
+    T, d = shape
     res = None if residual is None else _rows(residual, "residual", shape, dtype, index)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=x.device)
-    st = lib.maxsim_dropout(src, res, shape[0], shape[1], p, _rng(p, rng), _DTYPE_CODE[dtype],
-                            _rows(out, "out", shape, dtype, index), _stream_on(stream, index))
-    _check(st, "maxsim_dropout")
+        dst = _new_rows(out, d)
+    else:
+        dst = _rows(out, "out", shape, dtype, index)
+    st = lib.maxsim_dropout(src, res, T, d, p, _rng(p, rng), _DTYPE_CODE[dtype], dst, _stream_on(stream, index))
+    if st:
+        _check(st, "maxsim_dropout")
     return out
 
 
 def _norm_spec(x, name, weight, eps, p, rng, fmt):
-    shape, dtype, index = _shape_of_rows(x, name, _DTYPE_CODE, "bf16, fp16 or fp32")
-    code = _DTYPE_CODE[dtype]
-    wcode = FP32
+    shape, dtype, index, view = _first_rows(x, name, _DTYPE_CODE, "bf16, fp16 or fp32")
+    T, d = shape
+    code, wptr = FP32, None
     if weight is not None:
-        if _dev(weight, "weight").dtype not in (torch.float32, dtype):
-            raise TypeError(f"weight must be fp32 or {dtype}, got {weight.dtype}")
-        if weight.numel() != shape[1]:
+        wtype = _dev(weight, "weight").dtype
+        if wtype != dtype and wtype != torch.float32:
+            raise TypeError(f"weight must be fp32 or {dtype}, got {wtype}")
+        if weight.numel() != d:
             raise ValueError("weight must have one entry a column")
-        wcode = _DTYPE_CODE[weight.dtype]
+        code, wptr = _DTYPE_CODE[wtype], weight.data_ptr()
     if fmt not in NORM_FORMATS:
         raise ValueError(f"fmt must be one of {tuple(NORM_FORMATS)}")
-    spec = _NormSpec(shape[0], shape[1], code, wcode, NORM_FORMATS[fmt][0], eps, p, _rng(p, rng),
-                     None if weight is None else weight.data_ptr())
-    return spec, shape, dtype, index
+    spec = _NormSpec(T, d, _DTYPE_CODE[dtype], code, NORM_FORMATS[fmt][0], eps, p, _rng(p, rng), wptr)
+    return spec, shape, dtype, index, view
 
 
 @_entry
@@ -986,25 +1006,34 @@ def encoder_rms_norm(x, weight=None, residual=None, eps=1e-6, p=0.0, rng=None, f
     takes). Returns out, then scale with a ``fmt``, then h with ``want_sum`` or
     ``sum_out`` (which may be x or residual): one tensor, or a tuple."""
     lib = load_library()
-    spec, shape, dtype, index = _norm_spec(x, "x", weight, eps, p, rng, fmt)
-    src = _rows(x, "x", shape, dtype, index)
+    spec, shape, dtype, index, src = _norm_spec(x, "x", weight, eps, p, rng, fmt)
+    device, d = x.device, shape[1]
     res = None if residual is None else _rows(residual, "residual", shape, dtype, index)
-    otype = NORM_FORMATS[fmt][1] or dtype
+    otype = dtype if fmt is None else NORM_FORMATS[fmt][1]
     if out is None:
-        out = torch.empty(shape, dtype=otype, device=x.device)
-    if sum_out is None and want_sum:
-        sum_out = torch.empty(shape, dtype=dtype, device=x.device)
+        out = torch.empty(shape, dtype=otype, device=device)
+        dst = _new_rows(out, d)
+    else:
+        dst = _rows(out, "out", shape, otype, index)
+    total = None
+    if sum_out is not None:
+        total = _rows(sum_out, "sum_out", shape, dtype, index)
+    elif want_sum:
+        sum_out = torch.empty(shape, dtype=dtype, device=device)
+        total = _new_rows(sum_out, d)
+    sptr = None
     if fmt is None:
         if scale is not None:
             raise ValueError("scale goes with an 8-bit fmt")
-    elif scale is None:
-        scale = torch.empty(shape[0], dtype=torch.float32, device=x.device)
-    elif _dev(scale, "scale", torch.float32).numel() != shape[0]:
-        raise ValueError("scale must have one entry a row")
-    st = lib.maxsim_rms_norm(spec, src, res, None if sum_out is None else _rows(sum_out, "sum_out", shape, dtype, index),
-                             _rows(out, "out", shape, otype, index), None if scale is None else scale.data_ptr(),
-                             _stream_on(stream, index))
-    _check(st, "maxsim_rms_norm")
+    else:
+        if scale is None:
+            scale = torch.empty(shape[0], dtype=torch.float32, device=device)
+        elif _dev(scale, "scale", torch.float32).numel() != shape[0]:
+            raise ValueError("scale must have one entry a row")
+        sptr = scale.data_ptr()
+    st = lib.maxsim_rms_norm(spec, src, res, total, dst, sptr, _stream_on(stream, index))
+    if st:
+        _check(st, "maxsim_rms_norm")
     if fmt is None:
         return out if sum_out is None else (out, sum_out)
     return (out, scale) if sum_out is None else (out, scale, sum_out)
@@ -1024,10 +1053,10 @@ def encoder_rms_norm_backward(dy, h, weight=None, dsum=None, eps=1e-6, p=0.0, rn
     from elsewhere. Returns dx, dresidual and dweight (None without a weight). Without
     dropout dx and dresidual are one tensor, unless both are given."""
     lib = load_library()
-    spec, shape, dtype, index = _norm_spec(h, "h", weight, eps, p, rng, None)
+    spec, shape, dtype, index, hv = _norm_spec(h, "h", weight, eps, p, rng, None)
     device = h.device
-    views = [_rows(dy, "dy", shape, dtype, index), _rows(h, "h", shape, dtype, index),
-             None if dsum is None else _rows(dsum, "dsum", shape, dtype, index)]
+    views = (_rows(dy, "dy", shape, dtype, index), hv,
+             None if dsum is None else _rows(dsum, "dsum", shape, dtype, index))
     if not p and (dx is None or dresidual is None):
         dx = dx if dx is not None else dresidual if dresidual is not None else torch.empty(shape, dtype=dtype, device=device)
         dresidual, second = dx, None
@@ -1058,13 +1087,13 @@ _LOSS_TYPES = {torch.bfloat16: BF16, torch.float16: FP16}
 
 
 def _loss_spec(x, weight, targets, scale):
-    shape, dtype, index = _shape_of_rows(x, "x", _LOSS_TYPES, "bf16 or fp16")
+    shape, dtype, index, view = _first_rows(x, "x", _LOSS_TYPES, "bf16 or fp16")
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2 or weight.shape[1] != shape[1]:
         raise ValueError("weight must be [V, d], with x's d")
     if _dev(targets, "targets", torch.int64).numel() != shape[0]:
         raise ValueError("targets must have one entry a row")
     spec = _LossSpec(shape[0], weight.shape[0], shape[1], _LOSS_TYPES[dtype], scale, targets.data_ptr())
-    return spec, _rows(x, "x", shape, dtype, index), _rows(weight, "weight", weight.shape, dtype, index), index
+    return spec, view, _rows(weight, "weight", weight.shape, dtype, index), index
 
 
 def encoder_cross_entropy_workspace_size(x, weight, targets):

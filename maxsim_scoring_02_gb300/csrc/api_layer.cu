@@ -127,7 +127,7 @@ maxsim_status maxsim_rms_norm(const maxsim_norm_spec* spec, const maxsim_rows* x
   p.weight = spec->weight;
   p.weight_fp32 = spec->weight_dtype == MAXSIM_FP32;
   p.scale = scale;
-  p.T = static_cast<int>(T), p.d = d, p.format = spec->format, p.eps = spec->eps, p.drop = drop;
+  p.T = static_cast<int>(T), p.d = d, p.per = 1.f / d, p.format = spec->format, p.eps = spec->eps, p.drop = drop;
   const bool whole = whole_rows(x, d, e) && whole_rows(residual, d, e) && whole_rows(sum, d, e) &&
                      whole_rows(out, d, eo) && multiple(spec->weight, 16);
   return launch_norm(p, spec->dtype, whole, static_cast<cudaStream_t>(stream));
@@ -173,7 +173,7 @@ maxsim_status maxsim_rms_norm_backward(const maxsim_norm_spec* spec, const maxsi
   p.weight = spec->weight;
   p.weight_fp32 = spec->weight_dtype == MAXSIM_FP32;
   p.parts = dweight ? static_cast<float*>(workspace) : nullptr;
-  p.T = static_cast<int>(T), p.d = d, p.eps = spec->eps, p.drop = drop;
+  p.T = static_cast<int>(T), p.d = d, p.per = 1.f / d, p.eps = spec->eps, p.drop = drop;
   const bool whole = whole_rows(dy, d, e) && whole_rows(h, d, e) && whole_rows(dsum, d, e) && whole_rows(dx, d, e) &&
                      whole_rows(dresidual, d, e) && multiple(spec->weight, 16);
   return launch_norm_bwd(p, spec->dtype, whole, dweight, s);

@@ -10,8 +10,15 @@
 namespace msim {
 namespace {
 
+#ifndef KW
+#define KW 3
+#define KN 2
+#endif
 constexpr int kThreads = 256;
-constexpr int kUnits = 2;  // groups of 8 columns of a thread
+// groups of 8 columns of a thread
+template <bool kWhole>
+constexpr int kUnits = kWhole ? KW : KN;
+
 
 struct DropoutParams {
   const void *x, *res;
@@ -29,31 +36,45 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p
   const int lane = threadIdx.x & 31;
   // a warp's lanes share a run of 256 columns where rows are not whole
   const uint32_t per = kWhole ? kThreads : kThreads / 32, mine = kWhole ? threadIdx.x : threadIdx.x >> 5;
-  alignas(16) T x[kUnits][8], r[kUnits][8];
-  uint32_t row[kUnits], part[kUnits];
-  bool live[kUnits];
+  constexpr int N = kUnits<kWhole>;
+  // whole groups stay packed until their turn
+  std::conditional_t<kWhole, Raw<T>, Eight> x[N], r[N];
+  uint32_t row[N], part[N];
+  bool live[N];
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const uint32_t n = (blockIdx.x * kUnits + u) * per + mine;
+  for (int u = 0; u < N; ++u) {
+    const uint32_t n = (blockIdx.x * N + u) * per + mine;
     live[u] = n < p.count;
     const uint32_t q = p.parts.of(live[u] ? n : 0);
     part[u] = (live[u] ? n : 0) - q * p.parts.d;
     row[u] = p.row0 + q;
     const Cols<kWhole> c(part[u], lane, p.d);
-    load8<T, kWhole>(static_cast<const T*>(p.x) + row[u] * p.x_stride, c, x[u]);
-    if (p.res) load8<T, kWhole>(static_cast<const T*>(p.res) + row[u] * p.res_stride, c, r[u]);
+    const T *from = static_cast<const T*>(p.x) + row[u] * p.x_stride, *res = static_cast<const T*>(p.res) + row[u] * p.res_stride;
+    if constexpr (kWhole) x[u] = load8<T, true>(from, c);
+    else x[u] = load_up8<T, false>(from, c);
+    if (p.res) {
+      if constexpr (kWhole) r[u] = load8<T, true>(res, c);
+      else r[u] = load_up8<T, false>(res, c);
+    }
   }
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
+  for (int u = 0; u < N; ++u) {
     const Cols<kWhole> c(part[u], lane, p.d);
-    const uint32_t keep = p.drop.limit ? kept<kWhole>(key, c, row[u], p.drop.limit) : 0xFFu;
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float add = p.res ? up(r[u][j]) : 0.f;
-      v[j] = keep >> j & 1 ? fmaf(up(x[u][j]), p.drop.factor, add) : add;
+    Eight v, add;
+    if constexpr (kWhole) v = up8<T>(x[u]);
+    else v = x[u];
+    if (p.res) {
+      if constexpr (kWhole) add = up8<T>(r[u]);
+      else add = r[u];
     }
-    if (live[u]) store8<T, kWhole>(static_cast<T*>(p.out) + row[u] * p.out_stride, c, v);
+    if (p.drop.limit) {
+      const Kept<kWhole> keep(key, c, row[u], p.drop.limit);
+      v = keep.of(v, p.drop.factor, add, p.res != nullptr);
+    } else if (p.res) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v.p[i] = add2(v.p[i], add.p[i]);
+    }
+    if (live[u]) store_down8<T, kWhole>(static_cast<T*>(p.out) + row[u] * p.out_stride, c, v);
   }
 }
 
@@ -65,7 +86,8 @@ maxsim_status run(DropoutParams p, int T_, bool whole, cudaStream_t stream) {
     const int rows = T_ - row0 < most ? static_cast<int>(T_ - row0) : most;
     p.row0 = static_cast<int>(row0);
     p.count = static_cast<uint32_t>(rows) * parts;
-    const int grid = static_cast<int>((p.count + per * kUnits - 1) / (per * kUnits));
+    const uint32_t each = per * (whole ? kUnits<true> : kUnits<false>);
+    const int grid = static_cast<int>((p.count + each - 1) / each);
     if (whole) dropout_kernel<T, true><<<grid, kThreads, 0, stream>>>(p);
     else dropout_kernel<T, false><<<grid, kThreads, 0, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return MAXSIM_ERR_CUDA;

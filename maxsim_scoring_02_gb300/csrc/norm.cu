@@ -19,139 +19,210 @@ namespace {
 constexpr float kLeast = 1e-30f;
 
 template <typename T, int kTeam, int kGroups, bool kWhole>
-__global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256) norm_kernel(const NormParams p) {
-  constexpr int kRows = kTeam > 32 ? 1 : 256 / kTeam;
+struct Shape {
+  static constexpr int kBlock = kTeam > 32 ? kTeam : 256, kRows = kBlock / kTeam;
+  using Rows = Queue<T, kBlock, kGroups, 2, 75000, kWhole>;
+  // blocks of an SM that the registers have to allow; rows of a team, where a row takes a warp or more
+  static constexpr int kFit = kTeam > 256 ? 1 : kTeam > 32 ? 1024 / kTeam : 2, kRounds = 8;
+};
+
+template <typename T, int kTeam, int kGroups, bool kWhole, bool k8>
+__global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256, Shape<T, kTeam, kGroups, kWhole>::kFit) norm_kernel(const NormParams p) {
+  using S = Shape<T, kTeam, kGroups, kWhole>;
+  constexpr int kRows = S::kRows, kStages = S::Rows::kStages, kAhead = kStages - 1;
+  constexpr bool kHold = kGroups <= 2;  // weights stay in registers
+  extern __shared__ uint4 smem[];
   const int t = threadIdx.x % kTeam, lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTeam;
-  const bool live = row < p.T;
-  const int r = live ? static_cast<int>(row) : p.T - 1;
   const Key key = load_key(p.drop);
   const auto cols = [&](int g) {
     return Cols<kWhole>(kWhole ? g * kTeam + t : g * (kTeam / 32) + (kTeam > 32 ? t >> 5 : 0), lane, p.d);
   };
-  alignas(16) T x[kGroups][8], add[kGroups][8];
+  Eight held[kHold ? kGroups : 1];
+  if constexpr (kHold)
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) load8<T, kWhole>(static_cast<const T*>(p.x) + r * p.x_stride, cols(g), x[g]);
-  if (p.res)
+    for (int g = 0; g < kGroups; ++g) held[g] = load_weights<T, kWhole>(p, cols(g));
+  const auto weights = [&](int g) -> Eight {
+    if constexpr (kHold) return held[g];
+    else return load_weights<T, kWhole>(p, cols(g));
+  };
+  typename S::Rows rows(smem);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTeam;
+  const auto fetch = [&](int stage, int64_t r) {
+    const bool there = r < p.T;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g)
-      load8<T, kWhole>(static_cast<const T*>(p.res) + r * p.res_stride, cols(g), add[g]);
-  float h[kGroups][8], ss = 0.f, most = 0.f;
+    for (int g = 0; g < kGroups; ++g) rows.fetch(stage, 0, g, static_cast<const T*>(p.x) + r * p.x_stride, cols(g), there);
+    if (p.res)
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    const Cols<kWhole> c = cols(g);
-    const uint32_t keep = p.drop.limit ? kept<kWhole>(key, c, r, p.drop.limit) : 0xFFu;
+      for (int g = 0; g < kGroups; ++g)
+        rows.fetch(stage, 1, g, static_cast<const T*>(p.res) + r * p.res_stride, cols(g), there);
+    if constexpr (kAhead > 0) cp_async_commit();
+  };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = p.res ? up(add[g][j]) : 0.f;
-      const float v = keep >> j & 1 ? fmaf(up(x[g][j]), p.drop.factor, a) : a;
-      h[g][j] = up(static_cast<T>(v));  // the norm is that of the sum as it is kept
-      ss = fmaf(h[g][j], h[g][j], ss);
-    }
-    if (p.sum && live) store8<T, kWhole>(static_cast<T*>(p.sum) + r * p.sum_stride, c, h[g]);
-    if (p.format != MAXSIM_NORM_SAME) {
-      float w[8];
-      load_weights<T, kWhole>(p, c, w);
+  for (int i = 0; i < kAhead; ++i) fetch(i, row + i * step);
+  int at = 0, stage = 0;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.T;
+       first += step, at ^= 1, row += step, stage = stage + 1 < kStages ? stage + 1 : 0) {
+    const bool live = row < p.T;
+    fetch(stage + kAhead < kStages ? stage + kAhead : stage + kAhead - kStages, row + kAhead * step);
+    if constexpr (kAhead > 0) cp_async_wait<kAhead>();
+    Raw<T> in[kGroups];  // becomes the sum
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float u = h[g][j] * w[j];
-        most = max_nan(most, c.in(j) ? fabsf(u) : 0.f);
-      }
-    }
-  }
-  team_all<kTeam>(ss, most, AddAndMax(), 0);
-  const float rstd = [&] {
-    const bool fits = ss < 3e38f;
-    const float usual = 1.f / sqrtf(ss / p.d + p.eps);
-    if (!any_of_team<kTeam>(!fits)) return usual;
-    double wide = 0., none = 0.;  // squares out of fp32's range: once more in fp64
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) wide += static_cast<double>(h[g][j]) * h[g][j];
-    team_all<kTeam>(wide, none, AddBoth(), 1);
-    return fits ? usual : static_cast<float>(1. / sqrt(wide / p.d + p.eps));
-  }();
-  if (p.format == MAXSIM_NORM_SAME) {
+    for (int g = 0; g < kGroups; ++g) in[g] = rows.get(stage, 0, g);
+    Pair squares(0.f, 0.f);
+    float most = 0.f;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const Cols<kWhole> c = cols(g);
-      float w[8];
-      load_weights<T, kWhole>(p, c, w);
+      Eight v = up8<T>(in[g]);
+      if (p.drop.limit || p.res) {
+        Eight a;
+        if (p.res) a = up8<T>(rows.get(stage, 1, g));
+        if (p.drop.limit) {
+          const Kept<kWhole> keep(key, c, static_cast<uint32_t>(row), p.drop.limit);
+          v = keep.of(v, p.drop.factor, a, p.res != nullptr);
+        } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] *= h[g][j] * rstd;
-      if (live) store8<T, kWhole>(static_cast<T*>(p.out) + r * p.out_stride, c, w);
-    }
-    return;
-  }
-  const float top = p.format == MAXSIM_NORM_INT8 ? 127.f : 448.f;
-  float reach = most * rstd;
-  reach = reach < kLeast ? kLeast : reach;  // NaN stays
-  const float factor = top * rstd / reach;
-  if (t == 0 && live) p.scale[r] = reach / top;
-  uint8_t* out = static_cast<uint8_t*>(p.out) + r * p.out_stride;
+          for (int i = 0; i < 4; ++i) v.p[i] = add2(v.p[i], a.p[i]);
+        }
+        in[g] = down8<T>(v);
+        v = up8<T>(in[g]);  // the norm is that of the sum as it is kept
+      }
+      if (p.sum && live) store8<T, kWhole>(static_cast<T*>(p.sum) + row * p.sum_stride, c, in[g]);
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    const Cols<kWhole> c = cols(g);
-    float w[8];
-    load_weights<T, kWhole>(p, c, w);
-    uint32_t code[8];
+      for (int i = 0; i < 4; ++i) squares = fma2(v.p[i], v.p[i], squares);
+      if constexpr (k8) {  // columns past the end are 0
+        const Eight w = weights(g);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float v = h[g][j] * w[j] * factor;
-      if (p.format == MAXSIM_NORM_INT8) {
-        const int q = __float2int_rn(v);
-        code[j] = static_cast<uint32_t>(max(-127, min(127, q))) & 0xFFu;
-      } else {
-        code[j] = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+        for (int i = 0; i < 4; ++i) {
+          float a, b;
+          mul2(v.p[i], w.p[i]).get(a, b);
+          most = max_nan(most, fabsf(a), fabsf(b));
+        }
       }
     }
-    if (!live) continue;
-    if constexpr (kWhole) {
-      if (c.in(0))
-        *reinterpret_cast<uint2*>(out + c.first) =
-            make_uint2(code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
-                       code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24);
-    } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c.in(j)) out[c.at(j)] = static_cast<uint8_t>(code[j]);
+    for (int g = 0; g < kGroups; ++g) forget<T>(in[g]);
+    float ss, odd;
+    squares.get(ss, odd);
+    ss += odd;
+    team_all<kTeam>(ss, most, AddAndMax(), at);
+    const bool fits = ss < 3e38f;
+    float rstd = root_of(fmaf(ss, p.per, p.eps));
+    if (any_of_team<kTeam>(!fits)) {  // squares out of fp32's range: once more in fp64
+      double wide = 0., none = 0.;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const Eight h = up8<T>(in[g]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float a, b;
+          h.p[i].get(a, b);
+          wide += static_cast<double>(a) * a + static_cast<double>(b) * b;
+        }
+      }
+      team_all<kTeam>(wide, none, AddBoth(), at);
+      if (!fits) rstd = static_cast<float>(1. / sqrt(wide / p.d + p.eps));
+    }
+    if constexpr (!k8) {
+      const Pair r2(rstd, rstd);
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        Eight y = weights(g);
+        const Eight h = up8<T>(in[g]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y.p[i] = mul2(y.p[i], mul2(h.p[i], r2));
+        if (live) store8<T, kWhole>(static_cast<T*>(p.out) + row * p.out_stride, cols(g), down8<T>(y));
+      }
+    } else {
+      const bool whole_numbers = p.format == MAXSIM_NORM_INT8;
+      const float top = whole_numbers ? 127.f : 448.f;
+      float reach = most * rstd;
+      reach = reach < kLeast ? kLeast : reach;  // NaN stays
+      const float factor = __fdividef(top * rstd, reach);
+      const Pair f2(factor, factor);
+      if (t == 0 && live) p.scale[row] = reach / top;
+      uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.out_stride;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const Cols<kWhole> c = cols(g);
+        const Eight w = weights(g), h = up8<T>(in[g]);
+        uint32_t two[4];  // codes of two columns each
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float a, b;
+          mul2(mul2(h.p[i], w.p[i]), f2).get(a, b);
+          if (whole_numbers) {  // |a| <= 127 (1 + 2^-21): no code is -128
+            int q, s;
+            asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(q) : "f"(a));
+            asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(s) : "f"(b));
+            two[i] = __byte_perm(q, s, 0x7740);  // the upper half is not used
+          } else {
+            two[i] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+          }
+        }
+        if (!live) continue;
+        if constexpr (kWhole) {
+          if (c.in(0))
+            *reinterpret_cast<uint2*>(out + c.first) =
+                make_uint2(__byte_perm(two[0], two[1], 0x5410), __byte_perm(two[2], two[3], 0x5410));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (c.in(j)) out[c.at(j)] = static_cast<uint8_t>(two[j / 2] >> (8 * (j & 1)));
+        }
+      }
     }
   }
 }
 
 template <typename T, int kTeam, int kGroups, bool kWhole>
-cudaError_t go(const NormParams& p, cudaStream_t stream) {
-  constexpr int kRows = kTeam > 32 ? 1 : 256 / kTeam;
-  const int grid = static_cast<int>((static_cast<int64_t>(p.T) + kRows - 1) / kRows);
-  norm_kernel<T, kTeam, kGroups, kWhole><<<grid, kTeam > 32 ? kTeam : 256, 0, stream>>>(p);
-  return cudaGetLastError();
+cudaError_t go(const NormParams& p, int sms, cudaStream_t stream) {
+  using S = Shape<T, kTeam, kGroups, kWhole>;
+  const auto launch = [&](auto kernel) {
+    cudaError_t e = cudaSuccess;
+    if (S::Rows::kBytes > 40 * 1024)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::Rows::kBytes);
+    int fit = 1;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, S::kBlock, S::Rows::kBytes);
+    if (e != cudaSuccess) return e;
+    const int64_t need = (static_cast<int64_t>(p.T) + S::kRows - 1) / S::kRows;
+    int64_t most = static_cast<int64_t>(sms) * fit;
+    if (kTeam > 16 && need / S::kRounds > most) most = need / S::kRounds;
+    kernel<<<static_cast<int>(need < most ? need : most), S::kBlock, S::Rows::kBytes, stream>>>(p);
+    return cudaGetLastError();
+  };
+  return p.format == MAXSIM_NORM_SAME ? launch(norm_kernel<T, kTeam, kGroups, kWhole, false>)
+                                      : launch(norm_kernel<T, kTeam, kGroups, kWhole, true>);
 }
 
 template <typename T>
-cudaError_t pick(const NormParams& p, bool whole, cudaStream_t stream) {
+cudaError_t pick(const NormParams& p, bool whole, int sms, cudaStream_t stream) {
   if (whole) {
-    if (p.d <= 128) return go<T, 16, 1, true>(p, stream);
-    if (p.d <= 256) return go<T, 32, 1, true>(p, stream);
-    if (p.d <= 512) return go<T, 32, 2, true>(p, stream);
-    if (p.d <= 1024) return go<T, 32, 4, true>(p, stream);
-    if (p.d <= 2048) return go<T, 128, 2, true>(p, stream);
-    if (p.d <= 4096) return go<T, 256, 2, true>(p, stream);
-    if (p.d <= 8192) return go<T, 512, 2, true>(p, stream);
-    return go<T, 512, 4, true>(p, stream);
+    if (p.d <= 64) return go<T, 8, 1, true>(p, sms, stream);
+    if (p.d <= 128) return go<T, 8, 2, true>(p, sms, stream);
+    if (p.d <= 256) return go<T, 16, 2, true>(p, sms, stream);
+    if (p.d <= 512) return go<T, 32, 2, true>(p, sms, stream);
+    if (p.d <= 1024) return go<T, 32, 4, true>(p, sms, stream);
+    if (p.d <= 2048) return go<T, 128, 2, true>(p, sms, stream);
+    if (p.d <= 4096) return go<T, 256, 2, true>(p, sms, stream);
+    if (p.d <= 8192) return go<T, 512, 2, true>(p, sms, stream);
+    return go<T, 512, 4, true>(p, sms, stream);
   }
-  if (p.d <= 256) return go<T, 32, 1, false>(p, stream);
-  if (p.d <= 1024) return go<T, 32, 4, false>(p, stream);
-  if (p.d <= 4096) return go<T, 256, 2, false>(p, stream);
-  return go<T, 512, 4, false>(p, stream);
+  if (p.d <= 256) return go<T, 32, 1, false>(p, sms, stream);
+  if (p.d <= 1024) return go<T, 128, 1, false>(p, sms, stream);
+  if (p.d <= 4096) return go<T, 256, 2, false>(p, sms, stream);
+  return go<T, 512, 4, false>(p, sms, stream);
 }
 
 }  // namespace
 
 maxsim_status launch_norm(const NormParams& p, int dtype, bool whole, cudaStream_t stream) {
-  const cudaError_t e = dtype == MAXSIM_BF16   ? pick<__nv_bfloat16>(p, whole, stream)
-                        : dtype == MAXSIM_FP16 ? pick<__half>(p, whole, stream)
-                                               : pick<float>(p, whole, stream);
+  const DeviceInfo* dev = device_info();
+  if (!dev) return MAXSIM_ERR_CUDA;
+  const cudaError_t e = dtype == MAXSIM_BF16   ? pick<__nv_bfloat16>(p, whole, dev->sm_count, stream)
+                        : dtype == MAXSIM_FP16 ? pick<__half>(p, whole, dev->sm_count, stream)
+                                               : pick<float>(p, whole, dev->sm_count, stream);
   return e == cudaSuccess ? MAXSIM_OK : MAXSIM_ERR_CUDA;
 }
 

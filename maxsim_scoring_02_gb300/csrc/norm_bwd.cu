@@ -15,78 +15,113 @@
 namespace msim {
 namespace {
 
-constexpr int kMaxBlocks = 8 * 160;
+constexpr int kMaxBlocks = 1280;
 
 template <typename T, int kTeam, int kGroups, bool kWhole>
-__global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256) norm_bwd_kernel(const NormParams p) {
-  constexpr int kTeams = kTeam > 32 ? 1 : 256 / kTeam;
+struct Shape {
+  static constexpr int kBlock = kTeam > 32 ? kTeam : 256, kTeams = kBlock / kTeam;
+  using Rows = Queue<T, kBlock, kGroups, 3, 40000, kWhole>;
+  // blocks of an SM that the registers have to allow
+  static constexpr int kFit = kTeam > 256 ? 1 : kTeam > 64 ? 768 / kTeam : 512 / kBlock;
+};
+
+template <typename T, int kTeam, int kGroups, bool kWhole>
+__global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256, Shape<T, kTeam, kGroups, kWhole>::kFit) norm_bwd_kernel(const NormParams p) {
+  using S = Shape<T, kTeam, kGroups, kWhole>;
+  constexpr int kTeams = S::kTeams, kStages = S::Rows::kStages, kAhead = kStages - 1;
+  extern __shared__ uint4 smem[];
   const int t = threadIdx.x % kTeam, lane = threadIdx.x & 31, team = threadIdx.x / kTeam;
   const Key key = load_key(p.drop);
   const auto cols = [&](int g) {
     return Cols<kWhole>(kWhole ? g * kTeam + t : g * (kTeam / 32) + (kTeam > 32 ? t >> 5 : 0), lane, p.d);
   };
-  float acc[kGroups][8] = {};
-  int at = 0;
-  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kTeams; first < p.T;
-       first += static_cast<int64_t>(gridDim.x) * kTeams) {
-    const bool live = first + team < p.T;
-    const int r = live ? static_cast<int>(first + team) : p.T - 1;
-    alignas(16) T dy[kGroups][8], hh[kGroups][8], more[kGroups][8];
+  Eight acc[kGroups];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[g].p[i] = Pair(0.f, 0.f);
+  typename S::Rows rows(smem);  // dy, h, and what reaches the sum from elsewhere
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kTeams + team;
+  const auto fetch = [&](int stage, int64_t r) {
+    const bool there = r < p.T;  // else all of it is 0, and adds 0
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      load8<T, kWhole>(static_cast<const T*>(p.x) + r * p.x_stride, cols(g), dy[g]);
-      load8<T, kWhole>(static_cast<const T*>(p.res) + r * p.res_stride, cols(g), hh[g]);
-      if (p.more) load8<T, kWhole>(static_cast<const T*>(p.more) + r * p.more_stride, cols(g), more[g]);
+      rows.fetch(stage, 0, g, static_cast<const T*>(p.x) + r * p.x_stride, cols(g), there);
+      rows.fetch(stage, 1, g, static_cast<const T*>(p.res) + r * p.res_stride, cols(g), there);
+      if (p.more) rows.fetch(stage, 2, g, static_cast<const T*>(p.more) + r * p.more_stride, cols(g), there);
     }
-    float ss = 0.f, gh = 0.f, w[kGroups][8];
+    if constexpr (kAhead > 0) cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(i, row + i * step);
+  int at = 0, stage = 0;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kTeams; first < p.T;
+       first += step, at ^= 1, row += step, stage = stage + 1 < kStages ? stage + 1 : 0) {
+    const bool live = row < p.T;
+    fetch(stage + kAhead < kStages ? stage + kAhead : stage + kAhead - kStages, row + kAhead * step);
+    if constexpr (kAhead > 0) cp_async_wait<kAhead>();
+    Pair squares(0.f, 0.f), cross(0.f, 0.f);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      load_weights<T, kWhole>(p, cols(g), w[g]);
+      const Eight y = up8<T>(rows.get(stage, 0, g)), v = up8<T>(rows.get(stage, 1, g)), w = load_weights<T, kWhole>(p, cols(g));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float h = up(hh[g][j]);
-        w[g][j] *= up(dy[g][j]);
-        ss = fmaf(h, h, ss);
-        gh = fmaf(w[g][j], h, gh);
+      for (int i = 0; i < 4; ++i) {
+        squares = fma2(v.p[i], v.p[i], squares);
+        cross = fma2(mul2(w.p[i], y.p[i]), v.p[i], cross);
       }
     }
+    float ss, gh, odd;
+    squares.get(ss, odd);
+    ss += odd;
+    cross.get(gh, odd);
+    gh += odd;
     team_all<kTeam>(ss, gh, AddBoth(), at);
+    asm volatile("" ::: "memory");  // what was read is read again, not kept
     const bool fits = ss < 3e38f && fabsf(gh) < 3e38f;
-    float rstd = 1.f / sqrtf(ss / p.d + p.eps), c = gh / p.d * rstd * rstd;
+    float rstd = root_of(fmaf(ss, p.per, p.eps)), c = gh * p.per * rstd * rstd;
     if (any_of_team<kTeam>(!fits)) {  // out of fp32's range: once more in fp64
       double a = 0., b = 0.;
+#pragma unroll 1
+      for (int g = 0; g < kGroups; ++g) {
+        const Eight y = up8<T>(rows.get(stage, 0, g)), v = up8<T>(rows.get(stage, 1, g)), w = load_weights<T, kWhole>(p, cols(g));
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const double h = up(hh[g][j]);
-          a += h * h;
-          b += w[g][j] * h;
+        for (int i = 0; i < 4; ++i) {
+          float v0, v1, g0, g1;
+          v.p[i].get(v0, v1);
+          mul2(w.p[i], y.p[i]).get(g0, g1);
+          a += static_cast<double>(v0) * v0 + static_cast<double>(v1) * v1;
+          b += static_cast<double>(g0) * v0 + static_cast<double>(g1) * v1;
         }
+      }
       team_all<kTeam>(a, b, AddBoth(), at);
       if (!fits) {
         const double wide = 1. / sqrt(a / p.d + p.eps);
         rstd = static_cast<float>(wide), c = static_cast<float>(b / p.d * wide * wide);
       }
     }
-    at ^= 1;
+    const Pair r2(rstd, rstd), c2(-c, -c);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const Cols<kWhole> cc = cols(g);
-      float back[8];
+      const Eight y = up8<T>(rows.get(stage, 0, g)), v = up8<T>(rows.get(stage, 1, g)), w = load_weights<T, kWhole>(p, cc);
+      Eight back;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float h = up(hh[g][j]);
-        back[j] = fmaf(rstd, w[g][j] - h * c, p.more ? up(more[g][j]) : 0.f);
-        if (live) acc[g][j] = fmaf(up(dy[g][j]), h * rstd, acc[g][j]);
+      for (int i = 0; i < 4; ++i) {
+        back.p[i] = mul2(r2, fma2(v.p[i], c2, mul2(w.p[i], y.p[i])));
+        acc[g].p[i] = fma2(y.p[i], mul2(v.p[i], r2), acc[g].p[i]);
       }
-      if (p.sum && live) store8<T, kWhole>(static_cast<T*>(p.sum) + r * p.sum_stride, cc, back);
+      if (p.more) {
+        const Eight m = up8<T>(rows.get(stage, 2, g));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) back.p[i] = add2(back.p[i], m.p[i]);
+      }
+      if (p.sum && live) store8<T, kWhole>(static_cast<T*>(p.sum) + row * p.sum_stride, cc, down8<T>(back));
       if (p.drop.limit) {
-        const uint32_t keep = kept<kWhole>(key, cc, r, p.drop.limit);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) back[j] = keep >> j & 1 ? back[j] * p.drop.factor : 0.f;
+        const Kept<kWhole> keep(key, cc, static_cast<uint32_t>(row), p.drop.limit);
+        back = keep.of(back, p.drop.factor, back, false);
       }
-      if (p.out && live) store8<T, kWhole>(static_cast<T*>(p.out) + r * p.out_stride, cc, back);
+      if (p.out && live) store8<T, kWhole>(static_cast<T*>(p.out) + row * p.out_stride, cc, down8<T>(back));
     }
   }
   if (!p.parts) return;
@@ -95,9 +130,12 @@ __global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256) norm_bwd_kernel(cons
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const Cols<kWhole> c = cols(g);
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[g].p[i].get(v[2 * i], v[2 * i + 1]);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (c.in(j)) part[c.at(j)] = acc[g][j];
+        if (c.in(j)) part[c.at(j)] = v[j];
     }
   } else {
     __shared__ float s[kTeam * kGroups * 8];
@@ -106,9 +144,12 @@ __global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256) norm_bwd_kernel(cons
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
           const Cols<kWhole> c = cols(g);
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[g].p[i].get(v[2 * i], v[2 * i + 1]);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (c.in(j)) s[c.at(j)] = k ? s[c.at(j)] + acc[g][j] : acc[g][j];
+            if (c.in(j)) s[c.at(j)] = k ? s[c.at(j)] + v[j] : v[j];
         }
       __syncthreads();
     }
@@ -135,16 +176,19 @@ __global__ void __launch_bounds__(1024) fold_kernel(const float* parts, int bloc
 
 template <typename T, int kTeam, int kGroups, bool kWhole>
 cudaError_t go(const NormParams& p, int sms, int* blocks, cudaStream_t stream) {
-  constexpr int kTeams = kTeam > 32 ? 1 : 256 / kTeam, kBlock = kTeam > 32 ? kTeam : 256;
-  int fit = 0;
-  cudaError_t e =
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, norm_bwd_kernel<T, kTeam, kGroups, kWhole>, kBlock, 0);
+  using S = Shape<T, kTeam, kGroups, kWhole>;
+  const auto kernel = norm_bwd_kernel<T, kTeam, kGroups, kWhole>;
+  cudaError_t e = cudaSuccess;
+  if (S::Rows::kBytes > 40 * 1024)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::Rows::kBytes);
+  int fit = 1;
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, S::kBlock, S::Rows::kBytes);
   if (e != cudaSuccess) return e;
   int grid = sms * (fit < 8 ? fit : 8);
+  const int64_t need = (static_cast<int64_t>(p.T) + S::kTeams - 1) / S::kTeams;
   if (grid > kMaxBlocks) grid = kMaxBlocks;
-  const int64_t need = (static_cast<int64_t>(p.T) + kTeams - 1) / kTeams;
   if (need < grid) grid = static_cast<int>(need);
-  norm_bwd_kernel<T, kTeam, kGroups, kWhole><<<grid, kBlock, 0, stream>>>(p);
+  kernel<<<grid, S::kBlock, S::Rows::kBytes, stream>>>(p);
   *blocks = grid;
   return cudaGetLastError();
 }
@@ -152,12 +196,14 @@ cudaError_t go(const NormParams& p, int sms, int* blocks, cudaStream_t stream) {
 template <typename T>
 cudaError_t pick(const NormParams& p, bool whole, int sms, int* blocks, cudaStream_t stream) {
   if (whole) {
-    if (p.d <= 128) return go<T, 16, 1, true>(p, sms, blocks, stream);
-    if (p.d <= 256) return go<T, 32, 1, true>(p, sms, blocks, stream);
+    if (p.d <= 64) return go<T, 8, 1, true>(p, sms, blocks, stream);
+    if (p.d <= 128) return go<T, 8, 2, true>(p, sms, blocks, stream);
+    if (p.d <= 256) return go<T, 16, 2, true>(p, sms, blocks, stream);
     if (p.d <= 512) return go<T, 32, 2, true>(p, sms, blocks, stream);
-    if (p.d <= 1024) return go<T, 128, 1, true>(p, sms, blocks, stream);
-    if (p.d <= 2048) return go<T, 256, 1, true>(p, sms, blocks, stream);
-    if (p.d <= 4096) return go<T, 512, 1, true>(p, sms, blocks, stream);
+    if (p.d <= 768) return go<T, 32, 3, true>(p, sms, blocks, stream);
+    if (p.d <= 1024) return go<T, 32, 4, true>(p, sms, blocks, stream);
+    if (p.d <= 2048) return go<T, 128, 2, true>(p, sms, blocks, stream);
+    if (p.d <= 4096) return go<T, 256, 2, true>(p, sms, blocks, stream);
     if (p.d <= 8192) return go<T, 512, 2, true>(p, sms, blocks, stream);
     return go<T, 1024, 2, true>(p, sms, blocks, stream);
   }
