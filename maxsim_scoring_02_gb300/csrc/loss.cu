@@ -20,6 +20,7 @@
 // Bound by the tensor cores (and by the power limit in long runs).
 #include <cmath>
 
+#include "after.cuh"
 #include "attn_common.cuh"
 #include "loss.cuh"
 
@@ -518,6 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fence_mbar_init_cluster();
   }
   if (warp == kMmaWarp) tmem_alloc_pair(sm.tmem_slot, 512);
+  let_next_begin();
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
@@ -548,6 +550,7 @@ __global__ void __launch_bounds__(1024) join_kernel(const float2* parts, int n, 
   __shared__ float2 s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x * 32 + lane;
   float top = -INFINITY, sum = 0.f;
+  wait_for_previous();
   if (row < T)
     for (int i = warp; i < n; i += 256) {
       float2 q[8];
@@ -557,9 +560,10 @@ __global__ void __launch_bounds__(1024) join_kernel(const float2* parts, int n, 
       float m = top;
 #pragma unroll
       for (int u = 0; u < 8; ++u) m = fmaxf(m, q[u].x);
-      sum *= exp2f(top - m);  // the first: exp2(-inf) = 0
+      const float base = m == -INFINITY ? 0.f : m;  // the first, or a part without a number
+      sum *= exp2f(top - base);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) sum += q[u].y * exp2f(q[u].x - m);
+      for (int u = 0; u < 8; ++u) sum += q[u].y * exp2f(q[u].x - base);
       top = m;
     }
   s[warp][lane] = make_float2(top, sum);
@@ -569,7 +573,7 @@ __global__ void __launch_bounds__(1024) join_kernel(const float2* parts, int n, 
   top = mine.x;
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  sum = lane < n ? mine.y * exp2f(mine.x - top) : 0.f;
+  sum = mine.y * exp2f(mine.x - (top == -INFINITY ? 0.f : top));
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
   const int mine_row = blockIdx.x * 32 + warp;
@@ -715,9 +719,10 @@ maxsim_status launch_loss(const LossShape& s, const maxsim_rows& x, const maxsim
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   const int most = dev->sm_count / 2, pairs = tiles < most ? static_cast<int>(tiles) : most;
   if (launch<kStats>(maps, p, pairs, stream) != cudaSuccess) return MAXSIM_ERR_CUDA;
-  join_kernel<<<up_to(s.T, 32), 1024, 0, stream>>>(p.parts, up_to(s.V, kHalf), s.T, s.V, targets, p.hit, s.scale, loss,
-                                                  lse, dev->status);
-  return cudaGetLastError() == cudaSuccess ? MAXSIM_OK : MAXSIM_ERR_CUDA;
+  return launch_after(join_kernel, up_to(s.T, 32), 1024, stream, p.parts, up_to(s.V, kHalf), s.T, s.V, targets, p.hit, s.scale,
+                      loss, lse, dev->status) == cudaSuccess
+             ? MAXSIM_OK
+             : MAXSIM_ERR_CUDA;
 }
 
 size_t loss_bwd_workspace_bytes(const LossShape& s) {

@@ -10,6 +10,7 @@
 // registers; a block's teams are added in order, each block writes one row of
 // partial sums, and a second kernel adds those in order: no atomics, and results
 // depend on the number of SMs alone. Bound by HBM.
+#include "after.cuh"
 #include "norm.cuh"
 
 namespace msim {
@@ -28,6 +29,7 @@ struct Shape {
 template <typename T, int kTeam, int kGroups, bool kWhole>
 __global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256, Shape<T, kTeam, kGroups, kWhole>::kFit) norm_bwd_kernel(const NormParams p) {
   using S = Shape<T, kTeam, kGroups, kWhole>;
+  let_next_begin();
   constexpr int kTeams = S::kTeams, kStages = S::Rows::kStages, kAhead = kStages - 1;
   extern __shared__ uint4 smem[];
   const int t = threadIdx.x % kTeam, lane = threadIdx.x & 31, team = threadIdx.x / kTeam;
@@ -162,6 +164,7 @@ template <typename W>
 __global__ void __launch_bounds__(1024) fold_kernel(const float* parts, int blocks, int d, W* dw) {
   __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+  wait_for_previous();
   float a = 0.f;
   if (col < d)
 #pragma unroll 8
@@ -215,8 +218,7 @@ cudaError_t pick(const NormParams& p, bool whole, int sms, int* blocks, cudaStre
 
 template <typename W>
 cudaError_t fold(const float* parts, int blocks, int d, void* dw, cudaStream_t stream) {
-  fold_kernel<W><<<(d + 31) / 32, 1024, 0, stream>>>(parts, blocks, d, static_cast<W*>(dw));
-  return cudaGetLastError();
+  return launch_after(fold_kernel<W>, (d + 31) / 32, 1024, stream, parts, blocks, d, static_cast<W*>(dw));
 }
 
 }  // namespace
