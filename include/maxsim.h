@@ -79,7 +79,8 @@ typedef enum maxsim_dtype {
  *   flags          MAXSIM_DEBUG_STALL_FWD_LOADER: the loader role of the
  *                  tensor-core forward kernel (maxsim_score / _varlen with
  *                  bf16 or fp16 and queries below 256 tokens) and of the
- *                  attention kernels (maxsim_attention / _backward) issues no copy,
+ *                  attention kernels (maxsim_attention / _backward) and the
+ *                  cross entropy's (maxsim_cross_entropy / _backward) issues no copy,
  *                  so the kernel's other roles wait on barriers nothing will
  *                  complete; their bounded waits run out, record
  *                  MAXSIM_DEVERR_TIMEOUT and the kernel exits with no copy or
@@ -674,10 +675,11 @@ maxsim_status maxsim_rms_norm_backward(const maxsim_norm_spec *spec, const maxsi
  * A target >= V counts as none and sets MAXSIM_DEVERR_BAD_INPUT.
  *   x            [T, d] view, weight [V, d] view (dtype BF16 or FP16)
  *   loss, lse    [T] fp32
- * Products are fp32 sums on the tensor cores, statistics fp32. A logit that is not
- * finite makes its row's lse and loss NaN (minus infinity: a weight of 0).
+ * Products are fp32 sums on the tensor cores, in parts of 512 along d that are added
+ * with rounding; statistics are fp32. x and weight must be finite: a row of x that is
+ * not makes its own lse and loss NaN, no other row's.
  * workspace: at least maxsim_cross_entropy_workspace_size(spec) bytes, 16-byte
- * aligned.
+ * aligned; calls that may run at the same time need one each, here and below.
  * Limits: FP32 returns MAXSIM_ERR_UNSUPPORTED; d a multiple of 8, d <= 65536;
  * V >= 1; T, V < 2^31 - 256; scale from 2^-60 to 2^60; views 16-byte aligned with
  * strides that are multiples of 8 and at least d.

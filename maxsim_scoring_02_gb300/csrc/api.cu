@@ -21,7 +21,6 @@ __device__ __align__(16) unsigned g_status_block[4];
 
 namespace {
 
-constexpr int kMaxDevices = 64;
 std::mutex g_dev_mutex;
 DeviceInfo g_dev[kMaxDevices];
 bool g_dev_ready[kMaxDevices];
@@ -46,6 +45,7 @@ const DeviceInfo* device_info() {
   std::lock_guard<std::mutex> lock(g_dev_mutex);
   if (!g_dev_ready[dev]) {
     DeviceInfo info;
+    info.id = dev;
     if (cudaDeviceGetAttribute(&info.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return nullptr;
     if (cudaDeviceGetAttribute(&info.max_smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
       return nullptr;

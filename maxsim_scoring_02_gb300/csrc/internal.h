@@ -2,6 +2,7 @@
 // the C-ABI layer. Not installed; the public interface is include/maxsim.h.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -12,13 +13,32 @@ namespace msim {
 
 // Per-device facts the launchers need (cached by the C-ABI layer).
 struct DeviceInfo {
+  int id;
   int sm_count;
   int max_smem_optin;
   unsigned* status;  // device address of the per-device status word
 };
 
 // Returns nullptr if the device could not be queried.
+constexpr int kMaxDevices = 64;
 const DeviceInfo* device_info();
+
+// What a launcher found out about a kernel on each device, so that it asks once: how
+// many blocks of it fit an SM, after its dynamic shared memory has been allowed.
+struct Fits {
+  std::atomic<int> n[kMaxDevices];
+};
+template <typename K>
+cudaError_t blocks_that_fit(Fits& known, const DeviceInfo& dev, K kernel, int block, int smem_bytes, int* fit) {
+  *fit = known.n[dev.id].load(std::memory_order_relaxed);
+  if (*fit) return cudaSuccess;
+  cudaError_t e = cudaSuccess;
+  if (smem_bytes > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(fit, kernel, block, smem_bytes);
+  if (e == cudaSuccess && *fit < 1) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess) known.n[dev.id].store(*fit, std::memory_order_relaxed);
+  return e;
+}
 
 // Forward scoring on tcgen05 tensor cores (bf16 / fp16 inputs).
 // Documents are given either padded (csr = 0: rows b*nd .. b*nd+L_b-1, L_b

@@ -39,7 +39,7 @@ constexpr int kAcc = 2;
 constexpr int kStageOut = 32 * 128;            // a warp's way out: 32 rows of 128 bytes
 constexpr int kBars = 2 * kStages + 2 * kAcc + 1;
 constexpr int kSmallBytes = kBars * 8 + 16;
-constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kEpiWarps * kStageOut + kSmallBytes;
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiWarps * kStageOut + kSmallBytes;
 // The tensor core cuts each sum towards zero, so a logit of d = 2048 is off by some
 // 1e-6 of itself in one direction. kStats adds no more than this many steps there and
 // the parts in registers, with rounding: a quarter of that, and no more time.
@@ -666,14 +666,17 @@ bool map_out(CUtensorMap* m, int type, int esize, void* data, int64_t stride, in
 }
 
 template <int kMode>
-cudaError_t launch(const Maps& maps, const Params& p, int pairs, cudaStream_t stream) {
-  const auto go = [&](auto kernel) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+cudaError_t launch(const Maps& maps, const Params& p, const DeviceInfo& dev, int64_t tiles, cudaStream_t stream) {
+  static Fits known[2];
+  const auto go = [&](auto kernel, Fits& seen) {
+    int fit = 1;
+    const cudaError_t e = blocks_that_fit(seen, dev, kernel, kThreads, kSmemBytes, &fit);
     if (e != cudaSuccess) return e;
-    kernel<<<2 * pairs, kThreads, kSmemBytes, stream>>>(maps, p);
+    const int64_t most = dev.sm_count / 2, pairs = tiles < most ? tiles : most;
+    kernel<<<static_cast<int>(2 * pairs), kThreads, kSmemBytes, stream>>>(maps, p);
     return cudaGetLastError();
   };
-  return p.s.is_bf16 ? go(loss_kernel<kMode, true>) : go(loss_kernel<kMode, false>);
+  return p.s.is_bf16 ? go(loss_kernel<kMode, true>, known[0]) : go(loss_kernel<kMode, false>, known[1]);
 }
 
 struct Space {  // of the backward's workspace
@@ -716,9 +719,8 @@ maxsim_status launch_loss(const LossShape& s, const maxsim_rows& x, const maxsim
   p.parts = reinterpret_cast<float2*>(static_cast<char*>(workspace) + padded(static_cast<size_t>(s.T) * 4));
   p.z2 = s.scale * kLog2e;
   p.status = dev->status;
-  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-  const int most = dev->sm_count / 2, pairs = tiles < most ? static_cast<int>(tiles) : most;
-  if (launch<kStats>(maps, p, pairs, stream) != cudaSuccess) return MAXSIM_ERR_CUDA;
+  if (launch<kStats>(maps, p, *dev, static_cast<int64_t>(p.tiles_m) * p.tiles_n, stream) != cudaSuccess)
+    return MAXSIM_ERR_CUDA;
   return launch_after(join_kernel, up_to(s.T, 32), 1024, stream, p.parts, up_to(s.V, kHalf), s.T, s.V, targets, p.hit, s.scale,
                       loss, lse, dev->status) == cudaSuccess
              ? MAXSIM_OK
@@ -735,8 +737,7 @@ maxsim_status launch_loss_bwd(const LossShape& s, const float* dloss, const maxs
                               void* workspace, cudaStream_t stream) {
   const DeviceInfo* dev = device_info();
   if (!dev) return MAXSIM_ERR_CUDA;
-  const int most = dev->sm_count / 2;
-  const Space at = plan(s, most);
+  const Space at = plan(s, dev->sm_count / 2);
   char* base = static_cast<char*>(workspace);
   float *gain = reinterpret_cast<float*>(base), *coef = reinterpret_cast<float*>(base + at.coef);
   float* sums = reinterpret_cast<float*>(base + at.sums);
@@ -761,8 +762,7 @@ maxsim_status launch_loss_bwd(const LossShape& s, const float* dloss, const maxs
     p.gain = gain;
     p.z2 = s.scale * kLog2e;
     p.status = dev->status;
-    int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-    if (launch<kGrad>(maps, p, tiles < most ? static_cast<int>(tiles) : most, stream) != cudaSuccess)
+    if (launch<kGrad>(maps, p, *dev, static_cast<int64_t>(p.tiles_m) * p.tiles_n, stream) != cudaSuccess)
       return MAXSIM_ERR_CUDA;
     if (!map_in(&maps.a, s, base + at.dz, at.columns, columns, s.T, kHalf) ||
         !map_in(&maps.b, s, w.data, w.row_stride, s.d, s.V, kBox) ||
@@ -786,9 +786,8 @@ maxsim_status launch_loss_bwd(const LossShape& s, const float* dloss, const maxs
       p.rounds = (dx_cost + dw_cost / 2) / dw_cost;
       if (!map_out(&maps.out1, s.is_bf16 ? 1 : 0, 2, dw->data, dw->row_stride, s.d, s.V, 1)) return MAXSIM_ERR_CUDA;
     }
-    tiles = static_cast<int64_t>(p.dx_m) * p.dx_n * p.splits + static_cast<int64_t>(p.dw_m) * p.dw_n;
-    if (tiles && launch<kSums>(maps, p, tiles < most ? static_cast<int>(tiles) : most, stream) != cudaSuccess)
-      return MAXSIM_ERR_CUDA;
+    const int64_t tiles = static_cast<int64_t>(p.dx_m) * p.dx_n * p.splits + static_cast<int64_t>(p.dw_m) * p.dw_n;
+    if (tiles && launch<kSums>(maps, p, *dev, tiles, stream) != cudaSuccess) return MAXSIM_ERR_CUDA;
   }
   if (dx && at.wide) {
     const int64_t n = static_cast<int64_t>(s.T) * s.d;

@@ -177,42 +177,40 @@ __global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256, Shape<T, kTeam, kGro
 }
 
 template <typename T, int kTeam, int kGroups, bool kWhole>
-cudaError_t go(const NormParams& p, int sms, cudaStream_t stream) {
+cudaError_t go(const NormParams& p, const DeviceInfo& dev, cudaStream_t stream) {
   using S = Shape<T, kTeam, kGroups, kWhole>;
-  const auto launch = [&](auto kernel) {
-    cudaError_t e = cudaSuccess;
-    if (S::Rows::kBytes > 40 * 1024)
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::Rows::kBytes);
+  const auto launch = [&](auto kernel, Fits& known) {
     int fit = 1;
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, S::kBlock, S::Rows::kBytes);
+    const cudaError_t e = blocks_that_fit(known, dev, kernel, S::kBlock, S::Rows::kBytes, &fit);
     if (e != cudaSuccess) return e;
     const int64_t need = (static_cast<int64_t>(p.T) + S::kRows - 1) / S::kRows;
-    int64_t most = static_cast<int64_t>(sms) * fit;
+    int64_t most = static_cast<int64_t>(dev.sm_count) * fit;
     if (kTeam > 16 && need / S::kRounds > most) most = need / S::kRounds;
     kernel<<<static_cast<int>(need < most ? need : most), S::kBlock, S::Rows::kBytes, stream>>>(p);
     return cudaGetLastError();
   };
-  return p.format == MAXSIM_NORM_SAME ? launch(norm_kernel<T, kTeam, kGroups, kWhole, false>)
-                                      : launch(norm_kernel<T, kTeam, kGroups, kWhole, true>);
+  static Fits known[2];
+  return p.format == MAXSIM_NORM_SAME ? launch(norm_kernel<T, kTeam, kGroups, kWhole, false>, known[0])
+                                      : launch(norm_kernel<T, kTeam, kGroups, kWhole, true>, known[1]);
 }
 
 template <typename T>
-cudaError_t pick(const NormParams& p, bool whole, int sms, cudaStream_t stream) {
+cudaError_t pick(const NormParams& p, bool whole, const DeviceInfo& dev, cudaStream_t stream) {
   if (whole) {
-    if (p.d <= 64) return go<T, 8, 1, true>(p, sms, stream);
-    if (p.d <= 128) return go<T, 8, 2, true>(p, sms, stream);
-    if (p.d <= 256) return go<T, 16, 2, true>(p, sms, stream);
-    if (p.d <= 512) return go<T, 32, 2, true>(p, sms, stream);
-    if (p.d <= 1024) return go<T, 32, 4, true>(p, sms, stream);
-    if (p.d <= 2048) return go<T, 128, 2, true>(p, sms, stream);
-    if (p.d <= 4096) return go<T, 256, 2, true>(p, sms, stream);
-    if (p.d <= 8192) return go<T, 512, 2, true>(p, sms, stream);
-    return go<T, 512, 4, true>(p, sms, stream);
+    if (p.d <= 64) return go<T, 8, 1, true>(p, dev, stream);
+    if (p.d <= 128) return go<T, 8, 2, true>(p, dev, stream);
+    if (p.d <= 256) return go<T, 16, 2, true>(p, dev, stream);
+    if (p.d <= 512) return go<T, 32, 2, true>(p, dev, stream);
+    if (p.d <= 1024) return go<T, 32, 4, true>(p, dev, stream);
+    if (p.d <= 2048) return go<T, 128, 2, true>(p, dev, stream);
+    if (p.d <= 4096) return go<T, 256, 2, true>(p, dev, stream);
+    if (p.d <= 8192) return go<T, 512, 2, true>(p, dev, stream);
+    return go<T, 512, 4, true>(p, dev, stream);
   }
-  if (p.d <= 256) return go<T, 32, 1, false>(p, sms, stream);
-  if (p.d <= 1024) return go<T, 128, 1, false>(p, sms, stream);
-  if (p.d <= 4096) return go<T, 256, 2, false>(p, sms, stream);
-  return go<T, 512, 4, false>(p, sms, stream);
+  if (p.d <= 256) return go<T, 32, 1, false>(p, dev, stream);
+  if (p.d <= 1024) return go<T, 128, 1, false>(p, dev, stream);
+  if (p.d <= 4096) return go<T, 256, 2, false>(p, dev, stream);
+  return go<T, 512, 4, false>(p, dev, stream);
 }
 
 }  // namespace
@@ -220,9 +218,9 @@ cudaError_t pick(const NormParams& p, bool whole, int sms, cudaStream_t stream) 
 maxsim_status launch_norm(const NormParams& p, int dtype, bool whole, cudaStream_t stream) {
   const DeviceInfo* dev = device_info();
   if (!dev) return MAXSIM_ERR_CUDA;
-  const cudaError_t e = dtype == MAXSIM_BF16   ? pick<__nv_bfloat16>(p, whole, dev->sm_count, stream)
-                        : dtype == MAXSIM_FP16 ? pick<__half>(p, whole, dev->sm_count, stream)
-                                               : pick<float>(p, whole, dev->sm_count, stream);
+  const cudaError_t e = dtype == MAXSIM_BF16   ? pick<__nv_bfloat16>(p, whole, *dev, stream)
+                        : dtype == MAXSIM_FP16 ? pick<__half>(p, whole, *dev, stream)
+                                               : pick<float>(p, whole, *dev, stream);
   return e == cudaSuccess ? MAXSIM_OK : MAXSIM_ERR_CUDA;
 }
 

@@ -178,16 +178,14 @@ __global__ void __launch_bounds__(1024) fold_kernel(const float* parts, int bloc
 }
 
 template <typename T, int kTeam, int kGroups, bool kWhole>
-cudaError_t go(const NormParams& p, int sms, int* blocks, cudaStream_t stream) {
+cudaError_t go(const NormParams& p, const DeviceInfo& dev, int* blocks, cudaStream_t stream) {
   using S = Shape<T, kTeam, kGroups, kWhole>;
   const auto kernel = norm_bwd_kernel<T, kTeam, kGroups, kWhole>;
-  cudaError_t e = cudaSuccess;
-  if (S::Rows::kBytes > 40 * 1024)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::Rows::kBytes);
+  static Fits known;
   int fit = 1;
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, S::kBlock, S::Rows::kBytes);
+  const cudaError_t e = blocks_that_fit(known, dev, kernel, S::kBlock, S::Rows::kBytes, &fit);
   if (e != cudaSuccess) return e;
-  int grid = sms * (fit < 8 ? fit : 8);
+  int grid = dev.sm_count * (fit < 8 ? fit : 8);
   const int64_t need = (static_cast<int64_t>(p.T) + S::kTeams - 1) / S::kTeams;
   if (grid > kMaxBlocks) grid = kMaxBlocks;
   if (need < grid) grid = static_cast<int>(need);
@@ -197,23 +195,23 @@ cudaError_t go(const NormParams& p, int sms, int* blocks, cudaStream_t stream) {
 }
 
 template <typename T>
-cudaError_t pick(const NormParams& p, bool whole, int sms, int* blocks, cudaStream_t stream) {
+cudaError_t pick(const NormParams& p, bool whole, const DeviceInfo& dev, int* blocks, cudaStream_t stream) {
   if (whole) {
-    if (p.d <= 64) return go<T, 8, 1, true>(p, sms, blocks, stream);
-    if (p.d <= 128) return go<T, 8, 2, true>(p, sms, blocks, stream);
-    if (p.d <= 256) return go<T, 16, 2, true>(p, sms, blocks, stream);
-    if (p.d <= 512) return go<T, 32, 2, true>(p, sms, blocks, stream);
-    if (p.d <= 768) return go<T, 32, 3, true>(p, sms, blocks, stream);
-    if (p.d <= 1024) return go<T, 32, 4, true>(p, sms, blocks, stream);
-    if (p.d <= 2048) return go<T, 128, 2, true>(p, sms, blocks, stream);
-    if (p.d <= 4096) return go<T, 256, 2, true>(p, sms, blocks, stream);
-    if (p.d <= 8192) return go<T, 512, 2, true>(p, sms, blocks, stream);
-    return go<T, 1024, 2, true>(p, sms, blocks, stream);
+    if (p.d <= 64) return go<T, 8, 1, true>(p, dev, blocks, stream);
+    if (p.d <= 128) return go<T, 8, 2, true>(p, dev, blocks, stream);
+    if (p.d <= 256) return go<T, 16, 2, true>(p, dev, blocks, stream);
+    if (p.d <= 512) return go<T, 32, 2, true>(p, dev, blocks, stream);
+    if (p.d <= 768) return go<T, 32, 3, true>(p, dev, blocks, stream);
+    if (p.d <= 1024) return go<T, 32, 4, true>(p, dev, blocks, stream);
+    if (p.d <= 2048) return go<T, 128, 2, true>(p, dev, blocks, stream);
+    if (p.d <= 4096) return go<T, 256, 2, true>(p, dev, blocks, stream);
+    if (p.d <= 8192) return go<T, 512, 2, true>(p, dev, blocks, stream);
+    return go<T, 1024, 2, true>(p, dev, blocks, stream);
   }
-  if (p.d <= 256) return go<T, 32, 1, false>(p, sms, blocks, stream);
-  if (p.d <= 1024) return go<T, 128, 1, false>(p, sms, blocks, stream);
-  if (p.d <= 4096) return go<T, 512, 1, false>(p, sms, blocks, stream);
-  return go<T, 1024, 2, false>(p, sms, blocks, stream);
+  if (p.d <= 256) return go<T, 32, 1, false>(p, dev, blocks, stream);
+  if (p.d <= 1024) return go<T, 128, 1, false>(p, dev, blocks, stream);
+  if (p.d <= 4096) return go<T, 512, 1, false>(p, dev, blocks, stream);
+  return go<T, 1024, 2, false>(p, dev, blocks, stream);
 }
 
 template <typename W>
@@ -232,9 +230,9 @@ maxsim_status launch_norm_bwd(const NormParams& p, int dtype, bool whole, void* 
   const DeviceInfo* dev = device_info();
   if (!dev) return MAXSIM_ERR_CUDA;
   int blocks = 0;
-  cudaError_t e = dtype == MAXSIM_BF16   ? pick<__nv_bfloat16>(p, whole, dev->sm_count, &blocks, stream)
-                  : dtype == MAXSIM_FP16 ? pick<__half>(p, whole, dev->sm_count, &blocks, stream)
-                                         : pick<float>(p, whole, dev->sm_count, &blocks, stream);
+  cudaError_t e = dtype == MAXSIM_BF16   ? pick<__nv_bfloat16>(p, whole, *dev, &blocks, stream)
+                  : dtype == MAXSIM_FP16 ? pick<__half>(p, whole, *dev, &blocks, stream)
+                                         : pick<float>(p, whole, *dev, &blocks, stream);
   if (e == cudaSuccess && dweight)
     e = p.weight_fp32          ? fold<float>(p.parts, blocks, p.d, dweight, stream)
         : dtype == MAXSIM_BF16 ? fold<__nv_bfloat16>(p.parts, blocks, p.d, dweight, stream)
