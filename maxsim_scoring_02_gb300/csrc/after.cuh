@@ -1,5 +1,5 @@
-// after.cuh -- launches a small kernel that follows another one on its stream: it
-// is brought up while that one still runs (programmatic dependent launch) and
+// after.cuh -- launches a kernel that follows another one of the same call: it is
+// brought up while that one still runs (programmatic dependent launch) and
 // begins with wait_for_previous(), which returns once that one has ended and its
 // writes are there.
 #pragma once
@@ -13,17 +13,18 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 __device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), int grid, int block, cudaStream_t stream, A... args) {
+cudaError_t launch_after(void (*kernel)(P...), int grid, int block, int smem_bytes, cudaStream_t stream, const A&... args) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(grid);
   c.blockDim = dim3(block);
+  c.dynamicSmemBytes = smem_bytes;
   c.stream = stream;
   c.attrs = &attr;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+  return cudaLaunchKernelEx(&c, kernel, static_cast<const P&>(args)...);
 }
 
 }  // namespace msim

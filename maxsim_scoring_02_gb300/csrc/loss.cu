@@ -64,7 +64,10 @@ struct Params {
   int dw_m, dw_n, rounds;   // dW tiles; how many of them are worth one of dx
   int dx_wide, dx_adds;     // dx goes to fp32 sums; they are added to
   const int64_t* targets;
-  const float *lse, *coef, *gain;
+  const float *lse, *dloss;
+  float* top;               // the largest |dloss|
+  int scan;                 // kGrad finds it (else it is there)
+  int more;                 // dz is held times 2^(more - e), e the exponent of the largest |dloss|
   float2* parts;
   float* hit;               // [T] the target's product
   float z2;                 // scale * log2(e)
@@ -338,6 +341,26 @@ __device__ __forceinline__ void send(const CUtensorMap* map, uint32_t stage, int
   }
 }
 
+// What dz is held times: 2^(more - e), so that the largest |dloss| becomes 1 to 2 (2^14
+// to 2^15 in fp16); the sums are multiplied by scale 2^(e - more) at the end.
+__device__ __forceinline__ int exponent_of(float top) { return top > 0.f && top < INFINITY ? ilogbf(top) : 0; }
+__device__ __forceinline__ float gain_of(const float* top, float scale, int more) {
+  return ldexpf(scale, exponent_of(*top) - more);
+}
+// The largest |dloss| of rows with a target, found by n threads; bad targets are reported.
+__device__ __forceinline__ float largest(const float* dloss, const int64_t* targets, int T, int64_t V, int thread, int n,
+                                         unsigned* status) {
+  float top = 0.f;
+  for (int i = thread; i < T; i += n) {
+    const int64_t t = targets[i];
+    if (t >= V) atomicOr(status, kDevErrBadInput);
+    if (t >= 0 && t < V) top = fmaxf(top, fabsf(dloss[i]));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  return top;
+}
+
 // Thread = row (TMEM lane); warps w and w + 4 share a lane quarter and take half of the columns each.
 template <int kMode, bool kBf16>
 __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32_t tmem_base, uint32_t rank) {
@@ -347,6 +370,24 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
   int a = 0;
   uint32_t aph = 0;
   Tile t;
+  int shift = 0;  // of dloss
+  float gain = 1.f;
+  if constexpr (kMode == kGrad) {
+    float top;
+    if (p.scan) {  // each block finds it for itself, while its first tile is made
+      top = largest(p.dloss, p.targets, p.s.T, p.s.V, threadIdx.x, 32 * kEpiWarps, p.status);
+      float* s = reinterpret_cast<float*>(sm.out);
+      if (lane == 0) s[warp * (kStageOut / 4)] = top;
+      named_bar_sync(1, 32 * kEpiWarps);
+      for (int w = 0; w < kEpiWarps; ++w) top = fmaxf(top, s[w * (kStageOut / 4)]);
+      named_bar_sync(1, 32 * kEpiWarps);
+      if (blockIdx.x == 0 && threadIdx.x == 0) *p.top = top;
+    } else {
+      top = *p.top;
+    }
+    shift = p.more - exponent_of(top);
+  }
+  if constexpr (kMode == kSums) gain = gain_of(p.top, p.s.scale, p.more);
   for (int i = 0; tile_of<kMode>(p, i, t); ++i) {
     if (t.steps == 0) continue;
     const int row0 = t.m0 + static_cast<int>(rank) * kHalf + quarter * 32, row = row0 + lane;
@@ -354,18 +395,16 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
     const int chunks = min(4, max(0, (t.n - col0 + 31) / 32));
     // what the row needs, asked for before the wait
     int target = -1;
-    float lse2 = 0.f, coef = 0.f, gain = 1.f;
+    float lse2 = 0.f, coef = 0.f;
     if constexpr (kMode != kSums) {
       if (row < p.s.T) {
-        const int64_t g = p.targets[row] - p.first - t.n0 - col0;
+        const int64_t to = p.targets[row], g = to - p.first - t.n0 - col0;
         target = g >= 0 && g < kHalf ? static_cast<int>(g) : -1;
         if constexpr (kMode == kGrad) {
           lse2 = p.lse[row] * kLog2e;
-          coef = p.coef[row];
+          coef = to >= 0 && to < p.s.V ? ldexpf(p.dloss[row], shift) : 0.f;
         }
       }
-    } else {
-      gain = t.kind == 1 && p.dx_wide ? 1.f : *p.gain;
     }
     uint32_t v[4][32];
     bool ok = true;
@@ -519,10 +558,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fence_mbar_init_cluster();
   }
   if (warp == kMmaWarp) tmem_alloc_pair(sm.tmem_slot, 512);
+  if (warp == kProducerWarp && (threadIdx.x & 31) == 0) {
+    tma_prefetch_desc(&maps.a);
+    tma_prefetch_desc(&maps.b);
+  }
   let_next_begin();
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
+  wait_for_previous();
   const uint32_t tmem_base = *sm.tmem_slot;
   if (warp >= kEpiWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
@@ -585,36 +629,28 @@ __global__ void __launch_bounds__(1024) join_kernel(const float2* parts, int n, 
   loss[mine_row] = t >= 0 && t < V ? l - hit[mine_row] * scale : 0.f;
 }
 
-// coef[t] = dloss[t] 2^-e (0 where the row has no target), gain = scale 2^e, with e
-// the exponent of the largest |dloss|. fp16: 2^14 more in coef, and less in gain.
-__global__ void __launch_bounds__(1024) coef_kernel(const float* dloss, const int64_t* targets, int T, int64_t V,
-                                                    float scale, int more, float* coef, float* gain, unsigned* status) {
+// The largest |dloss| of many rows: more than each block of kGrad should read.
+constexpr int kScanRows = 32768;
+__global__ void __launch_bounds__(1024) top_kernel(const float* dloss, const int64_t* targets, int T, int64_t V, float* out,
+                                                   unsigned* status) {
   __shared__ float s[32];
-  float top = 0.f;
-  for (int i = threadIdx.x; i < T; i += 1024) {
-    const int64_t t = targets[i];
-    if (t >= V) atomicOr(status, kDevErrBadInput);
-    if (t >= 0 && t < V) top = fmaxf(top, fabsf(dloss[i]));
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  let_next_begin();
+  float top = largest(dloss, targets, T, V, threadIdx.x, 1024, status);
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = top;
   __syncthreads();
-  for (int w = 0; w < 32; ++w) top = fmaxf(top, s[w]);
-  const int e = top > 0.f && top < INFINITY ? ilogbf(top) : 0;
-  for (int i = threadIdx.x; i < T; i += 1024) {
-    const int64_t t = targets[i];
-    coef[i] = t >= 0 && t < V ? ldexpf(dloss[i], more - e) : 0.f;
-  }
-  if (threadIdx.x == 0) *gain = ldexpf(scale, e - more);
+  if (threadIdx.x) return;
+  for (int w = 1; w < 32; ++w) top = fmaxf(top, s[w]);
+  *out = top;
 }
 
 // dx: the parts' fp32 sums, times the gain.
 template <typename T>
-__global__ void __launch_bounds__(256) dx_kernel(const float* sums, int splits, int64_t n, int d, const float* gain,
-                                                 T* dx, int64_t stride) {
+__global__ void __launch_bounds__(256) dx_kernel(const float* sums, int splits, int64_t n, int d, const float* top,
+                                                 float scale, int more, T* dx, int64_t stride) {
   const int64_t i = (blockIdx.x * int64_t(256) + threadIdx.x) * 8;
+  wait_for_previous();
   if (i >= n) return;
+  const float gain = gain_of(top, scale, more);
   float a[8] = {};
   for (int s = 0; s < splits; ++s) {
     const float4* q = reinterpret_cast<const float4*>(sums + s * n + i);
@@ -624,7 +660,7 @@ __global__ void __launch_bounds__(256) dx_kernel(const float* sums, int splits, 
   const int64_t row = i / d;
   alignas(16) T o[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = static_cast<T>(a[j] * *gain);
+  for (int j = 0; j < 8; ++j) o[j] = static_cast<T>(a[j] * gain);
   *reinterpret_cast<uint4*>(dx + row * stride + (i - row * d)) = *reinterpret_cast<uint4*>(o);
 }
 
@@ -666,21 +702,23 @@ bool map_out(CUtensorMap* m, int type, int esize, void* data, int64_t stride, in
 }
 
 template <int kMode>
-cudaError_t launch(const Maps& maps, const Params& p, const DeviceInfo& dev, int64_t tiles, cudaStream_t stream) {
+cudaError_t launch(const Maps& maps, const Params& p, const DeviceInfo& dev, int64_t tiles, bool follows, cudaStream_t stream) {
   static Fits known[2];
   const auto go = [&](auto kernel, Fits& seen) {
     int fit = 1;
     const cudaError_t e = blocks_that_fit(seen, dev, kernel, kThreads, kSmemBytes, &fit);
     if (e != cudaSuccess) return e;
     const int64_t most = dev.sm_count / 2, pairs = tiles < most ? tiles : most;
-    kernel<<<static_cast<int>(2 * pairs), kThreads, kSmemBytes, stream>>>(maps, p);
+    const int grid = static_cast<int>(2 * pairs);
+    if (follows) return launch_after(kernel, grid, kThreads, kSmemBytes, stream, maps, p);
+    kernel<<<grid, kThreads, kSmemBytes, stream>>>(maps, p);
     return cudaGetLastError();
   };
   return p.s.is_bf16 ? go(loss_kernel<kMode, true>, known[0]) : go(loss_kernel<kMode, false>, known[1]);
 }
 
 struct Space {  // of the backward's workspace
-  size_t coef, dz, sums, bytes;
+  size_t dz, sums, bytes;
   int columns, splits;
   bool wide;
 };
@@ -689,8 +727,7 @@ Space plan(const LossShape& s, int pairs) {
   w.columns = piece_columns(s);
   w.splits = split_count(s, w.columns < s.V ? w.columns : static_cast<int>(s.V), pairs);
   w.wide = w.splits > 1 || w.columns < s.V;
-  w.coef = 256;
-  w.dz = w.coef + padded(static_cast<size_t>(s.T) * 4);
+  w.dz = 256;  // after the largest |dloss|
   w.sums = w.dz + padded(static_cast<size_t>(s.T) * w.columns * 2);
   w.bytes = w.sums + (w.wide ? padded(static_cast<size_t>(w.splits) * s.T * s.d * 4) : 0);
   return w;
@@ -719,9 +756,9 @@ maxsim_status launch_loss(const LossShape& s, const maxsim_rows& x, const maxsim
   p.parts = reinterpret_cast<float2*>(static_cast<char*>(workspace) + padded(static_cast<size_t>(s.T) * 4));
   p.z2 = s.scale * kLog2e;
   p.status = dev->status;
-  if (launch<kStats>(maps, p, *dev, static_cast<int64_t>(p.tiles_m) * p.tiles_n, stream) != cudaSuccess)
+  if (launch<kStats>(maps, p, *dev, static_cast<int64_t>(p.tiles_m) * p.tiles_n, false, stream) != cudaSuccess)
     return MAXSIM_ERR_CUDA;
-  return launch_after(join_kernel, up_to(s.T, 32), 1024, stream, p.parts, up_to(s.V, kHalf), s.T, s.V, targets, p.hit, s.scale,
+  return launch_after(join_kernel, up_to(s.T, 32), 1024, 0, stream, p.parts, up_to(s.V, kHalf), s.T, s.V, targets, p.hit, s.scale,
                       loss, lse, dev->status) == cudaSuccess
              ? MAXSIM_OK
              : MAXSIM_ERR_CUDA;
@@ -739,10 +776,14 @@ maxsim_status launch_loss_bwd(const LossShape& s, const float* dloss, const maxs
   if (!dev) return MAXSIM_ERR_CUDA;
   const Space at = plan(s, dev->sm_count / 2);
   char* base = static_cast<char*>(workspace);
-  float *gain = reinterpret_cast<float*>(base), *coef = reinterpret_cast<float*>(base + at.coef);
+  float* top = reinterpret_cast<float*>(base);
   float* sums = reinterpret_cast<float*>(base + at.sums);
-  coef_kernel<<<1, 1024, 0, stream>>>(dloss, targets, s.T, s.V, s.scale, s.is_bf16 ? 0 : 14, coef, gain, dev->status);
-  if (cudaGetLastError() != cudaSuccess) return MAXSIM_ERR_CUDA;
+  const int more = s.is_bf16 ? 0 : 14;
+  const bool scan = s.T <= kScanRows;
+  if (!scan) {
+    top_kernel<<<1, 1024, 0, stream>>>(dloss, targets, s.T, s.V, top, dev->status);
+    if (cudaGetLastError() != cudaSuccess) return MAXSIM_ERR_CUDA;
+  }
   for (int64_t first = 0; first < s.V; first += at.columns) {
     const int columns = s.V - first < at.columns ? static_cast<int>(s.V - first) : at.columns;
     alignas(64) Maps maps = {};
@@ -758,11 +799,13 @@ maxsim_status launch_loss_bwd(const LossShape& s, const float* dloss, const maxs
     p.tiles_n = up_to(columns, kTile);
     p.targets = targets;
     p.lse = lse;
-    p.coef = coef;
-    p.gain = gain;
+    p.dloss = dloss;
+    p.top = top;
+    p.scan = scan && first == 0;
+    p.more = more;
     p.z2 = s.scale * kLog2e;
     p.status = dev->status;
-    if (launch<kGrad>(maps, p, *dev, static_cast<int64_t>(p.tiles_m) * p.tiles_n, stream) != cudaSuccess)
+    if (launch<kGrad>(maps, p, *dev, static_cast<int64_t>(p.tiles_m) * p.tiles_n, first > 0 || !scan, stream) != cudaSuccess)
       return MAXSIM_ERR_CUDA;
     if (!map_in(&maps.a, s, base + at.dz, at.columns, columns, s.T, kHalf) ||
         !map_in(&maps.b, s, w.data, w.row_stride, s.d, s.V, kBox) ||
@@ -787,16 +830,17 @@ maxsim_status launch_loss_bwd(const LossShape& s, const float* dloss, const maxs
       if (!map_out(&maps.out1, s.is_bf16 ? 1 : 0, 2, dw->data, dw->row_stride, s.d, s.V, 1)) return MAXSIM_ERR_CUDA;
     }
     const int64_t tiles = static_cast<int64_t>(p.dx_m) * p.dx_n * p.splits + static_cast<int64_t>(p.dw_m) * p.dw_n;
-    if (tiles && launch<kSums>(maps, p, *dev, tiles, stream) != cudaSuccess) return MAXSIM_ERR_CUDA;
+    if (tiles && launch<kSums>(maps, p, *dev, tiles, true, stream) != cudaSuccess) return MAXSIM_ERR_CUDA;
   }
   if (dx && at.wide) {
     const int64_t n = static_cast<int64_t>(s.T) * s.d;
     const int grid = static_cast<int>((n / 8 + 255) / 256);
-    if (s.is_bf16)
-      dx_kernel<<<grid, 256, 0, stream>>>(sums, at.splits, n, s.d, gain, static_cast<__nv_bfloat16*>(dx->data), dx->row_stride);
-    else
-      dx_kernel<<<grid, 256, 0, stream>>>(sums, at.splits, n, s.d, gain, static_cast<__half*>(dx->data), dx->row_stride);
-    if (cudaGetLastError() != cudaSuccess) return MAXSIM_ERR_CUDA;
+    const auto go = [&](auto kernel, auto* to) {
+      return launch_after(kernel, grid, 256, 0, stream, sums, at.splits, n, s.d, top, s.scale, more, to, dx->row_stride);
+    };
+    const cudaError_t e = s.is_bf16 ? go(dx_kernel<__nv_bfloat16>, static_cast<__nv_bfloat16*>(dx->data))
+                                    : go(dx_kernel<__half>, static_cast<__half*>(dx->data));
+    if (e != cudaSuccess) return MAXSIM_ERR_CUDA;
   }
   return MAXSIM_OK;
 }

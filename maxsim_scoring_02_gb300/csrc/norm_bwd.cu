@@ -216,7 +216,7 @@ cudaError_t pick(const NormParams& p, bool whole, const DeviceInfo& dev, int* bl
 
 template <typename W>
 cudaError_t fold(const float* parts, int blocks, int d, void* dw, cudaStream_t stream) {
-  return launch_after(fold_kernel<W>, (d + 31) / 32, 1024, stream, parts, blocks, d, static_cast<W*>(dw));
+  return launch_after(fold_kernel<W>, (d + 31) / 32, 1024, 0, stream, parts, blocks, d, static_cast<W*>(dw));
 }
 
 }  // namespace
