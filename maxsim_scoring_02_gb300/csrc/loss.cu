@@ -61,8 +61,10 @@ struct Params {
   int first, columns;       // the piece
   int tiles_m, tiles_n;     // of z
   int dx_m, dx_n, splits;   // kSums: dx tiles, and parts of their K
-  int dw_m, dw_n, rounds;   // dW tiles; how many of them are worth one of dx
-  int dx_wide, dx_adds;     // dx goes to fp32 sums; they are added to
+  int dw_m, dw_n, dw_splits;
+  int dw_first, rounds;     // which kind is longer, and how many of the other are worth one
+  int dx_wide, dw_wide;     // goes to fp32 sums
+  int dx_adds;              // those of dx are added to
   const int64_t* targets;
   const float *lse, *dloss;
   float* top;               // the largest |dloss|
@@ -127,39 +129,37 @@ __device__ __forceinline__ bool tile_of(const Params& p, int i, Tile& t) {
     t.steps = (p.s.d + kStep - 1) / kStep;
     return true;
   } else {
-    // dx tiles in turn; then dW tiles, of which pairs with one dx tile less have `rounds` more
-    const int n_dx = p.dx_m * p.dx_n * p.splits, n_dw = p.dw_m * p.dw_n;
-    const int whole = n_dx / pairs, rest = n_dx - whole * pairs;
+    // The longer kind's tiles in turn, then the other's, of which pairs with one long
+    // tile less have `rounds` more.
+    const int n_dx = p.dx_m * p.dx_n * p.splits, n_dw = p.dw_m * p.dw_n * p.dw_splits;
+    const int n_long = p.dw_first ? n_dw : n_dx, n_short = p.dw_first ? n_dx : n_dw;
+    const int whole = n_long / pairs, rest = n_long - whole * pairs;
     const int mine = whole + (pair < rest);
-    if (i < mine) {
-      const int at = i * pairs + pair, per = p.dx_m * p.dx_n;
-      t.kind = 1;
-      t.split = at / per;
-      const int in = at - t.split * per, m = in / p.dx_n;
-      t.m0 = m * kTile;
-      t.n0 = (in - m * p.dx_n) * kTile;
-      t.n = width(p.s.d - t.n0);
-      const int steps = (p.columns + kStep - 1) / kStep;
-      t.k0 = static_cast<int>(static_cast<int64_t>(steps) * t.split / p.splits);
-      t.steps = static_cast<int>(static_cast<int64_t>(steps) * (t.split + 1) / p.splits) - t.k0;
-      return true;
-    }
-    int k = i - mine;
-    const int extra = rest ? p.rounds : 0, light = pairs - rest;
     int64_t at;
-    if (pair >= rest && k < extra) {
-      at = static_cast<int64_t>(k) * light + (pair - rest);
+    if (i < mine) {
+      at = static_cast<int64_t>(i) * pairs + pair;
     } else {
-      if (pair >= rest) k -= extra;
-      at = static_cast<int64_t>(extra) * light + static_cast<int64_t>(k) * pairs + pair;
+      int k = i - mine;
+      const int extra = rest ? p.rounds : 0, light = pairs - rest;
+      if (pair >= rest && k < extra) {
+        at = static_cast<int64_t>(k) * light + (pair - rest);
+      } else {
+        if (pair >= rest) k -= extra;
+        at = static_cast<int64_t>(extra) * light + static_cast<int64_t>(k) * pairs + pair;
+      }
+      if (at >= n_short) return false;
     }
-    if (at >= n_dw) return false;
-    const int m = static_cast<int>(at / p.dw_n);
-    t.kind = 2;
+    t.kind = (i < mine) == (p.dw_first != 0) ? 2 : 1;
+    const int tiles_n = t.kind == 1 ? p.dx_n : p.dw_n, per = (t.kind == 1 ? p.dx_m : p.dw_m) * tiles_n;
+    const int splits = t.kind == 1 ? p.splits : p.dw_splits;
+    const int steps = ((t.kind == 1 ? p.columns : p.s.T) + kStep - 1) / kStep;
+    t.split = static_cast<int>(at / per);
+    const int in = static_cast<int>(at - static_cast<int64_t>(t.split) * per), m = in / tiles_n;
     t.m0 = m * kTile;
-    t.n0 = static_cast<int>(at - static_cast<int64_t>(m) * p.dw_n) * kTile;
+    t.n0 = (in - m * tiles_n) * kTile;
     t.n = width(p.s.d - t.n0);
-    t.steps = (p.s.T + kStep - 1) / kStep;
+    t.k0 = static_cast<int>(static_cast<int64_t>(steps) * t.split / splits);
+    t.steps = static_cast<int>(static_cast<int64_t>(steps) * (t.split + 1) / splits) - t.k0;
     return true;
   }
 }
@@ -387,7 +387,7 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
     }
     shift = p.more - exponent_of(top);
   }
-  if constexpr (kMode == kSums) gain = gain_of(p.top, p.s.scale, p.more);
+  if constexpr (kMode == kSums) gain = gain_of(p.top, p.s.scale, p.more);  // for what is not summed on
   for (int i = 0; tile_of<kMode>(p, i, t); ++i) {
     if (t.steps == 0) continue;
     const int row0 = t.m0 + static_cast<int>(rank) * kHalf + quarter * 32, row = row0 + lane;
@@ -506,7 +506,7 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
       const bool dx = t.kind == 1;
       const int rows = dx ? p.s.T : p.columns;
       const int y = dx ? row0 : p.first + row0;
-      if (dx && p.dx_wide) {
+      if (dx ? p.dx_wide : p.dw_wide) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           if (c >= chunks) continue;
@@ -514,7 +514,7 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
           __syncwarp();
           put_row(stage, lane, v[c]);
           if (row0 < rows && t.n0 + col0 + c * 32 < p.s.d)
-            send(&maps.out0, stage, lane, t.n0 + col0 + c * 32, y, t.split, p.dx_adds);
+            send(dx ? &maps.out0 : &maps.out1, stage, lane, t.n0 + col0 + c * 32, row0, t.split, dx && p.dx_adds);
         }
       } else {
 #pragma unroll
@@ -643,10 +643,10 @@ __global__ void __launch_bounds__(1024) top_kernel(const float* dloss, const int
   *out = top;
 }
 
-// dx: the parts' fp32 sums, times the gain.
+// dx or dW: the parts' fp32 sums, times the gain.
 template <typename T>
-__global__ void __launch_bounds__(256) dx_kernel(const float* sums, int splits, int64_t n, int d, const float* top,
-                                                 float scale, int more, T* dx, int64_t stride) {
+__global__ void __launch_bounds__(256) fold_kernel(const float* sums, int splits, int64_t n, int d, const float* top,
+                                                   float scale, int more, T* out, int64_t stride) {
   const int64_t i = (blockIdx.x * int64_t(256) + threadIdx.x) * 8;
   wait_for_previous();
   if (i >= n) return;
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(256) dx_kernel(const float* sums, int splits, 
   alignas(16) T o[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) o[j] = static_cast<T>(a[j] * gain);
-  *reinterpret_cast<uint4*>(dx + row * stride + (i - row * d)) = *reinterpret_cast<uint4*>(o);
+  *reinterpret_cast<uint4*>(out + row * stride + (i - row * d)) = *reinterpret_cast<uint4*>(o);
 }
 
 // ---------------------------------------------------------------------- host
@@ -677,15 +677,15 @@ int piece_columns(const LossShape& s) {
   return static_cast<int>(most < kTile ? kTile : most < all ? most : all);
 }
 
-// How dx's tiles are cut along the vocabulary: no part longer than a pair's share
-// of the launch, with an epilogue counted as eight steps.
-int split_count(const LossShape& s, int columns, int pairs) {
-  const int64_t steps = up_to(columns, kStep), dx = static_cast<int64_t>(up_to(s.T, kTile)) * up_to(s.d, kTile);
-  const int64_t dw = static_cast<int64_t>(up_to(columns, kTile)) * up_to(s.d, kTile);
-  int64_t share = (dx * (steps + 8) + dw * (up_to(s.T, kStep) + 8)) / pairs;
+// How the tiles of dx are cut along the vocabulary, and those of dW along the rows: no
+// part longer than a pair's share of the launch, with an epilogue counted as eight steps.
+void split_counts(const LossShape& s, int columns, int pairs, int* dx, int* dw) {
+  const int64_t steps_v = up_to(columns, kStep), steps_t = up_to(s.T, kStep), n = up_to(s.d, kTile);
+  int64_t share = (up_to(s.T, kTile) * n * (steps_v + 8) + up_to(columns, kTile) * n * (steps_t + 8)) / pairs;
   if (share < 16) share = 16;
-  const int64_t n = (steps + share - 1) / share;
-  return static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
+  const auto count = [&](int64_t steps) { return static_cast<int>(steps <= share ? 1 : steps > 64 * share ? 64 : (steps + share - 1) / share); };
+  *dx = count(steps_v);
+  *dw = count(steps_t);
 }
 
 bool map_in(CUtensorMap* m, const LossShape& s, const void* data, int64_t stride, int64_t inner, int64_t rows, uint32_t box_rows) {
@@ -718,19 +718,29 @@ cudaError_t launch(const Maps& maps, const Params& p, const DeviceInfo& dev, int
 }
 
 struct Space {  // of the backward's workspace
-  size_t dz, sums, bytes;
-  int columns, splits;
-  bool wide;
+  size_t dz, sums, dw_sums, bytes;
+  int columns, splits, dw_splits;
+  bool wide;  // dx goes through fp32 sums
 };
 Space plan(const LossShape& s, int pairs) {
   Space w;
   w.columns = piece_columns(s);
-  w.splits = split_count(s, w.columns < s.V ? w.columns : static_cast<int>(s.V), pairs);
+  const int first = w.columns < s.V ? w.columns : static_cast<int>(s.V);
+  split_counts(s, first, pairs, &w.splits, &w.dw_splits);
   w.wide = w.splits > 1 || w.columns < s.V;
   w.dz = 256;  // after the largest |dloss|
   w.sums = w.dz + padded(static_cast<size_t>(s.T) * w.columns * 2);
-  w.bytes = w.sums + (w.wide ? padded(static_cast<size_t>(w.splits) * s.T * s.d * 4) : 0);
+  w.dw_sums = w.sums + (w.wide ? padded(static_cast<size_t>(w.splits) * s.T * s.d * 4) : 0);
+  w.bytes = w.dw_sums + (w.dw_splits > 1 ? padded(static_cast<size_t>(w.dw_splits) * first * s.d * 4) : 0);
   return w;
+}
+
+template <typename T>
+cudaError_t fold(const float* sums, int splits, int64_t rows, const LossShape& s, const float* top, int more, void* out,
+                 int64_t stride, cudaStream_t stream) {
+  const int64_t n = rows * s.d;
+  return launch_after(fold_kernel<T>, static_cast<int>((n / 8 + 255) / 256), 256, 0, stream, sums, splits, n, s.d, top,
+                      s.scale, more, static_cast<T*>(out), stride);
 }
 
 }  // namespace
@@ -813,6 +823,8 @@ maxsim_status launch_loss_bwd(const LossShape& s, const float* dloss, const maxs
         !map_in(&maps.b2, s, x.data, x.row_stride, s.d, s.T, kBox))
       return MAXSIM_ERR_CUDA;
     p.splits = at.splits;
+    p.dw_splits = at.dw_splits;
+    p.dw_wide = at.dw_splits > 1;
     if (dx) {
       p.dx_m = up_to(s.T, kTile);
       p.dx_n = up_to(s.d, kTile);
@@ -825,22 +837,27 @@ maxsim_status launch_loss_bwd(const LossShape& s, const float* dloss, const maxs
     if (dw) {
       p.dw_m = up_to(columns, kTile);
       p.dw_n = up_to(s.d, kTile);
-      const int dx_cost = up_to(columns, kStep) / at.splits + 8, dw_cost = up_to(s.T, kStep) + 8;
-      p.rounds = (dx_cost + dw_cost / 2) / dw_cost;
-      if (!map_out(&maps.out1, s.is_bf16 ? 1 : 0, 2, dw->data, dw->row_stride, s.d, s.V, 1)) return MAXSIM_ERR_CUDA;
+      if (!(p.dw_wide ? map_out(&maps.out1, 3, 4, base + at.dw_sums, s.d, s.d, columns, at.dw_splits)
+                      : map_out(&maps.out1, s.is_bf16 ? 1 : 0, 2, dw->data, dw->row_stride, s.d, s.V, 1)))
+        return MAXSIM_ERR_CUDA;
     }
-    const int64_t tiles = static_cast<int64_t>(p.dx_m) * p.dx_n * p.splits + static_cast<int64_t>(p.dw_m) * p.dw_n;
+    const int dx_cost = up_to(columns, kStep) / at.splits + 8, dw_cost = up_to(s.T, kStep) / at.dw_splits + 8;
+    p.dw_first = dw_cost > dx_cost;
+    const int longer = p.dw_first ? dw_cost : dx_cost, other = p.dw_first ? dx_cost : dw_cost;
+    p.rounds = (longer + other / 2) / other;
+    const int64_t tiles = static_cast<int64_t>(p.dx_m) * p.dx_n * p.splits +
+                          static_cast<int64_t>(p.dw_m) * p.dw_n * p.dw_splits;
     if (tiles && launch<kSums>(maps, p, *dev, tiles, true, stream) != cudaSuccess) return MAXSIM_ERR_CUDA;
+    if (dw && p.dw_wide) {
+      const auto go = s.is_bf16 ? fold<__nv_bfloat16> : fold<__half>;
+      if (go(reinterpret_cast<float*>(base + at.dw_sums), at.dw_splits, columns, s, top, more,
+             static_cast<char*>(dw->data) + first * dw->row_stride * 2, dw->row_stride, stream) != cudaSuccess)
+        return MAXSIM_ERR_CUDA;
+    }
   }
   if (dx && at.wide) {
-    const int64_t n = static_cast<int64_t>(s.T) * s.d;
-    const int grid = static_cast<int>((n / 8 + 255) / 256);
-    const auto go = [&](auto kernel, auto* to) {
-      return launch_after(kernel, grid, 256, 0, stream, sums, at.splits, n, s.d, top, s.scale, more, to, dx->row_stride);
-    };
-    const cudaError_t e = s.is_bf16 ? go(dx_kernel<__nv_bfloat16>, static_cast<__nv_bfloat16*>(dx->data))
-                                    : go(dx_kernel<__half>, static_cast<__half*>(dx->data));
-    if (e != cudaSuccess) return MAXSIM_ERR_CUDA;
+    const auto go = s.is_bf16 ? fold<__nv_bfloat16> : fold<__half>;
+    if (go(sums, at.splits, s.T, s, top, more, dx->data, dx->row_stride, stream) != cudaSuccess) return MAXSIM_ERR_CUDA;
   }
   return MAXSIM_OK;
 }

@@ -99,6 +99,12 @@ def test_many_columns_for_one_row():
     _check(*_inputs(1, (1 << 20) + 3, 64, torch.bfloat16))
 
 
+@pytest.mark.parametrize("T,V,d", [(40000, 3, 64), (20001, 300, 136), (5000, 40, 520)])
+def test_many_rows_for_few_columns(T, V, d):
+    """dW's sums over the rows are cut, too."""
+    _check(*_inputs(T, V, d, torch.bfloat16))
+
+
 def test_no_targets_and_bad_ones():
     x, w, t, dloss = _inputs(70, 300, 64, torch.bfloat16)
     none = torch.full_like(t, -100)
