@@ -23,7 +23,7 @@ struct Shape {
   static constexpr int kBlock = kTeam > 32 ? kTeam : 256, kTeams = kBlock / kTeam;
   using Rows = Queue<T, kBlock, kGroups, 3, 40000, kWhole>;
   // blocks of an SM that the registers have to allow
-  static constexpr int kFit = kTeam > 256 ? 1 : kTeam > 64 ? 768 / kTeam : 512 / kBlock;
+  static constexpr int kFit = kTeam > 256 ? 1 : 512 / kBlock;
 };
 
 template <typename T, int kTeam, int kGroups, bool kWhole>
@@ -42,6 +42,9 @@ __global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256, Shape<T, kTeam, kGro
   for (int g = 0; g < kGroups; ++g)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[g].p[i] = Pair(0.f, 0.f);
+  Eight w[kGroups];  // in registers: read from L1 twice a row they cost a fifth of the time
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) w[g] = load_weights<T, kWhole>(p, cols(g));
   typename S::Rows rows(smem);  // dy, h, and what reaches the sum from elsewhere
   const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
   int64_t row = static_cast<int64_t>(blockIdx.x) * kTeams + team;
@@ -66,11 +69,11 @@ __global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256, Shape<T, kTeam, kGro
     Pair squares(0.f, 0.f), cross(0.f, 0.f);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      const Eight y = up8<T>(rows.get(stage, 0, g)), v = up8<T>(rows.get(stage, 1, g)), w = load_weights<T, kWhole>(p, cols(g));
+      const Eight y = up8<T>(rows.get(stage, 0, g)), v = up8<T>(rows.get(stage, 1, g));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         squares = fma2(v.p[i], v.p[i], squares);
-        cross = fma2(mul2(w.p[i], y.p[i]), v.p[i], cross);
+        cross = fma2(mul2(w[g].p[i], y.p[i]), v.p[i], cross);
       }
     }
     float ss, gh, odd;
@@ -79,19 +82,19 @@ __global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256, Shape<T, kTeam, kGro
     cross.get(gh, odd);
     gh += odd;
     team_all<kTeam>(ss, gh, AddBoth(), at);
-    asm volatile("" ::: "memory");  // what was read is read again, not kept
+    asm volatile("" ::: "memory");  // elements are read and unpacked again, not held in 4 registers each
     const bool fits = ss < 3e38f && fabsf(gh) < 3e38f;
     float rstd = root_of(fmaf(ss, p.per, p.eps)), c = gh * p.per * rstd * rstd;
     if (any_of_team<kTeam>(!fits)) {  // out of fp32's range: once more in fp64
       double a = 0., b = 0.;
-#pragma unroll 1
+#pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        const Eight y = up8<T>(rows.get(stage, 0, g)), v = up8<T>(rows.get(stage, 1, g)), w = load_weights<T, kWhole>(p, cols(g));
+        const Eight y = up8<T>(rows.get(stage, 0, g)), v = up8<T>(rows.get(stage, 1, g));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float v0, v1, g0, g1;
           v.p[i].get(v0, v1);
-          mul2(w.p[i], y.p[i]).get(g0, g1);
+          mul2(w[g].p[i], y.p[i]).get(g0, g1);
           a += static_cast<double>(v0) * v0 + static_cast<double>(v1) * v1;
           b += static_cast<double>(g0) * v0 + static_cast<double>(g1) * v1;
         }
@@ -106,11 +109,11 @@ __global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256, Shape<T, kTeam, kGro
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const Cols<kWhole> cc = cols(g);
-      const Eight y = up8<T>(rows.get(stage, 0, g)), v = up8<T>(rows.get(stage, 1, g)), w = load_weights<T, kWhole>(p, cc);
+      const Eight y = up8<T>(rows.get(stage, 0, g)), v = up8<T>(rows.get(stage, 1, g));
       Eight back;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        back.p[i] = mul2(r2, fma2(v.p[i], c2, mul2(w.p[i], y.p[i])));
+        back.p[i] = mul2(r2, fma2(v.p[i], c2, mul2(w[g].p[i], y.p[i])));
         acc[g].p[i] = fma2(y.p[i], mul2(v.p[i], r2), acc[g].p[i]);
       }
       if (p.more) {
