@@ -1054,32 +1054,42 @@ def encoder_rms_norm_backward(dy, h, weight=None, dsum=None, eps=1e-6, p=0.0, rn
     dropout dx and dresidual are one tensor, unless both are given."""
     lib = load_library()
     spec, shape, dtype, index, hv = _norm_spec(h, "h", weight, eps, p, rng, None)
-    device = h.device
-    views = (_rows(dy, "dy", shape, dtype, index), hv,
-             None if dsum is None else _rows(dsum, "dsum", shape, dtype, index))
+    device, d = h.device, shape[1]
+
+    def result(t, name):
+        if t is not None:
+            return t, _rows(t, name, shape, dtype, index)
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, _new_rows(t, d)
+
+    dyv = _rows(dy, "dy", shape, dtype, index)
+    more = None if dsum is None else _rows(dsum, "dsum", shape, dtype, index)
+    second = None
     if not p and (dx is None or dresidual is None):
-        dx = dx if dx is not None else dresidual if dresidual is not None else torch.empty(shape, dtype=dtype, device=device)
-        dresidual, second = dx, None
+        dx, first = result(dx if dx is not None else dresidual, "dx")
+        dresidual = dx
     else:
-        dx = torch.empty(shape, dtype=dtype, device=device) if dx is None else dx
-        dresidual = torch.empty(shape, dtype=dtype, device=device) if dresidual is None else dresidual
-        second = _rows(dresidual, "dresidual", shape, dtype, index)
+        dx, first = result(dx, "dx")
+        dresidual, second = result(dresidual, "dresidual")
     if weight is not None:
         if dweight is None:
-            dweight = torch.empty(shape[1], dtype=weight.dtype, device=device)
-        if _dev(dweight, "dweight", weight.dtype).numel() != shape[1]:
+            dweight = torch.empty(d, dtype=weight.dtype, device=device)
+        elif _dev(dweight, "dweight", weight.dtype).numel() != d:
             raise ValueError("dweight must have one entry a column")
         if workspace is None:
             workspace = _scratch(lib.maxsim_rms_norm_backward_workspace_size(spec), device)
+        else:
+            _dev(workspace, "workspace", torch.uint8)
     elif dweight is not None:
         raise ValueError("dweight goes with a weight")
-    if workspace is not None:
+    elif workspace is not None:
         _dev(workspace, "workspace", torch.uint8)
-    st = lib.maxsim_rms_norm_backward(spec, *views, _rows(dx, "dx", shape, dtype, index), second,
+    st = lib.maxsim_rms_norm_backward(spec, dyv, hv, more, first, second,
                                       None if dweight is None else dweight.data_ptr(),
                                       None if workspace is None else workspace.data_ptr(),
                                       0 if workspace is None else workspace.numel(), _stream_on(stream, index))
-    _check(st, "maxsim_rms_norm_backward")
+    if st:
+        _check(st, "maxsim_rms_norm_backward")
     return dx, dresidual, dweight
 
 
@@ -1121,15 +1131,17 @@ def encoder_cross_entropy(x, weight, targets, scale=1.0, loss=None, lse=None, wo
     the backward needs."""
     lib = load_library()
     spec, xv, wv, index = _loss_spec(x, weight, targets, scale)
-    n = spec.T
-    loss = torch.empty(n, dtype=torch.float32, device=x.device) if loss is None else _row_values(loss, "loss", n)
-    lse = torch.empty(n, dtype=torch.float32, device=x.device) if lse is None else _row_values(lse, "lse", n)
+    n, device = spec.T, x.device
+    loss = torch.empty(n, dtype=torch.float32, device=device) if loss is None else _row_values(loss, "loss", n)
+    lse = torch.empty(n, dtype=torch.float32, device=device) if lse is None else _row_values(lse, "lse", n)
     if workspace is None:
-        workspace = _scratch(lib.maxsim_cross_entropy_workspace_size(spec), x.device)
-    _dev(workspace, "workspace", torch.uint8)
+        workspace = _scratch(lib.maxsim_cross_entropy_workspace_size(spec), device)
+    else:
+        _dev(workspace, "workspace", torch.uint8)
     st = lib.maxsim_cross_entropy(spec, xv, wv, loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
                                   workspace.numel(), _stream_on(stream, index))
-    _check(st, "maxsim_cross_entropy")
+    if st:
+        _check(st, "maxsim_cross_entropy")
     return loss, lse
 
 
@@ -1145,16 +1157,23 @@ def encoder_cross_entropy_backward(dloss, x, weight, targets, lse, scale=1.0, dx
     n, dtype, device = spec.T, x.dtype, x.device
     _row_values(dloss, "dloss", n)
     _row_values(lse, "lse", n)
-    if dx is None and want_dx:
+    dxv = dwv = None
+    if dx is not None:
+        dxv = _rows(dx, "dx", x.shape, dtype, index)
+    elif want_dx:
         dx = torch.empty(x.shape, dtype=dtype, device=device)
-    if dweight is None and want_dweight:
+        dxv = _new_rows(dx, spec.d)
+    if dweight is not None:
+        dwv = _rows(dweight, "dweight", weight.shape, dtype, index)
+    elif want_dweight:
         dweight = torch.empty(weight.shape, dtype=dtype, device=device)
+        dwv = _new_rows(dweight, spec.d)
     if workspace is None:
         workspace = _scratch(lib.maxsim_cross_entropy_backward_workspace_size(spec), device)
-    _dev(workspace, "workspace", torch.uint8)
-    st = lib.maxsim_cross_entropy_backward(
-        spec, dloss.data_ptr(), xv, wv, lse.data_ptr(), None if dx is None else _rows(dx, "dx", x.shape, dtype, index),
-        None if dweight is None else _rows(dweight, "dweight", weight.shape, dtype, index), workspace.data_ptr(),
-        workspace.numel(), _stream_on(stream, index))
-    _check(st, "maxsim_cross_entropy_backward")
+    else:
+        _dev(workspace, "workspace", torch.uint8)
+    st = lib.maxsim_cross_entropy_backward(spec, dloss.data_ptr(), xv, wv, lse.data_ptr(), dxv, dwv,
+                                           workspace.data_ptr(), workspace.numel(), _stream_on(stream, index))
+    if st:
+        _check(st, "maxsim_cross_entropy_backward")
     return dx, dweight

@@ -10,14 +10,11 @@
 namespace msim {
 namespace {
 
-#ifndef KW
-#define KW 3
-#define KN 2
-#endif
 constexpr int kThreads = 256;
-// groups of 8 columns of a thread
+// Groups of eight columns of a thread (98304 x 2048 bf16 with a residual: three 187 us,
+// two 189, four 194; 20011 x 1001 fp32, rows not whole: one 31 us, two 32).
 template <bool kWhole>
-constexpr int kUnits = kWhole ? KW : KN;
+constexpr int kUnits = kWhole ? 3 : 1;
 
 
 struct DropoutParams {

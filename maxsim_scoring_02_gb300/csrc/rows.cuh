@@ -191,13 +191,12 @@ __device__ __forceinline__ void store_down8(T* row, const Cols<kWhole>& c, const
   if constexpr (kWhole) {
     store8<T, kWhole>(row, c, down8<T>(e));
   } else {
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float a, b;
-      e.p[i].get(a, b);
-      if (c.in(2 * i)) row[c.at(2 * i)] = static_cast<T>(a);
-      if (c.in(2 * i + 1)) row[c.at(2 * i + 1)] = static_cast<T>(b);
-    }
+    for (int i = 0; i < 4; ++i) e.p[i].get(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c.in(j)) row[c.at(j)] = static_cast<T>(v[j]);
   }
 }
 
@@ -214,17 +213,19 @@ struct Kept {
     } else {
       const uint32_t lane = threadIdx.x & 31;
       const Lots mine = draw_lots(key, ((static_cast<uint32_t>(c.first) - lane) >> 3) + lane, row);
-      uint32_t set = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) set |= mine.stays(j, high) ? 1u << j : 0u;
+      // column j * 32 + lane is element lane % 8 of group j * 4 + lane / 8
       bits = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) bits |= (__shfl_sync(~0u, set, j * 4 + (lane >> 3)) >> (lane & 7) & 1u) << j;
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t all = __ballot_sync(~0u, mine.stays(j, high));
+        if ((lane & 7) == j) bits = all;
+      }
+      bits >>= lane >> 3;
     }
   }
   __device__ __forceinline__ bool operator()(int j) const {
     if constexpr (kWhole) return lots.stays(j, high);
-    return bits >> j & 1;
+    return bits >> (4 * j) & 1;
   }
   // add + (stays ? x * factor : 0), the sum rounded once; without `add`, 0 or the product.
   __device__ __forceinline__ Eight of(const Eight& x, float factor, const Eight& add, bool adds) const {
