@@ -678,8 +678,8 @@ maxsim_status maxsim_rms_norm_backward(const maxsim_norm_spec *spec, const maxsi
  * Products are fp32 sums on the tensor cores, in parts of 512 along d that are added
  * with rounding; statistics are fp32. x and weight must be finite: a row of x that is
  * not makes its own lse and loss NaN, no other row's.
- * workspace: at least maxsim_cross_entropy_workspace_size(spec) bytes, 16-byte
- * aligned; calls that may run at the same time need one each, here and below.
+ * workspace: at least maxsim_cross_entropy_workspace_size(spec) bytes (256 MB at the
+ * most, or what 256 rows need: 2048 bytes for 128 columns), 16-byte aligned; calls that may run at the same time need one each, here and below.
  * Limits: FP32 returns MAXSIM_ERR_UNSUPPORTED; d a multiple of 8, d <= 65536;
  * V >= 1; T, V < 2^31 - 256; scale from 2^-60 to 2^60; views 16-byte aligned with
  * strides that are multiples of 8 and at least d.

@@ -748,8 +748,15 @@ cudaError_t fold(const float* sums, int splits, int64_t rows, const LossShape& s
 
 }  // namespace
 
+// The forward takes as many rows at a time as 256 MB hold the parts of.
+static int stats_rows(const LossShape& s) {
+  const int64_t most = kPieceBytes / (up_to(s.V, kHalf) * static_cast<int64_t>(sizeof(float2))) / kTile * kTile;
+  return most < kTile ? kTile : most < s.T ? static_cast<int>(most) : s.T;
+}
+
 size_t loss_workspace_bytes(const LossShape& s) {
-  return padded(static_cast<size_t>(s.T) * 4) + static_cast<size_t>(up_to(s.V, kHalf)) * s.T * sizeof(float2);
+  const size_t rows = stats_rows(s);
+  return padded(rows * 4) + up_to(s.V, kHalf) * rows * sizeof(float2);
 }
 
 maxsim_status launch_loss(const LossShape& s, const maxsim_rows& x, const maxsim_rows& w, const int64_t* targets,
@@ -757,24 +764,28 @@ maxsim_status launch_loss(const LossShape& s, const maxsim_rows& x, const maxsim
   const DeviceInfo* dev = device_info();
   if (!dev) return MAXSIM_ERR_CUDA;
   alignas(64) Maps maps = {};
-  if (!map_in(&maps.a, s, x.data, x.row_stride, s.d, s.T, kHalf) || !map_in(&maps.b, s, w.data, w.row_stride, s.d, s.V, kHalf))
-    return MAXSIM_ERR_CUDA;
+  if (!map_in(&maps.b, s, w.data, w.row_stride, s.d, s.V, kHalf)) return MAXSIM_ERR_CUDA;
+  const int step = stats_rows(s);
   Params p = {};
   p.s = s;
   p.columns = static_cast<int>(s.V);
-  p.tiles_m = up_to(s.T, kTile);
   p.tiles_n = up_to(s.V, kTile);
-  p.targets = targets;
   p.hit = static_cast<float*>(workspace);
-  p.parts = reinterpret_cast<float2*>(static_cast<char*>(workspace) + padded(static_cast<size_t>(s.T) * 4));
+  p.parts = reinterpret_cast<float2*>(static_cast<char*>(workspace) + padded(static_cast<size_t>(step) * 4));
   p.z2 = s.scale * kLog2e;
   p.status = dev->status;
-  if (launch<kStats>(maps, p, *dev, static_cast<int64_t>(p.tiles_m) * p.tiles_n, false, stream) != cudaSuccess)
-    return MAXSIM_ERR_CUDA;
-  return launch_after(join_kernel, up_to(s.T, 32), 1024, 0, stream, p.parts, up_to(s.V, kHalf), s.T, s.V, targets, p.hit, s.scale,
-                      loss, lse, dev->status) == cudaSuccess
-             ? MAXSIM_OK
-             : MAXSIM_ERR_CUDA;
+  for (int64_t row = 0; row < s.T; row += step) {
+    p.s.T = s.T - row < step ? static_cast<int>(s.T - row) : step;
+    p.tiles_m = up_to(p.s.T, kTile);
+    p.targets = targets + row;
+    if (!map_in(&maps.a, s, static_cast<const char*>(x.data) + row * x.row_stride * 2, x.row_stride, s.d, p.s.T, kHalf))
+      return MAXSIM_ERR_CUDA;
+    if (launch<kStats>(maps, p, *dev, static_cast<int64_t>(p.tiles_m) * p.tiles_n, row > 0, stream) != cudaSuccess ||
+        launch_after(join_kernel, up_to(p.s.T, 32), 1024, 0, stream, p.parts, up_to(s.V, kHalf), p.s.T, s.V, p.targets,
+                     p.hit, s.scale, loss + row, lse + row, dev->status) != cudaSuccess)
+      return MAXSIM_ERR_CUDA;
+  }
+  return MAXSIM_OK;
 }
 
 size_t loss_bwd_workspace_bytes(const LossShape& s) {

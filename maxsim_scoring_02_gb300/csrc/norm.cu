@@ -27,7 +27,7 @@ struct Shape {
 };
 
 template <typename T, int kTeam, int kGroups, bool kWhole, bool k8>
-__global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256, Shape<T, kTeam, kGroups, kWhole>::kFit) norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256, Shape<T, kTeam, kGroups, kWhole>::kFit) rms_norm_kernel(const NormParams p) {
   using S = Shape<T, kTeam, kGroups, kWhole>;
   constexpr int kRows = S::kRows, kStages = S::Rows::kStages, kAhead = kStages - 1;
   constexpr bool kHold = kGroups <= 2;  // weights stay in registers
@@ -190,8 +190,8 @@ cudaError_t go(const NormParams& p, const DeviceInfo& dev, cudaStream_t stream) 
     return cudaGetLastError();
   };
   static Fits known[2];
-  return p.format == MAXSIM_NORM_SAME ? launch(norm_kernel<T, kTeam, kGroups, kWhole, false>, known[0])
-                                      : launch(norm_kernel<T, kTeam, kGroups, kWhole, true>, known[1]);
+  return p.format == MAXSIM_NORM_SAME ? launch(rms_norm_kernel<T, kTeam, kGroups, kWhole, false>, known[0])
+                                      : launch(rms_norm_kernel<T, kTeam, kGroups, kWhole, true>, known[1]);
 }
 
 template <typename T>

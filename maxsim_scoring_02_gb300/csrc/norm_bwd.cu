@@ -27,7 +27,7 @@ struct Shape {
 };
 
 template <typename T, int kTeam, int kGroups, bool kWhole>
-__global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256, Shape<T, kTeam, kGroups, kWhole>::kFit) norm_bwd_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256, Shape<T, kTeam, kGroups, kWhole>::kFit) rms_norm_bwd_kernel(const NormParams p) {
   using S = Shape<T, kTeam, kGroups, kWhole>;
   let_next_begin();
   constexpr int kTeams = S::kTeams, kStages = S::Rows::kStages, kAhead = kStages - 1;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(1024) fold_kernel(const float* parts, int bloc
 template <typename T, int kTeam, int kGroups, bool kWhole>
 cudaError_t go(const NormParams& p, const DeviceInfo& dev, int* blocks, cudaStream_t stream) {
   using S = Shape<T, kTeam, kGroups, kWhole>;
-  const auto kernel = norm_bwd_kernel<T, kTeam, kGroups, kWhole>;
+  const auto kernel = rms_norm_bwd_kernel<T, kTeam, kGroups, kWhole>;
   static Fits known;
   int fit = 1;
   const cudaError_t e = blocks_that_fit(known, dev, kernel, S::kBlock, S::Rows::kBytes, &fit);

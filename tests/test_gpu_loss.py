@@ -95,6 +95,44 @@ def test_several_pieces_of_the_vocabulary():
     _check(*_inputs(600001, 300, 8, torch.float16))
 
 
+def test_several_pieces_of_the_rows():
+    """The parts of 60000 rows and 40000 columns take two pieces in the forward (rows
+    against the fp64 form, some of them); a vocabulary of 2^31 elements."""
+    x, w, t, _ = _inputs(60000, 40000, 64, torch.bfloat16)
+    loss, lse = m.encoder_cross_entropy(x, w, t)
+    for a in (0, 20000, 59000):
+        want = ref.cross_entropy(x[a:a + 999], w, t[a:a + 999])
+        ref.within(lse[a:a + 999], want["lse"], want["lse_tol"], "lse")
+        ref.within(loss[a:a + 999], want["loss"], want["loss_tol"], "loss")
+
+
+def test_more_than_31_bits_of_elements():
+    """Columns whose rows of weight lie beyond 2^31 elements: their gradients, and a
+    target there."""
+    T, V, d, n = 5, (1 << 20) + 777, 2056, 300
+    x = workloads.normal((T, d), seed=1, device=DEV).bfloat16()
+    w = torch.zeros((V, d), dtype=torch.bfloat16, device=DEV)
+    w[-n:] = (workloads.normal((n, d), seed=2, device=DEV) * 0.1).bfloat16()
+    t = torch.tensor([V - 1, 3, V - n, -1, V - 7], device=DEV)
+    dloss = torch.rand(T, generator=torch.Generator().manual_seed(3)).to(DEV)
+    loss, lse = m.encoder_cross_entropy(x, w, t)
+    # V - n columns have logit 0
+    z = x.double() @ w[-n:].double().T
+    want = torch.logaddexp(torch.logsumexp(z, 1), torch.full((T,), math.log(V - n), device=DEV, dtype=torch.float64))
+    off = (x.double().abs() @ w[-n:].double().abs().T).amax(1) * d * 2.0 ** -23 + 2.0 ** -16 + 2.0 ** -22 * want
+    assert ((lse.double() - want).abs() <= off).all()
+    dx, dw = m.encoder_cross_entropy_backward(dloss, x, w, t, lse)
+    part = torch.where(t >= 0, dloss.double(), 0.0)[:, None]
+    for cols, zz in ((slice(V - n, V), z), (slice(0, 64), torch.zeros((T, 64), dtype=torch.float64, device=DEV))):
+        p = torch.exp(zz - want[:, None])
+        dz = p * part - part * (torch.arange(V, device=DEV)[cols][None] == t[:, None])
+        E = 2.0 ** -8 * dz.abs() + p * part * (4 * off[:, None] + 2.0 ** -17) + 2.0 ** -20 * dz.abs()
+        ref.within(dw[cols], dz.T @ x.double(), E.T @ x.double().abs() + 2.0 ** -8 * (dz.T @ x.double()).abs())
+        if cols.start:  # the other columns' weights are 0
+            ref.within(dx, dz @ w[cols].double(), E @ w[cols].double().abs() + 2.0 ** -8 * (dz @ w[cols].double()).abs()
+                       + 2.0 ** -15 * (dz.abs() @ w[cols].double().abs()))
+
+
 def test_many_columns_for_one_row():
     _check(*_inputs(1, (1 << 20) + 3, 64, torch.bfloat16))
 

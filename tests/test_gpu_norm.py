@@ -215,6 +215,25 @@ def test_gradients_against_differences():
         assert abs((ends[0] - ends[1]) / (2 * s) - want) <= (2e-4 + 1e-4) * size
 
 
+def test_many_rows():
+    """Rows whose offsets pass 32 bits: some of them against fp64, forward and backward."""
+    n, d = (1 << 21) + 5, 1032
+    x, w = torch.empty((n, d), dtype=torch.bfloat16, device=DEV), _weight(d, torch.float32)
+    for a in range(0, n, 1 << 19):
+        b = min(n, a + (1 << 19))
+        x[a:b] = workloads.normal((b - a, d), seed=a + 1, device=DEV).bfloat16()
+    y = m.encoder_rms_norm(x, w)
+    for a in (0, n // 2, n - 9):
+        _check_forward(x, x[a:a + 9], y[a:a + 9], w)
+    dx, _, _ = m.encoder_rms_norm_backward(y, x, w)
+    for a in (0, n // 2, n - 9):
+        back, tol, _, _ = ref.norm_backward(y[a:a + 9], x[a:a + 9], w, EPS)
+        ref.within(dx[a:a + 9], back, tol + 2.0 ** -8 * back.abs())
+    q, s = m.encoder_rms_norm(x, w, fmt="int8")
+    want, _ = ref.norm(x[-9:], w, EPS)
+    ref.within(q[-9:].float(), want / s[-9:, None].double(), 0.5 + 2.0 ** -20 * (want / s[-9:, None].double()).abs() + 2 * ref.ROW * 127)
+
+
 def test_repeatable_and_no_rows():
     dy, h, w = rows(3000, 520, 1, torch.bfloat16), rows(3000, 520, 2, torch.bfloat16), _weight(520, torch.float32)
     first = [t.clone() for t in m.encoder_rms_norm_backward(dy, h, w)]
