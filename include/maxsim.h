@@ -679,7 +679,8 @@ maxsim_status maxsim_rms_norm_backward(const maxsim_norm_spec *spec, const maxsi
  * with rounding; statistics are fp32. x and weight must be finite: a row of x that is
  * not makes its own lse and loss NaN, no other row's.
  * workspace: at least maxsim_cross_entropy_workspace_size(spec) bytes (256 MB at the
- * most, or what 256 rows need: 2048 bytes for 128 columns), 16-byte aligned; calls that may run at the same time need one each, here and below.
+ * most, or what 256 rows need: 2048 bytes for 128 columns; and a copy of x where d is
+ * no multiple of 64), 16-byte aligned; calls that may run at the same time need one each, here and below.
  * Limits: FP32 returns MAXSIM_ERR_UNSUPPORTED; d a multiple of 8, d <= 65536;
  * V >= 1; T, V < 2^31 - 256; scale from 2^-60 to 2^60; views 16-byte aligned with
  * strides that are multiples of 8 and at least d.
@@ -706,9 +707,12 @@ maxsim_status maxsim_cross_entropy(const maxsim_loss_spec *spec, const maxsim_ro
  * x has to be finite there, too (0 * infinity is NaN in dweight).
  * The logits are made again, a piece of the vocabulary at a time: the workspace
  * holds one piece's dz in the inputs' type (256 MB, or 256 columns where T is above
- * 524288), times a power of two so that small dloss lose no bits, and fp32 sums of
- * dx where the vocabulary has several pieces or few rows. Sums are added in an
+ * 524288), divided by the largest |dloss| so that small ones lose no bits, fp32 sums
+ * of dx where the vocabulary has several pieces or there are few rows, and of dweight
+ * where there are few columns. Sums are added in an
  * order that depends on the sizes and the number of SMs alone.
+ * d a multiple of 64 is faster (a third in the forward): rows then begin on 128-byte
+ * boundaries.
  * workspace: at least maxsim_cross_entropy_backward_workspace_size(spec) bytes,
  * 256-byte aligned. dx and dweight may overlap no input and not one another. With
  * T = 0 dweight is 0. Limits as in maxsim_cross_entropy, for the gradients too.

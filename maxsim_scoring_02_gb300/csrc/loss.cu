@@ -15,8 +15,10 @@
 //            and long tiles, dW many short ones that even out the pairs' work
 // A piece's dz is bounded by 256 MB; logits live in TMEM and registers alone. Making
 // them again costs a fourth product instead of T x V numbers kept between the calls.
-// dz is held times a power of two that brings the largest dloss to 1 (to 2^14 in fp16,
-// whose range ends there): small gradients keep their bits.
+// dz is held divided by the largest |dloss| (times 2^14 in fp16, whose range ends
+// there): small gradients keep their bits, and where all rows weigh the same, which is
+// usual, the -1 at the target is exact (scaled by powers of two alone it was off by up
+// to 2^-9 in the same direction in every row).
 // Bound by the tensor cores (and by the power limit in long runs).
 #include <cmath>
 
@@ -69,7 +71,7 @@ struct Params {
   const float *lse, *dloss;
   float* top;               // the largest |dloss|
   int scan;                 // kGrad finds it (else it is there)
-  int more;                 // dz is held times 2^(more - e), e the exponent of the largest |dloss|
+  float more;               // dz is held times this over the largest |dloss|
   float2* parts;
   float* hit;               // [T] the target's product
   float z2;                 // scale * log2(e)
@@ -341,12 +343,9 @@ __device__ __forceinline__ void send(const CUtensorMap* map, uint32_t stage, int
   }
 }
 
-// What dz is held times: 2^(more - e), so that the largest |dloss| becomes 1 to 2 (2^14
-// to 2^15 in fp16); the sums are multiplied by scale 2^(e - more) at the end.
-__device__ __forceinline__ int exponent_of(float top) { return top > 0.f && top < INFINITY ? ilogbf(top) : 0; }
-__device__ __forceinline__ float gain_of(const float* top, float scale, int more) {
-  return ldexpf(scale, exponent_of(*top) - more);
-}
+// The sums of dz's products are multiplied by this at the end.
+__device__ __forceinline__ float usable(float top) { return top > 0.f && top < INFINITY ? top : 1.f; }
+__device__ __forceinline__ float gain_of(const float* top, float scale, float more) { return usable(*top) / more * scale; }
 // The largest |dloss| of rows with a target, found by n threads; bad targets are reported.
 __device__ __forceinline__ float largest(const float* dloss, const int64_t* targets, int T, int64_t V, int thread, int n,
                                          unsigned* status) {
@@ -370,7 +369,7 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
   int a = 0;
   uint32_t aph = 0;
   Tile t;
-  int shift = 0;  // of dloss
+  float whole = 1.f;  // what dloss is divided by
   float gain = 1.f;
   if constexpr (kMode == kGrad) {
     float top;
@@ -385,7 +384,7 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
     } else {
       top = *p.top;
     }
-    shift = p.more - exponent_of(top);
+    whole = usable(top);
   }
   if constexpr (kMode == kSums) gain = gain_of(p.top, p.s.scale, p.more);  // for what is not summed on
   for (int i = 0; tile_of<kMode>(p, i, t); ++i) {
@@ -402,7 +401,7 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
         target = g >= 0 && g < kHalf ? static_cast<int>(g) : -1;
         if constexpr (kMode == kGrad) {
           lse2 = p.lse[row] * kLog2e;
-          coef = to >= 0 && to < p.s.V ? ldexpf(p.dloss[row], shift) : 0.f;
+          coef = to >= 0 && to < p.s.V ? p.dloss[row] / whole * p.more : 0.f;
         }
       }
     }
@@ -646,7 +645,7 @@ __global__ void __launch_bounds__(1024) top_kernel(const float* dloss, const int
 // dx or dW: the parts' fp32 sums, times the gain.
 template <typename T>
 __global__ void __launch_bounds__(256) fold_kernel(const float* sums, int splits, int64_t n, int d, const float* top,
-                                                   float scale, int more, T* out, int64_t stride) {
+                                                   float scale, float more, T* out, int64_t stride) {
   const int64_t i = (blockIdx.x * int64_t(256) + threadIdx.x) * 8;
   wait_for_previous();
   if (i >= n) return;
@@ -664,6 +663,15 @@ __global__ void __launch_bounds__(256) fold_kernel(const float* sums, int splits
   *reinterpret_cast<uint4*>(out + row * stride + (i - row * d)) = *reinterpret_cast<uint4*>(o);
 }
 
+// x with rows that begin on 128-byte boundaries.
+__global__ void __launch_bounds__(256) align_kernel(const uint16_t* x, int64_t stride, int64_t n, int d, uint16_t* out, int wide) {
+  const int64_t i = (blockIdx.x * int64_t(256) + threadIdx.x) * 8;
+  let_next_begin();
+  if (i >= n) return;
+  const int64_t row = i / d;
+  *reinterpret_cast<uint4*>(out + row * wide + (i - row * d)) = *reinterpret_cast<const uint4*>(x + row * stride + (i - row * d));
+}
+
 // ---------------------------------------------------------------------- host
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
 
@@ -675,6 +683,29 @@ int piece_columns(const LossShape& s) {
   const int64_t most = kPieceBytes / (2 * static_cast<int64_t>(s.T)) / kTile * kTile;
   const int64_t all = static_cast<int64_t>(up_to(s.V, kTile)) * kTile;
   return static_cast<int>(most < kTile ? kTile : most < all ? most : all);
+}
+
+// Rows of 128-byte multiples are read in whole lines. Others straddle two, and where
+// both operands of z do, the copies' requests bound the product (1531 rows, 50021 columns
+// of 1000: 117 us, 79 without copies): x, the smaller one, is then copied into aligned
+// rows first (101 us). That pays from 1e10 to 2e10 operations on (1000 rows, 4000 columns of
+// 1000, 8e9: 29 us against 25; 300 rows, 20000 columns, 1.2e10: 29 against 31).
+bool aligns(const LossShape& s) {
+  return s.d % kStep != 0 && 2. * s.T * s.V * s.d >= 2e10;
+}
+int aligned_width(const LossShape& s) { return up_to(s.d, kStep) * kStep; }
+size_t aligned_bytes(const LossShape& s, int64_t rows) {
+  return aligns(s) ? padded(static_cast<size_t>(rows) * aligned_width(s) * 2) : 0;
+}
+// The view that z's product reads: `x` itself, or its copy at `to`.
+bool aligned_rows(const LossShape& s, maxsim_rows* x, int64_t rows, void* to, cudaStream_t stream, bool* copied) {
+  *copied = aligns(s) && (x->row_stride % kStep != 0 || reinterpret_cast<uintptr_t>(x->data) % 128 != 0);
+  if (!*copied) return true;
+  const int64_t n = rows * s.d;
+  align_kernel<<<static_cast<int>((n / 8 + 255) / 256), 256, 0, stream>>>(
+      static_cast<const uint16_t*>(x->data), x->row_stride, n, s.d, static_cast<uint16_t*>(to), aligned_width(s));
+  *x = {to, aligned_width(s)};
+  return cudaGetLastError() == cudaSuccess;
 }
 
 // How the tiles of dx are cut along the vocabulary, and those of dW along the rows: no
@@ -721,7 +752,7 @@ cudaError_t launch(const Maps& maps, const Params& p, const DeviceInfo& dev, int
 }
 
 struct Space {  // of the backward's workspace
-  size_t dz, sums, dw_sums, bytes;
+  size_t x, dz, sums, dw_sums, bytes;
   int columns, splits, dw_splits;
   bool wide;  // dx goes through fp32 sums
 };
@@ -731,7 +762,8 @@ Space plan(const LossShape& s, int pairs) {
   const int first = w.columns < s.V ? w.columns : static_cast<int>(s.V);
   split_counts(s, first, pairs, &w.splits, &w.dw_splits);
   w.wide = w.splits > 1 || w.columns < s.V;
-  w.dz = 256;  // after the largest |dloss|
+  w.x = 256;  // after the largest |dloss|
+  w.dz = w.x + aligned_bytes(s, s.T);
   w.sums = w.dz + padded(static_cast<size_t>(s.T) * w.columns * 2);
   w.dw_sums = w.sums + (w.wide ? padded(static_cast<size_t>(w.splits) * s.T * s.d * 4) : 0);
   w.bytes = w.dw_sums + (w.dw_splits > 1 ? padded(static_cast<size_t>(w.dw_splits) * first * s.d * 4) : 0);
@@ -739,7 +771,7 @@ Space plan(const LossShape& s, int pairs) {
 }
 
 template <typename T>
-cudaError_t fold(const float* sums, int splits, int64_t rows, const LossShape& s, const float* top, int more, void* out,
+cudaError_t fold(const float* sums, int splits, int64_t rows, const LossShape& s, const float* top, float more, void* out,
                  int64_t stride, cudaStream_t stream) {
   const int64_t n = rows * s.d;
   return launch_after(fold_kernel<T>, static_cast<int>((n / 8 + 255) / 256), 256, 0, stream, sums, splits, n, s.d, top,
@@ -756,7 +788,7 @@ static int stats_rows(const LossShape& s) {
 
 size_t loss_workspace_bytes(const LossShape& s) {
   const size_t rows = stats_rows(s);
-  return padded(rows * 4) + up_to(s.V, kHalf) * rows * sizeof(float2);
+  return aligned_bytes(s, rows) + padded(rows * 4) + up_to(s.V, kHalf) * rows * sizeof(float2);
 }
 
 maxsim_status launch_loss(const LossShape& s, const maxsim_rows& x, const maxsim_rows& w, const int64_t* targets,
@@ -770,17 +802,20 @@ maxsim_status launch_loss(const LossShape& s, const maxsim_rows& x, const maxsim
   p.s = s;
   p.columns = static_cast<int>(s.V);
   p.tiles_n = up_to(s.V, kTile);
-  p.hit = static_cast<float*>(workspace);
-  p.parts = reinterpret_cast<float2*>(static_cast<char*>(workspace) + padded(static_cast<size_t>(step) * 4));
+  p.hit = reinterpret_cast<float*>(static_cast<char*>(workspace) + aligned_bytes(s, step));
+  p.parts = reinterpret_cast<float2*>(reinterpret_cast<char*>(p.hit) + padded(static_cast<size_t>(step) * 4));
   p.z2 = s.scale * kLog2e;
   p.status = dev->status;
   for (int64_t row = 0; row < s.T; row += step) {
     p.s.T = s.T - row < step ? static_cast<int>(s.T - row) : step;
     p.tiles_m = up_to(p.s.T, kTile);
     p.targets = targets + row;
-    if (!map_in(&maps.a, s, static_cast<const char*>(x.data) + row * x.row_stride * 2, x.row_stride, s.d, p.s.T, kHalf))
+    maxsim_rows from = {static_cast<char*>(x.data) + row * x.row_stride * 2, x.row_stride};
+    bool copied;
+    if (!aligned_rows(s, &from, p.s.T, workspace, stream, &copied) ||
+        !map_in(&maps.a, s, from.data, from.row_stride, s.d, p.s.T, kHalf))
       return MAXSIM_ERR_CUDA;
-    if (launch<kStats>(maps, p, *dev, static_cast<int64_t>(p.tiles_m) * p.tiles_n, row > 0, stream) != cudaSuccess ||
+    if (launch<kStats>(maps, p, *dev, static_cast<int64_t>(p.tiles_m) * p.tiles_n, copied || row > 0, stream) != cudaSuccess ||
         launch_after(join_kernel, up_to(p.s.T, 32), 1024, 0, stream, p.parts, up_to(s.V, kHalf), p.s.T, s.V, p.targets,
                      p.hit, s.scale, loss + row, lse + row, dev->status) != cudaSuccess)
       return MAXSIM_ERR_CUDA;
@@ -802,16 +837,19 @@ maxsim_status launch_loss_bwd(const LossShape& s, const float* dloss, const maxs
   char* base = static_cast<char*>(workspace);
   float* top = reinterpret_cast<float*>(base);
   float* sums = reinterpret_cast<float*>(base + at.sums);
-  const int more = s.is_bf16 ? 0 : 14;
+  const float more = s.is_bf16 ? 1.f : 16384.f;
   const bool scan = s.T <= kScanRows;
   if (!scan) {
     top_kernel<<<1, 1024, 0, stream>>>(dloss, targets, s.T, s.V, top, dev->status);
     if (cudaGetLastError() != cudaSuccess) return MAXSIM_ERR_CUDA;
   }
+  maxsim_rows from = x;
+  bool copied;
+  if (!aligned_rows(s, &from, s.T, base + at.x, stream, &copied)) return MAXSIM_ERR_CUDA;
   for (int64_t first = 0; first < s.V; first += at.columns) {
     const int columns = s.V - first < at.columns ? static_cast<int>(s.V - first) : at.columns;
     alignas(64) Maps maps = {};
-    if (!map_in(&maps.a, s, x.data, x.row_stride, s.d, s.T, kHalf) ||
+    if (!map_in(&maps.a, s, from.data, from.row_stride, s.d, s.T, kHalf) ||
         !map_in(&maps.b, s, w.data, w.row_stride, s.d, s.V, kHalf) ||
         !map_out(&maps.out0, s.is_bf16 ? 1 : 0, 2, base + at.dz, at.columns, columns, s.T, 1))
       return MAXSIM_ERR_CUDA;
@@ -829,12 +867,12 @@ maxsim_status launch_loss_bwd(const LossShape& s, const float* dloss, const maxs
     p.more = more;
     p.z2 = s.scale * kLog2e;
     p.status = dev->status;
-    if (launch<kGrad>(maps, p, *dev, static_cast<int64_t>(p.tiles_m) * p.tiles_n, first > 0 || !scan, stream) != cudaSuccess)
+    if (launch<kGrad>(maps, p, *dev, static_cast<int64_t>(p.tiles_m) * p.tiles_n, copied || first > 0 || !scan, stream) != cudaSuccess)
       return MAXSIM_ERR_CUDA;
     if (!map_in(&maps.a, s, base + at.dz, at.columns, columns, s.T, kHalf) ||
         !map_in(&maps.b, s, w.data, w.row_stride, s.d, s.V, kBox) ||
         !map_in(&maps.a2, s, base + at.dz, at.columns, columns, s.T, kBox) ||
-        !map_in(&maps.b2, s, x.data, x.row_stride, s.d, s.T, kBox))
+        !map_in(&maps.b2, s, from.data, from.row_stride, s.d, s.T, kBox))
       return MAXSIM_ERR_CUDA;
     p.splits = at.splits;
     p.dw_splits = at.dw_splits;

@@ -92,7 +92,7 @@ def cross_entropy(x, w, targets, scale=1.0, dloss=None):
     target's logit, on top of 2^-17 for exponentials, sums and logarithm, and of
     the rounding of numbers of lse's size (2^-22 of it). A weight exp(z - lse) is
     then off by twice that, relatively. dz is rounded to the type (u; in fp16 its
-    smallest step is 2^-25 in units of 2^-15 of the largest dloss), sums of n
+    smallest step is 2^-25 in units of 2^-14 of the largest dloss), sums of n
     products by n 2^-23, results once more (u)."""
     u, tiny = U[x.dtype], TINY[x.dtype]
     T, d = x.shape

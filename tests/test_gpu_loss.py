@@ -64,7 +64,7 @@ def test_scales(scale):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("factor", [1e-12, 1.0, 1e12])
 def test_small_and_large_gradients_keep_their_bits(dtype, factor):
-    """dz is held times a power of two: what a row gets does not depend on the sizes
+    """dz is held divided by the largest dloss: what a row gets does not depend on the sizes
     of all (results beyond the type's range excepted)."""
     x, w, t, dloss = _inputs(90, 800, 64, torch.bfloat16 if dtype == torch.bfloat16 else dtype)
     if dtype == torch.float16:
@@ -131,6 +131,21 @@ def test_more_than_31_bits_of_elements():
         if cols.start:  # the other columns' weights are 0
             ref.within(dx, dz @ w[cols].double(), E @ w[cols].double().abs() + 2.0 ** -8 * (dz @ w[cols].double()).abs()
                        + 2.0 ** -15 * (dz.abs() @ w[cols].double().abs()))
+
+
+def test_rows_off_line_boundaries():
+    """Rows of 2000 bytes are copied into aligned ones where products are long; the
+    same rows 2048 bytes apart, or from a wider buffer, give the same numbers."""
+    T, V, d = 700, 20001, 1000
+    x, w, t, dloss = _inputs(T, V, d, torch.bfloat16)
+    want = _check(x, w, t, dloss)
+    for wide, first in ((1024, 0), (1016, 8), (1024, 16)):
+        y = torch.full((T, wide), float("nan"), dtype=torch.bfloat16, device=DEV)
+        y[:, first:first + d] = x
+        y = y[:, first:first + d]
+        loss, lse = m.encoder_cross_entropy(y, w, t)
+        got = (loss, lse) + m.encoder_cross_entropy_backward(dloss, y, w, t, lse)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_many_columns_for_one_row():
