@@ -3,8 +3,11 @@
 //
 //   out = residual + (lot >= limit ? x * factor : 0)
 //
-// The mask is never stored: rows.cuh makes an element's lot from its place. Bound by
-// HBM where a thread's ten rounds of integer products hide behind its loads.
+// The mask is never stored: rows.cuh makes an element's lot from its place, ten rounds
+// of integer products for eight elements, which hide behind their loads (issue slots 58 %
+// busy). Bound by HBM with a residual: 98304 x 2048 bf16 185 us (6.5 TB/s), without one 152
+// (5.3, instructions and loads alike). Rows that are not whole: 20011 x 1001 fp32 31 us (5.1
+// TB/s), 200011 x 1001 bf16 250 (3.2), 2 bytes an access.
 #include "rows.cuh"
 
 namespace msim {

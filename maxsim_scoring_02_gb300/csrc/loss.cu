@@ -19,7 +19,10 @@
 // there): small gradients keep their bits, and where all rows weigh the same, which is
 // usual, the -1 at the target is exact (scaled by powers of two alone it was off by up
 // to 2^-9 in the same direction in every row).
-// Bound by the tensor cores (and by the power limit in long runs).
+// Bound by the tensor cores (and by the power limit in long runs): 8192 rows, 65536
+// columns of 2048 bf16: forward 1.04 ms (2.1 PFLOP/s), backward 3.4 (1.9); tensor pipe active
+// 87 % (kStats), 83 % (kGrad), 90 % (kSums). Few rows: 32, 30011 columns of 768 18 us on
+// the GPU, of which 7 are W's bytes and 8 what two kernels take for nothing.
 #include <cmath>
 
 #include "after.cuh"
@@ -46,7 +49,7 @@ constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiWarps * kStageOut 
 // 1e-6 of itself in one direction. kStats adds no more than this many steps there and
 // the parts in registers, with rounding: a quarter of that, and no more time.
 constexpr int kPartSteps = 8;
-constexpr int kGroupM = 32;                    // row tiles that share a pass over the vocabulary
+constexpr int kGroupM = 32;  // row tiles that share a pass over the vocabulary (4096 x 19456 x 2048: 32 165 us, 16 163, 8 166, 4 173)
 
 constexpr uint32_t kIdescAMnMajor = 1u << 15;  // flag of the instruction descriptor: A has its M dimension contiguous
 
