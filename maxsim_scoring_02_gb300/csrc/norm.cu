@@ -25,11 +25,14 @@ constexpr float kLeast = 1e-30f;
 template <typename T, int kTeam, int kGroups, bool kWhole>
 struct Shape {
   static constexpr int kBlock = kTeam > 32 ? kTeam : 256, kRows = kBlock / kTeam;
-  using Rows = Queue<T, kBlock, kGroups, 2, 75000, kWhole>;
+  using Rows = Queue<T, kBlock, kGroups, 2, sizeof(T) == 4 ? 0 : 75000, kWhole>;
   // Blocks of an SM that the registers have to allow; rows of a team, where a row takes a
-  // warp or more: blocks that come and go even out what SMs do, fixed ones (a million rows of
-  // 128: 66 us, 75 with 32 rows a team) wait for the slowest (98304 x 2048: 262 us, 235).
-  static constexpr int kFit = kTeam > 256 ? 1 : kTeam > 32 ? 1024 / kTeam : 2, kRounds = 8;
+  // warp or more, or of fp32: blocks that come and go even out what SMs do, fixed ones (a
+  // million rows of 128 to e4m3: 66 us, 75 with 32 rows a team) wait for the slowest (98304 x
+  // 2048: 262 us, 235). fp32: 512 threads 244 us for 50000 x 2048, 1024 259.
+  static constexpr int kFit = kTeam > 256 ? 1 : sizeof(T) == 4 ? 512 / kBlock : kTeam > 32 ? 1024 / kTeam : 2;
+  static constexpr int kRounds = 8;
+  static constexpr bool kComeAndGo = kTeam > 16 || sizeof(T) == 4;
 };
 
 template <typename T, int kTeam, int kGroups, bool kWhole, bool k8>
@@ -191,7 +194,7 @@ cudaError_t go(const NormParams& p, const DeviceInfo& dev, cudaStream_t stream) 
     if (e != cudaSuccess) return e;
     const int64_t need = (static_cast<int64_t>(p.T) + S::kRows - 1) / S::kRows;
     int64_t most = static_cast<int64_t>(dev.sm_count) * fit;
-    if (kTeam > 16 && need / S::kRounds > most) most = need / S::kRounds;
+    if (S::kComeAndGo && need / S::kRounds > most) most = need / S::kRounds;
     kernel<<<static_cast<int>(need < most ? need : most), S::kBlock, S::Rows::kBytes, stream>>>(p);
     return cudaGetLastError();
   };

@@ -94,9 +94,12 @@ __device__ __forceinline__ Eight load_weights(const NormParams& p, const Cols<kW
 // they come (one stage).
 // kDeep: bytes of a block up to which there are three stages. Forward 75000 (a million
 // rows of 128 to e4m3: three 67 us, two 117); backward 40000, beyond which more blocks are
-// worth more (30011 x 4096: two stages 178 us, three 195; others alike).
+// worth more (30011 x 4096: two stages 178 us, three 195; others alike). 0, fp32: none. A
+// thread then has as much in flight in registers, and copies of 16 of every 32 bytes are
+// worse than loads, whose other half L1 has (50000 x 2048 forward 244 us, with stages 330;
+// backward 248 and 413).
 __host__ __device__ constexpr int queue_stages(int row_bytes, int deep, bool whole) {
-  return !whole || 2 * row_bytes > 200000 ? 1 : 3 * row_bytes <= deep ? 3 : 2;
+  return !whole || deep == 0 || 2 * row_bytes > 200000 ? 1 : 3 * row_bytes <= deep ? 3 : 2;
 }
 template <typename T, int kBlock, int kGroups, int kStreams, int kDeep, bool kWhole>
 struct Queue {

@@ -23,7 +23,7 @@ constexpr int kMaxBlocks = 1280;  // partial sums; each block has its rows from 
 template <typename T, int kTeam, int kGroups, bool kWhole>
 struct Shape {
   static constexpr int kBlock = kTeam > 32 ? kTeam : 256, kTeams = kBlock / kTeam;
-  using Rows = Queue<T, kBlock, kGroups, 3, 40000, kWhole>;
+  using Rows = Queue<T, kBlock, kGroups, 3, sizeof(T) == 4 ? 0 : 40000, kWhole>;
   // blocks of an SM that the registers have to allow (24576 x 2048: 512 threads 99 us, 768 103)
   static constexpr int kFit = kTeam > 256 ? 1 : 512 / kBlock;
 };
