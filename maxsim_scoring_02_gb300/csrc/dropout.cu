@@ -5,20 +5,24 @@
 //
 // The mask is never stored: rows.cuh makes an element's lot from its place, ten rounds
 // of integer products for eight elements, which hide behind their loads (issue slots 58 %
-// busy). Bound by HBM with a residual: 98304 x 2048 bf16 185 us (6.5 TB/s), without one 152
-// (5.3, instructions and loads alike). Rows that are not whole: 20011 x 1001 fp32 31 us (5.1
-// TB/s), 200011 x 1001 bf16 250 (3.2), 2 bytes an access.
+// busy). Bound by HBM with a residual: 98304 x 2048 bf16 179 us (6.8 TB/s), without one 138
+// (5.8, instructions and loads alike). Rows that are not whole: 20011 x 1001 fp32 31 us (5.1
+// TB/s), 200011 x 1001 bf16 255 (3.1), 2 bytes an access.
 #include "rows.cuh"
 
 namespace msim {
 namespace {
 
 constexpr int kThreads = 256;
-// Groups of eight columns of a thread (98304 x 2048 bf16 with a residual: three 187 us,
-// two 189, four 194; 20011 x 1001 fp32, rows not whole: one 31 us, two 32).
-template <bool kWhole>
-constexpr int kUnits = kWhole ? 3 : 1;
-
+// Groups of eight columns of a thread, and blocks of an SM that the registers have to
+// allow. 98304 x 2048 bf16 with a residual, and without: four and four 179 and 138 us,
+// three with as many registers as asked for 187 and 150, six 186 and 142. 50000 x 2048
+// fp32: three 173 and 133, four and four 231 and 169. Rows that are not whole, 200011 x 1001
+// bf16: one 255, two 310.
+template <typename T, bool kWhole>
+constexpr int kUnits = !kWhole ? 1 : sizeof(T) == 4 ? 3 : 4;
+template <typename T, bool kWhole>
+constexpr int kFit = kWhole && sizeof(T) == 4 ? 1 : 4;
 
 struct DropoutParams {
   const void *x, *res;
@@ -31,12 +35,12 @@ struct DropoutParams {
 };
 
 template <typename T, bool kWhole>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p) {
+__global__ void __launch_bounds__(kThreads, kFit<T, kWhole>) dropout_kernel(const DropoutParams p) {
   const Key key = load_key(p.drop);
   const int lane = threadIdx.x & 31;
   // a warp's lanes share a run of 256 columns where rows are not whole
   const uint32_t per = kWhole ? kThreads : kThreads / 32, mine = kWhole ? threadIdx.x : threadIdx.x >> 5;
-  constexpr int N = kUnits<kWhole>;
+  constexpr int N = kUnits<T, kWhole>;
   // whole groups stay packed until their turn
   std::conditional_t<kWhole, Raw<T>, Eight> x[N], r[N];
   uint32_t row[N], part[N];
@@ -86,7 +90,7 @@ maxsim_status run(DropoutParams p, int T_, bool whole, cudaStream_t stream) {
     const int rows = T_ - row0 < most ? static_cast<int>(T_ - row0) : most;
     p.row0 = static_cast<int>(row0);
     p.count = static_cast<uint32_t>(rows) * parts;
-    const uint32_t each = per * (whole ? kUnits<true> : kUnits<false>);
+    const uint32_t each = per * (whole ? kUnits<T, true> : kUnits<T, false>);
     const int grid = static_cast<int>((p.count + each - 1) / each);
     if (whole) dropout_kernel<T, true><<<grid, kThreads, 0, stream>>>(p);
     else dropout_kernel<T, false><<<grid, kThreads, 0, stream>>>(p);
