@@ -121,15 +121,14 @@ __device__ __forceinline__ bool tile_of(const Params& p, int i, Tile& t) {
   t.split = 0;
   t.k0 = 0;
   if constexpr (kMode != kSums) {
-    const int64_t at = static_cast<int64_t>(i) * pairs + pair;
-    if (at >= static_cast<int64_t>(p.tiles_m) * p.tiles_n) return false;
-    const int64_t per = static_cast<int64_t>(kGroupM) * p.tiles_n;
-    const int group = static_cast<int>(at / per), in = static_cast<int>(at - group * per);
-    const int rows = min(kGroupM, p.tiles_m - group * kGroupM);
-    const int n = in / rows;
+    // 256 MB of parts or of dz are 2^16 tiles at the most, or as many as there are rows
+    const uint32_t at = static_cast<uint32_t>(i) * pairs + pair, tiles_n = p.tiles_n;
+    if (at >= static_cast<uint32_t>(p.tiles_m) * tiles_n) return false;
+    const uint32_t per = kGroupM * tiles_n, group = at / per, in = at - group * per;
+    const uint32_t rows = min(static_cast<uint32_t>(kGroupM), p.tiles_m - group * kGroupM), n = in / rows;
     t.kind = 0;
-    t.m0 = (group * kGroupM + in - n * rows) * kTile;
-    t.n0 = n * kTile;  // within the piece
+    t.m0 = static_cast<int>(group * kGroupM + in - n * rows) * kTile;
+    t.n0 = static_cast<int>(n) * kTile;  // within the piece
     t.n = width(p.columns - t.n0);
     t.steps = (p.s.d + kStep - 1) / kStep;
     return true;
@@ -390,24 +389,34 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
     whole = usable(top);
   }
   if constexpr (kMode == kSums) gain = gain_of(p.top, p.s.scale, p.more);  // for what is not summed on
-  for (int i = 0; tile_of<kMode>(p, i, t); ++i) {
-    if (t.steps == 0) continue;
+  // what a tile's rows need is asked for while the tile before is worked on
+  int64_t to_next = -1;
+  float lse_next = 0.f, dloss_next = 0.f;
+  const auto ask = [&](const Tile& u) {
+    const int row = u.m0 + static_cast<int>(rank) * kHalf + quarter * 32 + lane;
+    if (kMode == kSums || row >= p.s.T) return;
+    to_next = p.targets[row];
+    if constexpr (kMode == kGrad) lse_next = p.lse[row], dloss_next = p.dloss[row];
+  };
+  Tile next;
+  bool another = tile_of<kMode>(p, 0, next);
+  if (another) ask(next);
+  for (int i = 0; another; ++i) {
+    t = next;
     const int row0 = t.m0 + static_cast<int>(rank) * kHalf + quarter * 32, row = row0 + lane;
     const int col0 = half * kHalf;  // within the tile
     const int chunks = min(4, max(0, (t.n - col0 + 31) / 32));
-    // what the row needs, asked for before the wait
     int target = -1;
     float lse2 = 0.f, coef = 0.f;
-    if constexpr (kMode != kSums) {
-      if (row < p.s.T) {
-        const int64_t to = p.targets[row], g = to - p.first - t.n0 - col0;
-        target = g >= 0 && g < kHalf ? static_cast<int>(g) : -1;
-        if constexpr (kMode == kGrad) {
-          lse2 = p.lse[row] * kLog2e;
-          coef = to >= 0 && to < p.s.V ? p.dloss[row] / whole * p.more : 0.f;
-        }
-      }
+    if (kMode != kSums && row < p.s.T) {
+      const int64_t g = to_next - p.first - t.n0 - col0;
+      target = g >= 0 && g < kHalf ? static_cast<int>(g) : -1;
+      lse2 = lse_next * kLog2e;
+      coef = to_next >= 0 && to_next < p.s.V ? dloss_next / whole * p.more : 0.f;
     }
+    another = tile_of<kMode>(p, i + 1, next);
+    if (another) ask(next);
+    if (t.steps == 0) continue;
     uint32_t v[4][32];
     bool ok = true;
     for (int k = 0; k < t.steps; k += kMode == kStats ? kPartSteps : t.steps) {
@@ -445,24 +454,35 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
     if (!ok) break;
     if constexpr (kMode == kStats) {
       const int valid = p.columns - t.n0 - col0;  // of this warp's columns
-      float top = -INFINITY;
+      float tops[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
+        tops[c] = -INFINITY;
         if (c >= chunks) continue;
         if (c * 32 + 32 > valid)
 #pragma unroll
           for (int x = 0; x < 32; ++x)
             if (c * 32 + x >= valid) v[c][x] = __float_as_uint(-INFINITY);
+        float other = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < 32; x += 2) top = max3(top, __uint_as_float(v[c][x]), __uint_as_float(v[c][x + 1]));
+        for (int x = 0; x < 32; x += 4) {
+          tops[c] = max3(tops[c], __uint_as_float(v[c][x]), __uint_as_float(v[c][x + 1]));
+          other = max3(other, __uint_as_float(v[c][x + 2]), __uint_as_float(v[c][x + 3]));
+        }
+        tops[c] = fmaxf(tops[c], other);
       }
-      const float m2 = top * p.z2;
-      float sum[4] = {};
+      const float m2 = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * p.z2;
+      const Pair z2(p.z2, p.z2), less(-m2, -m2);
+      Pair sums[2] = {Pair(0.f, 0.f), Pair(0.f, 0.f)};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         if (c >= chunks) continue;
 #pragma unroll
-        for (int x = 0; x < 32; ++x) sum[x & 3] += fast_exp2(fmaf(__uint_as_float(v[c][x]), p.z2, -m2));
+        for (int x = 0; x < 32; x += 2) {
+          float e, f;
+          fma2(Pair(__uint_as_float(v[c][x]), __uint_as_float(v[c][x + 1])), z2, less).get(e, f);
+          sums[x / 2 & 1] = add2(sums[x / 2 & 1], Pair(fast_exp2(e), fast_exp2(f)));
+        }
         if (__any_sync(0xffffffffu, (target >> 5) == c)) {
           float z = 0.f;
 #pragma unroll
@@ -471,10 +491,13 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
           if ((target >> 5) == c) p.hit[row] = z;
         }
       }
-      if (row < p.s.T && valid > 0)
-        p.parts[static_cast<int64_t>((t.n0 + col0) / kHalf) * p.s.T + row] =
-            make_float2(m2, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+      if (row < p.s.T && valid > 0) {
+        float e, f;
+        add2(sums[0], sums[1]).get(e, f);
+        p.parts[static_cast<int64_t>((t.n0 + col0) / kHalf) * p.s.T + row] = make_float2(m2, e + f);
+      }
     } else if constexpr (kMode == kGrad) {
+      const Pair z2(p.z2, p.z2), less(-lse2, -lse2), factor(coef, coef);
 #pragma unroll
       for (int c = 0; c < 4; c += 2) {
         if (c >= chunks) continue;
@@ -482,11 +505,8 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
 #pragma unroll
         for (int x = 0; x < 64; x += 2) {
           float e[2];
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float q = fast_exp2(fmaf(__uint_as_float(v[c + (x + y) / 32][(x + y) % 32]), p.z2, -lse2));
-            e[y] = q * coef;
-          }
+          fma2(Pair(__uint_as_float(v[c + x / 32][x % 32]), __uint_as_float(v[c + x / 32][x % 32 + 1])), z2, less).get(e[0], e[1]);
+          mul2(Pair(fast_exp2(e[0]), fast_exp2(e[1])), factor).get(e[0], e[1]);
           w[x / 2] = pack2<kBf16>(e[0], e[1]);
         }
         if (__any_sync(0xffffffffu, (target >> 6) == c / 2)) {
@@ -676,7 +696,10 @@ __global__ void __launch_bounds__(256) align_kernel(const uint16_t* x, int64_t s
 }
 
 // ---------------------------------------------------------------------- host
-constexpr int64_t kPieceBytes = int64_t(256) << 20;
+#ifndef PB
+#define PB 256
+#endif
+constexpr int64_t kPieceBytes = int64_t(PB) << 20;
 
 int up_to(int64_t v, int to) { return static_cast<int>((v + to - 1) / to); }
 size_t padded(size_t bytes) { return (bytes + 255) & ~size_t(255); }
