@@ -24,6 +24,7 @@
 // 87 % (kStats), 83 % (kGrad), 90 % (kSums). Few rows: 32, 30011 columns of 768 18 us on
 // the GPU, of which 7 are W's bytes and 8 what two kernels take for nothing.
 #include <cmath>
+#include <type_traits>
 
 #include "after.cuh"
 #include "attn_common.cuh"
@@ -452,78 +453,94 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
       if (++a == kAcc) a = 0, aph ^= 1u;
     }
     if (!ok) break;
+    // Most tiles are whole and hold no row's target: code of their own, without a question
+    // for each 32 columns, across which the compiler would move nothing (8192 rows, 65536
+    // columns of 64, where the epilogue is what bounds the forward: 219 -> 175 us).
+    const int valid = kMode == kSums ? 0 : p.columns - t.n0 - col0;  // of this warp's columns
+    const bool full = __all_sync(0xffffffffu, valid >= kHalf), hits = __any_sync(0xffffffffu, target >= 0);
     if constexpr (kMode == kStats) {
-      const int valid = p.columns - t.n0 - col0;  // of this warp's columns
-      float tops[4];
+      const auto statistics = [&](auto is_full) {
+        constexpr bool kFull = decltype(is_full)::value;
+        float tops[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        tops[c] = -INFINITY;
-        if (c >= chunks) continue;
-        if (c * 32 + 32 > valid)
+        for (int c = 0; c < 4; ++c) {
+          tops[c] = -INFINITY;
+          if (!kFull && c >= chunks) continue;
+          if (!kFull)
 #pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (c * 32 + x >= valid) v[c][x] = __float_as_uint(-INFINITY);
-        float other = -INFINITY;
+            for (int x = 0; x < 32; ++x)
+              if (c * 32 + x >= valid) v[c][x] = __float_as_uint(-INFINITY);
+          float other = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < 32; x += 4) {
-          tops[c] = max3(tops[c], __uint_as_float(v[c][x]), __uint_as_float(v[c][x + 1]));
-          other = max3(other, __uint_as_float(v[c][x + 2]), __uint_as_float(v[c][x + 3]));
+          for (int x = 0; x < 32; x += 4) {
+            tops[c] = max3(tops[c], __uint_as_float(v[c][x]), __uint_as_float(v[c][x + 1]));
+            other = max3(other, __uint_as_float(v[c][x + 2]), __uint_as_float(v[c][x + 3]));
+          }
+          tops[c] = fmaxf(tops[c], other);
         }
-        tops[c] = fmaxf(tops[c], other);
-      }
-      const float m2 = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * p.z2;
-      const Pair z2(p.z2, p.z2), less(-m2, -m2);
-      Pair sums[2] = {Pair(0.f, 0.f), Pair(0.f, 0.f)};
+        const float m2 = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * p.z2;
+        const Pair z2(p.z2, p.z2), less(-m2, -m2);
+        Pair sums[2] = {Pair(0.f, 0.f), Pair(0.f, 0.f)};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c >= chunks) continue;
+        for (int c = 0; c < 4; ++c) {
+          if (!kFull && c >= chunks) continue;
 #pragma unroll
-        for (int x = 0; x < 32; x += 2) {
+          for (int x = 0; x < 32; x += 2) {
+            float e, f;
+            fma2(Pair(__uint_as_float(v[c][x]), __uint_as_float(v[c][x + 1])), z2, less).get(e, f);
+            sums[x / 2 & 1] = add2(sums[x / 2 & 1], Pair(fast_exp2(e), fast_exp2(f)));
+          }
+        }
+        if (row < p.s.T && valid > 0) {
           float e, f;
-          fma2(Pair(__uint_as_float(v[c][x]), __uint_as_float(v[c][x + 1])), z2, less).get(e, f);
-          sums[x / 2 & 1] = add2(sums[x / 2 & 1], Pair(fast_exp2(e), fast_exp2(f)));
+          add2(sums[0], sums[1]).get(e, f);
+          p.parts[static_cast<int64_t>((t.n0 + col0) / kHalf) * p.s.T + row] = make_float2(m2, e + f);
         }
-        if (__any_sync(0xffffffffu, (target >> 5) == c)) {
-          float z = 0.f;
+      };
+      if (hits) {
+        float z = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int x = 0; x < 32; ++x)
             if (target == c * 32 + x) z = __uint_as_float(v[c][x]);
-          if ((target >> 5) == c) p.hit[row] = z;
-        }
+        if (target >= 0) p.hit[row] = z;
       }
-      if (row < p.s.T && valid > 0) {
-        float e, f;
-        add2(sums[0], sums[1]).get(e, f);
-        p.parts[static_cast<int64_t>((t.n0 + col0) / kHalf) * p.s.T + row] = make_float2(m2, e + f);
-      }
+      if (full) statistics(std::true_type());
+      else statistics(std::false_type());
     } else if constexpr (kMode == kGrad) {
       const Pair z2(p.z2, p.z2), less(-lse2, -lse2), factor(coef, coef);
+      const auto gradients = [&](auto is_full) {
+        constexpr bool kFull = decltype(is_full)::value;
 #pragma unroll
-      for (int c = 0; c < 4; c += 2) {
-        if (c >= chunks) continue;
-        uint32_t w[32];
+        for (int c = 0; c < 4; c += 2) {
+          if (!kFull && c >= chunks) continue;
+          uint32_t w[32];
 #pragma unroll
-        for (int x = 0; x < 64; x += 2) {
-          float e[2];
-          fma2(Pair(__uint_as_float(v[c + x / 32][x % 32]), __uint_as_float(v[c + x / 32][x % 32 + 1])), z2, less).get(e[0], e[1]);
-          mul2(Pair(fast_exp2(e[0]), fast_exp2(e[1])), factor).get(e[0], e[1]);
-          w[x / 2] = pack2<kBf16>(e[0], e[1]);
+          for (int x = 0; x < 64; x += 2) {
+            float e[2];
+            fma2(Pair(__uint_as_float(v[c + x / 32][x % 32]), __uint_as_float(v[c + x / 32][x % 32 + 1])), z2, less).get(e[0], e[1]);
+            mul2(Pair(fast_exp2(e[0]), fast_exp2(e[1])), factor).get(e[0], e[1]);
+            w[x / 2] = pack2<kBf16>(e[0], e[1]);
+          }
+          if (hits) {
+#pragma unroll
+            for (int x = 0; x < 64; ++x)
+              if (target == c * 32 + x) {
+                const float q = fast_exp2(fmaf(__uint_as_float(v[c + x / 32][x % 32]), p.z2, -lse2));
+                const uint32_t one = pack2<kBf16>((q - 1.f) * coef, 0.f) & 0xFFFFu;
+                w[x / 2] = x & 1 ? (w[x / 2] & 0xFFFFu) | one << 16 : (w[x / 2] & 0xFFFF0000u) | one;
+              }
+          }
+          if (lane == 0) store_wait_read();
+          __syncwarp();
+          put_row(stage, lane, w);
+          if (row0 < p.s.T && (kFull || t.n0 + col0 + c * 32 < p.columns))
+            send(&maps.out0, stage, lane, t.n0 + col0 + c * 32, row0, 0, false);
         }
-        if (__any_sync(0xffffffffu, (target >> 6) == c / 2)) {
-#pragma unroll
-          for (int x = 0; x < 64; ++x)
-            if (target == c * 32 + x) {
-              const float q = fast_exp2(fmaf(__uint_as_float(v[c + x / 32][x % 32]), p.z2, -lse2));
-              const uint32_t one = pack2<kBf16>((q - 1.f) * coef, 0.f) & 0xFFFFu;
-              w[x / 2] = x & 1 ? (w[x / 2] & 0xFFFFu) | one << 16 : (w[x / 2] & 0xFFFF0000u) | one;
-            }
-        }
-        if (lane == 0) store_wait_read();
-        __syncwarp();
-        put_row(stage, lane, w);
-        if (row0 < p.s.T && t.n0 + col0 + c * 32 < p.columns)
-          send(&maps.out0, stage, lane, t.n0 + col0 + c * 32, row0, 0, false);
-      }
+      };
+      if (full) gradients(std::true_type());
+      else gradients(std::false_type());
     } else {
       const bool dx = t.kind == 1;
       const int rows = dx ? p.s.T : p.columns;
