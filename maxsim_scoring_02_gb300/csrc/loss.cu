@@ -347,16 +347,18 @@ __device__ __forceinline__ void send(const CUtensorMap* map, uint32_t stage, int
 }
 
 // The sums of dz's products are multiplied by this at the end.
-__device__ __forceinline__ float usable(float top) { return top > 0.f && top < INFINITY ? top : 1.f; }
+__device__ __forceinline__ float usable(float top) { return top > 0.f ? top : 1.f; }
 __device__ __forceinline__ float gain_of(const float* top, float scale, float more) { return usable(*top) / more * scale; }
-// The largest |dloss| of rows with a target, found by n threads; bad targets are reported.
+// The largest finite |dloss| of rows with a target, found by n threads (a row whose own is
+// not spoils no other one's); bad targets are reported.
 __device__ __forceinline__ float largest(const float* dloss, const int64_t* targets, int T, int64_t V, int thread, int n,
                                          unsigned* status) {
   float top = 0.f;
   for (int i = thread; i < T; i += n) {
     const int64_t t = targets[i];
     if (t >= V) atomicOr(status, kDevErrBadInput);
-    if (t >= 0 && t < V) top = fmaxf(top, fabsf(dloss[i]));
+    const float size = fabsf(dloss[i]);
+    if (t >= 0 && t < V && size < INFINITY) top = fmaxf(top, size);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
@@ -713,10 +715,7 @@ __global__ void __launch_bounds__(256) align_kernel(const uint16_t* x, int64_t s
 }
 
 // ---------------------------------------------------------------------- host
-#ifndef PB
-#define PB 256
-#endif
-constexpr int64_t kPieceBytes = int64_t(PB) << 20;
+constexpr int64_t kPieceBytes = int64_t(256) << 20;
 
 int up_to(int64_t v, int to) { return static_cast<int>((v + to - 1) / to); }
 size_t padded(size_t bytes) { return (bytes + 255) & ~size_t(255); }

@@ -191,6 +191,23 @@ def test_infinities_and_nan():
     assert torch.equal(d2[rows], dx[rows]) and torch.isnan(d2[~rows]).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T", [40, 33000])
+def test_a_gradient_that_is_not_finite(dtype, T):
+    """It spoils its own row of dx alone."""
+    x, w, t, dloss = _inputs(T, 300, 64, dtype, ignored=False)
+    dloss = dloss * 100
+    rows = torch.ones(T, dtype=torch.bool, device=DEV)
+    rows[[3, 9]] = False
+    dloss[~rows] = 0.0
+    _, lse = m.encoder_cross_entropy(x, w, t)
+    dx, _ = m.encoder_cross_entropy_backward(dloss, x, w, t, lse)
+    dloss[3], dloss[9] = float("inf"), float("nan")
+    d2, _ = m.encoder_cross_entropy_backward(dloss, x, w, t, lse)
+    assert torch.equal(d2[rows], dx[rows]) and torch.isfinite(d2[rows]).all()
+    assert torch.isnan(d2[9]).all() and not torch.isfinite(d2[3]).any()
+
+
 def test_large_logits():
     """Logits of thousands: one column has all the weight, exponentials of the others vanish."""
     x, w, t, dloss = _inputs(60, 400, 64, torch.bfloat16, spread=2000.0)
