@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256, Shape<T, kTeam, kGro
       const float top = whole_numbers ? 127.f : 448.f;
       float reach = most * rstd;
       reach = reach < kLeast ? kLeast : reach;  // NaN stays
-      const float factor = __fdividef(top * rstd, reach);
+      const float factor = __fdividef(0.25f * top * rstd, 0.25f * reach);  // whose divisors end at 2^126
       const Pair f2(factor, factor);
       if (t == 0 && live) p.scale[row] = reach / top;
       uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.out_stride;

@@ -188,6 +188,26 @@ def test_extreme_values():
     assert math.isclose(m.encoder_rms_norm(torch.full((1, 64), 3.0, device=DEV), eps=16.0)[0, 0].item(), 3 / 5, rel_tol=1e-6)
 
 
+@pytest.mark.parametrize("fmt,top", [("int8", 127.0), ("e4m3", 448.0)])
+@pytest.mark.parametrize("d", [64, 100, 768, 2048])
+def test_eight_bits_of_large_rows_and_weights(fmt, top, d):
+    """Up to the end of fp32's range; a row whose |h w| is beyond it has no scale, beside usual rows."""
+    x, w = rows(6, d, 1, torch.float32).contiguous(), _weight(d, torch.float32)
+    x[1], x[4] = x[1] * 2.0 ** 120, x[4] * 2.0 ** 64
+    for weight in (w * 2.0 ** 10, w * 2.0 ** 64, w * 2.0 ** 110, w * 2.0 ** 124):
+        q, scale = m.encoder_rms_norm(x, weight, fmt=fmt)
+        y, _ = ref.norm(x, weight, EPS)
+        there = torch.isfinite((x * weight).abs().amax(1))
+        assert there[[0, 2, 3, 5]].all() and not torch.isfinite(scale[~there]).any()
+        q, scale, y = q.float()[there], scale[there], y[there]
+        want = y.abs().amax(1) / top
+        assert ((scale.double() - want).abs() <= 2 * ref.ROW * want).all()
+        v = y / want[:, None]
+        step = 0.5 if fmt == "int8" else (v.abs() * 2.0 ** -4).clamp_min(2.0 ** -10)
+        ref.within(q, v, step + 2.0 ** -20 * v.abs())
+        assert (q.abs().amax(1) == top).all()
+
+
 def test_gradients_against_differences():
     """In fp32, along random directions: the change of <dy, y> + <more, h> for a
     step s is s times the gradient's product, to s^2 and the forward's rounding."""
