@@ -611,7 +611,8 @@ maxsim_status maxsim_dropout(const maxsim_rows *x, const maxsim_rows *residual, 
  *   scale[t] = max(max_j |y[t, j]|, 1e-30) / 127 (INT8) or / 448 (E4M3)
  *   out[t, j] = y[t, j] / scale[t], rounded to nearest, ties to even
  * INT8 rows and their scales are documents or queries of maxsim_score_i8. A row
- * with a y that is not finite gets a scale that is none, too.
+ * with a y that is not finite gets a scale that is none, too, and so does one whose
+ * largest |h[t, j] weight[j]| leaves fp32's range.
  *
  *   x, residual  [T, d] views of dtype; residual may be NULL
  *   sum          [T, d] view that receives h, or NULL; maxsim_rms_norm_backward
@@ -621,7 +622,8 @@ maxsim_status maxsim_dropout(const maxsim_rows *x, const maxsim_rows *residual, 
  *   spec         weight [d] of weight_dtype (FP32 or dtype), or NULL (all 1);
  *                p and rng as in maxsim_dropout (p = 0: no dropout)
  *
- * Overlaps as in maxsim_dropout; sum and out may not be the same. Sums are fp32, and
+ * Overlaps as in maxsim_dropout; sum and out may not be the same, scale overlaps no
+ * view, weight neither of those written. Sums are fp32, and
  * fp64 where squares leave fp32's range. Limits: d <= 16384, T < 2^31 - 256, eps
  * from 2^-60 to 2^60.
  */
@@ -656,7 +658,8 @@ maxsim_status maxsim_rms_norm(const maxsim_norm_spec *spec, const maxsim_rows *x
  *   dsum         the gradient that reaches the sum from elsewhere, or NULL
  *   dx, dresidual  [T, d] views of dtype, each or NULL; either may be dy, h or
  *                dsum (same stride). Without dropout they are the same numbers.
- *   dweight      [d] of weight_dtype, or NULL
+ *   dweight      [d] of weight_dtype, or NULL; neither it nor weight overlaps dx or
+ *                dresidual
  * dweight is added up in an order that depends on T, d and the number of SMs alone,
  * without atomics. workspace: at least maxsim_rms_norm_backward_workspace_size(spec)
  * bytes, 16-byte aligned, where dweight is given. With T = 0 dweight is 0.
@@ -674,7 +677,7 @@ maxsim_status maxsim_rms_norm_backward(const maxsim_norm_spec *spec, const maxsi
  *   loss[t] = lse[t] - z[t, targets[t]], or 0 where targets[t] < 0 (no target)
  * A target >= V counts as none and sets MAXSIM_DEVERR_BAD_INPUT.
  *   x            [T, d] view, weight [V, d] view (dtype BF16 or FP16)
- *   loss, lse    [T] fp32
+ *   loss, lse    [T] fp32; they overlap no input and not one another
  * Products are fp32 sums on the tensor cores, in parts of 512 along d that are added
  * with rounding; statistics are fp32. x and weight must be finite: a row of x that is
  * not makes its own lse and loss NaN, no other row's.
@@ -704,7 +707,8 @@ maxsim_status maxsim_cross_entropy(const maxsim_loss_spec *spec, const maxsim_ro
  *   dz[t, v] = dloss[t] * scale * (exp(z[t, v] - lse[t]) - (v == targets[t]))
  *   dx = dz W [T, d],  dweight = dz^T x [V, d], in the inputs' dtype
  * dx or dweight may be NULL (a frozen side). Rows without a target have gradient 0;
- * x has to be finite there, too (0 * infinity is NaN in dweight).
+ * x has to be finite there, too (0 * infinity is NaN in dweight). A dloss
+ * that is not finite spoils its row of dx and dweight, no other row of dx.
  * The logits are made again, a piece of the vocabulary at a time: the workspace
  * holds one piece's dz in the inputs' type (256 MB, or 256 columns where T is above
  * 524288), divided by the largest |dloss| so that small ones lose no bits, fp32 sums

@@ -49,6 +49,12 @@ bool apart(const View& a, const View& b, bool may_be_same = true) {
   return off >= a.d * a.e && off + b.d * b.e <= step;
 }
 
+// The same for n elements of e bytes in a row: no byte between the view's first and last.
+bool apart(const View& a, const void* p, int64_t n, int e) {
+  const uintptr_t first = reinterpret_cast<uintptr_t>(p);
+  return !a.given() || !p || a.last() <= first || first + n * e <= a.first();
+}
+
 // The chance of being dropped as a limit of 16-bit lots.
 bool drop_of(float p, const int64_t* rng, Drop& drop) {
   drop = {rng, 0, 1.f};
@@ -118,7 +124,12 @@ maxsim_status maxsim_rms_norm(const maxsim_norm_spec* spec, const maxsim_rows* x
     return MAXSIM_ERR_INVALID_ARG;
   if (!apart(vo, vx) || !apart(vo, vr) || !apart(vo, vs, false) || !apart(vs, vx) || !apart(vs, vr))
     return MAXSIM_ERR_INVALID_ARG;
-  if (spec->format != MAXSIM_NORM_SAME && (!scale || !multiple(scale, 4))) return MAXSIM_ERR_INVALID_ARG;
+  if (spec->format == MAXSIM_NORM_SAME) scale = nullptr;
+  else if (!scale || !multiple(scale, 4)) return MAXSIM_ERR_INVALID_ARG;
+  for (const View* v : {&vx, &vr, &vs, &vo})
+    if (!apart(*v, scale, T, 4)) return MAXSIM_ERR_INVALID_ARG;
+  for (const View* v : {&vs, &vo})
+    if (!apart(*v, spec->weight, d, size_of(spec->weight_dtype))) return MAXSIM_ERR_INVALID_ARG;
   NormParams p = {};
   p.x = x->data, p.x_stride = x->row_stride;
   if (residual) p.res = residual->data, p.res_stride = residual->row_stride;
@@ -159,7 +170,8 @@ maxsim_status maxsim_rms_norm_backward(const maxsim_norm_spec* spec, const maxsi
       (dresidual && !vr.writable()))
     return MAXSIM_ERR_INVALID_ARG;
   for (const View* w : {&vx, &vr})
-    if (!apart(*w, vy) || !apart(*w, vh) || !apart(*w, vm)) return MAXSIM_ERR_INVALID_ARG;
+    if (!apart(*w, vy) || !apart(*w, vh) || !apart(*w, vm) || !apart(*w, spec->weight, d, ew) || !apart(*w, dweight, d, ew))
+      return MAXSIM_ERR_INVALID_ARG;
   if (!apart(vx, vr, false)) return MAXSIM_ERR_INVALID_ARG;
   if (dweight && (!workspace || !multiple(workspace, 16) ||
                   workspace_bytes < norm_bwd_workspace_bytes(static_cast<int>(T), d)))
@@ -191,6 +203,12 @@ maxsim_status maxsim_cross_entropy(const maxsim_loss_spec* spec, const maxsim_ro
   if (st != MAXSIM_OK || s.T == 0) return st;
   if (!fits(x, s.T, s.d) || !fits(weight, s.V, s.d) || !loss || !lse || !multiple(loss, 4) || !multiple(lse, 4))
     return MAXSIM_ERR_INVALID_ARG;
+  const View vx{x, s.T, s.d, 2}, vw{weight, s.V, s.d, 2};
+  const maxsim_rows first{loss, 0}, second{lse, 0}, labels{const_cast<int64_t*>(spec->targets), 0};
+  const View vl{&first, 1, s.T, 4}, ve{&second, 1, s.T, 4}, vt{&labels, 1, s.T, 8};
+  for (const View* v : {&vl, &ve})
+    if (!apart(*v, vx, false) || !apart(*v, vw, false) || !apart(*v, vt, false)) return MAXSIM_ERR_INVALID_ARG;
+  if (!apart(vl, ve, false)) return MAXSIM_ERR_INVALID_ARG;
   if (!workspace || !multiple(workspace, 16) || workspace_bytes < loss_workspace_bytes(s)) return MAXSIM_ERR_WORKSPACE;
   return launch_loss(s, *x, *weight, spec->targets, loss, lse, workspace, static_cast<cudaStream_t>(stream));
 }
@@ -220,7 +238,9 @@ maxsim_status maxsim_cross_entropy_backward(const maxsim_loss_spec* spec, const 
   // operands are read by several blocks: a gradient may lie in none of them
   const View vx{x, s.T, s.d, 2}, vw{weight, s.V, s.d, 2}, vdx{dx, s.T, s.d, 2}, vdw{dweight, s.V, s.d, 2};
   for (const View* a : {&vdx, &vdw})
-    if (!apart(*a, vx, false) || !apart(*a, vw, false)) return MAXSIM_ERR_INVALID_ARG;
+    if (!apart(*a, vx, false) || !apart(*a, vw, false) || !apart(*a, dloss, s.T, 4) || !apart(*a, lse, s.T, 4) ||
+        !apart(*a, spec->targets, s.T, 8))
+      return MAXSIM_ERR_INVALID_ARG;
   if (!apart(vdx, vdw, false)) return MAXSIM_ERR_INVALID_ARG;
   if (!workspace || !multiple(workspace, 256) || workspace_bytes < loss_bwd_workspace_bytes(s))
     return MAXSIM_ERR_WORKSPACE;

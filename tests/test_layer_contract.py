@@ -149,6 +149,21 @@ def test_loss_spec_refusals(lib, change, status):
     assert lib.maxsim_cross_entropy_backward_workspace_size(_loss(**change)) == 0
 
 
+def test_rows_of_numbers_overlap_nothing_that_is_written(lib):
+    """x at 0x100000 has 10 rows of 64 bf16, 512 bytes apart: its last byte is 0x10127F."""
+    for kw in (dict(format=1, scale=0x900010), dict(format=1, scale=0x10127C), dict(format=1, scale=0x300000, res=_v(0x300000)),
+               dict(format=1, scale=0x300020, sum=_v(0x300000)), dict(weight=0x900040), dict(weight=0x300000, sum=_v(0x300000))):
+        assert _norm(lib, **kw) == INVALID, kw
+    out = _v(0x900000)
+    for kw in (dict(dx=out, weight=0x900000), dict(dres=out, weight=0x900000), dict(dx=out, dw=0x900040, ws=0x1000, n=BIG),
+               dict(dres=out, dw=0x900040, ws=0x1000, n=BIG)):
+        assert _norm_bwd(lib, **kw) == INVALID, kw
+    for kw in (dict(loss=0x4000), dict(loss=0x4024), dict(lse=0x100000), dict(loss=0x10127C), dict(lse=0x900000), dict(loss=0x2048)):
+        assert _forward(lib, **kw) == INVALID, kw
+    for kw in (dict(dx=_v(0x3000)), dict(dw=_v(0x4000)), dict(dx=_v(0x4000)), dict(dw=_v(0x2000, 64))):
+        assert _backward(lib, **kw) == INVALID, kw
+
+
 @pytest.mark.parametrize("bad", [_v(0), _v(0x100008), _v(stride=100), _v(stride=0), _v(stride=-64), _v(stride=56)])
 def test_loss_view_refusals(lib, bad):
     assert _forward(lib, x=bad) == INVALID and _forward(lib, w=bad) == INVALID
