@@ -5,8 +5,8 @@
 //   8 bits: scale = max(max |y|, 1e-30) / top,  code = round(y / scale)
 //
 // One pass: x and the residual are read once, and the sum stays in registers as it is
-// kept. With 8-bit output the sum of squares and the largest |h w| are found together,
-// and y / scale = h w (top / max |h w|) needs no second look at the row.
+// kept. With 8-bit output the sum of squares and the largest |h w| are found together:
+// max |y| = rstd max |h w| needs no second look at the row, and y / scale = (h w rstd) (top / max |y|).
 // A team of threads has a row, eight neighbouring columns a thread and group: part of
 // a warp up to 256 columns, a warp up to 1024, a block beyond. Its next rows are on
 // their way to shared memory (norm.cuh). Bound by HBM: 98304 x 2048 bf16 with residual
@@ -148,8 +148,10 @@ __global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256, Shape<T, kTeam, kGro
       const float top = whole_numbers ? 127.f : 448.f;
       float reach = most * rstd;
       reach = reach < kLeast ? kLeast : reach;  // NaN stays
-      const float factor = __fdividef(0.25f * top * rstd, 0.25f * reach);  // whose divisors end at 2^126
-      const Pair f2(factor, factor);
+      const float steps = __fdividef(0.25f * top, 0.25f * reach);  // whose divisors end at 2^126
+      // y first: its product with steps stays in range, while top rstd / reach and top / max |h w|
+      // leave it for small rows where eps is small
+      const Pair r2(rstd, rstd), s2(steps, steps);
       if (t == 0 && live) p.scale[row] = reach / top;
       uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.out_stride;
 #pragma unroll
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(kTeam > 32 ? kTeam : 256, Shape<T, kTeam, kGro
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float a, b;
-          mul2(mul2(h.p[i], w.p[i]), f2).get(a, b);
+          mul2(mul2(mul2(h.p[i], w.p[i]), r2), s2).get(a, b);
           if (whole_numbers) {  // |a| <= 127 (1 + 2^-21): no code is -128
             int q, s;
             asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(q) : "f"(a));
