@@ -709,7 +709,9 @@ maxsim_status maxsim_cross_entropy(const maxsim_loss_spec *spec, const maxsim_ro
  * dx or dweight may be NULL (a frozen side). Rows without a target have gradient 0;
  * x has to be finite there, too (0 * infinity is NaN in dweight). A dloss
  * that is not finite spoils its row of dx and dweight, no other row of dx.
- * The logits are made again, a piece of the vocabulary at a time: the workspace
+ * The logits are made again as the forward made them, to the last bit: what a target's
+ * exp(z - lse) - 1 is off by is the rounding of lse, |lse| 2^-22 at most, and of fp32 sums of the
+ * exponentials (2^-18 with 65536 columns). They come a piece of the vocabulary at a time: the workspace
  * holds one piece's dz in the inputs' type (256 MB, or 256 columns where T is above
  * 524288), divided by the largest |dloss| so that small ones lose no bits, fp32 sums
  * of dx where the vocabulary has several pieces or there are few rows, and of dweight

@@ -47,8 +47,10 @@ constexpr int kBars = 2 * kStages + 2 * kAcc + 1;
 constexpr int kSmallBytes = kBars * 8 + 16;
 constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiWarps * kStageOut + kSmallBytes;
 // The tensor core cuts each sum towards zero, so a logit of d = 2048 is off by some
-// 1e-6 of itself in one direction. kStats adds no more than this many steps there and
-// the parts in registers, with rounding: a quarter of that, and no more time.
+// 1e-6 of itself in one direction. kStats and kGrad add no more than this many steps there and
+// the parts in registers, with rounding: a quarter of that, and no more time (backward 8192 x
+// 65536 x 2048 3831 us as one sum and 3831 in parts, 4096 x 16384 x 2048 492 and 506). Both have to:
+// where exp(z - lse) is next to 1, what is left of it minus 1 is only as good as z is the forward's.
 constexpr int kPartSteps = 8;
 constexpr int kGroupM = 32;  // row tiles that share a pass over the vocabulary (4096 x 19456 x 2048: 32 165 us, 16 163, 8 166, 4 173)
 
@@ -281,7 +283,7 @@ __device__ void multiply(const Params& p, const Smem& sm, uint32_t tmem_base) {
     const uint64_t ad0 = a_mn ? mnmajor : kmajor, bd0 = (b_mn ? mnmajor : kmajor) + ((2 * kBoxBytes) >> 4);
     const uint64_t a_step = a_mn ? 2048 >> 4 : 2, b_step = b_mn ? 2048 >> 4 : 2;
     for (int k = 0; ok && k < t.steps;) {
-      const int part = kMode == kStats ? min(t.steps, k + kPartSteps) : t.steps;
+      const int part = kMode == kSums ? t.steps : min(t.steps, k + kPartSteps);
       if (!mbar_wait_warp(sm.accempty + 8 * a, aph ^ 1u, sm.abort_flag, p.status)) {
         ok = false;
         break;
@@ -422,7 +424,7 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
     if (t.steps == 0) continue;
     uint32_t v[4][32];
     bool ok = true;
-    for (int k = 0; k < t.steps; k += kMode == kStats ? kPartSteps : t.steps) {
+    for (int k = 0; k < t.steps; k += kMode == kSums ? t.steps : kPartSteps) {
       __syncwarp();
       ok = mbar_wait_warp(sm.accfull + 8 * a, aph, sm.abort_flag, p.status);
       if (!ok) break;

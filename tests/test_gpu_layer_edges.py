@@ -23,6 +23,13 @@ def _lib():
     assert m.maxsim_device_status() == (0, 0)
 
 
+def _uniform(shape, seed, lo=0.5, hi=1.5):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.rand(shape, generator=g) * (hi - lo) + lo).to(DEV)
+
+
+# ------------------------------------------------------------ rows in 8 bits
+
 @pytest.mark.parametrize("fmt,top", [("int8", 127.0), ("e4m3", 448.0)])
 @pytest.mark.parametrize("eps", [1e-6, 1e-12, 2.0 ** -60])
 @pytest.mark.parametrize("d", [64, 100, 200, 768, 2048])
@@ -47,3 +54,45 @@ def test_eight_bits_of_small_rows(fmt, top, eps, d):
 
 
 # -------------------------------------------------- logits, losses, gradients
+
+def _confident(d, V, z, dtype, seed=1, T=33):
+    """Rows whose target, column 0, has a logit of some z, the others of z - 17: all
+    products of one sign. The last element is the target's alone: what dx has there is q - 1
+    times dloss."""
+    x = _uniform((T, d), seed)
+    w = _uniform((V, d), seed + 1, 0.9, 1.1) * (z / d)
+    w[1:] *= (z - 17.0) / z
+    x, w = x.to(dtype), w.to(dtype)
+    x[:, -1], w[:, -1] = 0.0, 0.0
+    w[0, -1] = 1.0
+    return x, w, torch.zeros(T, dtype=torch.int64, device=DEV)
+
+
+# The sum of 300 exponentials, the largest of them 1, in fp32: an accumulator adds 32 (to 1 or
+# more, where what is small loses up to 2^-24 each time), two steps join four of them, one a
+# warp's parts, five the warps; the exponential of the largest is off by 2^-22, the logarithm
+# by 2^-23, the difference and its product with ln 2 by less: 32 + 2 + 1 + 5 + 4 + 2 + 2.
+SUMS = 48 * 2.0 ** -24
+
+
+def _softmax(x, w, scale=1.0):
+    z = x.double() @ w.double().T * scale
+    return z, torch.logsumexp(z, 1)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d,z", [(64, 30.0), (2048, 30.0), (2048, 100.0), (8192, 100.0), (65536, 60.0)])
+def test_gradient_of_confident_rows(dtype, d, z):
+    """The backward's logits are the forward's to the last bit, so q = exp(z - lse) near 1
+    is off by the rounding of numbers of lse's size alone: the sum, its product with ln 2, the
+    product with 1 / ln 2 (2^-24 each), both constants (2^-25); and by SUMS. What else q has is
+    off by 2^-17 of the logits. With all of d in one sum, cut towards zero, q was off
+    by 1e-4 at d = 2048 and z = 100."""
+    x, w, t = _confident(d, 300, z, dtype)
+    _, lse = m.encoder_cross_entropy(x, w, t)
+    dx, dw = m.encoder_cross_entropy_backward(torch.ones(33, device=DEV), x, w, t, lse)
+    zz, lse64 = _softmax(x, w)
+    want = torch.expm1(zz[:, 0] - lse64)
+    assert (want < 0).all() and (want > -0.01).all()
+    off = 4 * 2.0 ** -24 * lse64.abs() + SUMS
+    ref.within(dx[:, -1], want, off + (2 * ref.U[dtype] + 2.0 ** -17 * z) * want.abs() + 2 * ref.TINY[dtype])
