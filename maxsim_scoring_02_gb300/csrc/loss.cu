@@ -632,7 +632,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // A row's parts become its lse and loss: 32 rows a block, 32 warps along the parts,
 // each with eight loads in flight.
 __global__ void __launch_bounds__(1024) join_kernel(const float2* parts, int n, int T, int64_t V, const int64_t* targets,
-                                                    const float* hit, float scale, float* loss, float* lse,
+                                                    const float* hit, float z2, float* loss, float* lse,
                                                     unsigned* status) {
   __shared__ float2 s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x * 32 + lane;
@@ -665,11 +665,12 @@ __global__ void __launch_bounds__(1024) join_kernel(const float2* parts, int n, 
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
   const int mine_row = blockIdx.x * 32 + warp;
   if (lane || mine_row >= T) return;
-  const float l = (top + log2f(sum)) * kLn2;
-  lse[mine_row] = l;
+  const float over = log2f(sum);  // the maximum's own logit included
+  lse[mine_row] = (top + over) * kLn2;
   const int64_t t = targets[mine_row];
   if (t >= V) atomicOr(status, kDevErrBadInput);
-  loss[mine_row] = t >= 0 && t < V ? l - hit[mine_row] * scale : 0.f;
+  // from the maximum, not from lse: small losses are no difference of large rounded numbers
+  loss[mine_row] = t >= 0 && t < V ? (over - fmaf(hit[mine_row], z2, -top)) * kLn2 : 0.f;
 }
 
 // The largest |dloss| of many rows: more than each block of kGrad should read.
@@ -861,7 +862,7 @@ maxsim_status launch_loss(const LossShape& s, const maxsim_rows& x, const maxsim
       return MAXSIM_ERR_CUDA;
     if (launch<kStats>(maps, p, *dev, static_cast<int64_t>(p.tiles_m) * p.tiles_n, copied || row > 0, stream) != cudaSuccess ||
         launch_after(join_kernel, up_to(p.s.T, 32), 1024, 0, stream, p.parts, up_to(s.V, kHalf), p.s.T, s.V, p.targets,
-                     p.hit, s.scale, loss + row, lse + row, dev->status) != cudaSuccess)
+                     p.hit, p.z2, loss + row, lse + row, dev->status) != cudaSuccess)
       return MAXSIM_ERR_CUDA;
   }
   return MAXSIM_OK;

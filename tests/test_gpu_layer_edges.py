@@ -96,3 +96,16 @@ def test_gradient_of_confident_rows(dtype, d, z):
     assert (want < 0).all() and (want > -0.01).all()
     off = 4 * 2.0 ** -24 * lse64.abs() + SUMS
     ref.within(dx[:, -1], want, off + (2 * ref.U[dtype] + 2.0 ** -17 * z) * want.abs() + 2 * ref.TINY[dtype])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d,z", [(64, 30.0), (2048, 100.0), (2048, 1000.0)])
+def test_loss_of_confident_rows(dtype, d, z):
+    """A loss near 0 is no difference of two rounded numbers of lse's size: off by SUMS,
+    whatever the logits."""
+    x, w, t = _confident(d, 300, z, dtype)
+    loss, _ = m.encoder_cross_entropy(x, w, t)
+    zz, lse = _softmax(x, w)
+    want = torch.log1p(torch.exp(zz[:, 1:] - zz[:, :1]).sum(1))
+    # the others' logits, and the target's, are off by 2^-18 of themselves at most
+    ref.within(loss, want, SUMS + want * 2.0 ** -17 * z)
