@@ -350,7 +350,16 @@ __device__ __forceinline__ void send(const CUtensorMap* map, uint32_t stage, int
 
 // The sums of dz's products are multiplied by this at the end.
 __device__ __forceinline__ float usable(float top) { return top > 0.f ? top : 1.f; }
-__device__ __forceinline__ float gain_of(const float* top, float scale, float more) { return usable(*top) / more * scale; }
+// By both parts one after the other where their product leaves the normal numbers, which the
+// results need not do.
+struct Gain {
+  float first, then;
+  __device__ __forceinline__ float of(float sum) const { return sum * first * then; }
+};
+__device__ __forceinline__ Gain gain_of(const float* top, float scale, float more) {
+  const float a = usable(*top) / more, both = a * scale;
+  return both >= 0x1p-126f && both < INFINITY ? Gain{both, 1.f} : Gain{a, scale};
+}
 // The largest finite |dloss| of rows with a target, found by n threads (a row whose own is
 // not spoils no other one's); bad targets are reported.
 __device__ __forceinline__ float largest(const float* dloss, const int64_t* targets, int T, int64_t V, int thread, int n,
@@ -377,7 +386,7 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
   uint32_t aph = 0;
   Tile t;
   float whole = 1.f;  // what dloss is divided by
-  float gain = 1.f;
+  Gain gain = {};
   if constexpr (kMode == kGrad) {
     float top;
     if (p.scan) {  // each block finds it for itself, while its first tile is made
@@ -566,8 +575,8 @@ __device__ void finish(const Params& p, const Smem& sm, const Maps& maps, uint32
           uint32_t w[32];
 #pragma unroll
           for (int x = 0; x < 64; x += 2)
-            w[x / 2] = pack2<kBf16>(__uint_as_float(v[c + x / 32][x % 32]) * gain,
-                                    __uint_as_float(v[c + x / 32][x % 32 + 1]) * gain);
+            w[x / 2] = pack2<kBf16>(gain.of(__uint_as_float(v[c + x / 32][x % 32])),
+                                    gain.of(__uint_as_float(v[c + x / 32][x % 32 + 1])));
           if (lane == 0) store_wait_read();
           __syncwarp();
           put_row(stage, lane, w);
@@ -694,7 +703,7 @@ __global__ void __launch_bounds__(256) fold_kernel(const float* sums, int splits
   const int64_t i = (blockIdx.x * int64_t(256) + threadIdx.x) * 8;
   wait_for_previous();
   if (i >= n) return;
-  const float gain = gain_of(top, scale, more);
+  const Gain gain = gain_of(top, scale, more);
   float a[8] = {};
   for (int s = 0; s < splits; ++s) {
     const float4* q = reinterpret_cast<const float4*>(sums + s * n + i);
@@ -704,7 +713,7 @@ __global__ void __launch_bounds__(256) fold_kernel(const float* sums, int splits
   const int64_t row = i / d;
   alignas(16) T o[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = static_cast<T>(a[j] * gain);
+  for (int j = 0; j < 8; ++j) o[j] = static_cast<T>(gain.of(a[j]));
   *reinterpret_cast<uint4*>(out + row * stride + (i - row * d)) = *reinterpret_cast<uint4*>(o);
 }
 

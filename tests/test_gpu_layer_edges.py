@@ -109,3 +109,21 @@ def test_loss_of_confident_rows(dtype, d, z):
     want = torch.log1p(torch.exp(zz[:, 1:] - zz[:, :1]).sum(1))
     # the others' logits, and the target's, are off by 2^-18 of themselves at most
     ref.within(loss, want, SUMS + want * 2.0 ** -17 * z)
+
+
+def test_a_large_dloss_times_a_large_scale():
+    """Their product leaves fp32's range, results do not: they are what the formula says, and
+    0 in rows without a target."""
+    _check(*_many(90, 700, 64, torch.bfloat16, 2.0 ** -30, 2.0 ** 96), scale=2.0 ** 60)
+    _check(*_many(5000, 40, 64, torch.bfloat16, 2.0 ** -30, 2.0 ** 96), scale=2.0 ** 60)
+
+
+def test_a_small_dloss_times_a_small_scale():
+    """Their product is below the normal numbers, results are not."""
+    _check(*_many(90, 700, 64, torch.bfloat16, 2.0 ** 30, 2.0 ** -80), scale=2.0 ** -60)
+    _check(*_many(5000, 40, 64, torch.bfloat16, 2.0 ** 30, 2.0 ** -80), scale=2.0 ** -60)
+
+
+def _many(T, V, d, dtype, of, times):
+    x, w, t, dloss = _inputs(T, V, d, dtype)
+    return x * of, w * of, t, dloss * times
