@@ -477,7 +477,7 @@ maxsim_status maxsim_rotary(const maxsim_heads *x, int64_t T, int heads, int d, 
  *
  * Limits: dtype BF16 or FP16 (FP32 returns MAXSIM_ERR_UNSUPPORTED); d a
  * multiple of 8, 8 <= d <= 128; heads a multiple of kv_heads, heads <= 65535;
- * T < 2^31 - 256; B < 2^31, and not 0 unless T is; scale, and a cap > 0, from 2^-60 to 2^60; all views 16-byte aligned with strides that are
+ * T < 2^31 - 257; B < 2^31, and not 0 unless T is; scale, and a cap > 0, from 2^-60 to 2^60; all views 16-byte aligned with strides that are
  * multiples of 8 elements, positive and below 2^39. out may overlap no input.
  * Inconsistent offsets, a key_len outside [0, length] (clamped) or a negative
  * prefix_len (taken as 0) set MAXSIM_DEVERR_BAD_INPUT; a document whose offsets
@@ -594,7 +594,7 @@ typedef struct maxsim_rows {
  *                     captured call reads them when it is replayed.
  *
  * A dropped element is 0 (or the residual) even where x is not finite. Arithmetic is
- * fp32, rounded once. Limits: T < 2^31 - 256, row strides below 2^38. Views whose
+ * fp32, rounded once. Limits: T, d < 2^31 - 257, row strides below 2^38. Views whose
  * rows do not all begin on 16-byte boundaries, or whose d is not a multiple of 8, are
  * moved element by element.
  */
@@ -624,7 +624,7 @@ maxsim_status maxsim_dropout(const maxsim_rows *x, const maxsim_rows *residual, 
  *
  * Overlaps as in maxsim_dropout; sum and out may not be the same, scale overlaps no
  * view, weight neither of those written. Sums are fp32, and
- * fp64 where squares leave fp32's range. Limits: d <= 16384, T < 2^31 - 256, eps
+ * fp64 where squares leave fp32's range. Limits: d <= 16384, T < 2^31 - 257, eps
  * from 2^-60 to 2^60.
  */
 typedef enum maxsim_norm_format {
@@ -685,7 +685,7 @@ maxsim_status maxsim_rms_norm_backward(const maxsim_norm_spec *spec, const maxsi
  * most, or what 256 rows need: 2048 bytes for 128 columns; and a copy of x where d is
  * no multiple of 64), 16-byte aligned; calls that may run at the same time need one each, here and below.
  * Limits: FP32 returns MAXSIM_ERR_UNSUPPORTED; d a multiple of 8, d <= 65536;
- * V >= 1; T, V < 2^31 - 256; scale from 2^-60 to 2^60; views 16-byte aligned with
+ * V >= 1; T, V < 2^31 - 257; scale from 2^-60 to 2^60; views 16-byte aligned with
  * strides that are multiples of 8 and at least d.
  */
 typedef struct maxsim_loss_spec {

@@ -103,7 +103,7 @@ maxsim_status maxsim_dropout(const maxsim_rows* x, const maxsim_rows* residual, 
                              const int64_t* rng, maxsim_dtype dtype, const maxsim_rows* out, void* stream) {
   Drop drop;
   if (T < 0 || d < 1 || !known(dtype) || !drop_of(p, rng, drop)) return MAXSIM_ERR_INVALID_ARG;
-  if (T >= INT_MAX - 256) return MAXSIM_ERR_UNSUPPORTED;
+  if (T >= INT_MAX - 256 || d >= INT_MAX - 256) return MAXSIM_ERR_UNSUPPORTED;
   if (T == 0) return MAXSIM_OK;
   const int e = size_of(dtype);
   const View vx{x, T, d, e}, vr{residual, T, d, e}, vo{out, T, d, e};
