@@ -931,6 +931,8 @@ def _first_rows(x, name, dtypes, said):
     if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
     shape = x.shape
+    if shape[1] > 0x7FFFFFFF:  # the library takes a width in 32 bits, of which ctypes would pass on the lower ones
+        raise MaxSimError(2, f"{name} of {shape[1]} columns")
     row, last = x.stride()
     if last != 1 and shape[1] != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
