@@ -591,7 +591,8 @@ typedef struct maxsim_rows {
  *   p                 0 <= p < 1 - 2^-17; the chance is limit / 65536
  *   rng               [2] int64 on the DEVICE (NULL where limit is 0): a seed, and
  *                     a number that differs between the calls that share it. A
- *                     captured call reads them when it is replayed.
+ *                     captured call reads them when it is replayed. out does not overlap them
+ *                     (where limit is not 0).
  *
  * A dropped element is 0 (or the residual) even where x is not finite. Arithmetic is
  * fp32, rounded once. Limits: T, d < 2^31 - 257, row strides below 2^38. Views whose
@@ -623,7 +624,7 @@ maxsim_status maxsim_dropout(const maxsim_rows *x, const maxsim_rows *residual, 
  *                p and rng as in maxsim_dropout (p = 0: no dropout)
  *
  * Overlaps as in maxsim_dropout; sum and out may not be the same, scale overlaps no
- * view, weight neither of those written. Sums are fp32, and
+ * view, weight and rng nothing that is written. Sums are fp32, and
  * fp64 where squares leave fp32's range. Limits: d <= 16384, T < 2^31 - 257, eps
  * from 2^-60 to 2^60.
  */
@@ -659,10 +660,11 @@ maxsim_status maxsim_rms_norm(const maxsim_norm_spec *spec, const maxsim_rows *x
  *   dx, dresidual  [T, d] views of dtype, each or NULL; either may be dy, h or
  *                dsum (same stride). Without dropout they are the same numbers.
  *   dweight      [d] of weight_dtype, or NULL; neither it nor weight overlaps dx or
- *                dresidual
+ *                dresidual, and rng nothing that is written
  * dweight is added up in an order that depends on T, d and the number of SMs alone,
  * without atomics. workspace: at least maxsim_rms_norm_backward_workspace_size(spec)
- * bytes, 16-byte aligned, where dweight is given. With T = 0 dweight is 0.
+ * bytes, 16-byte aligned, where dweight is given; it overlaps nothing else of the call.
+ * With T = 0 dweight is 0.
  */
 size_t maxsim_rms_norm_backward_workspace_size(const maxsim_norm_spec *spec);
 maxsim_status maxsim_rms_norm_backward(const maxsim_norm_spec *spec, const maxsim_rows *dy, const maxsim_rows *h,
@@ -683,7 +685,8 @@ maxsim_status maxsim_rms_norm_backward(const maxsim_norm_spec *spec, const maxsi
  * not makes its own lse and loss NaN, no other row's.
  * workspace: at least maxsim_cross_entropy_workspace_size(spec) bytes (256 MB at the
  * most, or what 256 rows need: 2048 bytes for 128 columns; and a copy of x where d is
- * no multiple of 64), 16-byte aligned; calls that may run at the same time need one each, here and below.
+ * no multiple of 64), 16-byte aligned; it overlaps nothing else of the call, and calls that
+ * may run at the same time need one each, here and below.
  * Limits: FP32 returns MAXSIM_ERR_UNSUPPORTED; d a multiple of 8, d <= 65536;
  * V >= 1; T, V < 2^31 - 257; scale from 2^-60 to 2^60; views 16-byte aligned with
  * strides that are multiples of 8 and at least d.

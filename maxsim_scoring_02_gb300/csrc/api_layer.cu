@@ -4,6 +4,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "loss.cuh"
 #include "norm.cuh"
@@ -53,6 +54,24 @@ bool apart(const View& a, const View& b, bool may_be_same = true) {
 bool apart(const View& a, const void* p, int64_t n, int e) {
   const uintptr_t first = reinterpret_cast<uintptr_t>(p);
   return !a.given() || !p || a.last() <= first || first + n * e <= a.first();
+}
+
+// The same for other memory that the call reads or writes: `size` bytes at p.
+struct Bytes {
+  const void* p;
+  size_t size;
+  uintptr_t first() const { return reinterpret_cast<uintptr_t>(p); }
+};
+bool apart(const Bytes& a, const Bytes& b) {
+  return !a.p || !b.p || a.first() + a.size <= b.first() || b.first() + b.size <= a.first();
+}
+// Whether a workspace, or a row of results, leaves all views and all other memory of its call alone.
+bool alone(const Bytes& a, std::initializer_list<const View*> views, std::initializer_list<Bytes> others) {
+  for (const View* v : views)
+    if (!apart(*v, a.p, static_cast<int64_t>(a.size), 1)) return false;
+  for (const Bytes& b : others)
+    if (!apart(a, b)) return false;
+  return true;
 }
 
 // The chance of being dropped as a limit of 16-bit lots.
@@ -108,7 +127,7 @@ maxsim_status maxsim_dropout(const maxsim_rows* x, const maxsim_rows* residual, 
   const int e = size_of(dtype);
   const View vx{x, T, d, e}, vr{residual, T, d, e}, vo{out, T, d, e};
   if (!vx.readable() || (residual && !vr.readable()) || !vo.writable()) return MAXSIM_ERR_INVALID_ARG;
-  if (!apart(vo, vx) || !apart(vo, vr)) return MAXSIM_ERR_INVALID_ARG;
+  if (!apart(vo, vx) || !apart(vo, vr) || (drop.limit && !apart(vo, rng, 2, 8))) return MAXSIM_ERR_INVALID_ARG;
   return launch_dropout(*x, residual, static_cast<int>(T), d, drop, dtype, *out, static_cast<cudaStream_t>(stream));
 }
 
@@ -128,8 +147,9 @@ maxsim_status maxsim_rms_norm(const maxsim_norm_spec* spec, const maxsim_rows* x
   else if (!scale || !multiple(scale, 4)) return MAXSIM_ERR_INVALID_ARG;
   for (const View* v : {&vx, &vr, &vs, &vo})
     if (!apart(*v, scale, T, 4)) return MAXSIM_ERR_INVALID_ARG;
-  for (const View* v : {&vs, &vo})
-    if (!apart(*v, spec->weight, d, size_of(spec->weight_dtype))) return MAXSIM_ERR_INVALID_ARG;
+  const Bytes weight{spec->weight, static_cast<size_t>(d) * size_of(spec->weight_dtype)}, rng{drop.limit ? spec->rng : nullptr, 16};
+  if (!alone(weight, {&vs, &vo}, {}) || !alone(rng, {&vs, &vo}, {}) || !alone({scale, static_cast<size_t>(T) * 4}, {}, {weight, rng}))
+    return MAXSIM_ERR_INVALID_ARG;
   NormParams p = {};
   p.x = x->data, p.x_stride = x->row_stride;
   if (residual) p.res = residual->data, p.res_stride = residual->row_stride;
@@ -172,10 +192,12 @@ maxsim_status maxsim_rms_norm_backward(const maxsim_norm_spec* spec, const maxsi
   for (const View* w : {&vx, &vr})
     if (!apart(*w, vy) || !apart(*w, vh) || !apart(*w, vm) || !apart(*w, spec->weight, d, ew) || !apart(*w, dweight, d, ew))
       return MAXSIM_ERR_INVALID_ARG;
-  if (!apart(vx, vr, false)) return MAXSIM_ERR_INVALID_ARG;
-  if (dweight && (!workspace || !multiple(workspace, 16) ||
-                  workspace_bytes < norm_bwd_workspace_bytes(static_cast<int>(T), d)))
-    return MAXSIM_ERR_WORKSPACE;
+  const Bytes weight{spec->weight, static_cast<size_t>(d) * ew}, sums{dweight, static_cast<size_t>(d) * ew},
+      rng{drop.limit ? spec->rng : nullptr, 16};
+  if (!apart(vx, vr, false) || !alone(rng, {&vx, &vr}, {sums})) return MAXSIM_ERR_INVALID_ARG;
+  const size_t need = norm_bwd_workspace_bytes(static_cast<int>(T), d);
+  if (dweight && (!workspace || !multiple(workspace, 16) || workspace_bytes < need)) return MAXSIM_ERR_WORKSPACE;
+  if (dweight && !alone({workspace, need}, {&vy, &vh, &vm, &vx, &vr}, {weight, sums, rng})) return MAXSIM_ERR_INVALID_ARG;
   NormParams p = {};
   p.x = dy->data, p.x_stride = dy->row_stride;
   p.res = h->data, p.res_stride = h->row_stride;
@@ -209,7 +231,9 @@ maxsim_status maxsim_cross_entropy(const maxsim_loss_spec* spec, const maxsim_ro
   for (const View* v : {&vl, &ve})
     if (!apart(*v, vx, false) || !apart(*v, vw, false) || !apart(*v, vt, false)) return MAXSIM_ERR_INVALID_ARG;
   if (!apart(vl, ve, false)) return MAXSIM_ERR_INVALID_ARG;
-  if (!workspace || !multiple(workspace, 16) || workspace_bytes < loss_workspace_bytes(s)) return MAXSIM_ERR_WORKSPACE;
+  const size_t need = loss_workspace_bytes(s);
+  if (!workspace || !multiple(workspace, 16) || workspace_bytes < need) return MAXSIM_ERR_WORKSPACE;
+  if (!alone({workspace, need}, {&vx, &vw, &vl, &ve, &vt}, {})) return MAXSIM_ERR_INVALID_ARG;
   return launch_loss(s, *x, *weight, spec->targets, loss, lse, workspace, static_cast<cudaStream_t>(stream));
 }
 
@@ -242,8 +266,10 @@ maxsim_status maxsim_cross_entropy_backward(const maxsim_loss_spec* spec, const 
         !apart(*a, spec->targets, s.T, 8))
       return MAXSIM_ERR_INVALID_ARG;
   if (!apart(vdx, vdw, false)) return MAXSIM_ERR_INVALID_ARG;
-  if (!workspace || !multiple(workspace, 256) || workspace_bytes < loss_bwd_workspace_bytes(s))
-    return MAXSIM_ERR_WORKSPACE;
+  const size_t need = loss_bwd_workspace_bytes(s), row = static_cast<size_t>(s.T) * 4;
+  if (!workspace || !multiple(workspace, 256) || workspace_bytes < need) return MAXSIM_ERR_WORKSPACE;
+  if (!alone({workspace, need}, {&vx, &vw, &vdx, &vdw}, {{dloss, row}, {lse, row}, {spec->targets, 2 * row}}))
+    return MAXSIM_ERR_INVALID_ARG;
   return launch_loss_bwd(s, dloss, *x, *weight, spec->targets, lse, dx, dweight, workspace, on);
 }
 

@@ -36,3 +36,37 @@ def test_widths_beyond_32_bits_are_refused(monkeypatch):
             call()
         assert e.value.status == UNSUPPORTED
     assert not cuda.lib.calls
+
+
+# The views' places: x (or dy) at 0x100000, out at 0x900000, h at 0x600000; 10 rows of 64 bf16, 512 bytes apart.
+
+def test_rng_and_scale_overlap_nothing_that_is_written(lib):
+    assert _dropout(lib, rng=0x900010) == INVALID
+    assert _dropout(lib, rng=0x900000 + 9 * 512 + 120) == INVALID
+    for kw in (dict(rng=0x900010), dict(rng=0x800008, sum=_v(0x800000)), dict(rng=0x4000, format=1, scale=0x4008),
+               dict(weight=0x4000, format=1, scale=0x4000), dict(weight=0x4000, format=2, scale=0x40fc),
+               dict(weight=0x4000, format=1, scale=0x4000 - 36)):
+        assert _norm(lib, **kw) == INVALID, kw
+    for kw in (dict(dx=_v(0x900000), rng=0x900008), dict(dres=_v(0x900000), rng=0x900008),
+               dict(dw=0x7000, rng=0x70f8, ws=0x10000, n=BIG)):
+        assert _norm_bwd(lib, **kw) == INVALID, kw
+
+
+def test_workspaces_overlap_nothing_else(lib):
+    """A workspace that begins within what is read or written, or ends there."""
+    need = lib.maxsim_rms_norm_backward_workspace_size(_spec())
+    last = (need - 1) // 16 * 16
+    out, other = _v(0x900000), _v(0xa00000)
+    for at in (0x500000, 0x600000, 0x700000, 0x900000, 0xa00000, 0x3000, 0x7000, 0x2000):
+        for ws in (at, at - last):
+            assert _norm_bwd(lib, dsum=_v(0x700000), dx=out, dres=other, dw=0x7000, ws=ws, n=BIG) == INVALID, hex(ws)
+    need = lib.maxsim_cross_entropy_workspace_size(_loss())
+    last = (need - 1) // 16 * 16
+    for at in (0x100000, 0x900000, 0x2000, 0x3000, 0x4000):
+        for ws in (at, at - last):
+            assert _forward(lib, ws=ws, n=BIG) == INVALID, hex(ws)
+    need = lib.maxsim_cross_entropy_backward_workspace_size(_loss())
+    last = (need - 1) // 256 * 256
+    for at in (0x100000, 0x900000, 0x1100000, 0x1900000, 0x20000, 0x30000, 0x40000):
+        for ws in (at, at - last):
+            assert _backward(lib, dloss=0x30000, lse=0x40000, targets=0x20000, ws=ws, n=BIG) == INVALID, hex(ws)
