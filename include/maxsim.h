@@ -709,7 +709,8 @@ maxsim_status maxsim_cross_entropy(const maxsim_loss_spec *spec, const maxsim_ro
  * lse and the gradient dloss [T] fp32 of its loss:
  *   dz[t, v] = dloss[t] * scale * (exp(z[t, v] - lse[t]) - (v == targets[t]))
  *   dx = dz W [T, d],  dweight = dz^T x [V, d], in the inputs' dtype
- * dx or dweight may be NULL (a frozen side). Rows without a target have gradient 0;
+ * dx or dweight may be NULL (a frozen side, whose product is not made; with both NULL nothing
+ * is done); the workspace has room for both all the same. Rows without a target have gradient 0;
  * x has to be finite there, too (0 * infinity is NaN in dweight). A dloss
  * that is not finite spoils its row of dx and dweight, no other row of dx.
  * The logits are made again as the forward made them, to the last bit: what a target's

@@ -1153,7 +1153,7 @@ def encoder_cross_entropy_backward(dloss, x, weight, targets, lse, scale=1.0, dx
     """Gradients of encoder_cross_entropy for the gradient dloss [T] fp32 of its
     loss, from its lse; the other arguments as in that call. Returns dx [T, d]
     and dweight [V, d] in the inputs' type; a side that is not wanted, nor given, is
-    None and costs nothing."""
+    None, and its product is not made (the workspace has room for both all the same)."""
     lib = load_library()
     spec, xv, wv, index = _loss_spec(x, weight, targets, scale)
     n, dtype, device = spec.T, x.dtype, x.device
@@ -1170,12 +1170,13 @@ def encoder_cross_entropy_backward(dloss, x, weight, targets, lse, scale=1.0, dx
     elif want_dweight:
         dweight = torch.empty(weight.shape, dtype=dtype, device=device)
         dwv = _new_rows(dweight, spec.d)
-    if workspace is None:
-        workspace = _scratch(lib.maxsim_cross_entropy_backward_workspace_size(spec), device)
-    else:
+    if workspace is not None:
         _dev(workspace, "workspace", torch.uint8)
+    elif dxv is not None or dwv is not None:
+        workspace = _scratch(lib.maxsim_cross_entropy_backward_workspace_size(spec), device)
     st = lib.maxsim_cross_entropy_backward(spec, dloss.data_ptr(), xv, wv, lse.data_ptr(), dxv, dwv,
-                                           workspace.data_ptr(), workspace.numel(), _stream_on(stream, index))
+                                           None if workspace is None else workspace.data_ptr(),
+                                           0 if workspace is None else workspace.numel(), _stream_on(stream, index))
     if st:
         _check(st, "maxsim_cross_entropy_backward")
     return dx, dweight

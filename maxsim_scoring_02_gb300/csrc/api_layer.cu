@@ -266,6 +266,7 @@ maxsim_status maxsim_cross_entropy_backward(const maxsim_loss_spec* spec, const 
         !apart(*a, spec->targets, s.T, 8))
       return MAXSIM_ERR_INVALID_ARG;
   if (!apart(vdx, vdw, false)) return MAXSIM_ERR_INVALID_ARG;
+  if (!dx && !dweight) return MAXSIM_OK;
   const size_t need = loss_bwd_workspace_bytes(s), row = static_cast<size_t>(s.T) * 4;
   if (!workspace || !multiple(workspace, 256) || workspace_bytes < need) return MAXSIM_ERR_WORKSPACE;
   if (!alone({workspace, need}, {&vx, &vw, &vdx, &vdw}, {{dloss, row}, {lse, row}, {spec->targets, 2 * row}}))

@@ -70,3 +70,15 @@ def test_workspaces_overlap_nothing_else(lib):
     for at in (0x100000, 0x900000, 0x1100000, 0x1900000, 0x20000, 0x30000, 0x40000):
         for ws in (at, at - last):
             assert _backward(lib, dloss=0x30000, lse=0x40000, targets=0x20000, ws=ws, n=BIG) == INVALID, hex(ws)
+
+
+def test_gradients_that_nobody_wants(lib, monkeypatch):
+    """Neither dx nor dweight: the arguments are looked at, nothing is launched and no memory made."""
+    both = lambda **kw: lib.maxsim_cross_entropy_backward(_loss(**kw), 0x3000, _v(), _v(0x900000), 0x4000, None, None,  # noqa: E731
+                                                          None, 0, None)
+    assert both() == 0 and both(d=60) == UNSUPPORTED and both(targets=None) == INVALID
+    assert _backward(lib, ws=None, n=0) == WORKSPACE
+    cuda = fake.Cuda(monkeypatch, m)
+    x, w, t, row = cuda.tensor((6, 64), BF), cuda.tensor((9, 64), BF), cuda.tensor((6,), I64), cuda.tensor((6,), F32)
+    assert m.encoder_cross_entropy_backward(row, x, w, t, row, want_dx=False, want_dweight=False) == (None, None)
+    assert not cuda.made
