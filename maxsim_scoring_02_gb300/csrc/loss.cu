@@ -837,7 +837,8 @@ cudaError_t fold(const float* sums, int splits, int64_t rows, const LossShape& s
 // The forward takes as many rows at a time as 256 MB hold the parts of.
 static int stats_rows(const LossShape& s) {
   const int64_t most = kPieceBytes / (up_to(s.V, kHalf) * static_cast<int64_t>(sizeof(float2))) / kTile * kTile;
-  return most < kTile ? kTile : most < s.T ? static_cast<int>(most) : s.T;
+  const int64_t rows = most < kTile ? kTile : most;
+  return rows < s.T ? static_cast<int>(rows) : s.T;
 }
 
 size_t loss_workspace_bytes(const LossShape& s) {

@@ -127,3 +127,10 @@ def test_a_small_dloss_times_a_small_scale():
 def _many(T, V, d, dtype, of, times):
     x, w, t, dloss = _inputs(T, V, d, dtype)
     return x * of, w * of, t, dloss * times
+
+
+def test_a_few_rows_of_a_long_vocabulary():
+    """More columns than 256 MB hold the parts of for 256 rows: the workspace has room for the rows there are."""
+    x, w, t, _ = _inputs(3, (1 << 25) + 5, 8, torch.bfloat16)
+    assert m.encoder_cross_entropy_workspace_size(x, w, t) <= 3 * ((1 << 18) + 1) * 8 + 512
+    _check(x, w, t, None)

@@ -82,3 +82,11 @@ def test_gradients_that_nobody_wants(lib, monkeypatch):
     x, w, t, row = cuda.tensor((6, 64), BF), cuda.tensor((9, 64), BF), cuda.tensor((6,), I64), cuda.tensor((6,), F32)
     assert m.encoder_cross_entropy_backward(row, x, w, t, row, want_dx=False, want_dweight=False) == (None, None)
     assert not cuda.made
+
+
+@pytest.mark.parametrize("T,V", [(1, 2 ** 31 - 300), (3, 1 << 25), (255, 1 << 26), (256, 1 << 26), (1000, 1 << 26), (1, 1000)])
+def test_the_forwards_workspace_is_bounded(lib, T, V):
+    """A pair of numbers for 128 columns of a row: of all rows, of 256, or of what 256 MB hold."""
+    per = (V + 127) // 128 * 8
+    need = lib.maxsim_cross_entropy_workspace_size(_loss(T=T, V=V))
+    assert 0 < need <= max(min(T, 256) * per, min(T * per, 256 << 20)) + 4 * T + 512
