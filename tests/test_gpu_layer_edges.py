@@ -111,6 +111,42 @@ def test_loss_of_confident_rows(dtype, d, z):
     ref.within(loss, want, SUMS + want * 2.0 ** -17 * z)
 
 
+@pytest.mark.parametrize("d", [512, 1024, 2048, 8192, 65536])
+def test_long_rows(d):
+    """All products of one sign, evenly: a part of 512 is 32 additions cut towards zero,
+    each by up to 2^-23 of a sum that grows evenly, 33 / 2 steps of its whole; n parts are added with
+    rounding, (n + 1) / 2 steps of 2^-24. All of d = 8192 in one cut sum was off by 5e-6 of itself."""
+    T, V = 40, 9
+    x, w = _uniform((T, d), 3).bfloat16(), (_uniform((V, d), 4) * 60.0 / d).bfloat16()
+    t = torch.arange(T, device=DEV) % V
+    loss, lse = m.encoder_cross_entropy(x, w, t)
+    z, want = _softmax(x, w)
+    of = 33 / 2 * 2.0 ** -23 + (d / 512 + 1) / 2 * 2.0 ** -24
+    ref.within(lse, want, of * z.amax(1) + 2.0 ** -22 * want + 2.0 ** -20, "lse")
+    ref.within(loss, want - z.gather(1, t[:, None])[:, 0], 2 * of * z.amax(1) + 2.0 ** -20, "loss")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [4104, 65536])
+def test_gradients_of_long_rows(dtype, d):
+    """Random signs: the parts' cut is at most 32 * 2^-23 of the sizes' sum, and n steps of 2^-24."""
+    T, V = 40, 300
+    x, w, t, dloss = _inputs(T, V, d, dtype)
+    _, lse = m.encoder_cross_entropy(x, w, t)
+    dx, dw = m.encoder_cross_entropy_backward(dloss, x, w, t, lse)
+    z, want = _softmax(x, w)
+    X, W, u = x.double(), w.double(), ref.U[dtype]
+    off = (32 * 2.0 ** -23 + d / 512 * 2.0 ** -24) * (X.abs() @ W.abs().T).amax(1) + 2.0 ** -17 + 2.0 ** -22 * want.abs()
+    ref.within(lse, want, off, "lse")
+    part = torch.where(t >= 0, dloss.double(), 0.0)[:, None]
+    p = torch.exp(z - want[:, None])
+    hit = torch.nn.functional.one_hot(t.clamp_min(0), V).double()
+    dz = (p - hit) * part
+    E = u * dz.abs() + p * part.abs() * (2 * off[:, None] + 2.0 ** -18) + ref.TINY[dtype] * 2.0 ** -13 * dloss.abs().max().item()
+    ref.within(dx, dz @ W, (E + V * 2.0 ** -23 * dz.abs()) @ W.abs() + u * (dz @ W).abs() + ref.TINY[dtype], "dx")
+    ref.within(dw, dz.T @ X, (E + T * 2.0 ** -23 * dz.abs()).T @ X.abs() + u * (dz.T @ X).abs() + ref.TINY[dtype], "dw")
+
+
 def test_a_large_dloss_times_a_large_scale():
     """Their product leaves fp32's range, results do not: they are what the formula says, and
     0 in rows without a target."""
@@ -127,6 +163,76 @@ def test_a_small_dloss_times_a_small_scale():
 def _many(T, V, d, dtype, of, times):
     x, w, t, dloss = _inputs(T, V, d, dtype)
     return x * of, w * of, t, dloss * times
+
+
+# Rows by blocks, each of which has an element of its own, and one target: no sum of dW cancels.
+@pytest.mark.parametrize("T,V,d,dtype", [(40000, 3, 64, torch.bfloat16), (40000, 300, 64, torch.float16), (20001, 300, 136, torch.bfloat16),
+                                         (5000, 40, 520, torch.bfloat16), (600001, 300, 8, torch.float16), (9000, 17000, 64, torch.bfloat16)])
+def test_sums_that_do_not_cancel(T, V, d, dtype):
+    """dW[v, j] is the sum of dz[t, v] over the rows of block j: a part of the rows that is
+    lost, or added to another, changes an element by a part of itself. dz is rounded (u), n
+    additions of one sign cut by 2^-23 at most of what they have reached, (n + 1) / 2 of the
+    whole, and the result rounded (u)."""
+    block = torch.arange(T, device=DEV) * d // T
+    x = torch.nn.functional.one_hot(block, d).to(dtype)
+    w = (workloads.normal((V, d), seed=3, device=DEV)).to(dtype)
+    t = torch.where(torch.arange(T, device=DEV) % 5 == 4, -1, V // 2)
+    dloss = torch.full((T,), 0.75 * d / T, device=DEV)
+    _, lse = m.encoder_cross_entropy(x, w, t)
+    dx, dw = m.encoder_cross_entropy_backward(dloss, x, w, t, lse)
+    z = w.double().T                                   # of block j: all its rows are the same
+    p = torch.softmax(z, 1)
+    dz = (p - (torch.arange(V, device=DEV) == V // 2).double()) * dloss[0].double()
+    n = torch.zeros(d, dtype=torch.float64, device=DEV).index_add_(0, block, (t >= 0).double())
+    u, tiny = ref.U[dtype], ref.TINY[dtype]
+    E = u * dz.abs() + p * dloss[0].double() * 2.0 ** -15 + tiny * 2.0 ** -13 * dloss[0].double()
+    want = (dz * n[:, None]).T
+    fp = ((n + 1) / 2 * 2.0 ** -23)[None] * want.abs()
+    ref.within(dw, want, (E * n[:, None]).T + fp + u * want.abs() + tiny, "dw")
+    back = torch.where((t >= 0)[:, None], (dz @ w.double())[block], 0.0)
+    tol = ((E + (V + 1) / 2 * 2.0 ** -23 * dz.abs()) @ w.double().abs())[block]
+    ref.within(dx, back, torch.where((t >= 0)[:, None], tol, 0.0) + u * back.abs() + tiny, "dx")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [514, 40000])
+def test_columns_that_every_row_has_to_add_up(dtype, T):
+    """dx[t, j] is the sum of dz[t, v] over the columns of block j of the vocabulary: parts of the
+    columns (few rows) and pieces of it (a dloss a row)."""
+    V, d = (70001, 64) if T < 1000 else (9001, 16)
+    block = torch.arange(V, device=DEV) * d // V
+    w = torch.nn.functional.one_hot(block, d).to(dtype)
+    x = workloads.normal((T, d), seed=4, device=DEV).to(dtype)
+    t = torch.where(torch.arange(T, device=DEV) % 5 == 4, -1, V // 2)
+    dloss = _uniform((T,), 5)
+    _, lse = m.encoder_cross_entropy(x, w, t)
+    dx, _ = m.encoder_cross_entropy_backward(dloss, x, w, t, lse, want_dweight=False)
+    n = torch.bincount(block, minlength=d).double()
+    z = x.double()
+    each = torch.exp(z - torch.logsumexp(z + n.log(), 1)[:, None])       # p of a column of block j
+    part = torch.where(t >= 0, dloss.double(), 0.0)[:, None]
+    hit = (torch.arange(d, device=DEV) == block[V // 2]).double()
+    want = (each * n - hit) * part
+    u, tiny = ref.U[dtype], ref.TINY[dtype]
+    E = (each * n + hit) * part * (u + 2.0 ** -15) + tiny * 2.0 ** -13 * dloss.max().double() * n * (part > 0)
+    ref.within(dx, want, E + (n + 1) / 2 * 2.0 ** -23 * (each * n + hit) * part + u * want.abs() + tiny, "dx")
+
+
+@pytest.mark.parametrize("dtype,steps", [(torch.bfloat16, 257), (torch.float16, 2049)])
+def test_targets_of_equal_rows_are_exact(dtype, steps):
+    """dloss = (n + 1) / n is next to 1 in the inputs' type; n rows of it are n + 1, a number of
+    that type, and n (1 or its neighbour) if dz held dloss itself. Softmax's part, 1 / V a row, is
+    less than half a step there."""
+    V, d = 20000, 64
+    x = torch.zeros((steps, d), dtype=dtype, device=DEV)
+    x[:, 0] = 1.0
+    w = torch.zeros((V, d), dtype=dtype, device=DEV)
+    w[:, 1] = 1.0                                      # logits 0
+    t = torch.full((steps,), 777, device=DEV)
+    dloss = torch.full((steps,), (steps + 1) / steps, device=DEV)
+    _, lse = m.encoder_cross_entropy(x, w, t)
+    _, dw = m.encoder_cross_entropy_backward(dloss, x, w, t, lse)
+    assert dw[777, 0].item() == -(steps + 1)
 
 
 def test_a_few_rows_of_a_long_vocabulary():
