@@ -199,6 +199,13 @@ cudaError_t go(const NormParams& p, const DeviceInfo& dev, int* blocks, cudaStre
   return cudaGetLastError();
 }
 
+// Threads and groups of a row as in the forward, but for widths that are measured to be better
+// otherwise (one gradient, with what reaches the sum; us, bf16 and fp32, this form first):
+//   195312 x 768 three groups of a warp 187, 394; four 229, 565
+//   9155 x 16383 1024 threads 483, 785; 512 with four groups 508, 785; 16664 x 9001 707, 1134; 750, 1003
+// and as in the forward: 9155 x 16384 512 threads 191, 647; 1024 with two groups 190, 722; 74962 x 2001
+// 256 threads 480, 630; 512 with one group 961, 750; 37490 x 4001 388, 419; 554, 504.
+// fp32 rows of four groups, and rows of 1024 threads, spill.
 template <typename T>
 cudaError_t pick(const NormParams& p, bool whole, const DeviceInfo& dev, int* blocks, cudaStream_t stream) {
   if (whole) {
@@ -211,11 +218,11 @@ cudaError_t pick(const NormParams& p, bool whole, const DeviceInfo& dev, int* bl
     if (p.d <= 2048) return go<T, 128, 2, true>(p, dev, blocks, stream);
     if (p.d <= 4096) return go<T, 256, 2, true>(p, dev, blocks, stream);
     if (p.d <= 8192) return go<T, 512, 2, true>(p, dev, blocks, stream);
-    return go<T, 1024, 2, true>(p, dev, blocks, stream);
+    return go<T, 512, 4, true>(p, dev, blocks, stream);
   }
   if (p.d <= 256) return go<T, 32, 1, false>(p, dev, blocks, stream);
   if (p.d <= 1024) return go<T, 128, 1, false>(p, dev, blocks, stream);
-  if (p.d <= 4096) return go<T, 512, 1, false>(p, dev, blocks, stream);
+  if (p.d <= 4096) return go<T, 256, 2, false>(p, dev, blocks, stream);
   return go<T, 1024, 2, false>(p, dev, blocks, stream);
 }
 
