@@ -682,8 +682,11 @@ __global__ void __launch_bounds__(1024) join_kernel(const float2* parts, int n, 
   loss[mine_row] = t >= 0 && t < V ? (over - fmaf(hit[mine_row], z2, -top)) * kLn2 : 0.f;
 }
 
-// The largest |dloss| of many rows: more than each block of kGrad should read.
-constexpr int kScanRows = 32768;
+// The largest |dloss| of many rows: more than each block of kGrad should read. One block that
+// reads them all, against each for itself: 512 rows, 2 columns of 64 14.4 and 12.7 us for the whole
+// backward, 2048 16.8 and 16.9, 8192 20.7 and 24.9, 32768 29.0 and 47.5; 5000 columns of 512 29.0 and
+// 28.4, 45.9 and 44.9, 91.2 and 100, 408 and 434.
+constexpr int kScanRows = 2048;
 __global__ void __launch_bounds__(1024) top_kernel(const float* dloss, const int64_t* targets, int T, int64_t V, float* out,
                                                    unsigned* status) {
   __shared__ float s[32];
