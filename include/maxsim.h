@@ -717,7 +717,8 @@ maxsim_status maxsim_cross_entropy(const maxsim_loss_spec *spec, const maxsim_ro
  * exp(z - lse) - 1 is off by is the rounding of lse, |lse| 2^-22 at most, and of fp32 sums of the
  * exponentials (2^-18 with 65536 columns). They come a piece of the vocabulary at a time: the workspace
  * holds one piece's dz in the inputs' type (256 MB, or 256 columns where T is above
- * 524288), divided by the largest |dloss| so that small ones lose no bits, fp32 sums
+ * 524288), divided by the largest |dloss|: where all are small none loses bits (in FP16 its steps are
+ * 2^-38 of the largest or more: the dx of a row whose own is 2^-20 of that notices); fp32 sums
  * of dx where the vocabulary has several pieces or there are few rows, and of dweight
  * where there are few columns. Sums are added in an
  * order that depends on the sizes and the number of SMs alone.

@@ -11,7 +11,7 @@
 // a warp up to 256 columns, a warp up to 1024, a block beyond. Its next rows are on
 // their way to shared memory (norm.cuh). Bound by HBM: 98304 x 2048 bf16 with residual
 // and sum 235 us (6.9 TB/s), 30011 x 4096 to e4m3 130 (6.6), a million rows of 128 to
-// e4m3 66 (5.9; issue slots 72 % busy). With loads into registers the last two took 151
+// e4m3 68 (5.6; issue slots 71 % busy), to int8 74 (5.2). With loads into registers e4m3 took 151
 // and 169. Rows that are not whole: 200011 x 1001 bf16 200 us (4.0 TB/s), 2 bytes an access.
 #include <cuda_fp8.h>
 
@@ -28,7 +28,7 @@ struct Shape {
   using Rows = Queue<T, kBlock, kGroups, 2, sizeof(T) == 4 ? 0 : 75000, kWhole>;
   // Blocks of an SM that the registers have to allow; rows of a team, where a row takes a
   // warp or more, or of fp32: blocks that come and go even out what SMs do, fixed ones (a
-  // million rows of 128 to e4m3: 66 us, 75 with 32 rows a team) wait for the slowest (98304 x
+  // million rows of 128 to e4m3: 68 us, 75 with 32 rows a team) wait for the slowest (98304 x
   // 2048: 262 us, 235). fp32: 512 threads 244 us for 50000 x 2048, 1024 259.
   static constexpr int kFit = kTeam > 256 ? 1 : sizeof(T) == 4 ? 512 / kBlock : kTeam > 32 ? 1024 / kTeam : 2;
   static constexpr int kRounds = 8;

@@ -11,7 +11,9 @@
 // partial sums, and a second kernel adds those in order: no atomics, and results
 // depend on the sizes and the number of SMs alone. Bound by HBM: 24576 x 2048 bf16 with
 // dropout and both gradients 94 us and 5 for the second kernel (5.3 TB/s), 30011 x 4096
-// without 150 for both (6.5), a million rows of 128 124 (6.2).
+// without 150 for both (6.5), a million rows of 128 124 (6.2). By instructions where rows are not whole
+// (74962 x 2001 bf16 480, 2.5 TB/s), and by spilled registers where fp32 rows take four groups
+// (146484 x 1024 502, 4.8; bf16 208, 5.8; 195312 x 768 394, 6.1; 187, 6.4).
 #include "after.cuh"
 #include "norm.cuh"
 
@@ -205,7 +207,7 @@ cudaError_t go(const NormParams& p, const DeviceInfo& dev, int* blocks, cudaStre
 //   9155 x 16383 1024 threads 483, 785; 512 with four groups 508, 785; 16664 x 9001 707, 1134; 750, 1003
 // and as in the forward: 9155 x 16384 512 threads 191, 647; 1024 with two groups 190, 722; 74962 x 2001
 // 256 threads 480, 630; 512 with one group 961, 750; 37490 x 4001 388, 419; 554, 504.
-// fp32 rows of four groups, and rows of 1024 threads, spill.
+// fp32 rows of two groups or more, rows of four groups of a warp, and rows of 1024 threads spill.
 template <typename T>
 cudaError_t pick(const NormParams& p, bool whole, const DeviceInfo& dev, int* blocks, cudaStream_t stream) {
   if (whole) {
