@@ -1,5 +1,6 @@
 """Pretrains a one-layer token encoder on hidden tokens on a GPU, every operator but
-the matrix products of its projections from this library.
+the matrix products of its projections, and the embedding table's lookup with its
+gradient, from this library. The layer has no feed-forward part.
 
 Texts of random lengths, packed, in which some tokens are replaced by a mask token;
 the loss is the cross entropy of the hidden tokens over the whole vocabulary. The
